@@ -96,6 +96,7 @@ typedef enum {
 #define ATTN_DEV_TIMEOUT_DQ 0x8      /* ... in the dq kernel */
 #define ATTN_DEV_SMEM_ALIGN 0x10     /* dynamic shared memory base not 1024-byte aligned */
 #define ATTN_DEV_MASK_SPACE 0x20     /* keep-mask buffer smaller than the lengths need */
+#define ATTN_DEV_BAD_CACHE 0x40      /* a cache length or page number outside of its table or pool */
 
 /* Largest batch (number of sequences) accepted. */
 #define ATTN_MAX_BATCH 16384
@@ -567,6 +568,168 @@ attn_status attn_varlen_fvjp_fwd_bwd_noalloc(
     void *dk, int64_t dk_tok_stride, int64_t dk_head_stride,
     void *dv, int64_t dv_tok_stride, int64_t dv_head_stride,
     float *lse, int32_t *device_status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Generation: rotary positions, a paged K/V cache, attention over it with
+ * prefixes that sequences share, the attention weight each cached key has
+ * received, and eviction by it.
+ *
+ * The cache.  k_cache and v_cache are pools of pages [num_pages, page_size,
+ * Hkv, head_dim] of 16-bit elements with page, slot and head strides in
+ * elements (feature axis contiguous; strides multiples of 8, bases 16-byte
+ * aligned; page_size a power of two, 16 to 1024).  `table` is int32 [rows,
+ * table_width] with a row stride, `lens` int32 [rows]: slot j < lens[r] of
+ * row r is row j mod page_size of page table[r][j / page_size].  Whatever
+ * lies in the pages beyond a row's length, and table entries of pages that
+ * hold no slot below it, are never used (they may hold anything).  Inside the
+ * lengths every K and V row must be finite.
+ *
+ * Key positions.  Without a `key_pos` array the slot order is the position:
+ * slot j of a sequence has position prefix_len + j, slot j of a prefix
+ * position j.  Eviction leaves slots in another order; key_pos, int32 [rows,
+ * Hkv, >= table_width * page_size] with row and head strides, then says where
+ * each slot's key stands.  Positions lie in [0, 2^30).
+ *
+ * Errors.  These calls OR ATTN_DEV_* bits into `device_status` (an int32 on
+ * the device, or NULL), and never clear it: a caller zeroes it once and reads
+ * it when it likes.  Lengths that exceed the table or page numbers outside of
+ * the pool set ATTN_DEV_BAD_CACHE, inconsistent cu arrays ATTN_DEV_BAD_CU;
+ * the call then leaves out what they concern and never reads or writes out of
+ * range.  Query tokens at or behind cu_q[B] (a batch padded to the size of a
+ * captured graph) are left as they are in every output.  Workspaces belong to
+ * one call at a time: calls that may overlap need one each. */
+
+/* Rotary positions with several axes, in place or into other tensors.  Pair i
+ * of a row's first 2*pairs features -- (i, i + pairs), or (2i, 2i + 1) when
+ * `interleaved` -- is turned by positions[axis][token] * inv_freq[i], where
+ * axis = pair_axis[i] (int32 [pairs]; NULL: axis 0; values outside of [0,
+ * axes) are taken as the nearest axis):
+ *   a' = a cos t - b sin t,  b' = b cos t + a sin t.
+ * Features from 2*pairs on are copied.  `inverse` turns by -t: the
+ * vector-Jacobian product of the forward call (the map is orthogonal), so it
+ * takes dq, dk with respect to the turned q, k to those of the unturned ones.
+ * q is [total, Hq, head_dim] and k [total, Hkv, head_dim], packed and strided
+ * as elsewhere; k may be NULL (Hkv = 0).  positions is int32 [axes, total]
+ * with an axis stride, inv_freq float64 [pairs], all on the device.  The angle
+ * is reduced in integers, so far positions lose nothing.  q_out = q and k_out
+ * = k turn in place; other overlaps of an output with an input are not
+ * allowed. */
+attn_status attn_varlen_rotary(
+    attn_dtype dtype, int64_t total, int Hq, int Hkv, int head_dim,
+    const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+    const void *k, int64_t k_tok_stride, int64_t k_head_stride,
+    const int32_t *positions, int64_t axis_stride, int axes,
+    const double *inv_freq, const int32_t *pair_axis, int pairs, int interleaved, int inverse,
+    void *q_out, int64_t qo_tok_stride, int64_t qo_head_stride,
+    void *k_out, int64_t ko_tok_stride, int64_t ko_head_stride, void *stream);
+
+/* Append packed new tokens to the cache: token cu_new[b] + i of k, v
+ * ([total, Hkv, head_dim]) goes to slot lens[b] + i of sequence b, whose pages
+ * must be in the table already.  With inv_freq not NULL the K rows are turned
+ * on the way as in attn_varlen_rotary.  key_pos (may be NULL) receives, for
+ * every K/V head, positions[0][token] or, without positions, the slot number;
+ * scores (may be NULL; fp32, laid out like key_pos) receives 0.  lens_out (may
+ * be NULL, not `lens` itself) receives lens[b] plus the number of new tokens.
+ * The other slots are not touched.  No two rows of the table may share a page
+ * that is written here. */
+attn_status attn_varlen_cache_append(
+    attn_dtype dtype, int B, int Hkv, int head_dim, int64_t total,
+    const void *k, int64_t k_tok_stride, int64_t k_head_stride,
+    const void *v, int64_t v_tok_stride, int64_t v_head_stride,
+    void *k_cache, int64_t kc_page_stride, int64_t kc_slot_stride, int64_t kc_head_stride,
+    void *v_cache, int64_t vc_page_stride, int64_t vc_slot_stride, int64_t vc_head_stride,
+    int num_pages, int page_size, const int32_t *table, int64_t table_row_stride, int table_width,
+    const int32_t *lens, const int32_t *cu_new,
+    const int32_t *positions, int64_t axis_stride, int axes,
+    const double *inv_freq, const int32_t *pair_axis, int pairs, int interleaved,
+    int32_t *key_pos, int64_t kp_row_stride, int64_t kp_head_stride,
+    float *scores, int64_t sc_row_stride, int64_t sc_head_stride,
+    int32_t *lens_out, int32_t *device_status, void *stream);
+
+/* Attention of packed queries (one token per sequence or many) over the
+ * cache.  Sequence b reads its own slots and, when some p has cu_prefix[p] <=
+ * b < cu_prefix[p+1], first the slots of prefix p: prefix_table [P,
+ * prefix_width], prefix_lens [P], cu_prefix int32 [P+1] (non-decreasing,
+ * inside [0, B]).  The queries of all sequences of a prefix are put together,
+ * so its keys are read once.  With Lk = prefix length + own length, query i of
+ * Lq stands at position Lk - Lq + i, or at q_pos[token] when q_pos is given
+ * (required with key_pos).  Logits, softcap, ALiBi (fp32 slopes [B, Hq] times
+ * the distance of the positions), masks (on the positions), out and lse are
+ * those of attn_varlen_fwd (a slope batch stride of 0 gives every sequence the
+ * same slopes); rows without an admissible key get out = 0, lse =
+ * -inf.  lse is dense fp32 [total_q, Hq].  P = 0: no prefixes. */
+size_t attn_varlen_cache_fwd_workspace_size(int B, int P, int Hq, int Hkv, int head_dim,
+                                            int64_t total_q);
+attn_status attn_varlen_cache_fwd(
+    attn_dtype dtype, int B, int P, int Hq, int Hkv, int head_dim, int64_t total_q,
+    const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+    const void *k_cache, int64_t kc_page_stride, int64_t kc_slot_stride, int64_t kc_head_stride,
+    const void *v_cache, int64_t vc_page_stride, int64_t vc_slot_stride, int64_t vc_head_stride,
+    int num_pages, int page_size,
+    const int32_t *table, int64_t table_row_stride, int table_width, const int32_t *lens,
+    const int32_t *prefix_table, int64_t prefix_row_stride, int prefix_width,
+    const int32_t *prefix_lens, const int32_t *cu_prefix, const int32_t *cu_q,
+    const int32_t *q_pos, const int32_t *key_pos, int64_t kp_row_stride, int64_t kp_head_stride,
+    const int32_t *prefix_key_pos, int64_t pkp_row_stride, int64_t pkp_head_stride,
+    const float *alibi_slopes, int64_t slopes_batch_stride, int causal, int window_left,
+    int window_right, float softcap, float scale_multiplier,
+    void *out, int64_t out_tok_stride, int64_t out_head_stride, float *lse,
+    void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream);
+
+/* The attention weight that each cached key receives from these queries,
+ * summed over the query rows (tokens, and heads of the K/V head's group) that
+ * read it:  scores_out[b][g][j] = scores_in[b][g][j] + sum exp(z - lse), for
+ * j < lens[b] (the rest of scores_out is not touched); scores_in NULL: 0.
+ * scores_in and scores_out are fp32 [B, Hkv, >= max length] with row and head
+ * strides and may be the same array.  lse is what attn_varlen_cache_fwd wrote
+ * for the same queries, keys, masks and options.  With prefixes, prefix keys
+ * take part in prefix_scores_out [P, Hkv, ...] in the same way, summed over
+ * all sequences of the prefix; prefix_scores_out NULL: not wanted.  Sums are
+ * in a fixed order. */
+size_t attn_varlen_cache_weights_workspace_size(int B, int P, int Hq, int Hkv, int64_t total_q,
+                                                int64_t own_slots, int64_t prefix_slots);
+attn_status attn_varlen_cache_weights(
+    attn_dtype dtype, int B, int P, int Hq, int Hkv, int head_dim, int64_t total_q,
+    const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+    const void *k_cache, int64_t kc_page_stride, int64_t kc_slot_stride, int64_t kc_head_stride,
+    int num_pages, int page_size,
+    const int32_t *table, int64_t table_row_stride, int table_width, const int32_t *lens,
+    const int32_t *prefix_table, int64_t prefix_row_stride, int prefix_width,
+    const int32_t *prefix_lens, const int32_t *cu_prefix, const int32_t *cu_q,
+    const int32_t *q_pos, const int32_t *key_pos, int64_t kp_row_stride, int64_t kp_head_stride,
+    const int32_t *prefix_key_pos, int64_t pkp_row_stride, int64_t pkp_head_stride,
+    const float *alibi_slopes, int64_t slopes_batch_stride, int causal, int window_left,
+    int window_right, float softcap, float scale_multiplier, const float *lse,
+    const float *scores_in, int64_t si_row_stride, int64_t si_head_stride,
+    float *scores_out, int64_t so_row_stride, int64_t so_head_stride,
+    const float *prefix_scores_in, int64_t psi_row_stride, int64_t psi_head_stride,
+    float *prefix_scores_out, int64_t pso_row_stride, int64_t pso_head_stride,
+    void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream);
+
+/* Evict down to `budget` slots.  Of the n = lens[s] slots of row s, every K/V
+ * head keeps the min(n, budget) that rank first: those with key_pos >=
+ * next_pos[s] - recent (the most recent; 0 <= recent <= budget), then by
+ * scores descending (NaN last), equal scores by lowest slot.  In the K and V
+ * pages the i-th evicted slot below the new length takes the row of the i-th
+ * kept slot at or above it; other rows are not touched.  scores_out and
+ * key_pos_out receive the kept slots' values at their new places, lens_out the
+ * new lengths; each may be its input array (in place) or apart from it.  The
+ * rows may be sequences or shared prefixes (with their own tables); no two
+ * may share a page that holds slots. */
+size_t attn_varlen_cache_evict_workspace_size(int S, int Hkv, int table_width, int page_size,
+                                              int budget);
+attn_status attn_varlen_cache_evict(
+    int S, int Hkv, int head_dim,
+    void *k_cache, int64_t kc_page_stride, int64_t kc_slot_stride, int64_t kc_head_stride,
+    void *v_cache, int64_t vc_page_stride, int64_t vc_slot_stride, int64_t vc_head_stride,
+    int num_pages, int page_size, const int32_t *table, int64_t table_row_stride, int table_width,
+    const int32_t *lens, const float *scores, int64_t sc_row_stride, int64_t sc_head_stride,
+    const int32_t *key_pos, int64_t kp_row_stride, int64_t kp_head_stride,
+    const int32_t *next_pos, int budget, int recent,
+    float *scores_out, int64_t so_row_stride, int64_t so_head_stride,
+    int32_t *key_pos_out, int64_t po_row_stride, int64_t po_head_stride,
+    int32_t *lens_out, void *workspace, size_t workspace_bytes, int32_t *device_status,
+    void *stream);
 
 #ifdef __cplusplus
 }

@@ -17,7 +17,8 @@ LIB = os.path.join(PKG, "libattn_varlen.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["host.cu", "sched.cu", "fwd.cu", "bwd_dq.cu", "bwd_dkdv.cu", "bwd_dkdv_drop.cu", "bwd_dkdv_dmask.cu",
            "noalloc.cu",
-           "host_pipeline.cu", "shard.cu", "gate.cu"]
+           "host_pipeline.cu", "shard.cu", "gate.cu",
+           "cache_host.cu", "rotary.cu", "cache_attn.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-Wall"]

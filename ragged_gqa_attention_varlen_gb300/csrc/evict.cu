@@ -1,0 +1,250 @@
+// evict.cu -- eviction from the paged K/V cache by accumulated weight.
+//
+// Of the n = lens[s] slots of sequence s, K/V head g keeps the k = min(n,
+// budget) that rank first by (position >= next_pos[s] - recent, score, lowest
+// slot).  The kept keys behind the new end move into the evicted slots before
+// it: the i-th evicted slot below k takes the i-th kept slot at or above k.
+// Every destination is an evicted slot below k and every source lies at or
+// above k, so the moves never meet, run in any order and touch only the rows
+// that have to move (attention does not care about the order of its keys;
+// their positions travel with them).
+//
+// select_kernel: one block per (sequence, K/V head).  The k-th largest rank is
+// found digit by digit (four 8-bit histograms in shared memory; the ranks of
+// the first kSmemKeys slots stay there), then two counting passes over
+// contiguous slot ranges per warp number the ties, the holes and the movers
+// in slot order: no atomics decide an order, so results are repeatable.
+// move_kernel: the listed K and V rows, over the whole GPU.
+#include "../../include/attn_varlen.h"
+#include "cache.cuh"
+
+namespace attn {
+namespace kv {
+namespace {
+
+constexpr int kThreadsE = 1024;
+constexpr int kWarpsE = kThreadsE / 32;
+constexpr int kSmemKeys = 48 * 1024;  // ranks held in shared memory (192 KB)
+constexpr int kThreadsM = 256;
+
+struct EvictWs {
+  size_t newlen, counts, lists, total;
+  int64_t list_cap;
+};
+
+__host__ __device__ inline EvictWs evict_ws(int S, int Hkv, int64_t slots, int budget) {
+  EvictWs w;
+  const int64_t rest = slots > budget ? slots - budget : 0;
+  w.list_cap = rest < budget ? rest : budget;
+  w.newlen = 0;
+  w.counts = (static_cast<size_t>(S) * 4 + 255) / 256 * 256;
+  w.lists = w.counts + (static_cast<size_t>(S) * Hkv * 4 + 255) / 256 * 256;
+  w.total = w.lists + static_cast<size_t>(S) * Hkv * 2 * w.list_cap * 4 + 256;
+  return w;
+}
+
+// Scores as unsigned integers in the same order: NaN lowest, -0 = +0.  The
+// protected (recent) slots come above all.
+__device__ __forceinline__ uint32_t rank_key(float score, bool safe) {
+  if (safe) return 0xFFFFFFFFu;
+  if (!(score == score)) return 0u;
+  const uint32_t u = __float_as_uint(score + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__global__ void __launch_bounds__(kThreadsE)
+    select_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ uint32_t skey[];
+  __shared__ uint32_t hist[256];
+  __shared__ int s_digit, s_above;
+  __shared__ int cnt[3][kWarpsE];
+  const int s = blockIdx.x / p.Hkv, g = blockIdx.x - s * p.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t slots = static_cast<int64_t>(p.width) << p.page_log2;
+  const EvictWs w = evict_ws(p.S, p.Hkv, slots, p.budget);
+  int32_t* counts = reinterpret_cast<int32_t*>(p.ws + w.counts);
+  int32_t* newlen = reinterpret_cast<int32_t*>(p.ws + w.newlen);
+  int32_t* holes = reinterpret_cast<int32_t*>(p.ws + w.lists) + 2 * w.list_cap * blockIdx.x;
+  int32_t* movers = holes + w.list_cap;
+  const float* sc = p.scores + s * p.sc_rs + g * p.sc_hs;
+  const int32_t* kp = p.key_pos + s * p.kp_rs + g * p.kp_hs;
+  float* so = p.scores_out + s * p.so_rs + g * p.so_hs;
+  int32_t* po = p.pos_out + s * p.po_rs + g * p.po_hs;
+  const int n0 = __ldg(p.lens + s);
+  const bool bad = n0 < 0 || n0 > slots;
+  const int n = bad ? 0 : n0;
+  const int k = min(n, p.budget);
+  if (tid == 0) {
+    if (bad) report(p.status, ATTN_DEV_BAD_CACHE);
+    if (g == 0) newlen[s] = bad ? n0 : k;
+    if (n <= k) counts[blockIdx.x] = 0;
+  }
+  if (n <= k) {  // nothing to evict
+    for (int j = tid; j < n; j += kThreadsE) {
+      if (so != sc) so[j] = sc[j];
+      if (po != kp) po[j] = kp[j];
+    }
+    return;
+  }
+  const int from = __ldg(p.next_pos + s) - p.recent;
+  auto load_key = [&](int j) { return rank_key(sc[j], kp[j] >= from); };
+  auto key = [&](int j) { return j < kSmemKeys ? skey[j] : load_key(j); };
+
+  // the k-th largest key: its digits from the top
+  uint32_t prefix = 0;
+  int need = k;  // how many keys with the digits found so far are still to take
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256; i += kThreadsE) hist[i] = 0;
+    __syncthreads();
+    for (int j = tid; j < n; j += kThreadsE) {
+      uint32_t x;
+      if (shift == 24) {
+        x = load_key(j);
+        if (j < kSmemKeys) skey[j] = x;
+      } else {
+        x = key(j);
+      }
+      if (shift == 24 || ((x ^ prefix) >> (shift + 8)) == 0) atomicAdd(&hist[(x >> shift) & 255], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane l: digits 255 - 8l down to 248 - 8l
+      int c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += c[i] = static_cast<int>(hist[255 - 8 * lane - i]);
+      int above = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, above, o);
+        if (lane >= o) above += y;
+      }
+      above -= sum;  // keys with a digit above this lane's
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (above < need && above + c[i] >= need) {
+          s_digit = 255 - 8 * lane - i;
+          s_above = above;
+        }
+        above += c[i];
+      }
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(s_digit) << shift;
+    need -= s_above;
+    __syncthreads();
+  }
+  // kept: key > prefix, or key == prefix and among the first `need` such slots
+
+  const int span = ((n + kThreadsE - 1) / kThreadsE) * 32;  // slots of a warp, a multiple of 32
+  const int j0 = min(n, warp * span), j1 = min(n, j0 + span);
+  auto total_before = [&](int (&c)[kWarpsE]) {
+    int t = 0;
+    for (int i = 0; i < warp; ++i) t += c[i];
+    return t;
+  };
+  int c0 = 0;
+  for (int j = j0 + lane; j - lane < j1; j += 32)
+    c0 += __popc(__ballot_sync(0xffffffffu, j < j1 && key(j) == prefix));
+  if (lane == 0) cnt[0][warp] = c0;
+  __syncthreads();
+  const int eq0 = total_before(cnt[0]);
+  const uint32_t below = (1u << lane) - 1u;
+  // f(slot, kept) for this warp's slots in order, whole warps at a time
+  auto walk = [&](auto f) {
+    int eq = eq0;
+    for (int j = j0 + lane; j - lane < j1; j += 32) {
+      const bool in = j < j1;
+      const uint32_t x = in ? key(j) : 0u;
+      const uint32_t e = __ballot_sync(0xffffffffu, in && x == prefix);
+      const bool keep = in && (x > prefix || (x == prefix && eq + __popc(e & below) < need));
+      eq += __popc(e);
+      f(j, in, keep);
+    }
+  };
+  int nh = 0, nm = 0;
+  walk([&](int j, bool in, bool keep) {
+    nh += __popc(__ballot_sync(0xffffffffu, in && !keep && j < k));
+    nm += __popc(__ballot_sync(0xffffffffu, in && keep && j >= k));
+  });
+  if (lane == 0) {
+    cnt[1][warp] = nh;
+    cnt[2][warp] = nm;
+  }
+  __syncthreads();
+  int ih = total_before(cnt[1]), im = total_before(cnt[2]);
+  if (tid == kThreadsE - 1) counts[blockIdx.x] = im + nm;  // as many as holes
+  walk([&](int j, bool in, bool keep) {
+    const bool hole = in && !keep && j < k, mover = in && keep && j >= k;
+    const uint32_t bh = __ballot_sync(0xffffffffu, hole), bm = __ballot_sync(0xffffffffu, mover);
+    if (hole) holes[ih + __popc(bh & below)] = j;
+    if (mover) movers[im + __popc(bm & below)] = j;
+    ih += __popc(bh);
+    im += __popc(bm);
+    if (keep && j < k) {
+      if (so != sc) so[j] = sc[j];
+      if (po != kp) po[j] = kp[j];
+    }
+  });
+  __shared__ int s_moves;
+  if (tid == kThreadsE - 1) s_moves = im;
+  __syncthreads();  // the lists are complete (and visible to this block)
+  for (int i = tid; i < s_moves; i += kThreadsE) {
+    const int dst = holes[i], src = movers[i];
+    so[dst] = sc[src];
+    po[dst] = kp[src];
+  }
+}
+
+__global__ void __launch_bounds__(kThreadsM)
+    move_kernel(const __grid_constant__ EvictParams p) {
+  const int sg = blockIdx.x, s = sg / p.Hkv, g = sg - s * p.Hkv;
+  const EvictWs w =
+      evict_ws(p.S, p.Hkv, static_cast<int64_t>(p.width) << p.page_log2, p.budget);
+  const int32_t* holes = reinterpret_cast<const int32_t*>(p.ws + w.lists) + 2 * w.list_cap * sg;
+  const int32_t* movers = holes + w.list_cap;
+  const int count = reinterpret_cast<const int32_t*>(p.ws + w.counts)[sg];
+  if (g == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+    p.lens_out[s] = reinterpret_cast<const int32_t*>(p.ws + w.newlen)[s];
+  const int units = p.d / 8;  // 16-byte units of a row
+  const int32_t* row = p.table + s * p.table_rs;
+  const int64_t all = static_cast<int64_t>(count) * 2 * units;
+  for (int64_t u = static_cast<int64_t>(blockIdx.y) * kThreadsM + threadIdx.x; u < all;
+       u += static_cast<int64_t>(gridDim.y) * kThreadsM) {
+    const int i = static_cast<int>(u / (2 * units)), x = static_cast<int>(u - i * 2ll * units);
+    const int src = movers[i], dst = holes[i];
+    const int ps = __ldg(row + (src >> p.page_log2)), pd = __ldg(row + (dst >> p.page_log2));
+    if (static_cast<unsigned>(ps) >= static_cast<unsigned>(p.num_pages) ||
+        static_cast<unsigned>(pd) >= static_cast<unsigned>(p.num_pages)) {
+      report(p.status, ATTN_DEV_BAD_CACHE);
+      continue;
+    }
+    const Pages& pg = x < units ? p.k : p.v;
+    uint16_t* base = static_cast<uint16_t*>(const_cast<void*>(pg.base)) + g * pg.head +
+                     (x < units ? x : x - units) * 8;
+    *reinterpret_cast<uint4*>(base + pd * pg.page + (dst & (p.page_size - 1)) * pg.slot) =
+        *reinterpret_cast<const uint4*>(base + ps * pg.page + (src & (p.page_size - 1)) * pg.slot);
+  }
+}
+
+}  // namespace
+
+size_t evict_workspace(int S, int Hkv, int64_t slots, int budget) {
+  return evict_ws(S, Hkv, slots, budget).total;
+}
+
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
+  const int64_t slots = static_cast<int64_t>(p.width) << p.page_log2;
+  const int smem = static_cast<int>(slots < kSmemKeys ? slots : kSmemKeys) * 4;
+  cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys * 4);
+  select_kernel<<<p.S * p.Hkv, kThreadsE, smem, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int64_t units = evict_ws(p.S, p.Hkv, slots, p.budget).list_cap * 2 * (p.d / 8);
+  int64_t x = (units + kThreadsM * 4 - 1) / (kThreadsM * 4);
+  const int64_t most = 152 * 8 / (p.S * p.Hkv) + 1;
+  x = x < 1 ? 1 : (x > most ? most : x);
+  move_kernel<<<dim3(p.S * p.Hkv, static_cast<unsigned>(x)), kThreadsM, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace kv
+}  // namespace attn
