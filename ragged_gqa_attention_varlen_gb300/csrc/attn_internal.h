@@ -97,6 +97,13 @@ __host__ __device__ constexpr int feature_units(int d, int half) {
   return (d - 80 * half) / 8 < 0 ? 0 : ((d - 80 * half) / 8 > 10 ? 10 : (d - 80 * half) / 8);
 }
 
+// cuTensorMapEncodeTiled of the loaded driver (null: not found).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 // The call has a causal or window mask (selects the masked kernel instances).
 inline bool masked_call(const Params& p) { return p.causal || p.wl >= 0 || p.wr >= 0; }
 

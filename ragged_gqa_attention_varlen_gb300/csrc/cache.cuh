@@ -118,9 +118,17 @@ __device__ __forceinline__ uint16_t from_float(float x) {
   return BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
 }
 
+// Tensor maps of a page pool: 64-feature boxes (128-byte swizzle), and with
+// `tail` the 32 features from 128 on (64-byte swizzle).
+bool encode_pages(CUtensorMap* m, const CacheParams& p, const Pages& pg, bool tail);
+int device_ctas();  // CTAs of a persistent kernel on the current device
+
 size_t fwd_workspace(int B, int P, int Hq, int Hkv, int d, int64_t total_q);
 size_t weights_workspace(int B, int P, int Hkv, int64_t own_slots, int64_t prefix_slots);
 cudaError_t launch_fwd(const CacheParams& p, cudaStream_t s);
+template <int HD>
+cudaError_t launch_fwd_d(const CacheParams& p, const CUtensorMap& tk, const CUtensorMap& tkt,
+                         const CUtensorMap& tv, int grid, cudaStream_t s);
 cudaError_t launch_weights(const CacheParams& p, cudaStream_t s);
 
 // Rotary positions: x[H][d] rows of up to two tensors, or new K rows on their

@@ -1,0 +1,824 @@
+// cache_fwd.cuh -- attention of packed query rows over the paged K/V cache
+// (the tile kernel; cache_sched.cuh cuts the work, the merge kernel in
+// cache_fwd.cu joins cut rows).
+//
+// Per step (128 rows x 128 keys), with z the base-2 logit and m the row's
+// reference (a running maximum, or a bound known beforehand):
+//   S = Q K^T            tcgen05.mma, fp32 in TMEM
+//   P = 2^(z - m)        softmax warps, one TMEM lane per row, 16-bit to TMEM
+//   O += P V             tcgen05.mma with P from TMEM
+// and l = sum of P in fp32 (for lse), lr = the same of the rounded P that
+// multiplies V (for out: one key gives exactly its V row).
+//
+// Single-token calls read every K and V row once for R <= 128 rows of a group,
+// so the copies bound them; calls with many rows behind a shared prefix are
+// bound by the softmax warps' MUFU work and the hand-offs between them and
+// the tensor core, as the packed forward is.
+//
+// Warps (384 threads): 0 loads K (lanes 0-15) and V (lanes 16-31) by TMA, a
+// box of min(page_size, 128) rows x 64 features each; 1 issues S, 2 issues O
+// and clears the V rows of a cut tile that no row reads (the pages may hold
+// anything there, and 0 * NaN would reach O); 3 plans the CTA's pieces and
+// copies Q rows (a row is any (token, head), so Q is gathered with cp.async
+// into the swizzled layout rather than boxed by TMA); 4-11 softmax, two per
+// TMEM lane quadrant, each taking 64 of a step's keys.
+#pragma once
+#include "../../include/attn_varlen.h"
+#include "cache_sched.cuh"
+
+namespace attn {
+namespace kv {
+
+// Partial results of the forward in its workspace.
+struct FwdWs {
+  size_t info, meta, stats, rows, total;
+  int64_t cut_rows;  // rows of one CTA's border piece
+};
+struct FwdHead {  // at offset 0
+  int ok;
+  int pad;
+  int64_t per;
+};
+__host__ __device__ inline FwdWs fwd_ws(int B, int P, int Hq, int Hkv, int d, int64_t total_q) {
+  FwdWs w;
+  const int64_t R = Hq / Hkv, x = total_q * R;
+  const int64_t tiles = static_cast<int64_t>(Hkv) * (x / kRows + B + (P ? x / kRows + P : 0));
+  w.cut_rows = x < kRows ? x : kRows;
+  const int64_t rows = 2 * kMaxCtas * w.cut_rows + (P ? 2 * total_q * Hq : 0);
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  w.info = 256;
+  w.meta = w.info + up(static_cast<size_t>(B + P) * sizeof(int2));
+  w.stats = w.meta + up(static_cast<size_t>(tiles) * sizeof(int2));
+  w.rows = w.stats + up(static_cast<size_t>(rows) * sizeof(float4));
+  w.total = w.rows + up(static_cast<size_t>(rows) * d * sizeof(float));
+  return w;
+}
+// Partial row indices: CTA c's pieces of row tiles that continue from an
+// earlier CTA (2c) or into a later one (2c + 1), then whole row tiles that
+// wait for another segment's, by (own or prefix, token, head).
+__host__ __device__ inline int64_t cut_row(const FwdWs& w, int cta, bool first_part, int r) {
+  return (2 * static_cast<int64_t>(cta) + (first_part ? 1 : 0)) * w.cut_rows + r;
+}
+__host__ __device__ inline int64_t whole_row(const FwdWs& w, int64_t total_q, int Hq, bool own,
+                                             int64_t tok, int h) {
+  return 2 * kMaxCtas * w.cut_rows + ((own ? total_q : 0) + tok) * Hq + h;
+}
+
+struct Piece {
+  int row;  // of the segment's table; -1: the end
+  int own, g, tile, tok0, ntok, len;
+  int kt0, kt1;  // key tiles
+  int klo, khi;  // keys that some row of the tile may attend to
+  int mode;      // 0: writes out and lse; 1: partial of a cut tile; 2: partial of a whole tile
+  int first;     // mode 1: the tile's first part
+  int pad[3];
+};
+
+struct PieceRing {
+  Piece piece[4];
+  uint64_t full[4], empty[4];
+};
+
+__device__ __forceinline__ bool piece_take(PieceRing* r, uint32_t& k, Piece* out,
+                                           volatile int* abort) {
+  const int s = k & 3;
+  if (!mbar_wait(&r->full[s], (k >> 2) & 1, abort)) return false;
+  *out = r->piece[s];
+  ++k;
+  return true;
+}
+__device__ __forceinline__ void piece_done(PieceRing* r, uint32_t k_taken) {
+  mbar_arrive(&r->empty[(k_taken - 1) & 3]);
+}
+
+template <int HD>
+struct FwdShape {
+  static constexpr uint32_t kQ = HD == 160 ? 40960 : HD * 256;  // a K-major tile
+  static constexpr uint32_t kV = HD == 160 ? 49152 : HD * 256;  // V: 64-feature chunks of 16 KB
+  static constexpr int kChunksK = (HD + 63) / 64;
+  static constexpr int kKS = HD == 160 ? 2 : (HD == 128 ? 3 : 6);  // K stages
+  static constexpr int kVS = HD == 160 ? 2 : (HD == 128 ? 2 : 6);  // V stages
+  static constexpr uint32_t kOffK = kQ;
+  static constexpr uint32_t kOffV = kOffK + kKS * kQ;
+  static constexpr uint32_t kOffMax = kOffV + kVS * kV;          // [2 steps][2 halves][128]
+  static constexpr uint32_t kOffSum = kOffMax + 2 * 2 * 128 * 4;  // [2 pieces][2 halves][128] (l, lr)
+  static constexpr uint32_t kOffBar = kOffSum + 2 * 2 * 128 * 8;
+};
+
+struct FwdBars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t s_full[2], s_read[2], p_full[2], pv_done;
+  uint64_t o_full, o_empty, drain;
+  uint64_t mx_x[4][2], l_x[4];
+  PieceRing ring;
+  Plan plan;
+  uint32_t tmem;
+  int abort;
+};
+
+constexpr uint32_t kColPv = 256, kColOv = 320;  // S0 [0,128), S1 [128,256), P [256,320), O [320,480)
+constexpr float kLazy = 8.f;                    // rescale when the maximum grows by more (base 2)
+constexpr float kFixedCap = 9.5f;               // largest cap with a reference known beforehand
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh to a few units of 2^-24 relative: an odd polynomial below 0.55 (least
+// squares at Chebyshev nodes, 7e-8), 1 - 2 / (1 + e^2x) above.  tanh.approx
+// (2^-11) would leave a sum of weights in fp32 with an error of 16 bits.
+__device__ __forceinline__ float tanh_fp32(float x) {
+  const float y = x * x;
+  float s = fmaf(y, -0.006615754682570696f, 0.021312745288014412f);
+  s = fmaf(y, s, -0.053910065442323685f);
+  s = fmaf(y, s, 0.13333117961883545f);
+  s = fmaf(y, s, -0.3333333134651184f);
+  s = fmaf(x * y, s, x);
+  const float e = ex2_approx(x * 2.8853900817779268f);  // 2 log2 e
+  const float b = fmaf(-2.f, rcp_approx(1.f + e), 1.f);
+  return fabsf(x) < 0.55f ? s : b;
+}
+
+__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kWaitLimitNs) break;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Byte offset of 16-byte unit u of row r in a K-major tile: 64-feature chunks
+// of 128-byte rows (128-byte swizzle), features 128..159 in 64-byte rows
+// (64-byte swizzle).
+__device__ __forceinline__ uint32_t kmajor_unit(int r, int u) {
+  return u < 16 ? static_cast<uint32_t>((u >> 3) * 16384 + r * 128 + (((u & 7) ^ (r & 7)) << 4))
+                : static_cast<uint32_t>(32768 + r * 64 + (((u - 16) ^ ((r >> 1) & 3)) << 4));
+}
+// Descriptor of K step k (16 features) of such a tile.
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t base, int k) {
+  return k < 8 ? sdesc_sw128(base + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024)
+               : sdesc_sw64(base + 32768 + (k - 8) * 32);
+}
+
+// Copy the Q rows of a row tile into shared memory (whole warp; asynchronous).
+template <int HD>
+__device__ __forceinline__ void copy_q_rows(const CacheParams& p, uint8_t* dst, int g, int tile,
+                                            int tok0, int ntok, int lane, int lanes) {
+  constexpr int kU = HD / 8;
+  const int64_t x0 = static_cast<int64_t>(tile) * kRows;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(ntok) * p.R - x0));
+  const int t0 = static_cast<int>(x0 / p.R), h0 = static_cast<int>(x0 - static_cast<int64_t>(t0) * p.R);
+  const uint32_t base = smem_addr(dst);
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(g) * p.R * p.q_hs;
+  for (int i = lane; i < n * kU; i += lanes) {
+    const int r = i / kU, u = i - r * kU;
+    const int hh = h0 + r, dt = hh / p.R;
+    cp_async16(base + kmajor_unit(r, u),
+               q + static_cast<int64_t>(tok0 + t0 + dt) * p.q_ts + (hh - dt * p.R) * p.q_hs + u * 8);
+  }
+}
+
+// Pages of a key tile, one per box: lane `i` of a load group returns the page
+// of box row block i (of `pieces`), or the pool's size (reads as zeros) when
+// its number is out of the pool.
+__device__ __forceinline__ int tile_page(const CacheParams& p, const int32_t* row, int key) {
+  const int page = __ldg(row + (key >> p.page_log2));
+  if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) return page;
+  report(p.status, ATTN_DEV_BAD_CACHE);
+  return p.num_pages;
+}
+
+// CAP: the call has a softcap; FIXED: of at most kFixedCap and default key
+// positions, so P is taken against a bound and no maximum is tracked; POS:
+// the call has ALiBi, a mask or key positions.
+template <bool BF16, int HD, bool CAP, bool FIXED, bool POS>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_fwd_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ CUtensorMap tk,
+                     const __grid_constant__ CUtensorMap tkt, const __grid_constant__ CUtensorMap tv) {
+  using S = FwdShape<HD>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint8_t* sQ = sm;
+  uint8_t* sK = sm + S::kOffK;
+  uint8_t* sV = sm + S::kOffV;
+  float* sMax = reinterpret_cast<float*>(sm + S::kOffMax);
+  float2* sSum = reinterpret_cast<float2*>(sm + S::kOffSum);
+  FwdBars* bars = reinterpret_cast<FwdBars*>(sm + S::kOffBar);
+  volatile int* s_abort = &bars->abort;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const FwdWs w = fwd_ws(p.B, p.P, p.Hq, p.Hkv, p.d, p.total_q);
+  int2* info = reinterpret_cast<int2*>(p.ws + w.info);
+  int2* meta = reinterpret_cast<int2*>(p.ws + w.meta);
+  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- this CTA's share of the steps
+  int* klo_of = reinterpret_cast<int*>(sK);  // per prefix, until the loads start
+  const bool prefix_lo = p.P > 0 && p.wl >= 0 && !p.q_pos;
+  if (prefix_lo) {
+    for (int s = warp; s < p.P; s += kThreads / 32) {
+      const int lo = prefix_klo(p, s, __ldg(p.prefix.lens + s));
+      if (lane == 0) klo_of[s] = lo;
+    }
+    __syncthreads();
+  }
+  Plan* pl = &bars->plan;
+  const bool busy = make_plan(
+      p, pl, info,
+      [&](int s, int& each) -> int64_t {
+        Seg g = seg_load(p, s);
+        if (!g.own && prefix_lo) g.klo = klo_of[s];
+        const int nt = seg_tiles(p, g);
+        const int64_t n = seg_steps(p, g);
+        each = seg_varies(p, g) ? -1 : (nt ? static_cast<int>(n / nt) : 0);
+        return n * p.Hkv;
+      },
+      [&](int s) -> int { return seg_tiles(p, seg_load(p, s)) * p.Hkv; });
+  if (blockIdx.x == 0 && tid == 0) {
+    FwdHead* head = reinterpret_cast<FwdHead*>(p.ws);
+    int ok = pl->bad == 0;
+    if (smem_addr(sm) & 1023u) {
+      report(p.status, ATTN_DEV_SMEM_ALIGN);
+      ok = 0;
+    }
+    if (pl->bad) report(p.status, pl->bad);
+    head->ok = ok;
+    head->per = ok ? pl->per : 0;
+  }
+  if (!busy || (smem_addr(sm) & 1023u)) return;  // uniform
+  if (prefix_lo) fence_proxy_async_smem();  // klo_of's place is loaded into from here on
+
+  if (tid == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int b = 0; b < S::kKS; ++b) {
+      mbar_init(&bars->k_full[b], 1);
+      mbar_init(&bars->k_empty[b], 1);
+    }
+    for (int b = 0; b < S::kVS; ++b) {
+      mbar_init(&bars->v_full[b], 1);
+      mbar_init(&bars->v_empty[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->s_read[b], 8);
+      mbar_init(&bars->p_full[b], 8);
+    }
+    mbar_init(&bars->pv_done, 1);
+    mbar_init(&bars->o_full, 1);
+    mbar_init(&bars->o_empty, 8);
+    mbar_init(&bars->drain, 2);
+    for (int q = 0; q < 4; ++q) {
+      mbar_init(&bars->mx_x[q][0], 2);
+      mbar_init(&bars->mx_x[q][1], 2);
+      mbar_init(&bars->l_x[q], 2);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bars->ring.full[s], 1);
+      mbar_init(&bars->ring.empty[s], 12);  // K and V loads, two MMA issuers, 8 softmax warps
+    }
+    fence_barrier_init();
+    bars->abort = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  const int box = min(p.page_size, kKeys);  // rows of a load box
+  const int pieces = kKeys / box;           // boxes of a key tile and chunk
+
+  if (warp < 4) {
+    warpgroup_reg_dealloc<kRegsLow>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ K and V loads
+      const bool is_k = lane < 16;
+      const int gl = lane & 15;
+      const unsigned gmask = is_k ? 0x0000ffffu : 0xffff0000u;
+      const int lead = is_k ? 0 : 16;
+      if (gl == 0) {
+        prefetch_tensormap(is_k ? &tk : &tv);
+        if (is_k && HD == 160) prefetch_tensormap(&tkt);
+      }
+      const int stages = is_k ? S::kKS : S::kVS;
+      const uint32_t bytes = is_k ? S::kQ : S::kV;  // of a whole tile
+      uint64_t* full = is_k ? bars->k_full : bars->v_full;
+      uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+      uint8_t* dst0 = is_k ? sK : sV;
+      uint32_t take = 0, st = 0, ph = 0, loaded = 0;
+      Piece pc;
+      for (;;) {
+        if (!__all_sync(gmask, piece_take(&bars->ring, take, &pc, s_abort))) break;
+        __syncwarp(gmask);
+        if (gl == 0) piece_done(&bars->ring, take);
+        if (pc.row < 0) break;
+        const Table& t = pc.own ? p.own : p.prefix;
+        const int32_t* row = t.pages + pc.row * t.rs;
+        const int total = S::kChunksK * pieces;  // boxes of a tile: (chunk, row block)
+        bool ok = true;
+        for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
+          const int key0 = kt * kKeys;
+          const int have = min(pieces, (pc.len - key0 + box - 1) / box);  // row blocks in use
+          // page numbers before the wait for a free stage
+          int pages[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int x = gl + 16 * i, pi = x % pieces;
+            if (x < total && pi < have) pages[i] = tile_page(p, row, key0 + pi * box);
+          }
+          if (loaded >= static_cast<uint32_t>(stages) &&
+              !(ok = __all_sync(gmask, mbar_wait(&empty[st], ph ^ 1, s_abort))))
+            break;
+          if (gl == 0) mbar_arrive_expect_tx(&full[st], bytes / pieces * have);
+          __syncwarp(gmask);
+          uint8_t* dst = dst0 + st * bytes;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int x = gl + 16 * i, ch = x / pieces, pi = x % pieces;
+            if (x < total && pi < have) {
+              const int slot = p.page_size > kKeys ? key0 & (p.page_size - 1) : 0;
+              if (is_k && HD == 160 && ch == 2)
+                tma_load_4d(dst + 2 * 16384 + pi * box * 64, &tkt, &full[st], 128, pc.g, slot,
+                            pages[i]);
+              else
+                tma_load_4d(dst + ch * 16384 + pi * box * 128, is_k ? &tk : &tv, &full[st],
+                            ch * kChunk, pc.g, slot, pages[i]);
+            }
+          }
+          ++loaded;
+          if (++st == static_cast<uint32_t>(stages)) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+      }
+      if (*s_abort && lane == lead) {
+        // let every load of this group land before the CTA exits
+        const uint32_t n = min(loaded, static_cast<uint32_t>(stages));
+        for (uint32_t f = loaded - n; f < loaded; ++f) wait_drain(&full[f % stages], (f / stages) & 1);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ S = Q K^T
+      if (lane == 0) {
+        constexpr uint32_t kIdS = idesc_f16(128, 128, BF16, false, false);
+        uint32_t take = 0, step = 0, st = 0, ph = 0, tiles = 0;
+        Piece pc;
+        bool ok = true;
+        while (ok && piece_take(&bars->ring, take, &pc, s_abort)) {
+          piece_done(&bars->ring, take);
+          if (pc.row < 0) break;
+          if (!mbar_wait(&bars->q_full, tiles & 1, s_abort)) break;
+          for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++step) {
+            if (!(ok = mbar_wait(&bars->k_full[st], ph, s_abort))) break;
+            // the buffer's previous S (step - 2) has been read
+            if (step >= 2 && !(ok = mbar_wait(&bars->s_read[step & 1], ((step - 2) >> 1) & 1, s_abort)))
+              break;
+            tc_fence_after();
+            const uint32_t kb = smem_addr(sK + st * S::kQ), qb = smem_addr(sQ);
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+              umma_ss(tmem + (step & 1) * 128, kmajor_desc(qb, k), kmajor_desc(kb, k), kIdS, k > 0);
+            umma_commit(&bars->s_full[step & 1]);
+            umma_commit(&bars->k_empty[st]);
+            if (kt == pc.kt1 - 1) umma_commit(&bars->q_empty);
+            if (++st == S::kKS) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+          ++tiles;
+        }
+        umma_commit(&bars->drain);
+        wait_drain(&bars->drain, 0);
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ O += P V
+      constexpr uint32_t kIdO = idesc_f16(128, HD, BF16, false, true);
+      uint32_t take = 0, step = 0, st = 0, ph = 0, tiles = 0;
+      Piece pc;
+      bool ok = true;
+      while (ok) {
+        if (!__all_sync(0xffffffffu, piece_take(&bars->ring, take, &pc, s_abort))) break;
+        __syncwarp();
+        if (lane == 0) piece_done(&bars->ring, take);
+        if (pc.row < 0) break;
+        for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++step) {
+          const int key0 = kt * kKeys;
+          const int nk = min(kKeys, pc.len - key0);        // keys of the tile that exist
+          const int z0 = min(max(pc.klo - key0, 0), nk);   // those [z0, z1) that some row reads
+          const int z1 = max(min(pc.khi - key0, nk), z0);
+          const int ksteps = (nk + 15) / 16;
+          if (!(ok = mbar_wait_warp(&bars->v_full[st], ph, s_abort))) break;
+          if (z0 > 0 || z1 < ksteps * 16) {
+            // clear the other rows: they may hold anything, and P is 0 there
+            uint8_t* v = sV + st * S::kV;
+            const int rows = z0 + ksteps * 16 - z1;
+            for (int i = lane; i < rows * 8; i += 32) {
+              const int r0 = i >> 3, r = r0 < z0 ? r0 : r0 - z0 + z1;
+#pragma unroll
+              for (int c = 0; c < S::kChunksK; ++c)
+                *reinterpret_cast<uint4*>(v + c * 16384 + r * 128 + (i & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (!(ok = mbar_wait_warp(&bars->p_full[step & 1], (step >> 1) & 1, s_abort))) break;
+          if (kt == pc.kt0 && tiles > 0 &&
+              !(ok = mbar_wait_warp(&bars->o_empty, (tiles - 1) & 1, s_abort)))
+            break;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint32_t vb = smem_addr(sV + st * S::kV);
+            for (int k = 0; k < ksteps; ++k)
+              umma_ts(tmem + kColOv, tmem + kColPv + k * 8, sdesc_sw128(vb + k * 2048, 16384, 1024),
+                      kIdO, (kt > pc.kt0 || k > 0));
+            umma_commit(&bars->pv_done);
+            umma_commit(&bars->v_empty[st]);
+            if (kt == pc.kt1 - 1) umma_commit(&bars->o_full);
+          }
+          __syncwarp();
+          if (++st == S::kVS) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        ++tiles;
+      }
+      if (lane == 0) {
+        umma_commit(&bars->drain);
+        wait_drain(&bars->drain, 0);
+      }
+    } else {
+      // ------------------------------------------------------------ plan and Q rows
+      uint32_t npub = 0;
+      bool ok = true;
+      // the next piece for the whole CTA, and its Q rows
+      auto publish = [&](const Piece& pc) -> bool {
+        const int slot = npub & 3;
+        if (npub >= 4 && !mbar_wait_warp(&bars->ring.empty[slot], ((npub >> 2) - 1) & 1, s_abort))
+          return false;
+        if (lane == 0) {
+          bars->ring.piece[slot] = pc;
+          mbar_arrive(&bars->ring.full[slot]);
+        }
+        __syncwarp();
+        if (pc.row >= 0) {
+          if (npub > 0 && !mbar_wait_warp(&bars->q_empty, (npub - 1) & 1, s_abort)) return false;
+          copy_q_rows<HD>(p, sQ, pc.g, pc.tile, pc.tok0, pc.ntok, lane, 32);
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->q_full);
+        }
+        ++npub;
+        return true;
+      };
+      const int64_t per = pl->per, begin = pl->begin, end = pl->end;
+      int64_t first = pl->seg_begin;
+      int tile0 = pl->seg_tile;
+      for (int s = pl->seg; ok && first < end && s < p.P + p.B; ++s) {
+        Seg g = seg_load(p, s);
+        bool waits = !g.own;  // its rows have another segment
+        if (!g.own) {
+          g.klo = prefix_klo(p, g.row, g.len);
+        } else if (p.P) {
+          const int pfx = prefix_of(p, g.row);
+          if (pfx >= 0) {
+            const int n = __ldg(p.prefix.lens + pfx);
+            waits = prefix_klo(p, pfx, n) < n;
+          }
+        }
+        const int nt = seg_tiles(p, g);
+        const bool varies = seg_varies(p, g);
+        int lo = 0, hi = 0;
+        int64_t a = first;  // first step of the row tile
+        int gi = 0, t = 0;
+        if (!varies && nt > 0) {
+          tile_keys(p, g, 0, lo, hi);
+          const int n = tile_steps(lo, hi);
+          if (n > 0 && begin > a) {  // skip whole row tiles before this CTA's share
+            const int64_t skip = min((begin - a) / n, static_cast<int64_t>(nt) * p.Hkv);
+            a += skip * n;
+            gi = static_cast<int>(skip / nt);
+            t = static_cast<int>(skip - static_cast<int64_t>(gi) * nt);
+          }
+          if (n == 0) gi = p.Hkv;
+        }
+        if (nt == 0) gi = p.Hkv;
+        for (; ok && gi < p.Hkv && a < end; ++gi, t = 0) {
+          for (; ok && t < nt && a < end; ++t) {
+            if (varies) tile_keys(p, g, t, lo, hi);
+            const int n = tile_steps(lo, hi);
+            const int64_t s0 = max(a, begin), s1 = min(a + n, end);
+            if (s0 < s1) {
+              Piece pc;
+              pc.row = g.row;
+              pc.own = g.own;
+              pc.g = gi;
+              pc.tile = t;
+              pc.tok0 = g.tok0;
+              pc.ntok = g.ntok;
+              pc.len = g.len;
+              pc.klo = lo;
+              pc.khi = hi;
+              pc.kt0 = lo / kKeys + static_cast<int>(s0 - a);
+              pc.kt1 = lo / kKeys + static_cast<int>(s1 - a);
+              const int64_t c0 = a / per, c1 = (a + n - 1) / per;
+              pc.first = c0 == static_cast<int64_t>(blockIdx.x);
+              pc.mode = c1 > c0 ? 1 : (waits ? 2 : 0);
+              if (pc.first && lane == 0)
+                meta[tile0 + gi * nt + t] = make_int2(static_cast<int>(c0), static_cast<int>(c1 - c0 + 1));
+              ok = publish(pc);
+            }
+            a += n;
+          }
+        }
+        // first step of the next segment
+        if (varies) {
+          if (a < end) first = a;
+          else break;
+        } else {
+          const int n = tile_steps(lo, hi);
+          first += static_cast<int64_t>(n) * nt * p.Hkv;
+        }
+        tile0 += nt * p.Hkv;
+      }
+      Piece last = {};
+      last.row = -1;
+      if (ok) publish(last);
+    }
+  } else {
+    warpgroup_reg_alloc<kRegsHigh>();
+    // ------------------------------------------------------------ softmax
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    // z = out_scale * tanh(in_scale * x), or in_scale * x, in base-2 units
+    const float in_scale = CAP ? p.sigma / p.softcap : p.sigma * kLog2e;
+    const float out_scale = CAP ? p.softcap * kLog2e : 1.f;
+    uint32_t take = 0, step = 0, tiles = 0;
+    Piece pc;
+    bool ok = true;
+    while (ok) {
+      if (!__all_sync(0xffffffffu, piece_take(&bars->ring, take, &pc, s_abort))) break;
+      __syncwarp();
+      if (lane == 0) piece_done(&bars->ring, take);
+      if (pc.row < 0) break;
+      const int64_t x = static_cast<int64_t>(pc.tile) * kRows + r;
+      const int64_t rows = static_cast<int64_t>(pc.ntok) * p.R;
+      const bool valid = x < rows;
+      const bool any = x - lane < rows;  // some row of this warp
+      int tok = pc.tok0, h = pc.g * p.R;
+      if (valid) {
+        const int i = static_cast<int>(x / p.R);
+        tok += i;
+        h += static_cast<int>(x - static_cast<int64_t>(i) * p.R);
+      }
+      // the row's own slope, and the keys [jlo, jhi] it may attend to; default
+      // positions are counted from the segment's slot 0
+      float slope2 = 0.f;
+      int jlo = 0, jhi = pc.len - 1, pos = 0, base = 0;
+      bool kpos = false;
+      const int32_t* kp = nullptr;
+      if (POS && valid) {
+        int b = pc.row, off = 0;
+        const int pfx = pc.own ? (p.P ? prefix_of(p, b) : -1) : pc.row;
+        const int plen = pfx >= 0 ? __ldg(p.prefix.lens + pfx) : 0;
+        if (!pc.own) b = seq_of(p.cu_q, __ldg(p.cu_prefix + pfx), __ldg(p.cu_prefix + pfx + 1), tok);
+        if (p.slopes) slope2 = __ldg(p.slopes + b * p.slopes_bs + h) * kLog2e;
+        off = pc.own ? plen : 0;  // position of slot 0
+        if (p.q_pos)
+          pos = __ldg(p.q_pos + tok) - off;
+        else
+          pos = plen - off + __ldg(p.own.lens + b) - (__ldg(p.cu_q + b + 1) - tok);
+        base = off;
+      }
+      if (POS) {
+        const Table& t = pc.own ? p.own : p.prefix;
+        kpos = !FIXED && t.pos != nullptr;
+        if (kpos) {
+          kp = t.pos + pc.row * t.pos_rs + pc.g * t.pos_hs;
+          pos += base;  // compared with stored positions
+        } else {
+          if (p.wl >= 0) jlo = max(jlo, pos - p.wl);
+          if (p.wr >= 0) jhi = min(jhi, pos + p.wr);
+        }
+      }
+      float m_run = -INFINITY;
+      if (FIXED) {
+        m_run = 0.f;
+        if (POS && jlo <= jhi) {
+          // the ALiBi term of the nearest (or, rising, the farthest) key: every
+          // logit lies within the cap of it
+          const int d = slope2 >= 0.f ? (pos < jlo ? jlo - pos : (pos > jhi ? pos - jhi : 0))
+                                      : max(abs(pos - jlo), abs(pos - jhi));
+          m_run = -slope2 * static_cast<float>(d);
+        }
+      }
+      const float bref = FIXED ? m_run : 0.f;
+      uint64_t l2 = f2_make(0.f, 0.f), lr2 = l2;
+
+      for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++step) {
+        const int key0 = kt * kKeys + half * 64;
+        const uint32_t sb = tmem + (step & 1) * 128 + half * 64 + lane_addr;
+        int kpa = 0, kpb = 0;
+        if (POS && kpos) {
+          kpa = __ldg(kp + min(key0 + lane, pc.len - 1));
+          kpb = __ldg(kp + min(key0 + 32 + lane, pc.len - 1));
+        }
+        if (!(ok = mbar_wait_warp(&bars->s_full[step & 1], (step >> 1) & 1, s_abort))) break;
+        tc_fence_after();
+        float xs[64];
+        if (any) {
+          tmem_ld32(sb, *reinterpret_cast<float(*)[32]>(xs));
+          tmem_ld32(sb + 32, *reinterpret_cast<float(*)[32]>(xs + 32));
+          tmem_wait_ld();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->s_read[step & 1]);
+        uint32_t pk[32];
+        float alpha = 1.f;
+        bool need = false;
+        if (any) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            xs[c] = CAP ? out_scale * tanh_fp32(xs[c] * in_scale) : xs[c] * in_scale;
+          if (POS && kpos) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              const int kq = __shfl_sync(0xffffffffu, c < 32 ? kpa : kpb, c & 31);
+              const bool adm = key0 + c < pc.len && (p.wl < 0 || kq >= pos - p.wl) &&
+                               (p.wr < 0 || kq <= pos + p.wr);
+              xs[c] = adm ? fmaf(-slope2, static_cast<float>(abs(pos - kq)), xs[c]) : -INFINITY;
+            }
+          } else {
+            if (POS) {
+              const float pos0 = static_cast<float>(pos - key0);
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                xs[c] += fmaf(-slope2, fabsf(pos0 - static_cast<float>(c)), -bref);
+            }
+            // the bounds are applied per key only where they cut some row's keys
+            if (__any_sync(0xffffffffu, valid && (key0 < jlo || key0 + 63 > jhi))) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                xs[c] = key0 + c >= jlo && key0 + c <= jhi ? xs[c] : -INFINITY;
+            }
+          }
+        }
+        if (!FIXED) {
+          float* mxs = sMax + (step & 1) * 256;
+          if (any) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 64; ++c) mx = fmaxf(mx, xs[c]);
+            mxs[half * 128 + r] = mx;
+            // the row's maximum over both halves
+            if (!(ok = warp_exchange(&bars->mx_x[quad][step & 1], (step >> 1) & 1, s_abort))) break;
+            mx = fmaxf(mx, mxs[(half ^ 1) * 128 + r]);
+            need = mx > m_run + kLazy || (m_run == -INFINITY && mx > -INFINITY);
+            if (need) {
+              alpha = ex2_approx(m_run - mx);
+              m_run = mx;
+            }
+          } else if (!(ok = warp_exchange(&bars->mx_x[quad][step & 1], (step >> 1) & 1, s_abort))) {
+            break;
+          }
+        }
+        if (any) {
+          const float m_use = FIXED || m_run == -INFINITY ? 0.f : m_run;
+          if (!FIXED) {
+            l2 = f2_mul(l2, f2_make(alpha, alpha));
+            lr2 = f2_mul(lr2, f2_make(alpha, alpha));
+          }
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float e0 = ex2_approx(FIXED ? xs[c] : xs[c] - m_use);
+            const float e1 = ex2_approx(FIXED ? xs[c + 1] : xs[c + 1] - m_use);
+            pk[c >> 1] = Pack<BF16>::two(e0, e1);
+            l2 = f2_add(l2, f2_make(e0, e1));
+            lr2 = f2_add(lr2, Pack<BF16>::unpack(pk[c >> 1]));
+          }
+        }
+        // the previous P V has read the P region and added to O
+        if (step >= 1 && !(ok = mbar_wait_warp(&bars->pv_done, (step - 1) & 1, s_abort))) break;
+        tc_fence_after();
+        if (any) {
+          if (!FIXED && kt > pc.kt0 && __any_sync(0xffffffffu, need)) {
+            // O follows the new reference: this half's features
+            constexpr int kC = HD / 2;
+            const uint32_t ob = tmem + kColOv + half * kC + lane_addr;
+#pragma unroll 1
+            for (int c = 0; c < kC; c += 16) {
+              float o[16];
+              tmem_ld16(ob + c, o);
+              tmem_wait_ld();
+              uint32_t u[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * alpha);
+              tmem_st16(ob + c, u);
+            }
+            tmem_wait_st();
+          }
+          const uint32_t pb = tmem + kColPv + half * 32 + lane_addr;
+          tmem_st16(pb, *reinterpret_cast<uint32_t(*)[16]>(pk));
+          tmem_st16(pb + 16, *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[step & 1]);
+      }
+      if (!ok) break;
+      // ---- the row's sums over both halves, then O
+      float l = f2_lo(l2) + f2_hi(l2), lr = f2_lo(lr2) + f2_hi(lr2);
+      float2* sums = sSum + (tiles & 1) * 256;
+      sums[half * 128 + r] = make_float2(l, lr);
+      if (!(ok = warp_exchange(&bars->l_x[quad], tiles & 1, s_abort))) break;
+      {
+        const float2 other = sums[(half ^ 1) * 128 + r];
+        l = half ? other.x + l : l + other.x;
+        lr = half ? other.y + lr : lr + other.y;
+      }
+      if (!(ok = mbar_wait_warp(&bars->o_full, tiles & 1, s_abort))) break;
+      tc_fence_after();
+      constexpr int kC = HD / 2;
+      float o[kC];
+      if (any) {
+        const uint32_t ob = tmem + kColOv + half * kC + lane_addr;
+#pragma unroll
+        for (int c = 0; c < kC; c += 16) tmem_ld16(ob + c, *reinterpret_cast<float(*)[16]>(o + c));
+        tmem_wait_ld();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->o_empty);
+      ++tiles;
+      if (!valid) continue;
+      if (pc.mode == 0) {
+        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        if (half == 0)
+          p.lse[static_cast<int64_t>(tok) * p.Hq + h] = l > 0.f ? (m_run + log2f(l)) * kLn2 : -INFINITY;
+        uint16_t* orow = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(tok) * p.out_ts +
+                         static_cast<int64_t>(h) * p.out_hs + half * kC;
+#pragma unroll
+        for (int u = 0; u < kC / 8; ++u) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = o[8 * u + i] * inv;
+          *reinterpret_cast<uint4*>(orow + u * 8) = pack8<BF16>(v);
+        }
+      } else {
+        const int64_t pr = pc.mode == 1 ? cut_row(w, blockIdx.x, pc.first, r)
+                                        : whole_row(w, p.total_q, p.Hq, pc.own, tok, h);
+        if (half == 0) reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(m_run, l, lr, 0.f);
+        float4* orow = reinterpret_cast<float4*>(p.ws + w.rows) + (pr * HD + half * kC) / 4;
+#pragma unroll
+        for (int u = 0; u < kC / 4; ++u)
+          orow[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && *s_abort) report(p.status, ATTN_DEV_TIMEOUT_FWD);
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <bool B, int HD>
+auto pick_fwd(const CacheParams& p) {
+  const bool moved = p.own.pos || (p.P && p.prefix.pos);
+  const bool pos = p.slopes || p.wl >= 0 || p.wr >= 0 || moved;
+  if (!(p.softcap > 0.f))
+    return pos ? cache_fwd_kernel<B, HD, false, false, true>
+               : cache_fwd_kernel<B, HD, false, false, false>;
+  if (p.softcap <= kFixedCap && !moved)
+    return pos ? cache_fwd_kernel<B, HD, true, true, true>
+               : cache_fwd_kernel<B, HD, true, true, false>;
+  return pos ? cache_fwd_kernel<B, HD, true, false, true>
+             : cache_fwd_kernel<B, HD, true, false, false>;
+}
+
+template <int HD>
+cudaError_t launch_fwd_d(const CacheParams& p, const CUtensorMap& tk, const CUtensorMap& tkt,
+                         const CUtensorMap& tv, int grid, cudaStream_t s) {
+  constexpr uint32_t smem = FwdShape<HD>::kOffBar + sizeof(FwdBars);
+  static_assert(smem <= 232448, "shared memory");
+  auto k = p.dtype == 1 ? pick_fwd<true, HD>(p) : pick_fwd<false, HD>(p);
+  cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  k<<<grid, kThreads, smem, s>>>(p, tk, tkt, tv);
+  return cudaGetLastError();
+}
+
+}  // namespace kv
+}  // namespace attn

@@ -1,0 +1,9 @@
+// cache_fwd_d128.cu -- instances of the cache attention kernel at head dimension 128.
+#include "cache_fwd.cuh"
+
+namespace attn {
+namespace kv {
+template cudaError_t launch_fwd_d<128>(const CacheParams&, const CUtensorMap&, const CUtensorMap&,
+                                      const CUtensorMap&, int, cudaStream_t);
+}  // namespace kv
+}  // namespace attn

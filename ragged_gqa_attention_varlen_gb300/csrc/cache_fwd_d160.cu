@@ -1,0 +1,9 @@
+// cache_fwd_d160.cu -- instances of the cache attention kernel at head dimension 160.
+#include "cache_fwd.cuh"
+
+namespace attn {
+namespace kv {
+template cudaError_t launch_fwd_d<160>(const CacheParams&, const CUtensorMap&, const CUtensorMap&,
+                                      const CUtensorMap&, int, cudaStream_t);
+}  // namespace kv
+}  // namespace attn

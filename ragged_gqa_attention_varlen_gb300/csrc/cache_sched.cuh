@@ -1,0 +1,246 @@
+// cache_sched.cuh -- how attention over the paged cache is cut into pieces.
+//
+// A row tile is 128 consecutive packed rows of one segment and K/V head: row x
+// is token x / R of the segment's tokens and head x % R of the group (R query
+// heads per K/V head).  It visits the 128-key tiles that hold a key some row
+// of it may attend to.  All (row tile, key tile) steps of a call, segment by
+// segment, form one line of W steps, and the CTA c of G takes steps [c * per,
+// (c + 1) * per), per = ceil(W / G): however uneven the lengths, every CTA
+// does the same number of steps in one go, and a long sequence of a small
+// batch spreads over the whole GPU.  A row tile cut by such a border leaves
+// one partial result per CTA, which the merge kernel joins.  Every CTA derives
+// its share from the lengths itself, so nothing is launched before.
+#pragma once
+#include "cache.cuh"
+
+namespace attn {
+namespace kv {
+
+constexpr int kRows = 128;
+constexpr int kMaxCtas = 160;  // CTAs of the attention and weights kernels, at most
+
+struct Seg {
+  int row;         // row of its table
+  int tok0, ntok;  // its query tokens
+  int len;         // its keys
+  int klo;         // keys below are outside of every row's window
+  bool own;
+};
+
+// Masks cut the key range of each row tile of the segment differently.
+__device__ __forceinline__ bool seg_varies(const CacheParams& p, const Seg& s) {
+  return s.own && s.ntok > 1 && !p.q_pos && (p.wl >= 0 || p.wr >= 0);
+}
+
+// Keys [lo, hi) of which some row of row tile t may attend to one: exact
+// bounds for own slots at default positions, where slot j stands at prefix_len
+// + j and query i at prefix_len + len - ntok + i.
+__device__ __forceinline__ void tile_keys(const CacheParams& p, const Seg& s, int t, int& lo,
+                                          int& hi) {
+  lo = s.klo;
+  hi = s.len;
+  if (s.own && !p.q_pos) {
+    const int i0 = static_cast<int>(static_cast<int64_t>(t) * kRows / p.R);
+    const int i1 = static_cast<int>(min(static_cast<int64_t>(s.ntok - 1),
+                                        (static_cast<int64_t>(t) * kRows + kRows - 1) / p.R));
+    const int64_t k0 = static_cast<int64_t>(s.len) - s.ntok;
+    if (p.wl >= 0) lo = static_cast<int>(min(static_cast<int64_t>(s.len), max(static_cast<int64_t>(0), k0 + i0 - p.wl)));
+    if (p.wr >= 0) hi = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(s.len), k0 + i1 + p.wr + 1)));
+  }
+  if (lo >= hi) lo = hi = 0;
+}
+__device__ __forceinline__ int tile_steps(int lo, int hi) {
+  return hi > lo ? (hi + kKeys - 1) / kKeys - lo / kKeys : 0;
+}
+
+__device__ __forceinline__ int seg_tiles(const CacheParams& p, const Seg& s) {
+  return static_cast<int>((static_cast<int64_t>(s.ntok) * p.R + kRows - 1) / kRows);
+}
+
+// Steps of one K/V head's row tiles.
+__device__ __forceinline__ int64_t seg_steps(const CacheParams& p, const Seg& s) {
+  const int nt = seg_tiles(p, s);
+  int lo, hi;
+  if (!seg_varies(p, s)) {
+    if (nt == 0) return 0;
+    tile_keys(p, s, 0, lo, hi);
+    return static_cast<int64_t>(nt) * tile_steps(lo, hi);
+  }
+  int64_t n = 0;
+  for (int t = 0; t < nt; ++t) {
+    tile_keys(p, s, t, lo, hi);
+    n += tile_steps(lo, hi);
+  }
+  return n;
+}
+
+// The first slot of prefix pfx that some sequence's window reaches (whole
+// warp): at default positions query 0 of sequence b stands at prefix_len +
+// own_len - Lq.
+__device__ __forceinline__ int prefix_klo(const CacheParams& p, int pfx, int len) {
+  if (p.wl < 0 || p.q_pos) return 0;
+  const int b0 = __ldg(p.cu_prefix + pfx), b1 = __ldg(p.cu_prefix + pfx + 1);
+  int least = INT32_MAX;
+  for (int b = b0 + static_cast<int>(threadIdx.x & 31); b < b1; b += 32) {
+    const int nq = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b);
+    if (nq > 0) least = min(least, __ldg(p.own.lens + b) - nq);
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  const int64_t lo = static_cast<int64_t>(len) + least - p.wl;
+  return lo <= 0 ? 0 : static_cast<int>(min(lo, static_cast<int64_t>(len)));
+}
+
+// Segment s (0 .. P+B-1).  For prefixes klo is left to the caller.
+__device__ __forceinline__ Seg seg_load(const CacheParams& p, int s) {
+  Seg g;
+  g.own = s >= p.P;
+  g.row = g.own ? s - p.P : s;
+  const int b0 = g.own ? g.row : __ldg(p.cu_prefix + g.row);
+  const int b1 = g.own ? g.row + 1 : __ldg(p.cu_prefix + g.row + 1);
+  g.tok0 = __ldg(p.cu_q + b0);
+  g.ntok = __ldg(p.cu_q + b1) - g.tok0;
+  g.len = __ldg((g.own ? p.own.lens : p.prefix.lens) + g.row);
+  g.klo = 0;
+  return g;
+}
+
+// What is wrong with segment s's metadata, as status bits.
+__device__ __forceinline__ int seg_check(const CacheParams& p, int s) {
+  int bad = 0;
+  if (s >= p.P) {
+    const int b = s - p.P, c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
+    if ((b == 0 && c0 != 0) || c0 < 0 || c1 < c0 || c1 > p.total_q) bad |= ATTN_DEV_BAD_CU;
+    const int n = __ldg(p.own.lens + b);
+    if (n < 0 || n > (static_cast<int64_t>(p.own.width) << p.page_log2)) bad |= ATTN_DEV_BAD_CACHE;
+  } else {
+    const int c0 = __ldg(p.cu_prefix + s), c1 = __ldg(p.cu_prefix + s + 1);
+    if (c0 < 0 || c1 < c0 || c1 > p.B) bad |= ATTN_DEV_BAD_CU;
+    const int n = __ldg(p.prefix.lens + s);
+    if (n < 0 || n > (static_cast<int64_t>(p.prefix.width) << p.page_log2))
+      bad |= ATTN_DEV_BAD_CACHE;
+  }
+  return bad;
+}
+
+// Inclusive block sums of two values over all threads of a block of up to 32
+// warps; `tmp` holds two values per warp.
+__device__ __forceinline__ void block_scan2(int64_t& a, int& b, int64_t* tmp_a, int* tmp_b,
+                                            int64_t& total_a, int& total_b) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t xa = __shfl_up_sync(0xffffffffu, a, o);
+    const int xb = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += xa;
+      b += xb;
+    }
+  }
+  __syncthreads();  // tmp of an earlier call has been read
+  if (lane == 31) {
+    tmp_a[warp] = a;
+    tmp_b[warp] = b;
+  }
+  __syncthreads();
+  int64_t ba = 0;
+  int bb = 0;
+  total_a = 0;
+  total_b = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w == warp) {
+      ba = total_a;
+      bb = total_b;
+    }
+    total_a += tmp_a[w];
+    total_b += tmp_b[w];
+  }
+  a += ba;
+  b += bb;
+}
+
+// Results of the plan, in shared memory.
+struct Plan {
+  int64_t per, begin, end;  // this CTA's steps
+  int seg;                  // the segment that holds step `begin`
+  int64_t seg_begin;        // the first step of that segment
+  int seg_tile;             // row tiles (of all K/V heads) before it
+  int bad;
+  int64_t tmp_a[32];
+  int tmp_b[32];
+};
+
+// Whole block.  kRowSplit: pieces are cut along the keys of row tiles
+// (attention); else along the rows of key tiles (key weights, where a segment
+// that is not wanted has no steps).  info[s], if not null and for CTA 0
+// only: {row tiles before segment s, steps of a row tile or -1 when they
+// differ}.  Returns false (for every thread) when there is nothing to do.
+template <class StepsOf, class TilesOf>
+__device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, StepsOf steps_of,
+                          TilesOf tiles_of) {
+  const int nseg = p.P + p.B, tid = threadIdx.x, nt = blockDim.x;
+  if (tid == 0) pl->bad = 0;
+  __syncthreads();
+  int bad = 0;
+  for (int s = tid; s < nseg; s += nt) bad |= seg_check(p, s);
+  if (bad) atomicOr(&pl->bad, bad);
+  __syncthreads();
+  if (pl->bad) return false;
+  // one pass when the segments fit the block; else the total first
+  int64_t total = 0;
+  int tiles_total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t steps_before = 0;
+    int tiles_before = 0;
+    for (int s0 = 0; s0 < nseg; s0 += nt) {
+      const int s = s0 + tid;
+      int64_t a = 0;
+      int b = 0, each = 0;
+      if (s < nseg) {
+        a = steps_of(s, each);
+        b = tiles_of(s);
+      }
+      const int64_t mine = a;
+      const int mine_b = b;
+      int64_t ta;
+      int tb;
+      block_scan2(a, b, pl->tmp_a, pl->tmp_b, ta, tb);
+      if (pass == 0 && nseg > nt) {
+        steps_before += ta;
+        tiles_before += tb;
+        continue;
+      }
+      if (pass == 0) {
+        total = ta;
+        tiles_total = tb;
+      }
+      const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+      const int64_t begin = per * blockIdx.x, first = steps_before + a - mine;
+      if (s < nseg) {
+        if (mine > 0 && begin >= first && begin < first + mine) {
+          pl->seg = s;
+          pl->seg_begin = first;
+          pl->seg_tile = tiles_before + b - mine_b;
+        }
+        if (info && blockIdx.x == 0) info[s] = make_int2(tiles_before + b - mine_b, each);
+      }
+      if (s0 == 0 && tid == 0) {
+        pl->per = per;
+        pl->begin = begin;
+        pl->end = min(total, begin + per);
+      }
+      steps_before += ta;
+      tiles_before += tb;
+    }
+    if (pass == 0) {
+      if (nseg <= nt) break;
+      total = steps_before;
+      tiles_total = tiles_before;
+    }
+  }
+  (void)tiles_total;
+  __syncthreads();
+  return pl->begin < pl->end;
+}
+
+}  // namespace kv
+}  // namespace attn

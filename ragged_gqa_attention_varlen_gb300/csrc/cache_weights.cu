@@ -1,5 +1,4 @@
-// cache_attn.cu -- attention of packed query rows over the paged K/V cache,
-// and the weight that each cached key receives from them.
+// cache_weights.cu -- the attention weight that each cached key receives.
 #include "../../include/attn_varlen.h"
 #include "cache.cuh"
 
@@ -66,61 +65,6 @@ __device__ __forceinline__ int key_position(const Table& t, int row, int g, int 
   return t.pos ? __ldg(t.pos + row * t.pos_rs + g * t.pos_hs + j) : base + j;
 }
 
-// One block per packed row; its warps take keys in turn.
-template <bool BF16>
-__global__ void __launch_bounds__(kThreadsA) fwd_rows_kernel(const __grid_constant__ CacheParams p) {
-  const int tok = blockIdx.x / p.Hq, h = blockIdx.x - tok * p.Hq;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float s_m[4], s_l[4], s_o[4][kHeadDim];
-  Row r;
-  if (!find_row(p, tok, h, r)) return;
-  const float slope = p.slopes ? __ldg(p.slopes + r.b * p.slopes_bs + h) : 0.f;
-  float q[kPerLane], o[kPerLane] = {}, m = -INFINITY, l = 0.f;
-  load_lane<BF16>(static_cast<const uint16_t*>(p.q) + tok * p.q_ts + h * p.q_hs, p.d, q);
-  for (int part = 0; part < 2; ++part) {
-    const Table& t = part ? p.own : p.prefix;
-    const int row = part ? r.b : r.prefix, len = part ? r.own_len : r.prefix_len;
-    for (int j = warp; j < len; j += 4) {
-      const int32_t* pages = t.pages + row * t.rs;
-      const int64_t ko = slot_row(p, p.k, pages, j), vo = slot_row(p, p.v, pages, j);
-      float k[kPerLane] = {}, v[kPerLane] = {};
-      if (ko >= 0) {
-        load_lane<BF16>(static_cast<const uint16_t*>(p.k.base) + ko + r.g * p.k.head, p.d, k);
-        load_lane<BF16>(static_cast<const uint16_t*>(p.v.base) + vo + r.g * p.v.head, p.d, v);
-      } else if (lane == 0) {
-        report(p.status, ATTN_DEV_BAD_CACHE);
-      }
-      const float z = logit(p, dot(q, k), r.qpos,
-                            key_position(t, row, r.g, j, part ? r.prefix_len : 0), slope);
-      if (z == -INFINITY) continue;
-      const float mn = fmaxf(m, z), a = expf(m - mn), e = expf(z - mn);
-      m = mn;
-      l = l * a + e;
-#pragma unroll
-      for (int i = 0; i < kPerLane; ++i) o[i] = o[i] * a + e * v[i];
-    }
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) s_o[warp][i * 32 + lane] = o[i];
-  __syncthreads();
-  float top = -INFINITY, total = 0.f;
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[w]);
-  for (int w = 0; w < 4; ++w) total += s_m[w] == -INFINITY ? 0.f : s_l[w] * expf(s_m[w] - top);
-  uint16_t* out = static_cast<uint16_t*>(p.out) + tok * p.out_ts + h * p.out_hs;
-  for (int f = threadIdx.x; f < p.d; f += kThreadsA) {
-    float x = 0.f;
-    for (int w = 0; w < 4; ++w)
-      if (s_m[w] != -INFINITY) x += s_o[w][f] * expf(s_m[w] - top);
-    out[f] = from_float<BF16>(total > 0.f ? x / total : 0.f);
-  }
-  if (threadIdx.x == 0)
-    p.lse[static_cast<int64_t>(tok) * p.Hq + h] = total > 0.f ? top + logf(total) : -INFINITY;
-}
-
 // One warp per (segment, K/V head, slot): gridDim.y = segment * Hkv + head.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreadsA) weights_rows_kernel(const __grid_constant__ CacheParams p) {
@@ -170,14 +114,7 @@ __global__ void __launch_bounds__(kThreadsA) weights_rows_kernel(const __grid_co
 
 }  // namespace
 
-size_t fwd_workspace(int, int, int, int, int, int64_t) { return 256; }
 size_t weights_workspace(int, int, int, int64_t, int64_t) { return 256; }
-
-cudaError_t launch_fwd(const CacheParams& p, cudaStream_t s) {
-  const unsigned rows = static_cast<unsigned>(p.total_q * p.Hq);
-  (p.dtype == 1 ? fwd_rows_kernel<true> : fwd_rows_kernel<false>)<<<rows, kThreadsA, 0, s>>>(p);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_weights(const CacheParams& p, cudaStream_t s) {
   const dim3 grid(256, static_cast<unsigned>((p.P + p.B) * p.Hkv));

@@ -12,13 +12,6 @@
 #include "common.cuh"
 
 namespace attn {
-namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
   static std::atomic<EncodeTiledFn> fn{nullptr};
   EncodeTiledFn f = fn.load();
@@ -33,6 +26,8 @@ EncodeTiledFn encode_fn() {
   fn.store(f);
   return f;
 }
+
+namespace {
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
