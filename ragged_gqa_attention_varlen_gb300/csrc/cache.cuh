@@ -34,6 +34,7 @@ struct CacheParams {
   int dtype;  // 0 fp16, 1 bf16
   int B, P, Hq, Hkv, d;
   int R;      // query heads per K/V head
+  float inv_R;
   int64_t total_q;
   const void* q;
   int64_t q_ts, q_hs;
@@ -126,9 +127,6 @@ int device_ctas();  // CTAs of a persistent kernel on the current device
 size_t fwd_workspace(int B, int P, int Hq, int Hkv, int d, int64_t total_q);
 size_t weights_workspace(int B, int P, int Hkv, int64_t own_slots, int64_t prefix_slots);
 cudaError_t launch_fwd(const CacheParams& p, cudaStream_t s);
-template <int HD>
-cudaError_t launch_fwd_d(const CacheParams& p, const CUtensorMap& tk, const CUtensorMap& tkt,
-                         const CUtensorMap& tv, int grid, cudaStream_t s);
 cudaError_t launch_weights(const CacheParams& p, cudaStream_t s);
 
 // Rotary positions: x[H][d] rows of up to two tensors, or new K rows on their

@@ -5,7 +5,8 @@
 // Per step (128 rows x 128 keys), with z the base-2 logit and m the row's
 // reference (a running maximum, or a bound known beforehand):
 //   S = Q K^T            tcgen05.mma, fp32 in TMEM
-//   P = 2^(z - m)        softmax warps, one TMEM lane per row, 16-bit to TMEM
+//   P = 2^(z - m)        softmax warps, one TMEM lane per row; the 16-bit pairs
+//                        overwrite S, whose buffer is free again after P V
 //   O += P V             tcgen05.mma with P from TMEM
 // and l = sum of P in fp32 (for lse), lr = the same of the rounded P that
 // multiplies V (for out: one key gives exactly its V row).
@@ -29,22 +30,20 @@
 namespace attn {
 namespace kv {
 
-// Partial results of the forward in its workspace.
+// Partial results of the forward in its workspace: byte offsets.
 struct FwdWs {
   size_t info, meta, stats, rows, total;
   int64_t cut_rows;  // rows of one CTA's border piece
 };
 struct FwdHead {  // at offset 0
   int ok;
-  int pad;
-  int64_t per;
 };
-__host__ __device__ inline FwdWs fwd_ws(int B, int P, int Hq, int Hkv, int d, int64_t total_q) {
+inline FwdWs fwd_ws(int B, int P, int Hq, int Hkv, int d, int64_t total_q) {
   FwdWs w;
   const int64_t R = Hq / Hkv, x = total_q * R;
   const int64_t tiles = static_cast<int64_t>(Hkv) * (x / kRows + B + (P ? x / kRows + P : 0));
-  w.cut_rows = x < kRows ? x : kRows;
-  const int64_t rows = 2 * kMaxCtas * w.cut_rows + (P ? 2 * total_q * Hq : 0);
+  w.cut_rows = ((x < kRows ? x : kRows) + 7) / 8 * 8;
+  const int64_t rows = (2 * kMaxCtas * w.cut_rows + (P ? 2 * total_q * Hq : 0) + 7) / 8 * 8;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.info = 256;
   w.meta = w.info + up(static_cast<size_t>(B + P) * sizeof(int2));
@@ -56,22 +55,33 @@ __host__ __device__ inline FwdWs fwd_ws(int B, int P, int Hq, int Hkv, int d, in
 // Partial row indices: CTA c's pieces of row tiles that continue from an
 // earlier CTA (2c) or into a later one (2c + 1), then whole row tiles that
 // wait for another segment's, by (own or prefix, token, head).
-__host__ __device__ inline int64_t cut_row(const FwdWs& w, int cta, bool first_part, int r) {
+__device__ __forceinline__ int64_t cut_row(const FwdWs& w, int cta, bool first_part, int r) {
   return (2 * static_cast<int64_t>(cta) + (first_part ? 1 : 0)) * w.cut_rows + r;
 }
-__host__ __device__ inline int64_t whole_row(const FwdWs& w, int64_t total_q, int Hq, bool own,
+__device__ __forceinline__ int64_t whole_row(const FwdWs& w, int64_t total_q, int Hq, bool own,
                                              int64_t tok, int h) {
   return 2 * kMaxCtas * w.cut_rows + ((own ? total_q : 0) + tok) * Hq + h;
+}
+// Place of features [4f, 4f + 4) of partial row `row`, in float4: eight rows'
+// equal features share a 128-byte line.  The tile kernel holds a row per lane,
+// so a warp's store then covers whole lines; row by row, each of its lanes
+// would touch a line of its own (a 128-row tile took 11000 clk to store).
+template <int HD>
+__device__ __forceinline__ int64_t part_at(int64_t row, int f) {
+  return ((row >> 3) * (HD / 4) + f) * 8 + (row & 7);
 }
 
 struct Piece {
   int row;  // of the segment's table; -1: the end
-  int own, g, tile, tok0, ntok, len;
-  int kt0, kt1;  // key tiles
-  int klo, khi;  // keys that some row of the tile may attend to
-  int mode;      // 0: writes out and lse; 1: partial of a cut tile; 2: partial of a whole tile
-  int first;     // mode 1: the tile's first part
-  int pad[3];
+  int own, g;
+  int tok, head;    // of the tile's first row: packed token, head in the group
+  int rows;         // rows of the tile
+  int tok0, ntok;   // the segment's tokens
+  int len, plen;    // the segment's keys; the prefix's (position of own slot 0)
+  int kt0, kt1;     // key tiles
+  int klo, khi;     // keys that some row of the tile may attend to
+  int mode;         // 0: writes out and lse; 1: partial of a cut tile; 2: partial of a whole tile
+  int first;        // mode 1: the tile's first part
 };
 
 struct PieceRing {
@@ -106,9 +116,9 @@ struct FwdShape {
 };
 
 struct FwdBars {
-  uint64_t q_full, q_empty;
+  uint64_t q_first, q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
-  uint64_t s_full[2], s_read[2], p_full[2], pv_done;
+  uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t o_full, o_empty, drain;
   uint64_t mx_x[4][2], l_x[4];
   PieceRing ring;
@@ -117,7 +127,7 @@ struct FwdBars {
   int abort;
 };
 
-constexpr uint32_t kColPv = 256, kColOv = 320;  // S0 [0,128), S1 [128,256), P [256,320), O [320,480)
+constexpr uint32_t kColOv = 256;  // TMEM: S0 / P0 [0,128), S1 / P1 [128,256), O [256, 256 + d)
 constexpr float kLazy = 8.f;                    // rescale when the maximum grows by more (base 2)
 constexpr float kFixedCap = 9.5f;               // largest cap with a reference known beforehand
 
@@ -127,19 +137,26 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// tanh to a few units of 2^-24 relative: an odd polynomial below 0.55 (least
-// squares at Chebyshev nodes, 7e-8), 1 - 2 / (1 + e^2x) above.  tanh.approx
-// (2^-11) would leave a sum of weights in fp32 with an error of 16 bits.
-__device__ __forceinline__ float tanh_fp32(float x) {
-  const float y = x * x;
-  float s = fmaf(y, -0.006615754682570696f, 0.021312745288014412f);
-  s = fmaf(y, s, -0.053910065442323685f);
-  s = fmaf(y, s, 0.13333117961883545f);
-  s = fmaf(y, s, -0.3333333134651184f);
-  s = fmaf(x * y, s, x);
-  const float e = ex2_approx(x * 2.8853900817779268f);  // 2 log2 e
-  const float b = fmaf(-2.f, rcp_approx(1.f + e), 1.f);
-  return fabsf(x) < 0.55f ? s : b;
+// tanh of a pair to a few units of 2^-24 relative: an odd polynomial below
+// 0.55 (least squares at Chebyshev nodes, 7e-8), 1 - 2 / (1 + e^2x) above, the
+// two reciprocals from one of the product (the exponent is cut at 2^60, where
+// tanh is 1).  tanh.approx (2^-11) would leave a sum of weights in fp32 with an
+// error of 16 bits.  `small`: every |x| of the warp is below 0.55.
+__device__ __forceinline__ uint64_t tanh2_fp32(uint64_t x, bool small) {
+  const uint64_t y = f2_mul(x, x);
+  auto c = [](float v) { return f2_make(v, v); };
+  uint64_t s = f2_fma(y, c(-0.006615754682570696f), c(0.021312745288014412f));
+  s = f2_fma(y, s, c(-0.053910065442323685f));
+  s = f2_fma(y, s, c(0.13333117961883545f));
+  s = f2_fma(y, s, c(-0.3333333134651184f));
+  s = f2_fma(f2_mul(x, y), s, x);
+  if (small) return s;
+  const uint64_t e = f2_mul(x, c(2.8853900817779268f));  // 2 log2 e
+  const float d0 = 1.f + ex2_approx(fminf(f2_lo(e), 60.f)), d1 = 1.f + ex2_approx(fminf(f2_hi(e), 60.f));
+  const float r = rcp_approx(d0 * d1);
+  const uint64_t b = f2_fma(f2_make(r * d1, r * d0), c(-2.f), c(1.f));
+  return f2_make(fabsf(f2_lo(x)) < 0.55f ? f2_lo(s) : f2_lo(b),
+                 fabsf(f2_hi(x)) < 0.55f ? f2_hi(s) : f2_hi(b));
 }
 
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
@@ -165,21 +182,22 @@ __device__ __forceinline__ uint64_t kmajor_desc(uint32_t base, int k) {
                : sdesc_sw64(base + 32768 + (k - 8) * 32);
 }
 
-// Copy the Q rows of a row tile into shared memory (whole warp; asynchronous).
+// Copy the Q rows of a piece into shared memory (warp wi of nw; asynchronous):
+// four lanes a row, eight rows at a time.
 template <int HD>
-__device__ __forceinline__ void copy_q_rows(const CacheParams& p, uint8_t* dst, int g, int tile,
-                                            int tok0, int ntok, int lane, int lanes) {
-  constexpr int kU = HD / 8;
-  const int64_t x0 = static_cast<int64_t>(tile) * kRows;
-  const int n = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(ntok) * p.R - x0));
-  const int t0 = static_cast<int>(x0 / p.R), h0 = static_cast<int>(x0 - static_cast<int64_t>(t0) * p.R);
+__device__ __forceinline__ void copy_q_rows(const CacheParams& p, uint8_t* dst, const Piece& pc,
+                                            int wi, int nw) {
+  const int lane = threadIdx.x & 31, u0 = lane & 3;
   const uint32_t base = smem_addr(dst);
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(g) * p.R * p.q_hs;
-  for (int i = lane; i < n * kU; i += lanes) {
-    const int r = i / kU, u = i - r * kU;
-    const int hh = h0 + r, dt = hh / p.R;
-    cp_async16(base + kmajor_unit(r, u),
-               q + static_cast<int64_t>(tok0 + t0 + dt) * p.q_ts + (hh - dt * p.R) * p.q_hs + u * 8);
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(pc.g) * p.R * p.q_hs;
+#pragma unroll 2
+  for (int r = wi * 8 + (lane >> 2); r < pc.rows; r += nw * 8) {
+    const int hh = pc.head + r, dt = head_div(p, hh);
+    const uint16_t* src = q + static_cast<int64_t>(pc.tok + dt) * p.q_ts +
+                          static_cast<int64_t>(hh - dt * p.R) * p.q_hs;
+#pragma unroll
+    for (int k = 0; k < HD / 32; ++k)
+      cp_async16(base + kmajor_unit(r, u0 + 4 * k), src + (u0 + 4 * k) * 8);
   }
 }
 
@@ -198,7 +216,8 @@ __device__ __forceinline__ int tile_page(const CacheParams& p, const int32_t* ro
 // the call has ALiBi, a mask or key positions.
 template <bool BF16, int HD, bool CAP, bool FIXED, bool POS>
 __global__ void __launch_bounds__(kThreads, 1)
-    cache_fwd_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ CUtensorMap tk,
+    cache_fwd_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ FwdWs w,
+                     const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tkt, const __grid_constant__ CUtensorMap tv) {
   using S = FwdShape<HD>;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -211,33 +230,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* s_abort = &bars->abort;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const FwdWs w = fwd_ws(p.B, p.P, p.Hq, p.Hkv, p.d, p.total_q);
   int2* info = reinterpret_cast<int2*>(p.ws + w.info);
   int2* meta = reinterpret_cast<int2*>(p.ws + w.meta);
   if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this CTA's share of the steps
-  int* klo_of = reinterpret_cast<int*>(sK);  // per prefix, until the loads start
-  const bool prefix_lo = p.P > 0 && p.wl >= 0 && !p.q_pos;
-  if (prefix_lo) {
-    for (int s = warp; s < p.P; s += kThreads / 32) {
-      const int lo = prefix_klo(p, s, __ldg(p.prefix.lens + s));
-      if (lane == 0) klo_of[s] = lo;
-    }
-    __syncthreads();
-  }
   Plan* pl = &bars->plan;
   const bool busy = make_plan(
       p, pl, info,
-      [&](int s, int& each) -> int64_t {
-        Seg g = seg_load(p, s);
-        if (!g.own && prefix_lo) g.klo = klo_of[s];
-        const int nt = seg_tiles(p, g);
-        const int64_t n = seg_steps(p, g);
-        each = seg_varies(p, g) ? -1 : (nt ? static_cast<int>(n / nt) : 0);
-        return n * p.Hkv;
+      [&](const SegPlan& g, int& each) -> int64_t {
+        each = g.each;
+        return seg_steps(p, g) * p.Hkv;
       },
-      [&](int s) -> int { return seg_tiles(p, seg_load(p, s)) * p.Hkv; });
+      [&](const SegPlan& g) -> int { return g.tiles * p.Hkv; });
   if (blockIdx.x == 0 && tid == 0) {
     FwdHead* head = reinterpret_cast<FwdHead*>(p.ws);
     int ok = pl->bad == 0;
@@ -247,12 +252,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (pl->bad) report(p.status, pl->bad);
     head->ok = ok;
-    head->per = ok ? pl->per : 0;
   }
   if (!busy || (smem_addr(sm) & 1023u)) return;  // uniform
-  if (prefix_lo) fence_proxy_async_smem();  // klo_of's place is loaded into from here on
 
   if (tid == 0) {
+    mbar_init(&bars->q_first, 8);
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     for (int b = 0; b < S::kKS; ++b) {
@@ -265,10 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->s_full[b], 1);
-      mbar_init(&bars->s_read[b], 8);
       mbar_init(&bars->p_full[b], 8);
+      mbar_init(&bars->pv_done[b], 1);
     }
-    mbar_init(&bars->pv_done, 1);
     mbar_init(&bars->o_full, 1);
     mbar_init(&bars->o_empty, 8);
     mbar_init(&bars->drain, 2);
@@ -375,11 +378,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && piece_take(&bars->ring, take, &pc, s_abort)) {
           piece_done(&bars->ring, take);
           if (pc.row < 0) break;
-          if (!mbar_wait(&bars->q_full, tiles & 1, s_abort)) break;
+          if (!(tiles == 0 ? mbar_wait(&bars->q_first, 0, s_abort)
+                           : mbar_wait(&bars->q_full, (tiles - 1) & 1, s_abort)))
+            break;
           for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++step) {
             if (!(ok = mbar_wait(&bars->k_full[st], ph, s_abort))) break;
-            // the buffer's previous S (step - 2) has been read
-            if (step >= 2 && !(ok = mbar_wait(&bars->s_read[step & 1], ((step - 2) >> 1) & 1, s_abort)))
+            // the product with the P that took the buffer's previous S (step - 2) is done
+            if (step >= 2 && !(ok = mbar_wait(&bars->pv_done[step & 1], ((step - 2) >> 1) & 1, s_abort)))
               break;
             tc_fence_after();
             const uint32_t kb = smem_addr(sK + st * S::kQ), qb = smem_addr(sQ);
@@ -438,10 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             tc_fence_after();
             const uint32_t vb = smem_addr(sV + st * S::kV);
+            // keys 16k .. 16k + 15: pair columns 8 (k mod 4) of half k / 4
             for (int k = 0; k < ksteps; ++k)
-              umma_ts(tmem + kColOv, tmem + kColPv + k * 8, sdesc_sw128(vb + k * 2048, 16384, 1024),
-                      kIdO, (kt > pc.kt0 || k > 0));
-            umma_commit(&bars->pv_done);
+              umma_ts(tmem + kColOv, tmem + (step & 1) * 128 + (k >> 2) * 64 + (k & 3) * 8,
+                      sdesc_sw128(vb + k * 2048, 16384, 1024), kIdO, (kt > pc.kt0 || k > 0));
+            umma_commit(&bars->pv_done[step & 1]);
             umma_commit(&bars->v_empty[st]);
             if (kt == pc.kt1 - 1) umma_commit(&bars->o_full);
           }
@@ -471,9 +477,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&bars->ring.full[slot]);
         }
         __syncwarp();
-        if (pc.row >= 0) {
-          if (npub > 0 && !mbar_wait_warp(&bars->q_empty, (npub - 1) & 1, s_abort)) return false;
-          copy_q_rows<HD>(p, sQ, pc.g, pc.tile, pc.tok0, pc.ntok, lane, 32);
+        if (pc.row >= 0 && npub > 0) {  // (the softmax warps fetch the first piece's)
+          if (!mbar_wait_warp(&bars->q_empty, (npub - 1) & 1, s_abort)) return false;
+          copy_q_rows<HD>(p, sQ, pc, 0, 1);
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async_smem();
           __syncwarp();
@@ -485,71 +491,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t per = pl->per, begin = pl->begin, end = pl->end;
       int64_t first = pl->seg_begin;
       int tile0 = pl->seg_tile;
-      for (int s = pl->seg; ok && first < end && s < p.P + p.B; ++s) {
-        Seg g = seg_load(p, s);
-        bool waits = !g.own;  // its rows have another segment
-        if (!g.own) {
-          g.klo = prefix_klo(p, g.row, g.len);
-        } else if (p.P) {
-          const int pfx = prefix_of(p, g.row);
-          if (pfx >= 0) {
-            const int n = __ldg(p.prefix.lens + pfx);
-            waits = prefix_klo(p, pfx, n) < n;
-          }
+      const int s0 = pl->seg, known = pl->window;
+      for (int s = s0; ok && first < end && s < p.P + p.B; ++s) {
+        if (s - s0 >= known && ((s - s0) & 31) == 0) {  // the next 32 segments
+          __syncwarp();
+          if (s + lane < p.P + p.B) pl->segs[lane] = seg_plan(p, s + lane);
+          __syncwarp();
         }
-        const int nt = seg_tiles(p, g);
-        const bool varies = seg_varies(p, g);
-        int lo = 0, hi = 0;
+        const SegPlan g = pl->segs[(s - s0) & 31];
+        const int nt = g.tiles;
+        const bool varies = g.each < 0;
+        int lo = g.lo, hi = g.hi;
         int64_t a = first;  // first step of the row tile
         int gi = 0, t = 0;
-        if (!varies && nt > 0) {
-          tile_keys(p, g, 0, lo, hi);
-          const int n = tile_steps(lo, hi);
-          if (n > 0 && begin > a) {  // skip whole row tiles before this CTA's share
-            const int64_t skip = min((begin - a) / n, static_cast<int64_t>(nt) * p.Hkv);
-            a += skip * n;
+        if (!varies) {
+          if (g.each > 0 && begin > a) {  // skip whole row tiles before this CTA's share
+            const int64_t skip = min((begin - a) / g.each, static_cast<int64_t>(nt) * p.Hkv);
+            a += skip * g.each;
             gi = static_cast<int>(skip / nt);
             t = static_cast<int>(skip - static_cast<int64_t>(gi) * nt);
           }
-          if (n == 0) gi = p.Hkv;
+          if (g.each == 0) gi = p.Hkv;
         }
-        if (nt == 0) gi = p.Hkv;
         for (; ok && gi < p.Hkv && a < end; ++gi, t = 0) {
+          int64_t x0 = static_cast<int64_t>(t) * kRows;  // the tile's first row
+          int i0 = static_cast<int>(x0 / p.R), h0 = static_cast<int>(x0 - static_cast<int64_t>(i0) * p.R);
           for (; ok && t < nt && a < end; ++t) {
-            if (varies) tile_keys(p, g, t, lo, hi);
-            const int n = tile_steps(lo, hi);
-            const int64_t s0 = max(a, begin), s1 = min(a + n, end);
-            if (s0 < s1) {
+            if (varies) tile_keys(p, g.s, t, lo, hi);
+            const int n = varies ? tile_steps(lo, hi) : g.each;
+            const int64_t s1 = min(a + n, end);
+            const int64_t sb = max(a, begin);
+            if (sb < s1) {
               Piece pc;
-              pc.row = g.row;
-              pc.own = g.own;
+              pc.row = g.s.row;
+              pc.own = g.s.own;
               pc.g = gi;
-              pc.tile = t;
-              pc.tok0 = g.tok0;
-              pc.ntok = g.ntok;
-              pc.len = g.len;
+              pc.tok = g.s.tok0 + i0;
+              pc.head = h0;
+              pc.rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(g.s.ntok) * p.R - x0));
+              pc.tok0 = g.s.tok0;
+              pc.ntok = g.s.ntok;
+              pc.len = g.s.len;
+              pc.plen = g.plen;
               pc.klo = lo;
               pc.khi = hi;
-              pc.kt0 = lo / kKeys + static_cast<int>(s0 - a);
+              pc.kt0 = lo / kKeys + static_cast<int>(sb - a);
               pc.kt1 = lo / kKeys + static_cast<int>(s1 - a);
-              const int64_t c0 = a / per, c1 = (a + n - 1) / per;
-              pc.first = c0 == static_cast<int64_t>(blockIdx.x);
-              pc.mode = c1 > c0 ? 1 : (waits ? 2 : 0);
-              if (pc.first && lane == 0)
-                meta[tile0 + gi * nt + t] = make_int2(static_cast<int>(c0), static_cast<int>(c1 - c0 + 1));
+              const bool before = a < begin, after = a + n > end;  // parts elsewhere
+              pc.first = !before;
+              pc.mode = before || after ? 1 : (g.waits ? 2 : 0);
+              if (!before && lane == 0)
+                meta[tile0 + gi * nt + t] = make_int2(
+                    blockIdx.x, after ? static_cast<int>((a + n - 1) / per) - static_cast<int>(blockIdx.x) + 1 : 1);
               ok = publish(pc);
             }
             a += n;
+            x0 += kRows;
+            h0 += kRows;
+            if (p.R < 2 * kRows) {
+              const int dt = head_div(p, h0);
+              i0 += dt;
+              h0 -= dt * p.R;
+            } else if (h0 >= p.R) {
+              ++i0;
+              h0 -= p.R;
+            }
           }
         }
-        // first step of the next segment
-        if (varies) {
-          if (a < end) first = a;
-          else break;
-        } else {
-          const int n = tile_steps(lo, hi);
-          first += static_cast<int64_t>(n) * nt * p.Hkv;
-        }
+        if (varies && a >= end) break;
+        first = varies ? a : first + static_cast<int64_t>(g.each) * nt * p.Hkv;
         tile0 += nt * p.Hkv;
       }
       Piece last = {};
@@ -573,42 +583,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) piece_done(&bars->ring, take);
       if (pc.row < 0) break;
-      const int64_t x = static_cast<int64_t>(pc.tile) * kRows + r;
-      const int64_t rows = static_cast<int64_t>(pc.ntok) * p.R;
-      const bool valid = x < rows;
-      const bool any = x - lane < rows;  // some row of this warp
-      int tok = pc.tok0, h = pc.g * p.R;
-      if (valid) {
-        const int i = static_cast<int>(x / p.R);
-        tok += i;
-        h += static_cast<int>(x - static_cast<int64_t>(i) * p.R);
+      if (tiles == 0) {
+        copy_q_rows<HD>(p, sQ, pc, warp - 4, 8);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_first);
+      }
+      const bool valid = r < pc.rows;
+      const bool any = quad * 32 < pc.rows;  // some row of this warp
+      int tok = pc.tok, h = pc.head + r;     // packed token, head
+      {
+        const int dt = head_div(p, h);
+        tok += dt;
+        h += (pc.g - dt) * p.R;
       }
       // the row's own slope, and the keys [jlo, jhi] it may attend to; default
       // positions are counted from the segment's slot 0
       float slope2 = 0.f;
-      int jlo = 0, jhi = pc.len - 1, pos = 0, base = 0;
+      int jlo = 0, jhi = pc.len - 1, pos = 0;
       bool kpos = false;
       const int32_t* kp = nullptr;
-      if (POS && valid) {
-        int b = pc.row, off = 0;
-        const int pfx = pc.own ? (p.P ? prefix_of(p, b) : -1) : pc.row;
-        const int plen = pfx >= 0 ? __ldg(p.prefix.lens + pfx) : 0;
-        if (!pc.own) b = seq_of(p.cu_q, __ldg(p.cu_prefix + pfx), __ldg(p.cu_prefix + pfx + 1), tok);
-        if (p.slopes) slope2 = __ldg(p.slopes + b * p.slopes_bs + h) * kLog2e;
-        off = pc.own ? plen : 0;  // position of slot 0
-        if (p.q_pos)
-          pos = __ldg(p.q_pos + tok) - off;
-        else
-          pos = plen - off + __ldg(p.own.lens + b) - (__ldg(p.cu_q + b + 1) - tok);
-        base = off;
-      }
       if (POS) {
         const Table& t = pc.own ? p.own : p.prefix;
+        const int base = pc.own ? pc.plen : 0;  // position of slot 0
         kpos = !FIXED && t.pos != nullptr;
-        if (kpos) {
-          kp = t.pos + pc.row * t.pos_rs + pc.g * t.pos_hs;
-          pos += base;  // compared with stored positions
-        } else {
+        if (kpos) kp = t.pos + pc.row * t.pos_rs + pc.g * t.pos_hs;
+        if (valid) {
+          int b = pc.row;
+          if (!pc.own) {
+            const int b0 = __ldg(p.cu_prefix + pc.row), b1 = __ldg(p.cu_prefix + pc.row + 1);
+            // one token each: no search
+            b = b1 - b0 == pc.ntok && __ldg(p.cu_q + b0 + tok - pc.tok0) == tok &&
+                        __ldg(p.cu_q + b0 + tok - pc.tok0 + 1) > tok
+                    ? b0 + tok - pc.tok0
+                    : seq_of(p.cu_q, b0, b1, tok);
+          }
+          if (p.slopes) slope2 = __ldg(p.slopes + b * p.slopes_bs + h) * kLog2e;
+          if (p.q_pos)
+            pos = __ldg(p.q_pos + tok) - (kpos ? 0 : base);
+          else if (pc.own)
+            pos = pc.len - pc.ntok + tok - pc.tok0;
+          else
+            pos = pc.plen + __ldg(p.own.lens + b) - (__ldg(p.cu_q + b + 1) - tok);
+        }
+        if (!kpos) {
           if (p.wl >= 0) jlo = max(jlo, pos - p.wl);
           if (p.wr >= 0) jhi = min(jhi, pos + p.wr);
         }
@@ -635,87 +654,124 @@ __global__ void __launch_bounds__(kThreads, 1)
           kpa = __ldg(kp + min(key0 + lane, pc.len - 1));
           kpb = __ldg(kp + min(key0 + 32 + lane, pc.len - 1));
         }
-        if (!(ok = mbar_wait_warp(&bars->s_full[step & 1], (step >> 1) & 1, s_abort))) break;
-        tc_fence_after();
-        float xs[64];
-        if (any) {
-          tmem_ld32(sb, *reinterpret_cast<float(*)[32]>(xs));
-          tmem_ld32(sb + 32, *reinterpret_cast<float(*)[32]>(xs + 32));
-          tmem_wait_ld();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->s_read[step & 1]);
-        uint32_t pk[32];
-        float alpha = 1.f;
-        bool need = false;
-        if (any) {
+        // the bounds are applied per key only where they cut some row's keys
+        const bool edge = __any_sync(0xffffffffu, valid && (key0 < jlo || key0 + 63 > jhi));
+        // base-2 logits (less bref) of columns [c0, c0 + 16) from their products
+        auto logits16 = [&](float (&x)[16], int c0) {
+          if (CAP) {
+            bool small = false;
+            if (!FIXED) {  // with a large cap, most calls stay far below it
+              float top = 0.f;
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            xs[c] = CAP ? out_scale * tanh_fp32(xs[c] * in_scale) : xs[c] * in_scale;
-          if (POS && kpos) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              const int kq = __shfl_sync(0xffffffffu, c < 32 ? kpa : kpb, c & 31);
-              const bool adm = key0 + c < pc.len && (p.wl < 0 || kq >= pos - p.wl) &&
-                               (p.wr < 0 || kq <= pos + p.wr);
-              xs[c] = adm ? fmaf(-slope2, static_cast<float>(abs(pos - kq)), xs[c]) : -INFINITY;
+              for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+              small = !__any_sync(0xffffffffu, !(top * in_scale < 0.55f));
             }
-          } else {
-            if (POS) {
-              const float pos0 = static_cast<float>(pos - key0);
 #pragma unroll
-              for (int c = 0; c < 64; ++c)
-                xs[c] += fmaf(-slope2, fabsf(pos0 - static_cast<float>(c)), -bref);
-            }
-            // the bounds are applied per key only where they cut some row's keys
-            if (__any_sync(0xffffffffu, valid && (key0 < jlo || key0 + 63 > jhi))) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                xs[c] = key0 + c >= jlo && key0 + c <= jhi ? xs[c] : -INFINITY;
+            for (int i = 0; i < 16; i += 2) {
+              const uint64_t th = tanh2_fp32(f2_mul(f2_make(x[i], x[i + 1]), f2_make(in_scale, in_scale)), small);
+              x[i] = f2_lo(th);
+              x[i + 1] = f2_hi(th);
             }
           }
-        }
+          const float sc = CAP ? out_scale : in_scale;
+          if (POS && kpos) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int kq = __shfl_sync(0xffffffffu, c0 < 32 ? kpa : kpb, (c0 & 31) + i);
+              const bool adm = key0 + c0 + i < pc.len && (p.wl < 0 || kq >= pos - p.wl) &&
+                               (p.wr < 0 || kq <= pos + p.wr);
+              x[i] = adm ? fmaf(x[i], sc, -slope2 * static_cast<float>(abs(pos - kq))) : -INFINITY;
+            }
+            return;
+          }
+          if (POS) {
+            const float pos0 = static_cast<float>(pos - key0 - c0);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const uint64_t dist = f2_make(fabsf(pos0 - i), fabsf(pos0 - (i + 1)));
+              const uint64_t z = f2_fma(f2_make(x[i], x[i + 1]), f2_make(sc, sc),
+                                        f2_fma(dist, f2_make(-slope2, -slope2), f2_make(-bref, -bref)));
+              x[i] = f2_lo(z);
+              x[i + 1] = f2_hi(z);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] *= sc;
+          }
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              x[i] = key0 + c0 + i >= jlo && key0 + c0 + i <= jhi ? x[i] : -INFINITY;
+          }
+        };
+        if (!(ok = mbar_wait_warp(&bars->s_full[step & 1], (step >> 1) & 1, s_abort))) break;
+        tc_fence_after();
+        float alpha = 1.f;
+        bool need = false;
+        // without logits to keep, the second pass scales the products itself
+        const bool keep = CAP || POS || edge || !(in_scale > 0.f);
         if (!FIXED) {
           float* mxs = sMax + (step & 1) * 256;
+          float mx = -INFINITY;
           if (any) {
-            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c0 = 0; c0 < 64; c0 += 16) {
+              float x[16];
+              tmem_ld16(sb + c0, x);
+              tmem_wait_ld();
+              if (keep) {
+                logits16(x, c0);
+                tmem_st16(sb + c0, reinterpret_cast<uint32_t(&)[16]>(x));
+              }
 #pragma unroll
-            for (int c = 0; c < 64; ++c) mx = fmaxf(mx, xs[c]);
+              for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[i]);
+            }
+            if (keep)
+              tmem_wait_st();
+            else
+              mx *= in_scale;
             mxs[half * 128 + r] = mx;
-            // the row's maximum over both halves
-            if (!(ok = warp_exchange(&bars->mx_x[quad][step & 1], (step >> 1) & 1, s_abort))) break;
+          }
+          // the row's maximum over both halves
+          if (!(ok = warp_exchange(&bars->mx_x[quad][step & 1], (step >> 1) & 1, s_abort))) break;
+          if (any) {
             mx = fmaxf(mx, mxs[(half ^ 1) * 128 + r]);
-            need = mx > m_run + kLazy || (m_run == -INFINITY && mx > -INFINITY);
+            need = mx > m_run + kLazy;
             if (need) {
               alpha = ex2_approx(m_run - mx);
               m_run = mx;
             }
-          } else if (!(ok = warp_exchange(&bars->mx_x[quad][step & 1], (step >> 1) & 1, s_abort))) {
-            break;
+            l2 = f2_mul(l2, f2_make(alpha, alpha));
+            lr2 = f2_mul(lr2, f2_make(alpha, alpha));
           }
         }
         if (any) {
           const float m_use = FIXED || m_run == -INFINITY ? 0.f : m_run;
-          if (!FIXED) {
-            l2 = f2_mul(l2, f2_make(alpha, alpha));
-            lr2 = f2_mul(lr2, f2_make(alpha, alpha));
-          }
+          const float sc = keep ? 1.f : in_scale;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 64; c0 += 16) {
+            float x[16];
+            tmem_ld16(sb + c0, x);
+            tmem_wait_ld();
+            if (FIXED) logits16(x, c0);
+            uint32_t pk[8];
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float e0 = ex2_approx(FIXED ? xs[c] : xs[c] - m_use);
-            const float e1 = ex2_approx(FIXED ? xs[c + 1] : xs[c + 1] - m_use);
-            pk[c >> 1] = Pack<BF16>::two(e0, e1);
-            l2 = f2_add(l2, f2_make(e0, e1));
-            lr2 = f2_add(lr2, Pack<BF16>::unpack(pk[c >> 1]));
+            for (int i = 0; i < 16; i += 2) {
+              uint64_t z = f2_make(x[i], x[i + 1]);
+              if (!FIXED) z = f2_fma(z, f2_make(sc, sc), f2_make(-m_use, -m_use));
+              const float e0 = ex2_approx(f2_lo(z)), e1 = ex2_approx(f2_hi(z));
+              pk[i >> 1] = Pack<BF16>::two(e0, e1);
+              l2 = f2_add(l2, f2_make(e0, e1));
+              lr2 = f2_add(lr2, Pack<BF16>::unpack(pk[i >> 1]));
+            }
+            tmem_st8(sb + c0 / 2, pk);
           }
-        }
-        // the previous P V has read the P region and added to O
-        if (step >= 1 && !(ok = mbar_wait_warp(&bars->pv_done, (step - 1) & 1, s_abort))) break;
-        tc_fence_after();
-        if (any) {
           if (!FIXED && kt > pc.kt0 && __any_sync(0xffffffffu, need)) {
-            // O follows the new reference: this half's features
+            // O follows the new reference, once the previous products are in
+            // it: this half's features
+            if (!(ok = mbar_wait_warp(&bars->pv_done[(step - 1) & 1], ((step - 1) >> 1) & 1, s_abort)))
+              break;
+            tc_fence_after();
             constexpr int kC = HD / 2;
             const uint32_t ob = tmem + kColOv + half * kC + lane_addr;
 #pragma unroll 1
@@ -728,11 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * alpha);
               tmem_st16(ob + c, u);
             }
-            tmem_wait_st();
           }
-          const uint32_t pb = tmem + kColPv + half * 32 + lane_addr;
-          tmem_st16(pb, *reinterpret_cast<uint32_t(*)[16]>(pk));
-          tmem_st16(pb + 16, *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
           tmem_wait_st();
         }
         tc_fence_before();
@@ -782,10 +834,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t pr = pc.mode == 1 ? cut_row(w, blockIdx.x, pc.first, r)
                                         : whole_row(w, p.total_q, p.Hq, pc.own, tok, h);
         if (half == 0) reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(m_run, l, lr, 0.f);
-        float4* orow = reinterpret_cast<float4*>(p.ws + w.rows) + (pr * HD + half * kC) / 4;
+        float4* part = reinterpret_cast<float4*>(p.ws + w.rows) + part_at<HD>(pr, half * kC / 4);
 #pragma unroll
         for (int u = 0; u < kC / 4; ++u)
-          orow[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          part[u * 8] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
       }
     }
   }
@@ -810,13 +862,13 @@ auto pick_fwd(const CacheParams& p) {
 }
 
 template <int HD>
-cudaError_t launch_fwd_d(const CacheParams& p, const CUtensorMap& tk, const CUtensorMap& tkt,
+cudaError_t launch_fwd_d(const CacheParams& p, const FwdWs& w, const CUtensorMap& tk, const CUtensorMap& tkt,
                          const CUtensorMap& tv, int grid, cudaStream_t s) {
   constexpr uint32_t smem = FwdShape<HD>::kOffBar + sizeof(FwdBars);
   static_assert(smem <= 232448, "shared memory");
   auto k = p.dtype == 1 ? pick_fwd<true, HD>(p) : pick_fwd<false, HD>(p);
   cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  k<<<grid, kThreads, smem, s>>>(p, tk, tkt, tv);
+  k<<<grid, kThreads, smem, s>>>(p, w, tk, tkt, tv);
   return cudaGetLastError();
 }
 

@@ -3,7 +3,7 @@
 
 namespace attn {
 namespace kv {
-template cudaError_t launch_fwd_d<64>(const CacheParams&, const CUtensorMap&, const CUtensorMap&,
-                                      const CUtensorMap&, int, cudaStream_t);
+template cudaError_t launch_fwd_d<64>(const CacheParams&, const FwdWs&, const CUtensorMap&,
+                                      const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 }  // namespace kv
 }  // namespace attn

@@ -63,7 +63,7 @@ attn_status read_args(CacheParams& p, attn_dtype dtype, int B, int P, int Hq, in
   if (B < 0 || P < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || total_q < 0) return ATTN_ERR_INVALID;
   if (!dim_ok(head_dim)) return ATTN_ERR_UNSUPPORTED;
   if (B > ATTN_MAX_BATCH || P > ATTN_MAX_BATCH) return ATTN_ERR_UNSUPPORTED;
-  if (total_q * Hq > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+  if (total_q * Hq > INT32_MAX || Hq > 65536) return ATTN_ERR_UNSUPPORTED;
   if (!(softcap == softcap) || !(scale_multiplier == scale_multiplier)) return ATTN_ERR_INVALID;
   if ((B == 0 && total_q > 0) || (B == 0 && P > 0)) return ATTN_ERR_INVALID;
   if (B == 0) return ATTN_OK;
@@ -87,6 +87,7 @@ attn_status read_args(CacheParams& p, attn_dtype dtype, int B, int P, int Hq, in
   p.Hkv = Hkv;
   p.d = head_dim;
   p.R = Hq / Hkv;
+  p.inv_R = 1.f / static_cast<float>(p.R);
   p.total_q = total_q;
   p.q = q;
   p.q_ts = q_ts;

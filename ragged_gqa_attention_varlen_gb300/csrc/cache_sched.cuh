@@ -24,7 +24,7 @@ struct Seg {
   int tok0, ntok;  // its query tokens
   int len;         // its keys
   int klo;         // keys below are outside of every row's window
-  bool own;
+  int own;
 };
 
 // Masks cut the key range of each row tile of the segment differently.
@@ -57,40 +57,21 @@ __device__ __forceinline__ int seg_tiles(const CacheParams& p, const Seg& s) {
   return static_cast<int>((static_cast<int64_t>(s.ntok) * p.R + kRows - 1) / kRows);
 }
 
-// Steps of one K/V head's row tiles.
-__device__ __forceinline__ int64_t seg_steps(const CacheParams& p, const Seg& s) {
-  const int nt = seg_tiles(p, s);
-  int lo, hi;
-  if (!seg_varies(p, s)) {
-    if (nt == 0) return 0;
-    tile_keys(p, s, 0, lo, hi);
-    return static_cast<int64_t>(nt) * tile_steps(lo, hi);
-  }
-  int64_t n = 0;
-  for (int t = 0; t < nt; ++t) {
-    tile_keys(p, s, t, lo, hi);
-    n += tile_steps(lo, hi);
-  }
-  return n;
-}
 
-// The first slot of prefix pfx that some sequence's window reaches (whole
-// warp): at default positions query 0 of sequence b stands at prefix_len +
-// own_len - Lq.
+// The first slot of prefix pfx that some sequence's window reaches: at default
+// positions query 0 of sequence b stands at prefix_len + own_len - Lq.
 __device__ __forceinline__ int prefix_klo(const CacheParams& p, int pfx, int len) {
   if (p.wl < 0 || p.q_pos) return 0;
   const int b0 = __ldg(p.cu_prefix + pfx), b1 = __ldg(p.cu_prefix + pfx + 1);
-  int least = INT32_MAX;
-  for (int b = b0 + static_cast<int>(threadIdx.x & 31); b < b1; b += 32) {
+  int64_t lo = len;
+  for (int b = b0; b < b1 && lo > 0; ++b) {
     const int nq = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b);
-    if (nq > 0) least = min(least, __ldg(p.own.lens + b) - nq);
+    if (nq > 0) lo = min(lo, static_cast<int64_t>(len) + __ldg(p.own.lens + b) - nq - p.wl);
   }
-  least = __reduce_min_sync(0xffffffffu, least);
-  const int64_t lo = static_cast<int64_t>(len) + least - p.wl;
-  return lo <= 0 ? 0 : static_cast<int>(min(lo, static_cast<int64_t>(len)));
+  return static_cast<int>(max(lo, static_cast<int64_t>(0)));
 }
 
-// Segment s (0 .. P+B-1).  For prefixes klo is left to the caller.
+// Segment s (0 .. P+B-1).
 __device__ __forceinline__ Seg seg_load(const CacheParams& p, int s) {
   Seg g;
   g.own = s >= p.P;
@@ -100,8 +81,58 @@ __device__ __forceinline__ Seg seg_load(const CacheParams& p, int s) {
   g.tok0 = __ldg(p.cu_q + b0);
   g.ntok = __ldg(p.cu_q + b1) - g.tok0;
   g.len = __ldg((g.own ? p.own.lens : p.prefix.lens) + g.row);
-  g.klo = 0;
+  g.klo = g.own ? 0 : prefix_klo(p, g.row, g.len);
   return g;
+}
+
+// What a planner needs of a segment.
+struct SegPlan {
+  Seg s;
+  int plen;    // keys of the prefix that it follows, or its own for a prefix
+  int waits;   // its rows have results of another segment to be joined with
+  int tiles;   // row tiles of a K/V head
+  int each;    // steps of each row tile, -1: they differ
+  int lo, hi;  // keys of the row tiles when they are all the same
+};
+
+__device__ __forceinline__ SegPlan seg_plan(const CacheParams& p, int s) {
+  SegPlan g;
+  g.s = seg_load(p, s);
+  g.plen = g.s.own ? 0 : g.s.len;
+  g.waits = !g.s.own;
+  if (g.s.own && p.P) {
+    const int pfx = prefix_of(p, g.s.row);
+    if (pfx >= 0) {
+      g.plen = __ldg(p.prefix.lens + pfx);
+      g.waits = prefix_klo(p, pfx, g.plen) < g.plen;
+    }
+  }
+  g.tiles = seg_tiles(p, g.s);
+  g.each = seg_varies(p, g.s) ? -1 : 0;
+  g.lo = g.hi = 0;
+  if (g.each == 0 && g.tiles > 0) {
+    tile_keys(p, g.s, 0, g.lo, g.hi);
+    g.each = tile_steps(g.lo, g.hi);
+  }
+  return g;
+}
+
+// Steps of one K/V head's row tiles (when they differ: one by one).
+__device__ __forceinline__ int64_t seg_steps(const CacheParams& p, const SegPlan& g) {
+  if (g.each >= 0) return static_cast<int64_t>(g.tiles) * g.each;
+  int64_t n = 0;
+  for (int t = 0; t < g.tiles; ++t) {
+    int lo, hi;
+    tile_keys(p, g.s, t, lo, hi);
+    n += tile_steps(lo, hi);
+  }
+  return n;
+}
+
+// x / R for 0 <= x < 2^20: the quotient's distance from an integer border is
+// at least 1 / (2R), far above the error of the fp32 product.
+__device__ __forceinline__ int head_div(const CacheParams& p, int x) {
+  return static_cast<int>((static_cast<float>(x) + 0.5f) * p.inv_R);
 }
 
 // What is wrong with segment s's metadata, as status bits.
@@ -162,82 +193,90 @@ __device__ __forceinline__ void block_scan2(int64_t& a, int& b, int64_t* tmp_a, 
 struct Plan {
   int64_t per, begin, end;  // this CTA's steps
   int seg;                  // the segment that holds step `begin`
+  int seg_tile;             // tiles (of all K/V heads) before it
   int64_t seg_begin;        // the first step of that segment
-  int seg_tile;             // row tiles (of all K/V heads) before it
   int bad;
+  int window;               // segments [seg, seg + window) of this array are filled
+  SegPlan segs[32];
   int64_t tmp_a[32];
   int tmp_b[32];
 };
 
-// Whole block.  kRowSplit: pieces are cut along the keys of row tiles
-// (attention); else along the rows of key tiles (key weights, where a segment
-// that is not wanted has no steps).  info[s], if not null and for CTA 0
-// only: {row tiles before segment s, steps of a row tile or -1 when they
-// differ}.  Returns false (for every thread) when there is nothing to do.
+// Whole block: this CTA's share of the steps.  steps_of(s, plan of s, &each)
+// gives the steps of segment s, tiles_of(plan) its tiles, and what info[s].y
+// says (info is written by CTA 0: {tiles before segment s, each}).  Returns
+// false, for every thread, when there is nothing to do.  With as many threads
+// as segments or more, every segment is read once, in one round of loads.
 template <class StepsOf, class TilesOf>
 __device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, StepsOf steps_of,
                           TilesOf tiles_of) {
   const int nseg = p.P + p.B, tid = threadIdx.x, nt = blockDim.x;
-  if (tid == 0) pl->bad = 0;
-  __syncthreads();
+  const bool one = nseg <= nt;
+  SegPlan g = SegPlan();
   int bad = 0;
-  for (int s = tid; s < nseg; s += nt) bad |= seg_check(p, s);
-  if (bad) atomicOr(&pl->bad, bad);
-  __syncthreads();
-  if (pl->bad) return false;
-  // one pass when the segments fit the block; else the total first
+  if (one) {
+    if (tid < nseg) {
+      bad = seg_check(p, tid);
+      if (!bad) g = seg_plan(p, tid);
+    }
+  } else {
+    for (int s = tid; s < nseg; s += nt) bad |= seg_check(p, s);
+  }
+  if (tid == 0) {
+    pl->bad = 0;
+    pl->window = 0;
+  }
+  if (__syncthreads_or(bad)) {
+    if (bad) atomicOr(&pl->bad, bad);
+    __syncthreads();
+    return false;
+  }
   int64_t total = 0;
-  int tiles_total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t steps_before = 0;
+  for (int pass = one ? 1 : 0; pass < 2; ++pass) {  // pass 0: the total of many segments
+    int64_t before = 0;
     int tiles_before = 0;
     for (int s0 = 0; s0 < nseg; s0 += nt) {
       const int s = s0 + tid;
       int64_t a = 0;
       int b = 0, each = 0;
       if (s < nseg) {
-        a = steps_of(s, each);
-        b = tiles_of(s);
+        if (!one) g = seg_plan(p, s);
+        a = steps_of(g, each);
+        b = tiles_of(g);
       }
       const int64_t mine = a;
       const int mine_b = b;
       int64_t ta;
       int tb;
       block_scan2(a, b, pl->tmp_a, pl->tmp_b, ta, tb);
-      if (pass == 0 && nseg > nt) {
-        steps_before += ta;
-        tiles_before += tb;
-        continue;
-      }
-      if (pass == 0) {
-        total = ta;
-        tiles_total = tb;
-      }
-      const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-      const int64_t begin = per * blockIdx.x, first = steps_before + a - mine;
-      if (s < nseg) {
-        if (mine > 0 && begin >= first && begin < first + mine) {
+      if (pass == 1) {
+        if (one) total = ta;
+        const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+        const int64_t begin = per * blockIdx.x, first = before + a - mine;
+        const bool here = mine > 0 && begin >= first && begin < first + mine;
+        if (here) {
           pl->seg = s;
           pl->seg_begin = first;
           pl->seg_tile = tiles_before + b - mine_b;
         }
-        if (info && blockIdx.x == 0) info[s] = make_int2(tiles_before + b - mine_b, each);
+        if (info && blockIdx.x == 0 && s < nseg) info[s] = make_int2(tiles_before + b - mine_b, each);
+        if (s0 == 0 && tid == 0) {
+          pl->per = per;
+          pl->begin = begin;
+          pl->end = min(total, begin + per);
+        }
+        if (one) {
+          __syncthreads();
+          const int at = s - pl->seg;
+          if (pl->begin < pl->end && at >= 0 && at < 32 && s < nseg) pl->segs[at] = g;
+          if (tid == 0) pl->window = 32;
+        }
       }
-      if (s0 == 0 && tid == 0) {
-        pl->per = per;
-        pl->begin = begin;
-        pl->end = min(total, begin + per);
-      }
-      steps_before += ta;
+      before += ta;
       tiles_before += tb;
     }
-    if (pass == 0) {
-      if (nseg <= nt) break;
-      total = steps_before;
-      tiles_total = tiles_before;
-    }
+    if (pass == 0) total = before;
   }
-  (void)tiles_total;
   __syncthreads();
   return pl->begin < pl->end;
 }
