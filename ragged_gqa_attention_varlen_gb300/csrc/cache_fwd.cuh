@@ -131,6 +131,16 @@ constexpr uint32_t kColOv = 256;  // TMEM: S0 / P0 [0,128), S1 / P1 [128,256), O
 constexpr float kLazy = 8.f;                    // rescale when the maximum grows by more (base 2)
 constexpr float kFixedCap = 9.5f;               // largest cap with a reference known beforehand
 
+#ifndef KCH
+#define KCH 16
+#endif
+constexpr int kCh = KCH;
+__device__ __forceinline__ void tmem_ldn(uint32_t a, float (&x)[16]) { tmem_ld16(a, x); }
+__device__ __forceinline__ void tmem_ldn(uint32_t a, float (&x)[32]) { tmem_ld32(a, x); }
+__device__ __forceinline__ void tmem_stn(uint32_t a, float (&x)[16]) { tmem_st16(a, reinterpret_cast<uint32_t(&)[16]>(x)); }
+__device__ __forceinline__ void tmem_stn(uint32_t a, float (&x)[32]) { tmem_st32(a, x); }
+__device__ __forceinline__ void tmem_stp(uint32_t a, uint32_t (&x)[8]) { tmem_st8(a, x); }
+__device__ __forceinline__ void tmem_stp(uint32_t a, uint32_t (&x)[16]) { tmem_st16(a, x); }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       p, pl, info,
       [&](const SegPlan& g, int& each) -> int64_t {
         each = g.each;
-        return seg_steps(p, g) * p.Hkv;
+        return seg_cost(p, g) * p.Hkv;
       },
       [&](const SegPlan& g) -> int { return g.tiles * p.Hkv; });
   if (blockIdx.x == 0 && tid == 0) {
@@ -502,12 +512,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt = g.tiles;
         const bool varies = g.each < 0;
         int lo = g.lo, hi = g.hi;
-        int64_t a = first;  // first step of the row tile
+        int64_t a = first;  // first unit of the row tile
         int gi = 0, t = 0;
         if (!varies) {
           if (g.each > 0 && begin > a) {  // skip whole row tiles before this CTA's share
-            const int64_t skip = min((begin - a) / g.each, static_cast<int64_t>(nt) * p.Hkv);
-            a += skip * g.each;
+            const int cost = tile_cost(g.each);
+            const int64_t skip = min((begin - a) / cost, static_cast<int64_t>(nt) * p.Hkv);
+            a += skip * cost;
             gi = static_cast<int>(skip / nt);
             t = static_cast<int>(skip - static_cast<int64_t>(gi) * nt);
           }
@@ -519,9 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (; ok && t < nt && a < end; ++t) {
             if (varies) tile_keys(p, g.s, t, lo, hi);
             const int n = varies ? tile_steps(lo, hi) : g.each;
-            const int64_t s1 = min(a + n, end);
-            const int64_t sb = max(a, begin);
-            if (sb < s1) {
+            // units [a, a + kTileCost) carry no step
+            const int64_t at = a + kTileCost;  // of step 0
+            const int f0 = static_cast<int>(max(begin - at, static_cast<int64_t>(0)));
+            const int f1 = static_cast<int>(min(end - at, static_cast<int64_t>(n)));
+            if (f0 < f1) {
               Piece pc;
               pc.row = g.s.row;
               pc.own = g.s.own;
@@ -535,17 +548,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               pc.plen = g.plen;
               pc.klo = lo;
               pc.khi = hi;
-              pc.kt0 = lo / kKeys + static_cast<int>(sb - a);
-              pc.kt1 = lo / kKeys + static_cast<int>(s1 - a);
-              const bool before = a < begin, after = a + n > end;  // parts elsewhere
-              pc.first = !before;
-              pc.mode = before || after ? 1 : (g.waits ? 2 : 0);
-              if (!before && lane == 0)
+              pc.kt0 = lo / kKeys + f0;
+              pc.kt1 = lo / kKeys + f1;
+              pc.first = f0 == 0;
+              pc.mode = f0 > 0 || f1 < n ? 1 : (g.waits ? 2 : 0);  // parts elsewhere; another segment
+              if (f0 == 0 && lane == 0)
                 meta[tile0 + gi * nt + t] = make_int2(
-                    blockIdx.x, after ? static_cast<int>((a + n - 1) / per) - static_cast<int>(blockIdx.x) + 1 : 1);
+                    blockIdx.x, f1 < n ? static_cast<int>((at + n - 1) / per) - static_cast<int>(blockIdx.x) + 1 : 1);
               ok = publish(pc);
             }
-            a += n;
+            a += tile_cost(n);
             x0 += kRows;
             h0 += kRows;
             if (p.R < 2 * kRows) {
@@ -559,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (varies && a >= end) break;
-        first = varies ? a : first + static_cast<int64_t>(g.each) * nt * p.Hkv;
+        first = varies ? a : first + static_cast<int64_t>(tile_cost(g.each)) * nt * p.Hkv;
         tile0 += nt * p.Hkv;
       }
       Piece last = {};
@@ -657,17 +669,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the bounds are applied per key only where they cut some row's keys
         const bool edge = __any_sync(0xffffffffu, valid && (key0 < jlo || key0 + 63 > jhi));
         // base-2 logits (less bref) of columns [c0, c0 + 16) from their products
-        auto logits16 = [&](float (&x)[16], int c0) {
+        auto logits16 = [&](float (&x)[kCh], int c0) {
           if (CAP) {
             bool small = false;
             if (!FIXED) {  // with a large cap, most calls stay far below it
               float top = 0.f;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+              for (int i = 0; i < kCh; ++i) top = fmaxf(top, fabsf(x[i]));
               small = !__any_sync(0xffffffffu, !(top * in_scale < 0.55f));
             }
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
+            for (int i = 0; i < kCh; i += 2) {
               const uint64_t th = tanh2_fp32(f2_mul(f2_make(x[i], x[i + 1]), f2_make(in_scale, in_scale)), small);
               x[i] = f2_lo(th);
               x[i + 1] = f2_hi(th);
@@ -676,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float sc = CAP ? out_scale : in_scale;
           if (POS && kpos) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kCh; ++i) {
               const int kq = __shfl_sync(0xffffffffu, c0 < 32 ? kpa : kpb, (c0 & 31) + i);
               const bool adm = key0 + c0 + i < pc.len && (p.wl < 0 || kq >= pos - p.wl) &&
                                (p.wr < 0 || kq <= pos + p.wr);
@@ -687,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (POS) {
             const float pos0 = static_cast<float>(pos - key0 - c0);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
+            for (int i = 0; i < kCh; i += 2) {
               const uint64_t dist = f2_make(fabsf(pos0 - i), fabsf(pos0 - (i + 1)));
               const uint64_t z = f2_fma(f2_make(x[i], x[i + 1]), f2_make(sc, sc),
                                         f2_fma(dist, f2_make(-slope2, -slope2), f2_make(-bref, -bref)));
@@ -696,11 +708,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= sc;
+            for (int i = 0; i < kCh; ++i) x[i] *= sc;
           }
           if (edge) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < kCh; ++i)
               x[i] = key0 + c0 + i >= jlo && key0 + c0 + i <= jhi ? x[i] : -INFINITY;
           }
         };
@@ -709,22 +721,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool need = false;
         // without logits to keep, the second pass scales the products itself
-        const bool keep = CAP || POS || edge || !(in_scale > 0.f);
+        const bool keep = CAP || (POS && (kpos || p.slopes)) || edge || !(in_scale > 0.f);
         if (!FIXED) {
           float* mxs = sMax + (step & 1) * 256;
           float mx = -INFINITY;
           if (any) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < 64; c0 += 16) {
-              float x[16];
-              tmem_ld16(sb + c0, x);
+            for (int c0 = 0; c0 < 64; c0 += kCh) {
+              float x[kCh];
+              tmem_ldn(sb + c0, x);
               tmem_wait_ld();
               if (keep) {
                 logits16(x, c0);
-                tmem_st16(sb + c0, reinterpret_cast<uint32_t(&)[16]>(x));
+                tmem_stn(sb + c0, x);
               }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[i]);
+              for (int i = 0; i < kCh; ++i) mx = fmaxf(mx, x[i]);
             }
             if (keep)
               tmem_wait_st();
@@ -749,14 +761,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m_use = FIXED || m_run == -INFINITY ? 0.f : m_run;
           const float sc = keep ? 1.f : in_scale;
 #pragma unroll 1
-          for (int c0 = 0; c0 < 64; c0 += 16) {
-            float x[16];
-            tmem_ld16(sb + c0, x);
+          for (int c0 = 0; c0 < 64; c0 += kCh) {
+            float x[kCh];
+            tmem_ldn(sb + c0, x);
             tmem_wait_ld();
             if (FIXED) logits16(x, c0);
-            uint32_t pk[8];
+            uint32_t pk[kCh / 2];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
+            for (int i = 0; i < kCh; i += 2) {
               uint64_t z = f2_make(x[i], x[i + 1]);
               if (!FIXED) z = f2_fma(z, f2_make(sc, sc), f2_make(-m_use, -m_use));
               const float e0 = ex2_approx(f2_lo(z)), e1 = ex2_approx(f2_hi(z));
@@ -764,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               l2 = f2_add(l2, f2_make(e0, e1));
               lr2 = f2_add(lr2, Pack<BF16>::unpack(pk[i >> 1]));
             }
-            tmem_st8(sb + c0 / 2, pk);
+            tmem_stp(sb + c0 / 2, pk);
           }
           if (!FIXED && kt > pc.kt0 && __any_sync(0xffffffffu, need)) {
             // O follows the new reference, once the previous products are in

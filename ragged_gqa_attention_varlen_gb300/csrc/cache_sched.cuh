@@ -3,13 +3,14 @@
 // A row tile is 128 consecutive packed rows of one segment and K/V head: row x
 // is token x / R of the segment's tokens and head x % R of the group (R query
 // heads per K/V head).  It visits the 128-key tiles that hold a key some row
-// of it may attend to.  All (row tile, key tile) steps of a call, segment by
-// segment, form one line of W steps, and the CTA c of G takes steps [c * per,
-// (c + 1) * per), per = ceil(W / G): however uneven the lengths, every CTA
-// does the same number of steps in one go, and a long sequence of a small
-// batch spreads over the whole GPU.  A row tile cut by such a border leaves
-// one partial result per CTA, which the merge kernel joins.  Every CTA derives
-// its share from the lengths itself, so nothing is launched before.
+// of it may attend to.  A tile of n steps costs n + kTileCost units (its
+// Q rows, the first step's latency and its results cost about two steps); all
+// tiles of a call, segment by segment, form one line of W units, and the CTA c
+// of G takes units [c * per, (c + 1) * per), per = ceil(W / G): however uneven
+// the lengths, every CTA does the same work in one go, and a long sequence of
+// a small batch spreads over the whole GPU.  A row tile cut by such a border
+// leaves one partial result per CTA, which the join kernel adds up.  Every CTA
+// derives its share from the lengths itself, so nothing is launched before.
 #pragma once
 #include "cache.cuh"
 
@@ -17,6 +18,7 @@ namespace attn {
 namespace kv {
 
 constexpr int kRows = 128;
+constexpr int kTileCost = 2;
 constexpr int kMaxCtas = 160;  // CTAs of the attention and weights kernels, at most
 
 struct Seg {
@@ -117,14 +119,17 @@ __device__ __forceinline__ SegPlan seg_plan(const CacheParams& p, int s) {
   return g;
 }
 
-// Steps of one K/V head's row tiles (when they differ: one by one).
-__device__ __forceinline__ int64_t seg_steps(const CacheParams& p, const SegPlan& g) {
-  if (g.each >= 0) return static_cast<int64_t>(g.tiles) * g.each;
+// Cost of a tile of n steps.
+__device__ __forceinline__ int tile_cost(int n) { return n > 0 ? n + kTileCost : 0; }
+
+// Cost of one K/V head's row tiles (when they differ: one by one).
+__device__ __forceinline__ int64_t seg_cost(const CacheParams& p, const SegPlan& g) {
+  if (g.each >= 0) return static_cast<int64_t>(g.tiles) * tile_cost(g.each);
   int64_t n = 0;
   for (int t = 0; t < g.tiles; ++t) {
     int lo, hi;
     tile_keys(p, g.s, t, lo, hi);
-    n += tile_steps(lo, hi);
+    n += tile_cost(tile_steps(lo, hi));
   }
   return n;
 }
@@ -191,10 +196,10 @@ __device__ __forceinline__ void block_scan2(int64_t& a, int& b, int64_t* tmp_a, 
 
 // Results of the plan, in shared memory.
 struct Plan {
-  int64_t per, begin, end;  // this CTA's steps
-  int seg;                  // the segment that holds step `begin`
+  int64_t per, begin, end;  // this CTA's units
+  int seg;                  // the segment that holds unit `begin`
   int seg_tile;             // tiles (of all K/V heads) before it
-  int64_t seg_begin;        // the first step of that segment
+  int64_t seg_begin;        // the first unit of that segment
   int bad;
   int window;               // segments [seg, seg + window) of this array are filled
   SegPlan segs[32];
@@ -202,13 +207,13 @@ struct Plan {
   int tmp_b[32];
 };
 
-// Whole block: this CTA's share of the steps.  steps_of(s, plan of s, &each)
-// gives the steps of segment s, tiles_of(plan) its tiles, and what info[s].y
+// Whole block: this CTA's share of the work.  cost_of(plan of s, &each) gives
+// the cost of segment s, tiles_of(plan) its tiles, and what info[s].y
 // says (info is written by CTA 0: {tiles before segment s, each}).  Returns
 // false, for every thread, when there is nothing to do.  With as many threads
 // as segments or more, every segment is read once, in one round of loads.
-template <class StepsOf, class TilesOf>
-__device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, StepsOf steps_of,
+template <class CostOf, class TilesOf>
+__device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, CostOf cost_of,
                           TilesOf tiles_of) {
   const int nseg = p.P + p.B, tid = threadIdx.x, nt = blockDim.x;
   const bool one = nseg <= nt;
@@ -241,7 +246,7 @@ __device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, StepsOf st
       int b = 0, each = 0;
       if (s < nseg) {
         if (!one) g = seg_plan(p, s);
-        a = steps_of(g, each);
+        a = cost_of(g, each);
         b = tiles_of(g);
       }
       const int64_t mine = a;
