@@ -686,8 +686,7 @@ attn_status attn_varlen_cache_fwd(
  * take part in prefix_scores_out [P, Hkv, ...] in the same way, summed over
  * all sequences of the prefix; prefix_scores_out NULL: not wanted.  Sums are
  * in a fixed order. */
-size_t attn_varlen_cache_weights_workspace_size(int B, int P, int Hq, int Hkv, int64_t total_q,
-                                                int64_t own_slots, int64_t prefix_slots);
+size_t attn_varlen_cache_weights_workspace_size(void);
 attn_status attn_varlen_cache_weights(
     attn_dtype dtype, int B, int P, int Hq, int Hkv, int head_dim, int64_t total_q,
     const void *q, int64_t q_tok_stride, int64_t q_head_stride,

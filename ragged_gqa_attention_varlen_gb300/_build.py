@@ -18,8 +18,8 @@ OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["host.cu", "sched.cu", "fwd.cu", "bwd_dq.cu", "bwd_dkdv.cu", "bwd_dkdv_drop.cu", "bwd_dkdv_dmask.cu",
            "noalloc.cu",
            "host_pipeline.cu", "shard.cu", "gate.cu",
-           "cache_host.cu", "rotary.cu", "cache_fwd.cu", "cache_fwd_d160.cu", "cache_fwd_d128.cu",
-           "cache_fwd_d64.cu", "cache_weights.cu", "evict.cu"]
+           "cache_host.cu", "rotary.cu", "cache_fwd.cu", "cache_d160.cu", "cache_d128.cu",
+           "cache_d64.cu", "cache_weights.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-Wall"]

@@ -64,7 +64,7 @@ def load():
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes, f.restype = args, I
-    for name, n in (("fwd", [I, I, I, I, I, L]), ("weights", [I, I, I, I, L, L, L]),
+    for name, n in (("fwd", [I, I, I, I, I, L]), ("weights", []),
                     ("evict", [I, I, I, I, I])):
         f = getattr(lib, f"attn_varlen_cache_{name}_workspace_size")
         f.argtypes, f.restype = n, Z
@@ -383,7 +383,7 @@ def attention_varlen_cache_weights(q, k_cache, table, lens, cu_q, lse, scores=No
         binding._check_lse(lse, T, Hq)
         f32 = torch.float32
         ws, ws_bytes = _workspace(
-            workspace, lib.attn_varlen_cache_weights_workspace_size(B, P, Hq, Hkv, T, slots, pslots),
+            workspace, lib.attn_varlen_cache_weights_workspace_size(),
             q.device)
         code = lib.attn_varlen_cache_weights(
             *head, *_rows16("q", q, q.dtype, Hq, d, T), *_pages("k_cache", k_cache, q.dtype), *args,

@@ -125,7 +125,7 @@ bool encode_pages(CUtensorMap* m, const CacheParams& p, const Pages& pg, bool ta
 int device_ctas();  // CTAs of a persistent kernel on the current device
 
 size_t fwd_workspace(int B, int P, int Hq, int Hkv, int d, int64_t total_q);
-size_t weights_workspace(int B, int P, int Hkv, int64_t own_slots, int64_t prefix_slots);
+size_t weights_workspace();
 cudaError_t launch_fwd(const CacheParams& p, cudaStream_t s);
 cudaError_t launch_weights(const CacheParams& p, cudaStream_t s);
 

@@ -249,14 +249,7 @@ extern "C" attn_status attn_varlen_cache_fwd(
   return done(kv::launch_fwd(p, static_cast<cudaStream_t>(stream)));
 }
 
-extern "C" size_t attn_varlen_cache_weights_workspace_size(int B, int P, int Hq, int Hkv,
-                                                           int64_t total_q, int64_t own_slots,
-                                                           int64_t prefix_slots) {
-  if (B < 0 || P < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || total_q < 0 || own_slots < 0 ||
-      prefix_slots < 0)
-    return 0;
-  return weights_workspace(B, P, Hkv, own_slots, prefix_slots);
-}
+extern "C" size_t attn_varlen_cache_weights_workspace_size(void) { return weights_workspace(); }
 
 extern "C" attn_status attn_varlen_cache_weights(
     attn_dtype dtype, int B, int P, int Hq, int Hkv, int head_dim, int64_t total_q, const void* q,
@@ -296,10 +289,7 @@ extern "C" attn_status attn_varlen_cache_weights(
     p.wo_rs[0] = pso_rs;
     p.wo_hs[0] = pso_hs;
   }
-  if (!workspace_ok(workspace, workspace_bytes,
-                    weights_workspace(B, P, Hkv, static_cast<int64_t>(table_width) * page_size,
-                                      static_cast<int64_t>(P > 0 ? prefix_width : 0) * page_size)))
-    return ATTN_ERR_WORKSPACE;
+  if (!workspace_ok(workspace, workspace_bytes, weights_workspace())) return ATTN_ERR_WORKSPACE;
   p.ws = static_cast<uint8_t*>(workspace);
   return done(launch_weights(p, static_cast<cudaStream_t>(stream)));
 }

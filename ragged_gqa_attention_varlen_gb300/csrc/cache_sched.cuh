@@ -207,14 +207,15 @@ struct Plan {
   int tmp_b[32];
 };
 
-// Whole block: this CTA's share of the work.  cost_of(plan of s, &each) gives
-// the cost of segment s, tiles_of(plan) its tiles, and what info[s].y
-// says (info is written by CTA 0: {tiles before segment s, each}).  Returns
-// false, for every thread, when there is nothing to do.  With as many threads
-// as segments or more, every segment is read once, in one round of loads.
-template <class CostOf, class TilesOf>
-__device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, CostOf cost_of,
-                          TilesOf tiles_of) {
+// Whole block: this CTA's share of the work.  plan_of(s) plans segment s,
+// cost_of(plan) is the cost of its tiles, tiles_of(plan) their number.  info,
+// if not null, is written by CTA 0: info[s] = {tiles before segment s, each}.
+// Returns false, for every thread, when there is nothing to do.  With as many
+// threads as segments or more, every segment is read once, in one round of
+// loads.
+template <class PlanOf, class CostOf, class TilesOf>
+__device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, PlanOf plan_of,
+                          CostOf cost_of, TilesOf tiles_of) {
   const int nseg = p.P + p.B, tid = threadIdx.x, nt = blockDim.x;
   const bool one = nseg <= nt;
   SegPlan g = SegPlan();
@@ -222,7 +223,7 @@ __device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, CostOf cos
   if (one) {
     if (tid < nseg) {
       bad = seg_check(p, tid);
-      if (!bad) g = seg_plan(p, tid);
+      if (!bad) g = plan_of(tid);
     }
   } else {
     for (int s = tid; s < nseg; s += nt) bad |= seg_check(p, s);
@@ -245,9 +246,10 @@ __device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, CostOf cos
       int64_t a = 0;
       int b = 0, each = 0;
       if (s < nseg) {
-        if (!one) g = seg_plan(p, s);
-        a = cost_of(g, each);
+        if (!one) g = plan_of(s);
+        a = cost_of(g);
         b = tiles_of(g);
+        each = g.each;
       }
       const int64_t mine = a;
       const int mine_b = b;

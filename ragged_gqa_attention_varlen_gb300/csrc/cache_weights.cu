@@ -1,125 +1,69 @@
-// cache_weights.cu -- the attention weight that each cached key receives.
-#include "../../include/attn_varlen.h"
-#include "cache.cuh"
+// cache_weights.cu -- key weights over the paged cache: the sums of cut key
+// tiles and the launches.
+#include <cstring>
+
+#include "cache_weights.cuh"
 
 namespace attn {
 namespace kv {
+
+// the tile kernel's instances, in translation units of their own
+extern template cudaError_t launch_weights_d<160>(const CacheParams&, const WeightsWs&,
+                                                  const CUtensorMap&, const CUtensorMap&, int,
+                                                  cudaStream_t);
+extern template cudaError_t launch_weights_d<128>(const CacheParams&, const WeightsWs&,
+                                                  const CUtensorMap&, const CUtensorMap&, int,
+                                                  cudaStream_t);
+extern template cudaError_t launch_weights_d<64>(const CacheParams&, const WeightsWs&,
+                                                 const CUtensorMap&, const CUtensorMap&, int,
+                                                 cudaStream_t);
+
 namespace {
 
-constexpr int kThreadsA = 128;
-constexpr int kPerLane = kHeadDim / 32;
-
-struct Row {
-  int b, g, qpos, prefix, prefix_len, own_len;
-};
-
-// What packed row (token, head) reads; false: the token is behind the last
-// sequence, or the call's lengths are inconsistent.
-__device__ bool find_row(const CacheParams& p, int tok, int h, Row& r) {
-  if (p.B == 0 || tok >= __ldg(p.cu_q + p.B)) return false;
-  r.b = seq_of(p.cu_q, 0, p.B, tok);
-  const int c0 = __ldg(p.cu_q + r.b), c1 = __ldg(p.cu_q + r.b + 1);
-  r.own_len = __ldg(p.own.lens + r.b);
-  r.prefix = p.P ? prefix_of(p, r.b) : -1;
-  r.prefix_len = r.prefix >= 0 ? __ldg(p.prefix.lens + r.prefix) : 0;
-  if (c0 > tok || c1 <= tok || c1 > p.total_q) {
-    report(p.status, ATTN_DEV_BAD_CU);
-    return false;
-  }
-  if (r.own_len < 0 || r.own_len > (static_cast<int64_t>(p.own.width) << p.page_log2) ||
-      r.prefix_len < 0 ||
-      (r.prefix >= 0 && r.prefix_len > (static_cast<int64_t>(p.prefix.width) << p.page_log2))) {
-    report(p.status, ATTN_DEV_BAD_CACHE);
-    return false;
-  }
-  r.g = h / p.R;
-  r.qpos = p.q_pos ? __ldg(p.q_pos + tok) : r.prefix_len + r.own_len - (c1 - c0) + (tok - c0);
-  return true;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void load_lane(const uint16_t* row, int d, float (&x)[kPerLane]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) x[i] = i * 32 + lane < d ? to_float<BF16>(row[i * 32 + lane]) : 0.f;
-}
-
-__device__ __forceinline__ float dot(const float (&a)[kPerLane], const float (&b)[kPerLane]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// The logit of an admissible (query, key) pair, or -inf.
-__device__ __forceinline__ float logit(const CacheParams& p, float qk, int qpos, int kpos, float slope) {
-  if (kpos < pos_lo(p, qpos) || kpos > pos_hi(p, qpos)) return -INFINITY;
-  float x = qk * p.sigma;
-  if (p.softcap > 0.f) x = p.softcap * tanhf(x / p.softcap);
-  return x - slope * static_cast<float>(abs(qpos - kpos));
-}
-
-__device__ __forceinline__ int key_position(const Table& t, int row, int g, int j, int base) {
-  return t.pos ? __ldg(t.pos + row * t.pos_rs + g * t.pos_hs + j) : base + j;
-}
-
-// One warp per (segment, K/V head, slot): gridDim.y = segment * Hkv + head.
-template <bool BF16>
-__global__ void __launch_bounds__(kThreadsA) weights_rows_kernel(const __grid_constant__ CacheParams p) {
-  const int seg = blockIdx.y / p.Hkv, g = blockIdx.y - seg * p.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = seg >= p.P, row = part ? seg - p.P : seg;
-  if (!p.w_out[part]) return;
-  const Table& t = part ? p.own : p.prefix;
-  const int len = __ldg(t.lens + row);
-  if (len < 0 || len > (static_cast<int64_t>(t.width) << p.page_log2)) {
-    report(p.status, ATTN_DEV_BAD_CACHE);
-    return;
-  }
-  const int b0 = part ? row : __ldg(p.cu_prefix + row), b1 = part ? row + 1 : __ldg(p.cu_prefix + row + 1);
-  const int t0 = __ldg(p.cu_q + b0), t1 = __ldg(p.cu_q + b1);
-  if (t0 < 0 || t1 < t0 || t1 > p.total_q) {
-    report(p.status, ATTN_DEV_BAD_CU);
-    return;
-  }
-  for (int j = blockIdx.x * 4 + warp; j < len; j += gridDim.x * 4) {
-    const int64_t ko = slot_row(p, p.k, t.pages + row * t.rs, j);
-    float k[kPerLane] = {}, w = 0.f;
-    if (ko >= 0)
-      load_lane<BF16>(static_cast<const uint16_t*>(p.k.base) + ko + g * p.k.head, p.d, k);
-    else if (lane == 0)
-      report(p.status, ATTN_DEV_BAD_CACHE);
-    for (int tok = t0; tok < t1; ++tok) {
-      Row r;
-      if (!find_row(p, tok, g * p.R, r)) continue;
-      const int kpos = key_position(t, row, g, j, part ? r.prefix_len : 0);
-      for (int i = 0; i < p.R; ++i) {
-        const int h = g * p.R + i;
-        float q[kPerLane];
-        load_lane<BF16>(static_cast<const uint16_t*>(p.q) + tok * p.q_ts + h * p.q_hs, p.d, q);
-        const float z = logit(p, dot(q, k), r.qpos, kpos,
-                              p.slopes ? __ldg(p.slopes + r.b * p.slopes_bs + h) : 0.f);
-        const float e = __ldg(p.lse + static_cast<int64_t>(tok) * p.Hq + h);
-        if (z != -INFINITY && e != -INFINITY) w += expf(z - e);
-      }
-    }
-    if (lane == 0) {
-      const float in = p.w_in[part] ? p.w_in[part][row * p.wi_rs[part] + g * p.wi_hs[part] + j] : 0.f;
-      p.w_out[part][row * p.wo_rs[part] + g * p.wo_hs[part] + j] = in + w;
-    }
-  }
+// Block c: the key tile whose row tiles are cut from CTA c on; its parts are
+// added in the order of the row tiles.
+__global__ void __launch_bounds__(128)
+    join_weights_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ WeightsWs w) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const WeightsCut c = reinterpret_cast<const WeightsCut*>(p.ws + w.cuts)[blockIdx.x];
+  const float* parts = reinterpret_cast<const float*>(p.ws + w.sums);
+  const int r = threadIdx.x, key = c.kt * kKeys + r;
+  if (c.parts == 0 || key >= c.len) return;
+  float sum = parts[(2 * blockIdx.x + 1) * 128 + r];
+#pragma unroll 4
+  for (int i = 1; i < c.parts; ++i) sum += parts[2 * (blockIdx.x + i) * 128 + r];
+  const float* in = p.w_in[c.own];
+  const float before = in ? in[c.row * p.wi_rs[c.own] + c.g * p.wi_hs[c.own] + key] : 0.f;
+  p.w_out[c.own][c.row * p.wo_rs[c.own] + c.g * p.wo_hs[c.own] + key] = before + sum;
 }
 
 }  // namespace
 
-size_t weights_workspace(int, int, int, int64_t, int64_t) { return 256; }
+size_t weights_workspace() { return weights_ws().total; }
 
 cudaError_t launch_weights(const CacheParams& p, cudaStream_t s) {
-  const dim3 grid(256, static_cast<unsigned>((p.P + p.B) * p.Hkv));
-  (p.dtype == 1 ? weights_rows_kernel<true> : weights_rows_kernel<false>)<<<grid, kThreadsA, 0, s>>>(p);
-  return cudaGetLastError();
+  const int grid = device_ctas();
+  if (grid < 1 || !encode_fn()) return cudaErrorInitializationError;
+  const WeightsWs w = weights_ws();
+  CUtensorMap tk, tkt;
+  std::memset(&tkt, 0, sizeof tkt);
+  if (!encode_pages(&tk, p, p.k, false) || (p.d == 160 && !encode_pages(&tkt, p, p.k, true)))
+    return cudaErrorInvalidValue;
+  cudaError_t e = p.d == 160   ? launch_weights_d<160>(p, w, tk, tkt, grid, s)
+                  : p.d == 128 ? launch_weights_d<128>(p, w, tk, tkt, grid, s)
+                               : launch_weights_d<64>(p, w, tk, tkt, grid, s);
+  // with at most one row tile no key tile is cut
+  if (e != cudaSuccess || p.total_q * p.R <= kRows) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_weights_kernel, p, w);
 }
 
 }  // namespace kv

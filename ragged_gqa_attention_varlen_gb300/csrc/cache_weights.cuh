@@ -1,0 +1,629 @@
+// cache_weights.cuh -- the attention weight that each cached key receives: sum
+// over the query rows that read it of 2^(z - lse), z the base-2 logit.
+//
+// Keys lie in the TMEM lanes: S^T = K Q^T (128 keys x up to 128 query rows),
+// so a key's sum is a sum along one thread's columns and needs neither atomics
+// nor exchange.  Two ways to walk, by the number of 128-row tiles of a
+// segment's queries (as in cache_sched.cuh, which also cuts the work):
+//   one row tile (single tokens, a few drafts): Q stays, key tiles stream by;
+//     every step finishes its 128 keys.  Reading K once bounds it.
+//   several: a key tile stays, Q tiles stream by.  When the row tiles of a key
+//     tile are cut between CTAs, partial sums are added up by the join kernel.
+//     The elementwise work (one to three MUFU operations per element) bounds it.
+//
+// Warps (512 threads): 0 loads K by TMA, 1 issues the products into four TMEM
+// buffers, 2 plans, 4-11 sum (two groups of four, taking steps in turn, so
+// that each key's sum stays in one thread), 12-15 gather Q rows with cp.async,
+// with each row's lse, slope and position.
+#pragma once
+#include "../../include/attn_varlen.h"
+#include "cache_tile.cuh"
+
+namespace attn {
+namespace kv {
+
+// Workspace: the cut key tile that starts in each CTA, and partial sums.
+struct WeightsCut {
+  int parts;  // 0: none
+  int own, row, g, kt, len;
+};
+struct WeightsWs {
+  size_t cuts, sums, total;
+};
+inline WeightsWs weights_ws() {
+  WeightsWs w;
+  w.cuts = 0;
+  w.sums = (kMaxCtas * sizeof(WeightsCut) + 255) / 256 * 256;
+  w.total = w.sums + 2 * kMaxCtas * 128 * sizeof(float);
+  return w;
+}
+
+struct WPiece {
+  int row;  // of the segment's table; -1: the end
+  int own, g, tok0, ntok, len, plen;
+  int rows;      // query rows of a K/V head
+  int kt0, kt1;  // key tiles to write
+  int a0, a1;    // of these, those that some row reads
+  int t0, t1;    // row tiles
+  int cut;       // 0: whole; 1: partial sums, 2: those of the first part
+  int pad;
+};
+struct WPieceRing {
+  WPiece piece[4];
+  uint64_t full[4], empty[4];
+};
+
+struct RowInfo {  // of a Q tile
+  float nlse[128];    // -lse in base 2 (-inf: the row counts for nothing)
+  float nslope[128];  // -slope in base 2
+  int pos[128];
+  int least[4], most[4];  // positions of the valid rows, per loading warp
+};
+
+constexpr int kThreadsW = 512;
+
+template <int HD>
+struct WShape {
+  static constexpr uint32_t kT = HD == 160 ? 40960 : HD * 256;  // a K-major tile
+  static constexpr int kChunksK = (HD + 63) / 64;
+  static constexpr int kKS = HD == 160 ? 3 : (HD == 128 ? 4 : 6);
+  static constexpr int kQS = 2;
+  static constexpr uint32_t kOffQ = kKS * kT;
+  static constexpr uint32_t kOffInfo = kOffQ + kQS * kT;
+  static constexpr uint32_t kOffSum = kOffInfo + kQS * sizeof(RowInfo);  // [2 pieces][128]
+  static constexpr uint32_t kOffBar = (kOffSum + 2 * 128 * 4 + 15) / 16 * 16;
+};
+
+struct WBars {
+  uint64_t k_full[6], k_empty[6], q_full[2], q_empty[2], info_read[2];
+  uint64_t s_full[4], s_read[4], pair[4], drain;
+  WPieceRing ring;
+  Plan plan;
+  uint32_t tmem;
+  int abort;
+};
+
+// Row tiles [t0, t1) with a query that may attend to a key of tile kt.
+__device__ __forceinline__ void key_tile_rows(const CacheParams& p, const SegPlan& g, int nt, int kt,
+                                              int& t0, int& t1) {
+  t0 = 0;
+  t1 = nt;
+  const int64_t ja = static_cast<int64_t>(kt) * kKeys;
+  const int64_t jb = min(ja + kKeys, static_cast<int64_t>(g.s.len)) - 1;
+  if (jb < g.s.klo) {
+    t1 = 0;
+  } else if (g.s.own && !p.q_pos) {
+    const int64_t k0 = static_cast<int64_t>(g.s.len) - g.s.ntok;
+    int64_t i0 = 0, i1 = g.s.ntok - 1;
+    if (p.wr >= 0) i0 = max(i0, ja - p.wr - k0);
+    if (p.wl >= 0) i1 = min(i1, jb + p.wl - k0);
+    if (i0 > i1) {
+      t1 = 0;
+    } else {
+      t0 = static_cast<int>(i0 * p.R / kRows);
+      t1 = static_cast<int>((i1 * p.R + p.R - 1) / kRows) + 1;
+    }
+  }
+}
+
+// A segment as this kernel walks it: waits = row tiles; with one row tile or
+// none, tiles = 1 and each = key tiles; else tiles = key tiles and each = row
+// tiles (-1: they differ).  lo, hi: the keys that a single row tile reads.
+__device__ __forceinline__ SegPlan weights_plan(const CacheParams& p, int s) {
+  SegPlan g = seg_plan(p, s);
+  const int nt = g.tiles, kt = (g.s.len + kKeys - 1) / kKeys;
+  g.waits = nt;
+  if (!p.w_out[g.s.own] || kt == 0) {
+    g.tiles = g.each = 0;
+  } else if (nt <= 1) {
+    g.tiles = 1;
+    if (nt == 1 && seg_varies(p, g.s)) tile_keys(p, g.s, 0, g.lo, g.hi);
+    g.each = kt;
+  } else {
+    const bool varies = seg_varies(p, g.s) || g.s.klo > 0;
+    g.tiles = kt;
+    g.each = varies ? -1 : nt;
+  }
+  return g;
+}
+__device__ __forceinline__ int64_t weights_cost(const CacheParams& p, const SegPlan& g) {
+  if (g.each >= 0) return static_cast<int64_t>(g.tiles) * (g.each + kTileCost);
+  int64_t n = 0;
+  for (int kt = 0; kt < g.tiles; ++kt) {
+    int t0, t1;
+    key_tile_rows(p, g, g.waits, kt, t0, t1);
+    n += t1 - t0 + kTileCost;
+  }
+  return n;
+}
+
+__device__ __forceinline__ bool wpiece_take(WPieceRing* r, uint32_t& k, WPiece* out,
+                                            volatile int* abort) {
+  const int s = k & 3;
+  if (!mbar_wait(&r->full[s], (k >> 2) & 1, abort)) return false;
+  *out = r->piece[s];
+  ++k;
+  return true;
+}
+
+// A distance 0 <= d < 2^31 as fp32, from its low 12 and high bits: each, or-ed
+// into the mantissa of 2^23, is exact after 2^23 is taken off, and the sum is
+// rounded once.  (The conversion instruction shares the MUFU's pipe, which the
+// exponentials fill.)
+__device__ __forceinline__ float distance(int d) {
+  const float lo = __uint_as_float(0x4B000000u | (static_cast<uint32_t>(d) & 0xFFFu)) - 8388608.f;
+  const float hi = __uint_as_float(0x4B000000u | (static_cast<uint32_t>(d) >> 12)) - 8388608.f;
+  return fmaf(hi, 4096.f, lo);
+}
+
+template <bool BF16, int HD, bool CAP, bool POS>
+__global__ void __launch_bounds__(kThreadsW, 1)
+    cache_weights_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ WeightsWs w,
+                         const __grid_constant__ CUtensorMap tk,
+                         const __grid_constant__ CUtensorMap tkt) {
+  using S = WShape<HD>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint8_t* sK = sm;
+  uint8_t* sQ = sm + S::kOffQ;
+  RowInfo* sInfo = reinterpret_cast<RowInfo*>(sm + S::kOffInfo);
+  float* sSum = reinterpret_cast<float*>(sm + S::kOffSum);
+  WBars* bars = reinterpret_cast<WBars*>(sm + S::kOffBar);
+  volatile int* s_abort = &bars->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  WeightsCut* cuts = reinterpret_cast<WeightsCut*>(p.ws + w.cuts);
+  float* parts = reinterpret_cast<float*>(p.ws + w.sums);
+  if (tid == 0) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    cuts[blockIdx.x].parts = 0;
+  }
+
+  Plan* pl = &bars->plan;
+  bool busy = make_plan(
+      p, pl, nullptr, [&](int s) { return weights_plan(p, s); },
+      [&](const SegPlan& g) -> int64_t { return weights_cost(p, g) * p.Hkv; },
+      [&](const SegPlan&) -> int { return 0; });
+  if (blockIdx.x == 0 && tid == 0) {
+    if (pl->bad) report(p.status, pl->bad);
+    if (smem_addr(sm) & 1023u) report(p.status, ATTN_DEV_SMEM_ALIGN);
+  }
+  if (!busy || (smem_addr(sm) & 1023u)) return;  // uniform
+
+  if (tid == 0) {
+    for (int b = 0; b < S::kKS; ++b) {
+      mbar_init(&bars->k_full[b], 1);
+      mbar_init(&bars->k_empty[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->q_full[b], 4);
+      mbar_init(&bars->q_empty[b], 1);
+      mbar_init(&bars->info_read[b], 8);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->s_read[b], 4);
+      mbar_init(&bars->pair[b], 2);
+      mbar_init(&bars->ring.full[b], 1);
+      mbar_init(&bars->ring.empty[b], 14);  // K loads, products, 8 summing and 4 loading warps
+    }
+    mbar_init(&bars->drain, 1);
+    fence_barrier_init();
+    bars->abort = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  // one arrival per warp: the piece has been copied
+  auto take = [&](uint32_t& k, WPiece& pc) -> bool {
+    if (!__all_sync(0xffffffffu, wpiece_take(&bars->ring, k, &pc, s_abort))) return false;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->ring.empty[(k - 1) & 3]);
+    return pc.row >= 0;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K loads
+    if (lane == 0) {
+      prefetch_tensormap(&tk);
+      if (HD == 160) prefetch_tensormap(&tkt);
+    }
+    const int box = min(p.page_size, kKeys), pieces = kKeys / box;
+    uint32_t nt = 0, st = 0, ph = 0, loaded = 0;
+    WPiece pc;
+    bool ok = true;
+    while (ok && take(nt, pc)) {
+      const Table& t = pc.own ? p.own : p.prefix;
+      const int32_t* row = t.pages + pc.row * t.rs;
+      const int ch = lane / pieces, pi = lane - ch * pieces;  // box: (chunk, row block)
+      for (int kt = pc.a0; kt < pc.a1; ++kt) {
+        const int key0 = kt * kKeys;
+        const int have = min(pieces, (pc.len - key0 + box - 1) / box);
+        const bool mine = ch < S::kChunksK && pi < have;
+        const int page = mine ? tile_page(p, row, key0 + pi * box) : 0;
+        if (loaded >= S::kKS && !(ok = mbar_wait_warp(&bars->k_empty[st], ph ^ 1, s_abort))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], S::kT / pieces * have);
+        __syncwarp();
+        if (mine) {
+          uint8_t* dst = sK + st * S::kT;
+          const int slot = p.page_size > kKeys ? key0 & (p.page_size - 1) : 0;
+          if (HD == 160 && ch == 2)
+            tma_load_4d(dst + 2 * 16384 + pi * box * 64, &tkt, &bars->k_full[st], 128, pc.g, slot, page);
+          else
+            tma_load_4d(dst + ch * 16384 + pi * box * 128, &tk, &bars->k_full[st], ch * kChunk, pc.g,
+                        slot, page);
+        }
+        ++loaded;
+        if (++st == S::kKS) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (*s_abort && lane == 0) {  // let every load land before the CTA exits
+      const uint32_t n = min(loaded, static_cast<uint32_t>(S::kKS));
+      for (uint32_t f = loaded - n; f < loaded; ++f)
+        wait_drain(&bars->k_full[f % S::kKS], (f / S::kKS) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S^T = K Q^T
+    uint32_t nt = 0, step = 0, ks = 0, kph = 0, qs = 0, qph = 0;
+    WPiece pc;
+    bool ok = true;
+    while (ok && take(nt, pc)) {
+      const bool many = pc.t1 - pc.t0 > 1;  // a Q tile per step
+      for (int kt = pc.a0; ok && kt < pc.a1; ++kt) {
+        for (int t = pc.t0; t < pc.t1; ++t, ++step) {
+          if (t == pc.t0 && !(ok = mbar_wait_warp(&bars->k_full[ks], kph, s_abort))) break;
+          if ((many || kt == pc.a0) && !(ok = mbar_wait_warp(&bars->q_full[qs], qph, s_abort))) break;
+          if (step >= 4 && !(ok = mbar_wait_warp(&bars->s_read[step & 3], ((step - 4) >> 2) & 1, s_abort)))
+            break;
+          const bool last_q = many || kt == pc.a1 - 1, last_k = t == pc.t1 - 1;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint32_t kb = smem_addr(sK + ks * S::kT), qb = smem_addr(sQ + qs * S::kT);
+            const int cols = (min(kRows, pc.rows - t * kRows) + 15) / 16 * 16;
+            const uint32_t id = idesc_f16(128, cols, BF16, false, false);
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+              umma_ss(tmem + (step & 3) * 128, kmajor_desc(kb, k), kmajor_desc(qb, k), id, k > 0);
+            umma_commit(&bars->s_full[step & 3]);
+            if (last_q) umma_commit(&bars->q_empty[qs]);
+            if (last_k) umma_commit(&bars->k_empty[ks]);
+          }
+          __syncwarp();
+          if (last_q && ++qs == S::kQS) {
+            qs = 0;
+            qph ^= 1;
+          }
+          if (last_k && ++ks == S::kKS) {
+            ks = 0;
+            kph ^= 1;
+          }
+        }
+      }
+    }
+    if (lane == 0) {
+      umma_commit(&bars->drain);
+      wait_drain(&bars->drain, 0);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ plan
+    uint32_t npub = 0;
+    bool ok = true;
+    auto publish = [&](const WPiece& pc) -> bool {
+      const int slot = npub & 3;
+      if (npub >= 4 && !mbar_wait_warp(&bars->ring.empty[slot], ((npub >> 2) - 1) & 1, s_abort))
+        return false;
+      if (lane == 0) {
+        bars->ring.piece[slot] = pc;
+        mbar_arrive(&bars->ring.full[slot]);
+      }
+      __syncwarp();
+      ++npub;
+      return true;
+    };
+    const int64_t per = pl->per, begin = pl->begin, end = pl->end;
+    int64_t a = pl->seg_begin;  // first unit of the tile
+    const int s0 = pl->seg, known = pl->window;
+    for (int s = s0; ok && a < end && s < p.P + p.B; ++s) {
+      if (s - s0 >= known && ((s - s0) & 31) == 0) {  // the next 32 segments
+        __syncwarp();
+        if (s + lane < p.P + p.B) pl->segs[lane] = weights_plan(p, s + lane);
+        __syncwarp();
+      }
+      const SegPlan g = pl->segs[(s - s0) & 31];
+      const int nt = g.waits;
+      for (int gi = 0; ok && gi < p.Hkv && a < end; ++gi) {
+        for (int t = 0; ok && t < g.tiles && a < end; ++t) {
+          WPiece pc;
+          pc.row = g.s.row;
+          pc.own = g.s.own;
+          pc.g = gi;
+          pc.tok0 = g.s.tok0;
+          pc.ntok = g.s.ntok;
+          pc.len = g.s.len;
+          pc.plen = g.plen;
+          pc.rows = g.s.ntok * p.R;
+          pc.cut = 0;
+          pc.t0 = 0;
+          pc.t1 = nt;
+          int n = g.each;
+          if (nt > 1) {
+            if (g.each < 0) {
+              key_tile_rows(p, g, nt, t, pc.t0, pc.t1);
+              n = pc.t1 - pc.t0;
+            }
+          }
+          // units [a, a + kTileCost) carry no step; a tile without any step
+          // belongs to the CTA of its first unit
+          const int64_t at = a + kTileCost;
+          const int f0 = static_cast<int>(max(begin - at, static_cast<int64_t>(0)));
+          const int f1 = static_cast<int>(min(end - at, static_cast<int64_t>(n)));
+          if (f0 < f1 || (n == 0 && a >= begin)) {
+            if (nt <= 1) {
+              pc.kt0 = f0;
+              pc.kt1 = f1;
+              pc.a0 = max(f0, g.lo / kKeys);
+              pc.a1 = nt == 1 ? max(pc.a0, min(f1, (g.hi + kKeys - 1) / kKeys)) : pc.a0;
+            } else {
+              pc.kt0 = t;
+              pc.kt1 = t + 1;
+              pc.a0 = t;
+              pc.a1 = n > 0 ? t + 1 : t;
+              if (n > 0 && (f0 > 0 || f1 < n)) {
+                pc.cut = f0 == 0 ? 2 : 1;
+                if (f0 == 0 && lane == 0) {
+                  WeightsCut c = {static_cast<int>((at + n - 1) / per) - static_cast<int>(blockIdx.x) + 1,
+                                  g.s.own, g.s.row, gi, t, g.s.len};
+                  cuts[blockIdx.x] = c;
+                }
+                pc.t1 = pc.t0 + f1;
+                pc.t0 += f0;
+              }
+            }
+            ok = publish(pc);
+          }
+          a = at + n;
+        }
+      }
+    }
+    WPiece last = {};
+    last.row = -1;
+    if (ok) publish(last);
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ Q rows
+    uint32_t nt = 0, qs = 0, qph = 0, loaded = 0;
+    const int wi = warp - 12, r = wi * 32 + lane;
+    WPiece pc;
+    bool ok = true;
+    while (ok && take(nt, pc)) {
+      if (pc.a0 >= pc.a1) continue;
+      for (int t = pc.t0; t < pc.t1; ++t) {
+        const int x0 = t * kRows, i0 = x0 / p.R, h0 = x0 - i0 * p.R;
+        const int n = min(kRows, pc.rows - x0);
+        // the row's scalars, while the stage may still be in use
+        float nlse = -INFINITY, nslope = 0.f;
+        int pos = 0;
+        if (r < n) {
+          const int dt = head_div(p, h0 + r), tok = pc.tok0 + i0 + dt;
+          const int h = pc.g * p.R + h0 + r - dt * p.R;
+          const float l = __ldg(p.lse + static_cast<int64_t>(tok) * p.Hq + h);
+          nlse = l > -INFINITY ? -l * kLog2e : -INFINITY;
+          if (POS) {
+            int b = pc.row;
+            if (!pc.own) {
+              const int b0 = __ldg(p.cu_prefix + pc.row), b1 = __ldg(p.cu_prefix + pc.row + 1);
+              b = b1 - b0 == pc.ntok && __ldg(p.cu_q + b0 + tok - pc.tok0) == tok &&
+                          __ldg(p.cu_q + b0 + tok - pc.tok0 + 1) > tok
+                      ? b0 + tok - pc.tok0
+                      : seq_of(p.cu_q, b0, b1, tok);
+            }
+            if (p.slopes) nslope = -__ldg(p.slopes + b * p.slopes_bs + h) * kLog2e;
+            if (p.q_pos)
+              pos = __ldg(p.q_pos + tok);
+            else
+              pos = pc.plen + __ldg(p.own.lens + b) - (__ldg(p.cu_q + b + 1) - tok);
+          }
+        }
+        if (loaded >= S::kQS) {
+          if (!(ok = mbar_wait_warp(&bars->q_empty[qs], qph ^ 1, s_abort))) break;
+          if (!(ok = mbar_wait_warp(&bars->info_read[qs], qph ^ 1, s_abort))) break;
+        }
+        uint8_t* dst = sQ + qs * S::kT;
+        copy_q_rows<HD>(p, dst, pc.g, pc.tok0 + i0, h0, n, wi, 4);
+        // rows up to the next multiple of 16 take part in the product
+        const int pad = (n + 15) / 16 * 16 - n;
+        for (int i = wi * 32 + lane; i < pad * (HD / 8); i += 128) {
+          const int q = i / (HD / 8);
+          *reinterpret_cast<uint4*>(dst + kmajor_unit(n + q, i - q * (HD / 8))) = make_uint4(0, 0, 0, 0);
+        }
+        RowInfo& info = sInfo[qs];
+        info.nlse[r] = nlse;
+        if (POS) {
+          info.nslope[r] = nslope;
+          info.pos[r] = pos;
+          const int lo = __reduce_min_sync(0xffffffffu, r < n ? pos : INT32_MAX);
+          const int hi = __reduce_max_sync(0xffffffffu, r < n ? pos : INT32_MIN);
+          if (lane == 0) {
+            info.least[wi] = lo;
+            info.most[wi] = hi;
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full[qs]);
+        ++loaded;
+        if (++qs == S::kQS) {
+          qs = 0;
+          qph ^= 1;
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ sums
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int r = quad * 32 + lane;  // key of the tile
+    const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    const float in_scale = CAP ? p.sigma / p.softcap : p.sigma * kLog2e;
+    const float sc = CAP ? p.softcap * kLog2e : in_scale;
+    uint32_t nt = 0, step = 0, qs = 0, qph = 0, npair = 0;
+    WPiece pc;
+    bool ok = true;
+    while (ok && take(nt, pc)) {
+      const float* in = p.w_in[pc.own];
+      if (in) in += pc.row * p.wi_rs[pc.own] + pc.g * p.wi_hs[pc.own];
+      float* out = p.w_out[pc.own] + pc.row * p.wo_rs[pc.own] + pc.g * p.wo_hs[pc.own];
+      // keys that no row reads keep their sum
+      for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
+        if ((kt < pc.a0 || kt >= pc.a1) && (kt & 1) == half) {
+          const int key = kt * kKeys + r;
+          if (key < pc.len) out[key] = in ? in[key] : 0.f;
+        }
+      }
+      const bool many = pc.t1 - pc.t0 > 1;
+      for (int kt = pc.a0; ok && kt < pc.a1; ++kt) {
+        const int key = kt * kKeys + r;
+        const bool there = key < pc.len;
+        float before = 0.f;  // read while the products run
+        if (there && in && !pc.cut) before = in[key];
+        int kpos = 0;
+        if (POS) {
+          const Table& t = pc.own ? p.own : p.prefix;
+          kpos = t.pos ? __ldg(t.pos + pc.row * t.pos_rs + pc.g * t.pos_hs + min(key, pc.len - 1))
+                       : (pc.own ? pc.plen : 0) + key;
+        }
+        float total = 0.f;
+        for (int t = pc.t0; t < pc.t1; ++t, ++step) {
+          const bool last_q = many || kt == pc.a1 - 1;
+          if (static_cast<int>(step & 1) == half) {
+            const int cols = min(kRows, pc.rows - t * kRows);
+            const RowInfo& info = sInfo[qs];
+            if (!(ok = mbar_wait_warp(&bars->q_full[qs], qph, s_abort))) break;
+            if (!(ok = mbar_wait_warp(&bars->s_full[step & 3], (step >> 2) & 1, s_abort))) break;
+            tc_fence_after();
+            bool free = true;  // no key of this warp is masked for any row
+            if (POS) {
+              const int least = min(min(info.least[0], info.least[1]), min(info.least[2], info.least[3]));
+              const int most = max(max(info.most[0], info.most[1]), max(info.most[2], info.most[3]));
+              free = __all_sync(0xffffffffu, !there || ((p.wl < 0 || kpos >= most - p.wl) &&
+                                                        (p.wr < 0 || kpos <= least + p.wr)));
+            }
+            uint64_t sum = f2_make(0.f, 0.f);
+            const uint32_t sb = tmem + (step & 3) * 128 + lane_addr;
+#pragma unroll 1
+            for (int c0 = 0; c0 < cols; c0 += 16) {
+              float x[16];
+              tmem_ld16(sb + c0, x);
+              float nl[16];
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(nl + i) = *reinterpret_cast<const float4*>(info.nlse + c0 + i);
+              if (POS) {
+                int d[16];
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                  *reinterpret_cast<int4*>(d + i) = *reinterpret_cast<const int4*>(info.pos + c0 + i);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) d[i] -= kpos;
+                if (!free) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    if ((p.wl >= 0 && d[i] > p.wl) || (p.wr >= 0 && -d[i] > p.wr)) nl[i] = -INFINITY;
+                }
+                if (p.slopes) {
+                  float ns[16];
+#pragma unroll
+                  for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4*>(ns + i) =
+                        *reinterpret_cast<const float4*>(info.nslope + c0 + i);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) nl[i] = fmaf(distance(abs(d[i])), ns[i], nl[i]);
+                }
+              }
+              tmem_wait_ld();
+              bool small = false;
+              if (CAP) {
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+                small = !__any_sync(0xffffffffu, !(top * fabsf(in_scale) < 0.55f));
+              }
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                uint64_t z = f2_make(x[i], x[i + 1]);
+                if (CAP) z = tanh2_fp32(f2_mul(z, f2_make(in_scale, in_scale)), small);
+                z = f2_fma(z, f2_make(sc, sc), f2_make(nl[i], nl[i + 1]));
+                sum = f2_add(sum, f2_make(ex2_approx(f2_lo(z)), ex2_approx(f2_hi(z))));
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->s_read[step & 3]);
+            total += f2_lo(sum) + f2_hi(sum);
+            if (!many) {  // one row tile
+              if (pc.cut)
+                parts[(2 * blockIdx.x + (pc.cut == 2)) * 128 + r] = total;
+              else if (there)
+                out[key] = before + total;
+            }
+          } else if (last_q && !(ok = mbar_wait_warp(&bars->q_full[qs], qph, s_abort))) {
+            break;  // (not ahead of the stage's filling, or two would count as one)
+          }
+          if (last_q) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->info_read[qs]);
+            if (++qs == S::kQS) {
+              qs = 0;
+              qph ^= 1;
+            }
+          }
+        }
+        if (!ok || !many) continue;
+        // both groups' shares of the row tiles
+        float* mine = sSum + (npair & 1) * 128;
+        if (half) mine[r] = total;
+        if (!(ok = warp_exchange(&bars->pair[quad], npair & 1, s_abort))) break;
+        ++npair;
+        if (!half) {
+          total += mine[r];
+          if (pc.cut)
+            parts[(2 * blockIdx.x + (pc.cut == 2)) * 128 + r] = total;
+          else if (there)
+            out[key] = before + total;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && *s_abort) report(p.status, ATTN_DEV_TIMEOUT_FWD);
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <bool B, int HD>
+auto pick_weights(const CacheParams& p) {
+  const bool pos = p.slopes || p.wl >= 0 || p.wr >= 0 || p.own.pos || (p.P && p.prefix.pos);
+  if (p.softcap > 0.f)
+    return pos ? cache_weights_kernel<B, HD, true, true> : cache_weights_kernel<B, HD, true, false>;
+  return pos ? cache_weights_kernel<B, HD, false, true> : cache_weights_kernel<B, HD, false, false>;
+}
+
+template <int HD>
+cudaError_t launch_weights_d(const CacheParams& p, const WeightsWs& w, const CUtensorMap& tk,
+                             const CUtensorMap& tkt, int grid, cudaStream_t s) {
+  constexpr uint32_t smem = WShape<HD>::kOffBar + sizeof(WBars);
+  static_assert(smem <= 232448, "shared memory");
+  auto k = p.dtype == 1 ? pick_weights<true, HD>(p) : pick_weights<false, HD>(p);
+  cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  k<<<grid, kThreadsW, smem, s>>>(p, w, tk, tkt);
+  return cudaGetLastError();
+}
+
+}  // namespace kv
+}  // namespace attn
