@@ -1,4 +1,5 @@
-"""Build libattn_varlen.so in-tree with nvcc for sm_103a.
+"""Build libattn_varlen.so in-tree with nvcc for sm_103a, and the native Python
+entry points of the generation calls (_native.so) with the host compiler.
 
 Each translation unit compiles in parallel; the objects are linked into one
 shared library next to this file.  No GPU is needed to build.
@@ -10,10 +11,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libattn_varlen.so")
+NATIVE = os.path.join(PKG, "_native.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["host.cu", "sched.cu", "fwd.cu", "bwd_dq.cu", "bwd_dkdv.cu", "bwd_dkdv_drop.cu", "bwd_dkdv_dmask.cu",
            "noalloc.cu",
@@ -38,10 +41,30 @@ def _deps():
     return files
 
 
+def build_native() -> None:
+    """Compile _native.so against this interpreter's torch."""
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+           os.path.join(CSRC, "py_cache.cpp"), "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch_cpu",
+           "-ltorch", "-lc10_cuda", "-lc10", "-Wl,-rpath," + libs]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on py_cache.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     return any(os.path.getmtime(f) > t for f in _deps()) or os.path.getmtime(__file__) > t
 
 
@@ -61,8 +84,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{res.stdout}\n{res.stderr}")
         return obj, res.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        native = ex.submit(build_native)
         results = list(ex.map(compile_one, SOURCES))
+        native.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log:
