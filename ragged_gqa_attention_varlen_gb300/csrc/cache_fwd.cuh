@@ -577,19 +577,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the bounds are applied per key only where they cut some row's keys
         const bool edge = __any_sync(0xffffffffu, valid && (key0 < jlo || key0 + 63 > jhi));
+        const bool behind = POS && __all_sync(0xffffffffu, !valid || pos >= key0 + 63);
         // base-2 logits (less bref) of columns [c0, c0 + 16) from their products
         auto logits16 = [&](float (&x)[kCh], int c0) {
           if (CAP) {
-            bool small = false;
-            if (!FIXED) {  // with a large cap, most calls stay far below it
-              float top = 0.f;
-#pragma unroll
-              for (int i = 0; i < kCh; ++i) top = fmaxf(top, fabsf(x[i]));
-              small = !__any_sync(0xffffffffu, !(top * in_scale < 0.55f));
-            }
 #pragma unroll
             for (int i = 0; i < kCh; i += 2) {
-              const uint64_t th = tanh2_fp32(f2_mul(f2_make(x[i], x[i + 1]), f2_make(in_scale, in_scale)), small);
+              const uint64_t th = tanh2_fp32(f2_mul(f2_make(x[i], x[i + 1]), f2_make(in_scale, in_scale)));
               x[i] = f2_lo(th);
               x[i + 1] = f2_hi(th);
             }
@@ -605,7 +599,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return;
           }
-          if (POS) {
+          if (POS && behind) {
+            // every key stands at or before the row: the distance is linear
+            const float a = fmaf(static_cast<float>(pos - key0 - c0), -slope2, -bref);
+#pragma unroll
+            for (int i = 0; i < kCh; i += 2) {
+              const uint64_t z = f2_fma(f2_make(x[i], x[i + 1]), f2_make(sc, sc),
+                                        f2_fma(f2_make(i, i + 1), f2_make(slope2, slope2), f2_make(a, a)));
+              x[i] = f2_lo(z);
+              x[i + 1] = f2_hi(z);
+            }
+          } else if (POS) {
             const float pos0 = static_cast<float>(pos - key0 - c0);
 #pragma unroll
             for (int i = 0; i < kCh; i += 2) {
@@ -617,7 +621,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < kCh; ++i) x[i] *= sc;
+            for (int i = 0; i < kCh; i += 2) {
+              const uint64_t z = f2_mul(f2_make(x[i], x[i + 1]), f2_make(sc, sc));
+              x[i] = f2_lo(z);
+              x[i + 1] = f2_hi(z);
+            }
           }
           if (edge) {
 #pragma unroll

@@ -57,6 +57,7 @@ struct RowInfo {  // of a Q tile
   float nlse[128];    // -lse in base 2 (-inf: the row counts for nothing)
   float nslope[128];  // -slope in base 2
   int pos[128];
+  float fpos[128];
   int least[4], most[4];  // positions of the valid rows, per loading warp
 };
 
@@ -144,16 +145,6 @@ __device__ __forceinline__ bool wpiece_take(WPieceRing* r, uint32_t& k, WPiece* 
   *out = r->piece[s];
   ++k;
   return true;
-}
-
-// A distance 0 <= d < 2^31 as fp32, from its low 12 and high bits: each, or-ed
-// into the mantissa of 2^23, is exact after 2^23 is taken off, and the sum is
-// rounded once.  (The conversion instruction shares the MUFU's pipe, which the
-// exponentials fill.)
-__device__ __forceinline__ float distance(int d) {
-  const float lo = __uint_as_float(0x4B000000u | (static_cast<uint32_t>(d) & 0xFFFu)) - 8388608.f;
-  const float hi = __uint_as_float(0x4B000000u | (static_cast<uint32_t>(d) >> 12)) - 8388608.f;
-  return fmaf(hi, 4096.f, lo);
 }
 
 template <bool BF16, int HD, bool CAP, bool POS>
@@ -447,6 +438,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         if (POS) {
           info.nslope[r] = nslope;
           info.pos[r] = pos;
+          info.fpos[r] = static_cast<float>(pos);
           const int lo = __reduce_min_sync(0xffffffffu, r < n ? pos : INT32_MAX);
           const int hi = __reduce_max_sync(0xffffffffu, r < n ? pos : INT32_MIN);
           if (lane == 0) {
@@ -508,11 +500,13 @@ __global__ void __launch_bounds__(kThreadsW, 1)
             if (!(ok = mbar_wait_warp(&bars->s_full[step & 3], (step >> 2) & 1, s_abort))) break;
             tc_fence_after();
             bool free = true;  // no key of this warp is masked for any row
+            bool near = true;  // positions are exact in fp32
             if (POS) {
               const int least = min(min(info.least[0], info.least[1]), min(info.least[2], info.least[3]));
               const int most = max(max(info.most[0], info.most[1]), max(info.most[2], info.most[3]));
               free = __all_sync(0xffffffffu, !there || ((p.wl < 0 || kpos >= most - p.wl) &&
                                                         (p.wr < 0 || kpos <= least + p.wr)));
+              near = __all_sync(0xffffffffu, max(kpos, most) < (1 << 24) && min(kpos, least) >= 0);
             }
             uint64_t sum = f2_make(0.f, 0.f);
             const uint32_t sb = tmem + (step & 3) * 128 + lane_addr;
@@ -524,40 +518,34 @@ __global__ void __launch_bounds__(kThreadsW, 1)
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<float4*>(nl + i) = *reinterpret_cast<const float4*>(info.nlse + c0 + i);
-              if (POS) {
-                int d[16];
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                  *reinterpret_cast<int4*>(d + i) = *reinterpret_cast<const int4*>(info.pos + c0 + i);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) d[i] -= kpos;
-                if (!free) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    if ((p.wl >= 0 && d[i] > p.wl) || (p.wr >= 0 && -d[i] > p.wr)) nl[i] = -INFINITY;
-                }
+              if (POS && free && near) {
                 if (p.slopes) {
-                  float ns[16];
+                  const float kf = static_cast<float>(kpos);
 #pragma unroll
-                  for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<float4*>(ns + i) =
-                        *reinterpret_cast<const float4*>(info.nslope + c0 + i);
+                  for (int i = 0; i < 16; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(info.fpos + c0 + i);
+                    const float4 s = *reinterpret_cast<const float4*>(info.nslope + c0 + i);
+                    nl[i] = fmaf(fabsf(f.x - kf), s.x, nl[i]);
+                    nl[i + 1] = fmaf(fabsf(f.y - kf), s.y, nl[i + 1]);
+                    nl[i + 2] = fmaf(fabsf(f.z - kf), s.z, nl[i + 2]);
+                    nl[i + 3] = fmaf(fabsf(f.w - kf), s.w, nl[i + 3]);
+                  }
+                }
+              } else if (POS) {
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) nl[i] = fmaf(distance(abs(d[i])), ns[i], nl[i]);
+                for (int i = 0; i < 16; ++i) {
+                  const int d = info.pos[c0 + i] - kpos;
+                  const bool cut = (p.wl >= 0 && d > p.wl) || (p.wr >= 0 && -d > p.wr);
+                  const float b = p.slopes ? fmaf(static_cast<float>(abs(d)), info.nslope[c0 + i], info.nlse[c0 + i])
+                                           : info.nlse[c0 + i];
+                  nl[i] = cut ? -INFINITY : b;
                 }
               }
               tmem_wait_ld();
-              bool small = false;
-              if (CAP) {
-                float top = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
-                small = !__any_sync(0xffffffffu, !(top * fabsf(in_scale) < 0.55f));
-              }
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
                 uint64_t z = f2_make(x[i], x[i + 1]);
-                if (CAP) z = tanh2_fp32(f2_mul(z, f2_make(in_scale, in_scale)), small);
+                if (CAP) z = tanh2_fp32(f2_mul(z, f2_make(in_scale, in_scale)));
                 z = f2_fma(z, f2_make(sc, sc), f2_make(nl[i], nl[i + 1]));
                 sum = f2_add(sum, f2_make(ex2_approx(f2_lo(z)), ex2_approx(f2_hi(z))));
               }
