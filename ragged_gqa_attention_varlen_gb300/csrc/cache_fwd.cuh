@@ -8,8 +8,10 @@
 //   P = 2^(z - m)        softmax warps, one TMEM lane per row; the 16-bit pairs
 //                        overwrite S, whose buffer is free again after P V
 //   O += P V             tcgen05.mma with P from TMEM
-// and l = sum of P in fp32 (for lse), lr = the same of the rounded P that
-// multiplies V (for out: one key gives exactly its V row).
+//   L += P 1             the same product with a tile of ones: the row sums of
+//                        the rounded P, which divide O (one key then gives
+//                        exactly its V row) without an element's instruction
+// and l = sum of P in fp32 in the softmax warps (for lse).
 //
 // Single-token calls read every K and V row once for R <= 128 rows of a group,
 // so the copies bound them; calls with many rows behind a shared prefix are
@@ -111,8 +113,9 @@ struct FwdShape {
   static constexpr uint32_t kOffK = kQ;
   static constexpr uint32_t kOffV = kOffK + kKS * kQ;
   static constexpr uint32_t kOffMax = kOffV + kVS * kV;          // [2 steps][2 halves][128]
-  static constexpr uint32_t kOffSum = kOffMax + 2 * 2 * 128 * 4;  // [2 pieces][2 halves][128] (l, lr)
-  static constexpr uint32_t kOffBar = kOffSum + 2 * 2 * 128 * 8;
+  static constexpr uint32_t kOffSum = kOffMax + 2 * 2 * 128 * 4;  // [2 pieces][2 halves][128] l
+  static constexpr uint32_t kOffOne = kOffSum + 2 * 2 * 128 * 4;  // 16 x 16 ones in any layout (1 KB)
+  static constexpr uint32_t kOffBar = kOffOne + 1024;
 };
 
 struct FwdBars {
@@ -127,7 +130,7 @@ struct FwdBars {
   int abort;
 };
 
-constexpr uint32_t kColOv = 256;  // TMEM: S0 / P0 [0,128), S1 / P1 [128,256), O [256, 256 + d)
+constexpr uint32_t kColOv = 256;  // TMEM: S0 / P0 [0,128), S1 / P1 [128,256), O [256, 256 + d), L 16 more
 constexpr float kLazy = 8.f;                    // rescale when the maximum grows by more (base 2)
 constexpr float kFixedCap = 9.5f;               // largest cap with a reference known beforehand
 constexpr int kCh = 16;                         // columns of a softmax pass
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sK = sm + S::kOffK;
   uint8_t* sV = sm + S::kOffV;
   float* sMax = reinterpret_cast<float*>(sm + S::kOffMax);
-  float2* sSum = reinterpret_cast<float2*>(sm + S::kOffSum);
+  float* sSum = reinterpret_cast<float*>(sm + S::kOffSum);
   FwdBars* bars = reinterpret_cast<FwdBars*>(sm + S::kOffBar);
   volatile int* s_abort = &bars->abort;
 
@@ -206,6 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     bars->abort = 0;
   }
+  for (int i = tid; i < 256; i += kThreads)
+    reinterpret_cast<uint32_t*>(sm + S::kOffOne)[i] = Pack<BF16>::two(1.f, 1.f);
+  fence_proxy_async_smem();
   if (warp == 1) {
     tmem_alloc(&bars->tmem, 512);
     tmem_relinquish();
@@ -326,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
       // ------------------------------------------------------------ O += P V
       constexpr uint32_t kIdO = idesc_f16(128, HD, BF16, false, true);
+      constexpr uint32_t kIdL = idesc_f16(128, 16, BF16, false, false);
+      const uint64_t ones = sdesc_sw64(smem_addr(sm + S::kOffOne));
       uint32_t take = 0, step = 0, st = 0, ph = 0, tiles = 0;
       Piece pc;
       bool ok = true;
@@ -366,6 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < ksteps; ++k)
               umma_ts(tmem + kColOv, tmem + (step & 1) * 128 + (k >> 2) * 64 + (k & 3) * 8,
                       sdesc_sw128(vb + k * 2048, 16384, 1024), kIdO, (kt > pc.kt0 || k > 0));
+            for (int k = 0; k < ksteps; ++k)
+              umma_ts(tmem + kColOv + HD, tmem + (step & 1) * 128 + (k >> 2) * 64 + (k & 3) * 8, ones,
+                      kIdL, (kt > pc.kt0 || k > 0));
             umma_commit(&bars->pv_done[step & 1]);
             umma_commit(&bars->v_empty[st]);
             if (kt == pc.kt1 - 1) umma_commit(&bars->o_full);
@@ -496,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // z = out_scale * tanh(in_scale * x), or in_scale * x, in base-2 units
     const float in_scale = CAP ? p.sigma / p.softcap : p.sigma * kLog2e;
     const float out_scale = CAP ? p.softcap * kLog2e : 1.f;
+    const float exp_scale = 2.f * kLog2e * in_scale;
     uint32_t take = 0, step = 0, tiles = 0;
     Piece pc;
     bool ok = true;
@@ -564,8 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_run = -slope2 * static_cast<float>(d);
         }
       }
-      const float bref = FIXED ? m_run : 0.f;
-      uint64_t l2 = f2_make(0.f, 0.f), lr2 = l2;
+      // subtracted from the logits; with FIXED they come without their constant c
+      const float bref = FIXED ? m_run - out_scale : 0.f;
+      uint64_t l2 = f2_make(0.f, 0.f);
 
       for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++step) {
         const int key0 = kt * kKeys + half * 64;
@@ -583,12 +596,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (CAP) {
 #pragma unroll
             for (int i = 0; i < kCh; i += 2) {
+              if (FIXED) {
+                // c - 2c / (1 + e^2x): the cap is small, so its absolute error of
+                // c 2^-22 is that of the logit itself; the constant c is in bref
+                const float d0 = 1.f + ex2_approx(fminf(x[i] * exp_scale, 60.f));
+                const float d1 = 1.f + ex2_approx(fminf(x[i + 1] * exp_scale, 60.f));
+                const float rc = rcp_approx(d0 * d1);
+                x[i] = rc * d1;
+                x[i + 1] = rc * d0;
+                continue;
+              }
               const uint64_t th = tanh2_fp32(f2_mul(f2_make(x[i], x[i + 1]), f2_make(in_scale, in_scale)));
               x[i] = f2_lo(th);
               x[i + 1] = f2_hi(th);
             }
           }
-          const float sc = CAP ? out_scale : in_scale;
+          const float sc = FIXED ? -2.f * out_scale : (CAP ? out_scale : in_scale);
           if (POS && kpos) {
 #pragma unroll
             for (int i = 0; i < kCh; ++i) {
@@ -622,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
 #pragma unroll
             for (int i = 0; i < kCh; i += 2) {
-              const uint64_t z = f2_mul(f2_make(x[i], x[i + 1]), f2_make(sc, sc));
+              const uint64_t z = f2_fma(f2_make(x[i], x[i + 1]), f2_make(sc, sc), f2_make(-bref, -bref));
               x[i] = f2_lo(z);
               x[i + 1] = f2_hi(z);
             }
@@ -671,7 +694,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               m_run = mx;
             }
             l2 = f2_mul(l2, f2_make(alpha, alpha));
-            lr2 = f2_mul(lr2, f2_make(alpha, alpha));
           }
         }
         if (any) {
@@ -691,7 +713,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float e0 = ex2_approx(f2_lo(z)), e1 = ex2_approx(f2_hi(z));
               pk[i >> 1] = Pack<BF16>::two(e0, e1);
               l2 = f2_add(l2, f2_make(e0, e1));
-              lr2 = f2_add(lr2, Pack<BF16>::unpack(pk[i >> 1]));
             }
             tmem_st8(sb + c0 / 2, pk);
           }
@@ -713,6 +734,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * alpha);
               tmem_st16(ob + c, u);
             }
+            if (half) {  // and L
+              uint32_t u[8];
+              tmem_ld8(tmem + kColOv + HD + lane_addr, u);
+              tmem_wait_ld();
+              u[0] = __float_as_uint(__uint_as_float(u[0]) * alpha);
+              tmem_st8(tmem + kColOv + HD + lane_addr, u);
+            }
           }
           tmem_wait_st();
         }
@@ -721,25 +749,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->p_full[step & 1]);
       }
       if (!ok) break;
-      // ---- the row's sums over both halves, then O
-      float l = f2_lo(l2) + f2_hi(l2), lr = f2_lo(lr2) + f2_hi(lr2);
-      float2* sums = sSum + (tiles & 1) * 256;
-      sums[half * 128 + r] = make_float2(l, lr);
+      // ---- the row's sum over both halves, then O
+      float l = f2_lo(l2) + f2_hi(l2);
+      float* sums = sSum + (tiles & 1) * 256;
+      sums[half * 128 + r] = l;
       if (!(ok = warp_exchange(&bars->l_x[quad], tiles & 1, s_abort))) break;
-      {
-        const float2 other = sums[(half ^ 1) * 128 + r];
-        l = half ? other.x + l : l + other.x;
-        lr = half ? other.y + lr : lr + other.y;
-      }
+      l = sums[r] + sums[128 + r];
       if (!(ok = mbar_wait_warp(&bars->o_full, tiles & 1, s_abort))) break;
       tc_fence_after();
       constexpr int kC = HD / 2;
-      float o[kC];
+      float o[kC], lr = 0.f;
       if (any) {
+        uint32_t u[8];
+        tmem_ld8(tmem + kColOv + HD + lane_addr, u);
         const uint32_t ob = tmem + kColOv + half * kC + lane_addr;
 #pragma unroll
         for (int c = 0; c < kC; c += 16) tmem_ld16(ob + c, *reinterpret_cast<float(*)[16]>(o + c));
         tmem_wait_ld();
+        lr = __uint_as_float(u[0]);
       }
       tc_fence_before();
       __syncwarp();
