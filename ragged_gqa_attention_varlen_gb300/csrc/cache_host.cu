@@ -162,7 +162,7 @@ extern "C" attn_status attn_varlen_cache_append(
     int32_t* lens_out, int32_t* device_status, void* stream) {
   if (dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID;
   if (B < 0 || Hkv < 1 || total < 0 || total > INT32_MAX) return ATTN_ERR_INVALID;
-  if (!dim_ok(head_dim) || B > ATTN_MAX_BATCH) return ATTN_ERR_UNSUPPORTED;
+  if (!dim_ok(head_dim) || B > ATTN_MAX_BATCH || Hkv > 4096) return ATTN_ERR_UNSUPPORTED;
   if (B == 0) return total == 0 ? ATTN_OK : ATTN_ERR_INVALID;
   if (!page_ok(page_size) || num_pages < 1) return ATTN_ERR_UNSUPPORTED;
   if (!cu_new || !table_ok(B, table, table_rs, table_width, lens) || lens_out == lens)

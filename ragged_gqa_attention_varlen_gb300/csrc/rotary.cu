@@ -16,6 +16,8 @@
 //
 // Bound by memory: every row is read and written once.  A block takes a few
 // tokens, so that one pair's sine serves all heads.
+#include <type_traits>
+
 #include "../../include/attn_varlen.h"
 #include "cache.cuh"
 
@@ -24,7 +26,8 @@ namespace kv {
 namespace {
 
 constexpr int kThreadsR = 256;
-constexpr int kItemsR = 1024;      // 16-byte units (pairs of them for halves) a block takes, about
+constexpr int kItemsR = 4096;   // 16-byte units (pairs of them for halves) a block turns, at most
+constexpr int kItemsA = 2048;   // ... and appends
 constexpr int kMaxTokensR = 32;
 constexpr int kMaxPairs = kHeadDim / 2;
 
@@ -35,20 +38,61 @@ __device__ __forceinline__ uint64_t turn_fraction(double inv_freq) {
   return f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0ull;
 }
 
-// cos and sin of pairs [0, pairs) for ntok tokens from tok0 on.
-__device__ __forceinline__ void fill_turns(const RotaryTable& r, int64_t tok0, int ntok,
-                                           float2 (*cs)[kMaxPairs]) {
-  for (int u = threadIdx.x; u < ntok * r.pairs; u += blockDim.x) {
-    const int t = u / r.pairs, i = u - t * r.pairs;
+// x / n for 0 <= x < 2^20, as in head_div (n is fixed for a launch).
+__device__ __forceinline__ int quotient(int x, float inv_n) {
+  return static_cast<int>((static_cast<float>(x) + 0.5f) * inv_n);
+}
+
+struct Turns {
+  float2 cs[kMaxTokensR][kMaxPairs];  // cos, sin
+  uint64_t per_pos[kMaxPairs];        // turn_fraction of each pair
+  int64_t row[kMaxPairs];             // its axis' row of the positions
+};
+
+// cos and sin of every pair for ntok tokens from tok0 on (whole block; the
+// caller synchronises).  The 64-bit arithmetic is done once per pair and
+// block: it runs at 1/50 of the fp32 rate here, and once per (pair, token) it
+// took most of the time of calls with one head.
+__device__ __forceinline__ void fill_turns(const RotaryTable& r, int64_t tok0, int ntok, Turns& s) {
+  const bool once = ntok * r.pairs <= static_cast<int>(blockDim.x);  // no pair is met twice
+  for (int i = threadIdx.x; i < r.pairs && !once; i += blockDim.x) {
     int ax = r.pair_axis ? __ldg(r.pair_axis + i) : 0;
     ax = min(max(ax, 0), r.axes - 1);
-    const int64_t pos = __ldg(r.positions + ax * r.axis_stride + tok0 + t);
-    const uint64_t turns = static_cast<uint64_t>(pos) * turn_fraction(__ldg(r.inv_freq + i));
+    s.per_pos[i] = turn_fraction(__ldg(r.inv_freq + i));
+    s.row[i] = ax * r.axis_stride;
+  }
+  const float inv_pairs = 1.f / r.pairs;
+  auto turn = [&](int t, int i, int64_t pos, uint64_t per_pos) {
+    const uint64_t turns = static_cast<uint64_t>(pos) * per_pos;
     // the top 32 bits as a signed fraction of a turn, in half turns
     const float h = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;
     float sn, cn;
     sincospif(h, &sn, &cn);
-    cs[t][i] = make_float2(cn, r.inverse ? -sn : sn);
+    s.cs[t][i] = make_float2(cn, r.inverse ? -sn : sn);
+  };
+  const int all = ntok * r.pairs;
+  if (once) {
+    const int u = threadIdx.x, t = quotient(u, inv_pairs), i = u - t * r.pairs;
+    if (u < all) {
+      const int ax = r.pair_axis ? __ldg(r.pair_axis + i) : 0;
+      const int64_t row = min(max(ax, 0), r.axes - 1) * r.axis_stride;
+      turn(t, i, __ldg(r.positions + row + tok0 + t), turn_fraction(__ldg(r.inv_freq + i)));
+    }
+    return;
+  }
+  __syncthreads();
+  for (int u0 = threadIdx.x; u0 < all; u0 += 4 * blockDim.x) {
+    int pos[4];  // four positions in flight
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = u0 + k * blockDim.x, t = quotient(u, inv_pairs);
+      if (u < all) pos[k] = __ldg(r.positions + s.row[u - t * r.pairs] + tok0 + t);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = u0 + k * blockDim.x, t = quotient(u, inv_pairs), i = u - t * r.pairs;
+      if (u < all) turn(t, i, pos[k], s.per_pos[i]);
+    }
   }
 }
 
@@ -85,65 +129,104 @@ __host__ __device__ __forceinline__ RowItems row_items(int d, int pairs, bool in
   return it;
 }
 
-// Item u of one row.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void row_item(const uint16_t* x, uint16_t* y, int u, int turning,
-                                         int pairs, bool interleaved, const float2* cs) {
-  if (VEC) {
+// Item u of a row: loaded first, turned and stored later, so that a thread has
+// the loads of several items in flight.  Rows are read and written once:
+// streaming accesses, which leave the caches to others.
+template <bool BF16>
+struct VecItem {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const uint16_t* x, int u, int turning, int pairs,
+                                       bool interleaved) {
+    const int f = u < turning ? u * 8 : 2 * pairs + (u - turning) * 8;
+    a = __ldcs(reinterpret_cast<const uint4*>(x + f));
+    if (u < turning && !interleaved) b = __ldcs(reinterpret_cast<const uint4*>(x + pairs + f));
+  }
+  __device__ __forceinline__ void store(uint16_t* y, int u, int turning, int pairs,
+                                        bool interleaved, const float2* cs) {
     if (u >= turning) {
-      const int f = 2 * pairs + (u - turning) * 8;
-      *reinterpret_cast<uint4*>(y + f) = *reinterpret_cast<const uint4*>(x + f);
-    } else if (interleaved) {
-      float v[8];
-      unpack8<BF16>(*reinterpret_cast<const uint4*>(x + u * 8), v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) turn2<BF16>(cs[u * 4 + i], v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<uint4*>(y + u * 8) = pack8<BF16>(v);
-    } else {
-      float a[8], b[8];
-      const uint4 ua = *reinterpret_cast<const uint4*>(x + u * 8);
-      const uint4 ub = *reinterpret_cast<const uint4*>(x + pairs + u * 8);
-      unpack8<BF16>(ua, a);
-      unpack8<BF16>(ub, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) turn2<BF16>(cs[u * 8 + i], a[i], b[i]);
-      *reinterpret_cast<uint4*>(y + u * 8) = pack8<BF16>(a);
-      *reinterpret_cast<uint4*>(y + pairs + u * 8) = pack8<BF16>(b);
+      __stcs(reinterpret_cast<uint4*>(y + 2 * pairs + (u - turning) * 8), a);
+      return;
     }
-  } else {
-    if (u >= turning) {
-      y[2 * pairs + u - turning] = x[2 * pairs + u - turning];
+    float va[8], vb[8];
+    unpack8<BF16>(a, va);
+    if (interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) turn2<BF16>(cs[u * 4 + i], va[2 * i], va[2 * i + 1]);
     } else {
-      const int fa = interleaved ? 2 * u : u, fb = interleaved ? 2 * u + 1 : u + pairs;
-      float a = to_float<BF16>(x[fa]), b = to_float<BF16>(x[fb]);
-      turn2<BF16>(cs[u], a, b);
-      y[fa] = from_float<BF16>(a);
-      y[fb] = from_float<BF16>(b);
+      unpack8<BF16>(b, vb);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) turn2<BF16>(cs[u * 8 + i], va[i], vb[i]);
+      __stcs(reinterpret_cast<uint4*>(y + pairs + u * 8), pack8<BF16>(vb));
+    }
+    __stcs(reinterpret_cast<uint4*>(y + u * 8), pack8<BF16>(va));
+  }
+};
+template <bool BF16>
+struct ScalarItem {
+  uint16_t a, b;
+  __device__ __forceinline__ void load(const uint16_t* x, int u, int turning, int pairs,
+                                       bool interleaved) {
+    if (u >= turning) {
+      a = x[2 * pairs + u - turning];
+    } else {
+      a = x[interleaved ? 2 * u : u];
+      b = x[interleaved ? 2 * u + 1 : u + pairs];
     }
   }
-}
+  __device__ __forceinline__ void store(uint16_t* y, int u, int turning, int pairs,
+                                        bool interleaved, const float2* cs) {
+    if (u >= turning) {
+      y[2 * pairs + u - turning] = a;
+      return;
+    }
+    float va = to_float<BF16>(a), vb = to_float<BF16>(b);
+    turn2<BF16>(cs[u], va, vb);
+    y[interleaved ? 2 * u : u] = from_float<BF16>(va);
+    y[interleaved ? 2 * u + 1 : u + pairs] = from_float<BF16>(vb);
+  }
+};
+template <bool BF16, bool VEC>
+using Item = typename std::conditional<VEC, VecItem<BF16>, ScalarItem<BF16>>::type;
 
 // gridDim.x: runs of `ntok` tokens; gridDim.y: runs of `heads` heads over
 // both tensors.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreadsR)
     rotary_kernel(const __grid_constant__ RotaryParams p, int ntok, int heads) {
-  __shared__ float2 cs[kMaxTokensR][kMaxPairs];
+  __shared__ Turns turns;
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * ntok;
   ntok = static_cast<int>(min(static_cast<int64_t>(ntok), p.T - tok0));
   const int h0 = blockIdx.y * heads;
   const int nh = min(heads, p.t[0].H + p.t[1].H - h0);
-  fill_turns(p.r, tok0, ntok, cs);
+  fill_turns(p.r, tok0, ntok, turns);
   __syncthreads();
   const RowItems it = row_items<VEC>(p.d, p.r.pairs, p.r.interleaved);
-  for (int u = threadIdx.x; u < ntok * nh * it.total; u += kThreadsR) {
-    const int row = u / it.total, t = row / nh;
-    const int h = h0 + row - t * nh;
-    const RotaryTensor& x = p.t[h >= p.t[0].H];
-    const int hh = h >= p.t[0].H ? h - p.t[0].H : h;
-    row_item<BF16, VEC>(static_cast<const uint16_t*>(x.x) + (tok0 + t) * x.ts + hh * x.hs,
-                        static_cast<uint16_t*>(x.out) + (tok0 + t) * x.ots + hh * x.ohs,
-                        u - row * it.total, it.turning, p.r.pairs, p.r.interleaved, cs[t]);
+  const float inv_total = 1.f / it.total, inv_nh = 1.f / nh;
+  const int all = ntok * nh * it.total;
+  constexpr int kBatch = 4;
+  for (int u0 = threadIdx.x; u0 < all; u0 += kThreadsR * kBatch) {
+    Item<BF16, VEC> item[kBatch];
+    uint16_t* out[kBatch];
+    int at[kBatch], tok[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int u = u0 + k * kThreadsR;
+      if (u < all) {
+        const int row = quotient(u, inv_total), t = quotient(row, inv_nh);
+        const int h = h0 + row - t * nh;
+        const RotaryTensor& x = p.t[h >= p.t[0].H];
+        const int64_t hh = h >= p.t[0].H ? h - p.t[0].H : h;
+        tok[k] = t;
+        at[k] = u - row * it.total;
+        out[k] = static_cast<uint16_t*>(x.out) + (tok0 + t) * x.ots + hh * x.ohs;
+        item[k].load(static_cast<const uint16_t*>(x.x) + (tok0 + t) * x.ts + hh * x.hs, at[k],
+                     it.turning, p.r.pairs, p.r.interleaved);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (u0 + k * kThreadsR < all)
+        item[k].store(out[k], at[k], it.turning, p.r.pairs, p.r.interleaved, turns.cs[tok[k]]);
   }
 }
 
@@ -153,7 +236,7 @@ __global__ void __launch_bounds__(kThreadsR)
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreadsR)
     append_kernel(const __grid_constant__ AppendParams p, int ntok) {
-  __shared__ float2 cs[kMaxTokensR][kMaxPairs];
+  __shared__ Turns turns;
   __shared__ int64_t row_k[kMaxTokensR], row_v[kMaxTokensR];  // first element, or -1
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * ntok;
   ntok = static_cast<int>(min(static_cast<int64_t>(ntok), p.T - tok0));
@@ -190,31 +273,44 @@ __global__ void __launch_bounds__(kThreadsR)
     row_k[t] = rk;
     row_v[t] = rv;
   }
-  if (p.r.inv_freq) fill_turns(p.r, tok0, ntok, cs);
+  if (p.r.inv_freq) fill_turns(p.r, tok0, ntok, turns);
   __syncthreads();
   const int pairs = p.r.inv_freq ? p.r.pairs : 0;
   const RowItems it = row_items<VEC>(p.d, pairs, p.r.interleaved);
   const RowItems iv = row_items<true>(p.d, 0, false);
   const int per = p.Hkv * (it.total + iv.total);
+  const float inv_per = 1.f / per, inv_total = 1.f / it.total, inv_v = 1.f / iv.total;
   for (int u = threadIdx.x; u < ntok * per; u += kThreadsR) {
-    const int t = u / per;
+    const int t = quotient(u, inv_per);
     int w = u - t * per;
     if (row_k[t] < 0) continue;
     if (w < p.Hkv * it.total) {
-      const int g = w / it.total;
-      row_item<BF16, VEC>(
-          static_cast<const uint16_t*>(p.kx) + (tok0 + t) * p.k_ts + g * p.k_hs,
-          static_cast<uint16_t*>(const_cast<void*>(p.k.base)) + row_k[t] + g * p.k.head,
-          w - g * it.total, it.turning, pairs, p.r.interleaved, cs[t]);
+      const int64_t g = quotient(w, inv_total);
+      w -= static_cast<int>(g) * it.total;
+      Item<BF16, VEC> item;
+      item.load(static_cast<const uint16_t*>(p.kx) + (tok0 + t) * p.k_ts + g * p.k_hs, w, it.turning,
+                pairs, p.r.interleaved);
+      item.store(static_cast<uint16_t*>(const_cast<void*>(p.k.base)) + row_k[t] + g * p.k.head, w,
+                 it.turning, pairs, p.r.interleaved, turns.cs[t]);
     } else {
       w -= p.Hkv * it.total;
-      const int g = w / iv.total;
-      row_item<BF16, true>(
-          static_cast<const uint16_t*>(p.vx) + (tok0 + t) * p.v_ts + g * p.v_hs,
-          static_cast<uint16_t*>(const_cast<void*>(p.v.base)) + row_v[t] + g * p.v.head,
-          w - g * iv.total, 0, 0, false, nullptr);
+      const int64_t g = quotient(w, inv_v);
+      w -= static_cast<int>(g) * iv.total;
+      VecItem<BF16> item;
+      item.load(static_cast<const uint16_t*>(p.vx) + (tok0 + t) * p.v_ts + g * p.v_hs, w, 0, 0, false);
+      item.store(static_cast<uint16_t*>(const_cast<void*>(p.v.base)) + row_v[t] + g * p.v.head, w, 0, 0,
+                 false, nullptr);
     }
   }
+}
+
+// Tokens of a block: as many as `most` items hold, but enough blocks for four
+// rounds of the SMs (a single round of few blocks is a chain of latencies).
+int block_tokens(int64_t T, int64_t items_per_token, int most) {
+  int64_t n = most / items_per_token;
+  const int64_t spread = T / (4 * 152);
+  n = n < spread ? n : spread;
+  return static_cast<int>(n < 1 ? 1 : (n > kMaxTokensR ? kMaxTokensR : n));
 }
 
 bool vector_pairs(int pairs, bool interleaved) { return pairs % (interleaved ? 4 : 8) == 0; }
@@ -226,10 +322,10 @@ cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t s) {
   const int H = p.t[0].H + p.t[1].H;
   const RowItems it = vec ? row_items<true>(p.d, p.r.pairs, p.r.interleaved)
                           : row_items<false>(p.d, p.r.pairs, p.r.interleaved);
-  int ntok = kItemsR / (H * it.total);
-  ntok = ntok < 1 ? 1 : (ntok > kMaxTokensR ? kMaxTokensR : ntok);
+  const int ntok = block_tokens(p.T, static_cast<int64_t>(H) * it.total, kItemsR);
   int heads = H;
-  if (ntok == 1 && H * it.total > 2 * kItemsR) heads = (kItemsR + it.total - 1) / it.total;
+  // few tokens of many heads: the heads over several blocks
+  if (ntok == 1 && H * it.total > 1024) heads = (512 + it.total - 1) / it.total;
   const dim3 grid(static_cast<unsigned>((p.T + ntok - 1) / ntok), (H + heads - 1) / heads);
   auto k = p.dtype == 1 ? (vec ? rotary_kernel<true, true> : rotary_kernel<true, false>)
                         : (vec ? rotary_kernel<false, true> : rotary_kernel<false, false>);
@@ -241,8 +337,7 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
   const int pairs = p.r.inv_freq ? p.r.pairs : 0;
   const bool vec = vector_pairs(pairs, p.r.interleaved);
   const int per = p.Hkv * 2 * (p.d / 8);
-  int ntok = kItemsR / per;
-  ntok = ntok < 1 ? 1 : (ntok > kMaxTokensR ? kMaxTokensR : ntok);
+  const int ntok = block_tokens(p.T, per, kItemsA);
   const unsigned grid = p.T > 0 ? static_cast<unsigned>((p.T + ntok - 1) / ntok) : 1u;
   auto k = p.dtype == 1 ? (vec ? append_kernel<true, true> : append_kernel<true, false>)
                         : (vec ? append_kernel<false, true> : append_kernel<false, false>);
