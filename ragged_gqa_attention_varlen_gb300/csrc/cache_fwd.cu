@@ -24,9 +24,8 @@ constexpr int kWarpsJ = 4;
 constexpr int kHeadsJ = 8;  // rows (heads of a token) of a block
 
 // Joins the partial results of a row.  Its own slots were computed in one
-// part or several, and so was its prefix; part i has reference m_i, sums l_i
-// and lr_i and O_i, and with weights 2^(m_i - max m) the row is sum O_i / sum
-// lr_i.  Parts are added in the order of the keys, prefix last, so the result
+// part or several, and so was its prefix; part i has reference m_i, sum l_i and
+// O_i, and with weights 2^(m_i - max m) the row is sum O_i / sum l_i.  Parts are added in the order of the keys, prefix last, so the result
 // does not depend on which CTA finished first.  Rows that one part covers were
 // written by the tile kernel already; rows without any key are written here.
 // Eight heads of a token per block, eight lanes to the 128-byte line that holds
@@ -43,46 +42,47 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   const int f0 = (lane >> 3) + 4 * warp;
   if (h >= p.Hq || tok >= __ldg(p.cu_q + p.B)) return;  // (tokens behind the last sequence)
   const int g = h / p.R, hr = h - g * p.R;
-  const int2* info = reinterpret_cast<const int2*>(p.ws + w.info);
   const int2* meta = reinterpret_cast<const int2*>(p.ws + w.meta);
-  const float4* stats = reinterpret_cast<const float4*>(p.ws + w.stats);
+  const float2* stats = reinterpret_cast<const float2*>(p.ws + w.stats);
   const float4* part = reinterpret_cast<const float4*>(p.ws + w.rows);
   const int guess = min(tok, p.B - 1);  // one token each: no search
   const int b = __ldg(p.cu_q + guess) == tok && __ldg(p.cu_q + guess + 1) > tok
                     ? guess
                     : seq_of(p.cu_q, 0, p.B, tok);
-  const int pfx = p.P ? prefix_of(p, b) : -1;
-  Seg own;  // (of its own slots, the row tiles need no more)
-  own.own = 1;
-  own.klo = 0;
-  own.tok0 = __ldg(p.cu_q + b);
-  own.ntok = __ldg(p.cu_q + b + 1) - own.tok0;
-  own.len = __ldg(p.own.lens + b);
-  const int64_t xo = static_cast<int64_t>(tok - own.tok0) * p.R + hr;
-  const int to = static_cast<int>(xo / kRows), ro = static_cast<int>(xo % kRows);
-  int tp = 0, rp = 0, ntp = 0;
-  if (pfx >= 0) {
-    const int64_t n0 = __ldg(p.cu_q + __ldg(p.cu_prefix + pfx)), n1 = __ldg(p.cu_q + __ldg(p.cu_prefix + pfx + 1));
-    const int64_t xp = (tok - n0) * p.R + hr;
-    tp = static_cast<int>(xp / kRows);
-    rp = static_cast<int>(xp % kRows);
-    ntp = static_cast<int>(((n1 - n0) * p.R + kRows - 1) / kRows);
+  // whether the row's own slots and its prefix have any step, and the row's
+  // place in their row tiles
+  bool has_own, has_prefix = false;
+  int ro, rp = 0;
+  {
+    Seg own;
+    own.own = 1;
+    own.klo = 0;
+    own.tok0 = __ldg(p.cu_q + b);
+    own.ntok = __ldg(p.cu_q + b + 1) - own.tok0;
+    own.len = __ldg(p.own.lens + b);
+    const uint32_t x = static_cast<uint32_t>(tok - own.tok0) * p.R + hr;
+    int lo, hi;
+    tile_keys(p, own, x / kRows, lo, hi);
+    has_own = hi > lo;
+    ro = x % kRows;
+  }
+  if (p.P) {
+    const int pfx = prefix_of(p, b);
+    if (pfx >= 0) {
+      const int len = __ldg(p.prefix.lens + pfx);
+      has_prefix = prefix_klo(p, pfx, len) < len;
+      const int tok0 = __ldg(p.cu_q + max(__ldg(p.cu_prefix + pfx), 0));
+      rp = (static_cast<uint32_t>(tok - tok0) * p.R + hr) % kRows;
+    }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int ok = reinterpret_cast<const FwdHead*>(p.ws)->ok;
-  const int2 io = info[p.P + b];
-  const int2 ip = pfx >= 0 ? info[pfx] : make_int2(0, 0);
-  if (!ok) return;
-  int no = io.y;
-  if (no < 0) {
-    int lo, hi;
-    tile_keys(p, own, to, lo, hi);
-    no = tile_steps(lo, hi);
-  }
-  int2 mo = make_int2(0, 0), mp = mo;  // (first CTA, parts) of the two segments
-  if (no > 0) mo = meta[io.x + g * seg_tiles(p, own) + to];
-  if (ip.y > 0) mp = meta[ip.x + g * ntp + tp];
-  if (mo.y == 1 && mp.y == 0) return;
+  // (first CTA, parts) of the two segments
+  int2 mo = make_int2(0, 0), mp = mo;
+  const int64_t row = static_cast<int64_t>(tok) * p.Hq + h;
+  if (has_own) mo = meta[row];
+  if (has_prefix) mp = meta[p.total_q * p.Hq + row];
+  if (!ok || (mo.y == 1 && mp.y == 0)) return;
   const int parts = mo.y + mp.y;
   auto row_of = [&](int i) -> int64_t {
     if (i < mo.y)
@@ -94,23 +94,22 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   float top = -INFINITY;
 #pragma unroll 4
   for (int i = 0; i < parts; ++i) {
-    const float4 s = stats[row_of(i)];
+    const float2 s = stats[row_of(i)];
     if (s.y > 0.f) top = fmaxf(top, s.x);
   }
-  float l = 0.f, lr = 0.f;
+  float l = 0.f;
   float4 acc[kPer] = {};
 #pragma unroll 4
   for (int i = 0; i < parts; ++i) {
-    const int64_t row = row_of(i);
-    const float4 s = stats[row];
+    const int64_t pr = row_of(i);
+    const float2 s = stats[pr];
     float4 v[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
-      if (f0 + 4 * kWarpsJ * k < kUnits) v[k] = part[part_at<HD>(row, f0 + 4 * kWarpsJ * k)];
+      if (f0 + 4 * kWarpsJ * k < kUnits) v[k] = part[part_at<HD>(pr, f0 + 4 * kWarpsJ * k)];
     if (s.y > 0.f) {  // (a part without any weight may hold anything)
       const float a = ex2_approx(s.x - top);
       l = fmaf(a, s.y, l);
-      lr = fmaf(a, s.z, lr);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         acc[k].x = fmaf(a, v[k].x, acc[k].x);
@@ -120,7 +119,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
       }
     }
   }
-  const float inv = lr > 0.f ? 1.f / lr : 0.f;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
   uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(tok) * p.out_ts +
                   static_cast<int64_t>(h) * p.out_hs;
 #pragma unroll
@@ -130,7 +129,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
           make_uint2(Pack<BF16>::two(acc[k].x * inv, acc[k].y * inv),
                      Pack<BF16>::two(acc[k].z * inv, acc[k].w * inv));
   if (f0 == 0)
-    p.lse[static_cast<int64_t>(tok) * p.Hq + h] = l > 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
+    p.lse[row] = l > 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <int HD>

@@ -8,23 +8,28 @@
 //   P = 2^(z - m)        softmax warps, one TMEM lane per row; the 16-bit pairs
 //                        overwrite S, whose buffer is free again after P V
 //   O += P V             tcgen05.mma with P from TMEM
-//   L += P 1             the same product with a tile of ones: the row sums of
-//                        the rounded P, which divide O (one key then gives
-//                        exactly its V row) without an element's instruction
-// and l = sum of P in fp32 in the softmax warps (for lse).
+// and l = sum of P in fp32 in the softmax warps, which gives lse and divides O.
+// (O holds the rounded P: dividing by the sum of those as well makes a single
+// key give exactly its V row, but as two more instructions per element it took
+// 8 % of a capped call, and as a product with a tile of ones it doubled the
+// time of P V.  Roundings of many keys average out; a single key's moves the
+// result by at most half a step of the type.)
 //
 // Single-token calls read every K and V row once for R <= 128 rows of a group,
 // so the copies bound them; calls with many rows behind a shared prefix are
 // bound by the softmax warps' MUFU work and the hand-offs between them and
 // the tensor core, as the packed forward is.
 //
-// Warps (384 threads): 0 loads K (lanes 0-15) and V (lanes 16-31) by TMA, a
-// box of min(page_size, 128) rows x 64 features each; 1 issues S, 2 issues O
-// and clears the V rows of a cut tile that no row reads (the pages may hold
-// anything there, and 0 * NaN would reach O); 3 plans the CTA's pieces and
-// copies Q rows (a row is any (token, head), so Q is gathered with cp.async
-// into the swizzled layout rather than boxed by TMA); 4-11 softmax, two per
-// TMEM lane quadrant, each taking 64 of a step's keys.
+// Warps (512 threads): 0 loads K and 12 loads V by TMA, a box of min(page_size,
+// 128) rows x 64 features per lane; 1 issues S, 2 issues O and L and clears the
+// V rows of a cut tile that no row reads (the pages may hold anything there,
+// and 0 * NaN would reach O); 3 plans the CTA's pieces; 13-15 gather Q rows with
+// cp.async into the swizzled layout (a row is any (token, head), so TMA boxes
+// do not fit); 4-11 softmax, two per TMEM lane quadrant, each taking 64 of a
+// step's keys in passes of 16.  The passes are rolled loops: straight-line code
+// for all columns cost 8000 to 11000 clk of instruction fetches on a CTA's
+// first step and slowed the rest; four warps per quadrant with 32 keys each
+// gained nothing.
 #pragma once
 #include "../../include/attn_varlen.h"
 #include "cache_tile.cuh"
@@ -34,7 +39,7 @@ namespace kv {
 
 // Partial results of the forward in its workspace: byte offsets.
 struct FwdWs {
-  size_t info, meta, stats, rows, total;
+  size_t meta, stats, rows, total;
   int64_t cut_rows;  // rows of one CTA's border piece
 };
 struct FwdHead {  // at offset 0
@@ -42,18 +47,19 @@ struct FwdHead {  // at offset 0
 };
 inline FwdWs fwd_ws(int B, int P, int Hq, int Hkv, int d, int64_t total_q) {
   FwdWs w;
-  const int64_t R = Hq / Hkv, x = total_q * R;
-  const int64_t tiles = static_cast<int64_t>(Hkv) * (x / kRows + B + (P ? x / kRows + P : 0));
+  const int64_t x = total_q * (Hq / Hkv), all = total_q * Hq * (P ? 2 : 1);
   w.cut_rows = ((x < kRows ? x : kRows) + 7) / 8 * 8;
-  const int64_t rows = (2 * kMaxCtas * w.cut_rows + (P ? 2 * total_q * Hq : 0) + 7) / 8 * 8;
+  const int64_t rows = (2 * kMaxCtas * w.cut_rows + (P ? all : 0) + 7) / 8 * 8;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  w.info = 256;
-  w.meta = w.info + up(static_cast<size_t>(B + P) * sizeof(int2));
-  w.stats = w.meta + up(static_cast<size_t>(tiles) * sizeof(int2));
-  w.rows = w.stats + up(static_cast<size_t>(rows) * sizeof(float4));
+  w.meta = 256;
+  w.stats = w.meta + up(static_cast<size_t>(all) * sizeof(int2));
+  w.rows = w.stats + up(static_cast<size_t>(rows) * sizeof(float2));
   w.total = w.rows + up(static_cast<size_t>(rows) * d * sizeof(float));
+  (void)B;
   return w;
 }
+// meta: of every (own or prefix segment, token, head) whose row tile has steps,
+// the CTA of the tile's first part and the number of parts.
 // Partial row indices: CTA c's pieces of row tiles that continue from an
 // earlier CTA (2c) or into a later one (2c + 1), then whole row tiles that
 // wait for another segment's, by (own or prefix, token, head).
@@ -83,7 +89,9 @@ struct Piece {
   int kt0, kt1;     // key tiles
   int klo, khi;     // keys that some row of the tile may attend to
   int mode;         // 0: writes out and lse; 1: partial of a cut tile; 2: partial of a whole tile
-  int first;        // mode 1: the tile's first part
+  int first;        // the tile's first part
+  int parts;        // its parts
+  int pad[3];
 };
 
 struct PieceRing {
@@ -114,12 +122,11 @@ struct FwdShape {
   static constexpr uint32_t kOffV = kOffK + kKS * kQ;
   static constexpr uint32_t kOffMax = kOffV + kVS * kV;          // [2 steps][2 halves][128]
   static constexpr uint32_t kOffSum = kOffMax + 2 * 2 * 128 * 4;  // [2 pieces][2 halves][128] l
-  static constexpr uint32_t kOffOne = kOffSum + 2 * 2 * 128 * 4;  // 16 x 16 ones in any layout (1 KB)
-  static constexpr uint32_t kOffBar = kOffOne + 1024;
+  static constexpr uint32_t kOffBar = kOffSum + 2 * 2 * 128 * 4;
 };
 
 struct FwdBars {
-  uint64_t q_first, q_full, q_empty;
+  uint64_t q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t o_full, o_empty, drain;
@@ -130,20 +137,81 @@ struct FwdBars {
   int abort;
 };
 
-constexpr uint32_t kColOv = 256;  // TMEM: S0 / P0 [0,128), S1 / P1 [128,256), O [256, 256 + d), L 16 more
+constexpr int kThreadsF = 512;
+// registers per thread of warps 0-3, 4-11 and 12-15 (launched at 128)
+constexpr int kRegsPlan = 96, kRegsSoft = 168, kRegsLoad = 80;
+static_assert(kRegsPlan + 2 * kRegsSoft + kRegsLoad <= 4 * 128, "register split exceeds the launch");
+constexpr uint32_t kColOv = 256;  // TMEM: S0 / P0 [0,128), S1 / P1 [128,256), O [256, 256 + d)
 constexpr float kLazy = 8.f;                    // rescale when the maximum grows by more (base 2)
 constexpr float kFixedCap = 9.5f;               // largest cap with a reference known beforehand
-constexpr int kCh = 16;                         // columns of a softmax pass
+
+// One warp: the key tiles of every piece into the K (or V) stages, a box per
+// lane.
+template <int HD, bool K>
+__device__ __forceinline__ void load_pages(const CacheParams& p, FwdBars* bars, uint8_t* dst0,
+                                           const CUtensorMap* map, const CUtensorMap* tail, int box,
+                                           volatile int* s_abort) {
+  using S = FwdShape<HD>;
+  constexpr int kStages = K ? S::kKS : S::kVS;
+  constexpr uint32_t kBytes = K ? S::kQ : S::kV;  // of a whole tile
+  const int lane = threadIdx.x & 31;
+  uint64_t* full = K ? bars->k_full : bars->v_full;
+  uint64_t* empty = K ? bars->k_empty : bars->v_empty;
+  const int pieces = kKeys / box, ch = lane / pieces, pi = lane - ch * pieces;  // (chunk, row block)
+  uint32_t take = 0, st = 0, ph = 0, loaded = 0;
+  Piece pc;
+  bool ok = true;
+  while (ok) {
+    if (!__all_sync(0xffffffffu, piece_take(&bars->ring, take, &pc, s_abort))) break;
+    __syncwarp();
+    if (lane == 0) piece_done(&bars->ring, take);
+    if (pc.row < 0) break;
+    const Table& t = pc.own ? p.own : p.prefix;
+    const int32_t* row = t.pages + pc.row * t.rs;
+    auto page_of = [&](int kt) {  // this lane's page of key tile kt, or -1: no box
+      const int key = kt * kKeys + pi * box;
+      return ch < S::kChunksK && kt < pc.kt1 && key < pc.len ? tile_page(p, row, key) : -1;
+    };
+    int page = page_of(pc.kt0);
+    for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
+      const int key0 = kt * kKeys;
+      const int have = min(pieces, (pc.len - key0 + box - 1) / box);  // row blocks in use
+      const int next = page_of(kt + 1);  // read while this tile's stage is waited for
+      if (loaded >= kStages && !(ok = mbar_wait_warp(&empty[st], ph ^ 1, s_abort))) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], kBytes / pieces * have);
+      __syncwarp();
+      if (page >= 0) {
+        uint8_t* dst = dst0 + st * kBytes;
+        const int slot = p.page_size > kKeys ? key0 & (p.page_size - 1) : 0;
+        if (K && HD == 160 && ch == 2)
+          tma_load_4d(dst + 2 * 16384 + pi * box * 64, tail, &full[st], 128, pc.g, slot, page);
+        else
+          tma_load_4d(dst + ch * 16384 + pi * box * 128, map, &full[st], ch * kChunk, pc.g, slot, page);
+      }
+      page = next;
+      ++loaded;
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+  }
+  if (*s_abort && lane == 0) {  // let every load land before the CTA exits
+    const uint32_t n = min(loaded, static_cast<uint32_t>(kStages));
+    for (uint32_t f = loaded - n; f < loaded; ++f) wait_drain(&full[f % kStages], (f / kStages) & 1);
+  }
+}
 
 // CAP: the call has a softcap; FIXED: of at most kFixedCap and default key
 // positions, so P is taken against a bound and no maximum is tracked; POS:
 // the call has ALiBi, a mask or key positions.
 template <bool BF16, int HD, bool CAP, bool FIXED, bool POS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsF, 1)
     cache_fwd_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ FwdWs w,
                      const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tkt, const __grid_constant__ CUtensorMap tv) {
   using S = FwdShape<HD>;
+  constexpr int kCh = 16;  // columns of a softmax pass
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* sQ = sm;
   uint8_t* sK = sm + S::kOffK;
@@ -154,32 +222,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* s_abort = &bars->abort;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int2* info = reinterpret_cast<int2*>(p.ws + w.info);
   int2* meta = reinterpret_cast<int2*>(p.ws + w.meta);
-  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-  // ---- this CTA's share of the steps
-  Plan* pl = &bars->plan;
-  const bool busy = make_plan(
-      p, pl, info,
-      [&](int s) { return seg_plan(p, s); },
-      [&](const SegPlan& g) -> int64_t { return seg_cost(p, g) * p.Hkv; },
-      [&](const SegPlan& g) -> int { return g.tiles * p.Hkv; });
-  if (blockIdx.x == 0 && tid == 0) {
-    FwdHead* head = reinterpret_cast<FwdHead*>(p.ws);
-    int ok = pl->bad == 0;
-    if (smem_addr(sm) & 1023u) {
-      report(p.status, ATTN_DEV_SMEM_ALIGN);
-      ok = 0;
-    }
-    if (pl->bad) report(p.status, pl->bad);
-    head->ok = ok;
-  }
-  if (!busy || (smem_addr(sm) & 1023u)) return;  // uniform
-
   if (tid == 0) {
-    mbar_init(&bars->q_first, 8);
-    mbar_init(&bars->q_full, 1);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    mbar_init(&bars->q_full, 3);
     mbar_init(&bars->q_empty, 1);
     for (int b = 0; b < S::kKS; ++b) {
       mbar_init(&bars->k_full[b], 1);
@@ -204,95 +250,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&bars->ring.full[s], 1);
-      mbar_init(&bars->ring.empty[s], 12);  // K and V loads, two MMA issuers, 8 softmax warps
+      mbar_init(&bars->ring.empty[s], 15);  // K and V loads, two MMA issuers, 8 softmax, 3 Q warps
     }
     fence_barrier_init();
     bars->abort = 0;
   }
-  for (int i = tid; i < 256; i += kThreads)
-    reinterpret_cast<uint32_t*>(sm + S::kOffOne)[i] = Pack<BF16>::two(1.f, 1.f);
-  fence_proxy_async_smem();
   if (warp == 1) {
     tmem_alloc(&bars->tmem, 512);
     tmem_relinquish();
   }
+  if (warp == 13 && lane == 0) {
+    prefetch_tensormap(&tk);
+    prefetch_tensormap(&tv);
+    if (HD == 160) prefetch_tensormap(&tkt);
+  }
   tc_fence_before();
-  __syncthreads();
+
+  // ---- this CTA's share of the steps
+  Plan* pl = &bars->plan;
+  const bool busy = make_plan(
+      p, pl, [&](int s) { return seg_plan(p, s); },
+      [&](const SegPlan& g) -> int64_t { return seg_cost(p, g) * p.Hkv; });
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
+  if (blockIdx.x == 0 && tid == 0) {
+    FwdHead* head = reinterpret_cast<FwdHead*>(p.ws);
+    int ok = pl->bad == 0;
+    if (smem_addr(sm) & 1023u) {
+      report(p.status, ATTN_DEV_SMEM_ALIGN);
+      ok = 0;
+    }
+    if (pl->bad) report(p.status, pl->bad);
+    head->ok = ok;
+  }
+  if (!busy || (smem_addr(sm) & 1023u)) {  // uniform
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
   const int box = min(p.page_size, kKeys);  // rows of a load box
-  const int pieces = kKeys / box;           // boxes of a key tile and chunk
 
   if (warp < 4) {
-    warpgroup_reg_dealloc<kRegsLow>();
+    warpgroup_reg_dealloc<kRegsPlan>();
     if (warp == 0) {
-      // ------------------------------------------------------------ K and V loads
-      const bool is_k = lane < 16;
-      const int gl = lane & 15;
-      const unsigned gmask = is_k ? 0x0000ffffu : 0xffff0000u;
-      const int lead = is_k ? 0 : 16;
-      if (gl == 0) {
-        prefetch_tensormap(is_k ? &tk : &tv);
-        if (is_k && HD == 160) prefetch_tensormap(&tkt);
-      }
-      const int stages = is_k ? S::kKS : S::kVS;
-      const uint32_t bytes = is_k ? S::kQ : S::kV;  // of a whole tile
-      uint64_t* full = is_k ? bars->k_full : bars->v_full;
-      uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
-      uint8_t* dst0 = is_k ? sK : sV;
-      uint32_t take = 0, st = 0, ph = 0, loaded = 0;
-      Piece pc;
-      for (;;) {
-        if (!__all_sync(gmask, piece_take(&bars->ring, take, &pc, s_abort))) break;
-        __syncwarp(gmask);
-        if (gl == 0) piece_done(&bars->ring, take);
-        if (pc.row < 0) break;
-        const Table& t = pc.own ? p.own : p.prefix;
-        const int32_t* row = t.pages + pc.row * t.rs;
-        const int total = S::kChunksK * pieces;  // boxes of a tile: (chunk, row block)
-        bool ok = true;
-        for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
-          const int key0 = kt * kKeys;
-          const int have = min(pieces, (pc.len - key0 + box - 1) / box);  // row blocks in use
-          // page numbers before the wait for a free stage
-          int pages[2] = {0, 0};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int x = gl + 16 * i, pi = x % pieces;
-            if (x < total && pi < have) pages[i] = tile_page(p, row, key0 + pi * box);
-          }
-          if (loaded >= static_cast<uint32_t>(stages) &&
-              !(ok = __all_sync(gmask, mbar_wait(&empty[st], ph ^ 1, s_abort))))
-            break;
-          if (gl == 0) mbar_arrive_expect_tx(&full[st], bytes / pieces * have);
-          __syncwarp(gmask);
-          uint8_t* dst = dst0 + st * bytes;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int x = gl + 16 * i, ch = x / pieces, pi = x % pieces;
-            if (x < total && pi < have) {
-              const int slot = p.page_size > kKeys ? key0 & (p.page_size - 1) : 0;
-              if (is_k && HD == 160 && ch == 2)
-                tma_load_4d(dst + 2 * 16384 + pi * box * 64, &tkt, &full[st], 128, pc.g, slot,
-                            pages[i]);
-              else
-                tma_load_4d(dst + ch * 16384 + pi * box * 128, is_k ? &tk : &tv, &full[st],
-                            ch * kChunk, pc.g, slot, pages[i]);
-            }
-          }
-          ++loaded;
-          if (++st == static_cast<uint32_t>(stages)) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
-        if (!ok) break;
-      }
-      if (*s_abort && lane == lead) {
-        // let every load of this group land before the CTA exits
-        const uint32_t n = min(loaded, static_cast<uint32_t>(stages));
-        for (uint32_t f = loaded - n; f < loaded; ++f) wait_drain(&full[f % stages], (f / stages) & 1);
-      }
+      // ------------------------------------------------------------ K loads
+      load_pages<HD, true>(p, bars, sK, &tk, &tkt, box, s_abort);
     } else if (warp == 1) {
       // ------------------------------------------------------------ S = Q K^T
       if (lane == 0) {
@@ -303,9 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && piece_take(&bars->ring, take, &pc, s_abort)) {
           piece_done(&bars->ring, take);
           if (pc.row < 0) break;
-          if (!(tiles == 0 ? mbar_wait(&bars->q_first, 0, s_abort)
-                           : mbar_wait(&bars->q_full, (tiles - 1) & 1, s_abort)))
-            break;
+          if (!mbar_wait(&bars->q_full, tiles & 1, s_abort)) break;
           for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++step) {
             if (!(ok = mbar_wait(&bars->k_full[st], ph, s_abort))) break;
             // the product with the P that took the buffer's previous S (step - 2) is done
@@ -332,8 +331,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
       // ------------------------------------------------------------ O += P V
       constexpr uint32_t kIdO = idesc_f16(128, HD, BF16, false, true);
-      constexpr uint32_t kIdL = idesc_f16(128, 16, BF16, false, false);
-      const uint64_t ones = sdesc_sw64(smem_addr(sm + S::kOffOne));
       uint32_t take = 0, step = 0, st = 0, ph = 0, tiles = 0;
       Piece pc;
       bool ok = true;
@@ -374,9 +371,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < ksteps; ++k)
               umma_ts(tmem + kColOv, tmem + (step & 1) * 128 + (k >> 2) * 64 + (k & 3) * 8,
                       sdesc_sw128(vb + k * 2048, 16384, 1024), kIdO, (kt > pc.kt0 || k > 0));
-            for (int k = 0; k < ksteps; ++k)
-              umma_ts(tmem + kColOv + HD, tmem + (step & 1) * 128 + (k >> 2) * 64 + (k & 3) * 8, ones,
-                      kIdL, (kt > pc.kt0 || k > 0));
             umma_commit(&bars->pv_done[step & 1]);
             umma_commit(&bars->v_empty[st]);
             if (kt == pc.kt1 - 1) umma_commit(&bars->o_full);
@@ -394,10 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_drain(&bars->drain, 0);
       }
     } else {
-      // ------------------------------------------------------------ plan and Q rows
+      // ------------------------------------------------------------ plan
       uint32_t npub = 0;
       bool ok = true;
-      // the next piece for the whole CTA, and its Q rows
+      // the next piece for the whole CTA
       auto publish = [&](const Piece& pc) -> bool {
         const int slot = npub & 3;
         if (npub >= 4 && !mbar_wait_warp(&bars->ring.empty[slot], ((npub >> 2) - 1) & 1, s_abort))
@@ -407,20 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&bars->ring.full[slot]);
         }
         __syncwarp();
-        if (pc.row >= 0 && npub > 0) {  // (the softmax warps fetch the first piece's)
-          if (!mbar_wait_warp(&bars->q_empty, (npub - 1) & 1, s_abort)) return false;
-          copy_q_rows<HD>(p, sQ, pc.g, pc.tok, pc.head, pc.rows, 0, 1);
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->q_full);
-        }
         ++npub;
         return true;
       };
       const int64_t per = pl->per, begin = pl->begin, end = pl->end;
       int64_t first = pl->seg_begin;
-      int tile0 = pl->seg_tile;
       const int s0 = pl->seg, known = pl->window;
       for (int s = s0; ok && first < end && s < p.P + p.B; ++s) {
         if (s - s0 >= known && ((s - s0) & 31) == 0) {  // the next 32 segments
@@ -437,16 +422,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!varies) {
           if (g.each > 0 && begin > a) {  // skip whole row tiles before this CTA's share
             const int cost = tile_cost(g.each);
-            const int64_t skip = min((begin - a) / cost, static_cast<int64_t>(nt) * p.Hkv);
+            const int64_t skip = min(div64(begin - a, cost), static_cast<int64_t>(nt) * p.Hkv);
             a += skip * cost;
-            gi = static_cast<int>(skip / nt);
+            gi = static_cast<int>(div64(skip, nt));
             t = static_cast<int>(skip - static_cast<int64_t>(gi) * nt);
           }
           if (g.each == 0) gi = p.Hkv;
         }
         for (; ok && gi < p.Hkv && a < end; ++gi, t = 0) {
           int64_t x0 = static_cast<int64_t>(t) * kRows;  // the tile's first row
-          int i0 = static_cast<int>(x0 / p.R), h0 = static_cast<int>(x0 - static_cast<int64_t>(i0) * p.R);
+          int i0 = static_cast<int>(static_cast<uint32_t>(x0) / static_cast<uint32_t>(p.R));
+          int h0 = static_cast<int>(x0 - static_cast<int64_t>(i0) * p.R);
           for (; ok && t < nt && a < end; ++t) {
             if (varies) tile_keys(p, g.s, t, lo, hi);
             const int n = varies ? tile_steps(lo, hi) : g.each;
@@ -472,9 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               pc.kt1 = lo / kKeys + f1;
               pc.first = f0 == 0;
               pc.mode = f0 > 0 || f1 < n ? 1 : (g.waits ? 2 : 0);  // parts elsewhere; another segment
-              if (f0 == 0 && lane == 0)
-                meta[tile0 + gi * nt + t] = make_int2(
-                    blockIdx.x, f1 < n ? static_cast<int>((at + n - 1) / per) - static_cast<int>(blockIdx.x) + 1 : 1);
+              pc.parts = f1 < n ? static_cast<int>(div64(at + n - 1, per)) - static_cast<int>(blockIdx.x) + 1 : 1;
+              {  // the loads will soon ask for these
+                const int32_t* row = (pc.own ? p.own.pages + pc.row * p.own.rs : p.prefix.pages + pc.row * p.prefix.rs);
+                const int at = (pc.kt0 * kKeys >> p.page_log2) + lane;
+                if (at <= (pc.len - 1) >> p.page_log2) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + at));
+              }
               ok = publish(pc);
             }
             a += tile_cost(n);
@@ -492,14 +481,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (varies && a >= end) break;
         first = varies ? a : first + static_cast<int64_t>(tile_cost(g.each)) * nt * p.Hkv;
-        tile0 += nt * p.Hkv;
       }
       Piece last = {};
       last.row = -1;
       if (ok) publish(last);
     }
-  } else {
-    warpgroup_reg_alloc<kRegsHigh>();
+  } else if (warp < 12) {
+    warpgroup_reg_alloc<kRegsSoft>();
     // ------------------------------------------------------------ softmax
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const int r = quad * 32 + lane;
@@ -516,13 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) piece_done(&bars->ring, take);
       if (pc.row < 0) break;
-      if (tiles == 0) {
-        copy_q_rows<HD>(p, sQ, pc.g, pc.tok, pc.head, pc.rows, warp - 4, 8);
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->q_first);
-      }
       const bool valid = r < pc.rows;
       const bool any = quad * 32 < pc.rows;  // some row of this warp
       int tok = pc.tok, h = pc.head + r;     // packed token, head
@@ -531,6 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tok += dt;
         h += (pc.g - dt) * p.R;
       }
+      if (pc.first && valid && half == 0)
+        meta[(static_cast<int64_t>(pc.own ? 0 : p.total_q) + tok) * p.Hq + h] = make_int2(blockIdx.x, pc.parts);
       // the row's own slope, and the keys [jlo, jhi] it may attend to; default
       // positions are counted from the segment's slot 0
       float slope2 = 0.f;
@@ -591,11 +574,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the bounds are applied per key only where they cut some row's keys
         const bool edge = __any_sync(0xffffffffu, valid && (key0 < jlo || key0 + 63 > jhi));
         const bool behind = POS && __all_sync(0xffffffffu, !valid || pos >= key0 + 63);
+        // without logits to keep, both passes read the products and scale themselves
+        const bool keep = CAP || (POS && (kpos || p.slopes)) || !(in_scale > 0.f);
+        auto mask = [&](auto& x, int c0, int n) {
+          const int lo = jlo - key0 - c0, hi = jhi - key0 - c0;
+#pragma unroll
+          for (int i = 0; i < n; ++i) x[i] = i >= lo && i <= hi ? x[i] : -INFINITY;
+        };
         // base-2 logits (less bref) of columns [c0, c0 + 16) from their products
-        auto logits16 = [&](float (&x)[kCh], int c0) {
+        auto logits16 = [&](float (&x)[16], int c0) {
           if (CAP) {
 #pragma unroll
-            for (int i = 0; i < kCh; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
               if (FIXED) {
                 // c - 2c / (1 + e^2x): the cap is small, so its absolute error of
                 // c 2^-22 is that of the logit itself; the constant c is in bref
@@ -614,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float sc = FIXED ? -2.f * out_scale : (CAP ? out_scale : in_scale);
           if (POS && kpos) {
 #pragma unroll
-            for (int i = 0; i < kCh; ++i) {
+            for (int i = 0; i < 16; ++i) {
               const int kq = __shfl_sync(0xffffffffu, c0 < 32 ? kpa : kpb, (c0 & 31) + i);
               const bool adm = key0 + c0 + i < pc.len && (p.wl < 0 || kq >= pos - p.wl) &&
                                (p.wr < 0 || kq <= pos + p.wr);
@@ -626,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every key stands at or before the row: the distance is linear
             const float a = fmaf(static_cast<float>(pos - key0 - c0), -slope2, -bref);
 #pragma unroll
-            for (int i = 0; i < kCh; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
               const uint64_t z = f2_fma(f2_make(x[i], x[i + 1]), f2_make(sc, sc),
                                         f2_fma(f2_make(i, i + 1), f2_make(slope2, slope2), f2_make(a, a)));
               x[i] = f2_lo(z);
@@ -635,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (POS) {
             const float pos0 = static_cast<float>(pos - key0 - c0);
 #pragma unroll
-            for (int i = 0; i < kCh; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
               const uint64_t dist = f2_make(fabsf(pos0 - i), fabsf(pos0 - (i + 1)));
               const uint64_t z = f2_fma(f2_make(x[i], x[i + 1]), f2_make(sc, sc),
                                         f2_fma(dist, f2_make(-slope2, -slope2), f2_make(-bref, -bref)));
@@ -644,24 +634,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < kCh; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
               const uint64_t z = f2_fma(f2_make(x[i], x[i + 1]), f2_make(sc, sc), f2_make(-bref, -bref));
               x[i] = f2_lo(z);
               x[i + 1] = f2_hi(z);
             }
           }
-          if (edge) {
-#pragma unroll
-            for (int i = 0; i < kCh; ++i)
-              x[i] = key0 + c0 + i >= jlo && key0 + c0 + i <= jhi ? x[i] : -INFINITY;
-          }
+          if (edge) mask(x, c0, 16);
         };
         if (!(ok = mbar_wait_warp(&bars->s_full[step & 1], (step >> 1) & 1, s_abort))) break;
         tc_fence_after();
         float alpha = 1.f;
         bool need = false;
-        // without logits to keep, the second pass scales the products itself
-        const bool keep = CAP || (POS && (kpos || p.slopes)) || edge || !(in_scale > 0.f);
         if (!FIXED) {
           float* mxs = sMax + (step & 1) * 256;
           float mx = -INFINITY;
@@ -674,6 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (keep) {
                 logits16(x, c0);
                 tmem_st16(sb + c0, reinterpret_cast<uint32_t(&)[16]>(x));
+              } else if (edge) {
+                mask(x, c0, kCh);
               }
 #pragma unroll
               for (int i = 0; i < kCh; ++i) mx = fmaxf(mx, x[i]);
@@ -704,7 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float x[kCh];
             tmem_ld16(sb + c0, x);
             tmem_wait_ld();
-            if (FIXED) logits16(x, c0);
+            if constexpr (FIXED) logits16(x, c0);
+            if (!keep && edge) mask(x, c0, kCh);
             uint32_t pk[kCh / 2];
 #pragma unroll
             for (int i = 0; i < kCh; i += 2) {
@@ -734,13 +721,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * alpha);
               tmem_st16(ob + c, u);
             }
-            if (half) {  // and L
-              uint32_t u[8];
-              tmem_ld8(tmem + kColOv + HD + lane_addr, u);
-              tmem_wait_ld();
-              u[0] = __float_as_uint(__uint_as_float(u[0]) * alpha);
-              tmem_st8(tmem + kColOv + HD + lane_addr, u);
-            }
           }
           tmem_wait_st();
         }
@@ -757,43 +737,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       l = sums[r] + sums[128 + r];
       if (!(ok = mbar_wait_warp(&bars->o_full, tiles & 1, s_abort))) break;
       tc_fence_after();
-      constexpr int kC = HD / 2;
-      float o[kC], lr = 0.f;
       if (any) {
-        uint32_t u[8];
-        tmem_ld8(tmem + kColOv + HD + lane_addr, u);
-        const uint32_t ob = tmem + kColOv + half * kC + lane_addr;
+        constexpr int kC = HD / 2;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        int64_t pr = 0;
+        if (pc.mode)
+          pr = pc.mode == 1 ? cut_row(w, blockIdx.x, pc.first, r) : whole_row(w, p.total_q, p.Hq, pc.own, tok, h);
+        if (valid && half == 0) {
+          if (pc.mode)
+            reinterpret_cast<float2*>(p.ws + w.stats)[pr] = make_float2(m_run, l);
+          else
+            p.lse[static_cast<int64_t>(tok) * p.Hq + h] = l > 0.f ? (m_run + log2f(l)) * kLn2 : -INFINITY;
+        }
+        uint16_t* orow = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(tok) * p.out_ts +
+                         static_cast<int64_t>(h) * p.out_hs + half * kC;
+        float4* part = reinterpret_cast<float4*>(p.ws + w.rows) + part_at<HD>(pr, half * kC / 4);
+#pragma unroll 1
+        for (int c = 0; c < kC; c += 16, part += 32) {
+          float o[16];
+          tmem_ld16(tmem + kColOv + half * kC + c + lane_addr, o);
+          tmem_wait_ld();
+          if (!valid) continue;
+          if (pc.mode == 0) {
 #pragma unroll
-        for (int c = 0; c < kC; c += 16) tmem_ld16(ob + c, *reinterpret_cast<float(*)[16]>(o + c));
-        tmem_wait_ld();
-        lr = __uint_as_float(u[0]);
+            for (int i = 0; i < 16; ++i) o[i] *= inv;
+            *reinterpret_cast<uint4*>(orow + c) = pack8<BF16>(o);
+            *reinterpret_cast<uint4*>(orow + c + 8) = pack8<BF16>(o + 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              part[i * 8] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->o_empty);
       ++tiles;
-      if (!valid) continue;
-      if (pc.mode == 0) {
-        const float inv = lr > 0.f ? 1.f / lr : 0.f;
-        if (half == 0)
-          p.lse[static_cast<int64_t>(tok) * p.Hq + h] = l > 0.f ? (m_run + log2f(l)) * kLn2 : -INFINITY;
-        uint16_t* orow = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(tok) * p.out_ts +
-                         static_cast<int64_t>(h) * p.out_hs + half * kC;
-#pragma unroll
-        for (int u = 0; u < kC / 8; ++u) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = o[8 * u + i] * inv;
-          *reinterpret_cast<uint4*>(orow + u * 8) = pack8<BF16>(v);
-        }
-      } else {
-        const int64_t pr = pc.mode == 1 ? cut_row(w, blockIdx.x, pc.first, r)
-                                        : whole_row(w, p.total_q, p.Hq, pc.own, tok, h);
-        if (half == 0) reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(m_run, l, lr, 0.f);
-        float4* part = reinterpret_cast<float4*>(p.ws + w.rows) + part_at<HD>(pr, half * kC / 4);
-#pragma unroll
-        for (int u = 0; u < kC / 4; ++u)
-          part[u * 8] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+    }
+  } else {
+    warpgroup_reg_dealloc<kRegsLoad>();
+    if (warp == 12) {
+      // ------------------------------------------------------------ V loads
+      load_pages<HD, false>(p, bars, sV, &tv, nullptr, box, s_abort);
+    } else {
+      // ------------------------------------------------------------ Q rows
+      uint32_t take = 0, tiles = 0;
+      Piece pc;
+      for (;;) {
+        if (!__all_sync(0xffffffffu, piece_take(&bars->ring, take, &pc, s_abort))) break;
+        __syncwarp();
+        if (lane == 0) piece_done(&bars->ring, take);
+        if (pc.row < 0) break;
+        if (tiles > 0 && !mbar_wait_warp(&bars->q_empty, (tiles - 1) & 1, s_abort)) break;
+        copy_q_rows<HD>(p, sQ, pc.g, pc.tok, pc.head, pc.rows, warp - 13, 3);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full);
+        ++tiles;
       }
     }
   }
@@ -824,7 +826,7 @@ cudaError_t launch_fwd_d(const CacheParams& p, const FwdWs& w, const CUtensorMap
   static_assert(smem <= 232448, "shared memory");
   auto k = p.dtype == 1 ? pick_fwd<true, HD>(p) : pick_fwd<false, HD>(p);
   cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  k<<<grid, kThreads, smem, s>>>(p, w, tk, tkt, tv);
+  k<<<grid, kThreadsF, smem, s>>>(p, w, tk, tkt, tv);
   return cudaGetLastError();
 }
 

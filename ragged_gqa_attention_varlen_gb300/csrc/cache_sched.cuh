@@ -42,9 +42,9 @@ __device__ __forceinline__ void tile_keys(const CacheParams& p, const Seg& s, in
   lo = s.klo;
   hi = s.len;
   if (s.own && !p.q_pos) {
-    const int i0 = static_cast<int>(static_cast<int64_t>(t) * kRows / p.R);
-    const int i1 = static_cast<int>(min(static_cast<int64_t>(s.ntok - 1),
-                                        (static_cast<int64_t>(t) * kRows + kRows - 1) / p.R));
+    const uint32_t x0 = static_cast<uint32_t>(t) * kRows, R = p.R;
+    const int i0 = static_cast<int>(x0 / R);
+    const int i1 = min(s.ntok - 1, static_cast<int>((x0 + kRows - 1) / R));
     const int64_t k0 = static_cast<int64_t>(s.len) - s.ntok;
     if (p.wl >= 0) lo = static_cast<int>(min(static_cast<int64_t>(s.len), max(static_cast<int64_t>(0), k0 + i0 - p.wl)));
     if (p.wr >= 0) hi = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(s.len), k0 + i1 + p.wr + 1)));
@@ -64,7 +64,8 @@ __device__ __forceinline__ int seg_tiles(const CacheParams& p, const Seg& s) {
 // positions query 0 of sequence b stands at prefix_len + own_len - Lq.
 __device__ __forceinline__ int prefix_klo(const CacheParams& p, int pfx, int len) {
   if (p.wl < 0 || p.q_pos) return 0;
-  const int b0 = __ldg(p.cu_prefix + pfx), b1 = __ldg(p.cu_prefix + pfx + 1);
+  // (cut to the batch: the arrays may not have been checked yet)
+  const int b0 = max(__ldg(p.cu_prefix + pfx), 0), b1 = min(__ldg(p.cu_prefix + pfx + 1), p.B);
   int64_t lo = len;
   for (int b = b0; b < b1 && lo > 0; ++b) {
     const int nq = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b);
@@ -158,64 +159,50 @@ __device__ __forceinline__ int seg_check(const CacheParams& p, int s) {
   return bad;
 }
 
-// Inclusive block sums of two values over all threads of a block of up to 32
-// warps; `tmp` holds two values per warp.
-__device__ __forceinline__ void block_scan2(int64_t& a, int& b, int64_t* tmp_a, int* tmp_b,
-                                            int64_t& total_a, int& total_b) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+// Quotient of non-negative values, by 32-bit division where they fit.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// Inclusive sums over a block of which the first `warps` warps hold values.
+__device__ __forceinline__ int64_t block_scan(int64_t a, int warps, int64_t* tmp, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp < warps) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t xa = __shfl_up_sync(0xffffffffu, a, o);
-    const int xb = __shfl_up_sync(0xffffffffu, b, o);
-    if (lane >= o) {
-      a += xa;
-      b += xb;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, a, o);
+      if (lane >= o) a += x;
     }
-  }
-  __syncthreads();  // tmp of an earlier call has been read
-  if (lane == 31) {
-    tmp_a[warp] = a;
-    tmp_b[warp] = b;
+    if (lane == 31) tmp[warp] = a;
   }
   __syncthreads();
-  int64_t ba = 0;
-  int bb = 0;
-  total_a = 0;
-  total_b = 0;
-  for (int w = 0; w < nw; ++w) {
-    if (w == warp) {
-      ba = total_a;
-      bb = total_b;
-    }
-    total_a += tmp_a[w];
-    total_b += tmp_b[w];
+  int64_t before = 0;
+  total = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w == warp) before = total;
+    total += tmp[w];
   }
-  a += ba;
-  b += bb;
+  return a + before;
 }
 
 // Results of the plan, in shared memory.
 struct Plan {
   int64_t per, begin, end;  // this CTA's units
-  int seg;                  // the segment that holds unit `begin`
-  int seg_tile;             // tiles (of all K/V heads) before it
   int64_t seg_begin;        // the first unit of that segment
-  int bad;
+  int seg;                  // the segment that holds unit `begin`
   int window;               // segments [seg, seg + window) of this array are filled
+  int bad, pad;
   SegPlan segs[32];
-  int64_t tmp_a[32];
-  int tmp_b[32];
+  int64_t tmp[2][32];
 };
 
-// Whole block: this CTA's share of the work.  plan_of(s) plans segment s,
-// cost_of(plan) is the cost of its tiles, tiles_of(plan) their number.  info,
-// if not null, is written by CTA 0: info[s] = {tiles before segment s, each}.
-// Returns false, for every thread, when there is nothing to do.  With as many
-// threads as segments or more, every segment is read once, in one round of
-// loads.
-template <class PlanOf, class CostOf, class TilesOf>
-__device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, PlanOf plan_of,
-                          CostOf cost_of, TilesOf tiles_of) {
+// Whole block: this CTA's share of the work.  plan_of(s) plans segment s and
+// cost_of(plan) is the cost of its tiles.  Returns false, for every thread,
+// when there is nothing to do.  With as many threads as segments or more,
+// every segment is read once, in one round of loads.
+template <class PlanOf, class CostOf>
+__device__ bool make_plan(const CacheParams& p, Plan* pl, PlanOf plan_of, CostOf cost_of) {
   const int nseg = p.P + p.B, tid = threadIdx.x, nt = blockDim.x;
   const bool one = nseg <= nt;
   SegPlan g = SegPlan();
@@ -238,35 +225,25 @@ __device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, PlanOf pla
     return false;
   }
   int64_t total = 0;
+  int turn = 0;
   for (int pass = one ? 1 : 0; pass < 2; ++pass) {  // pass 0: the total of many segments
     int64_t before = 0;
-    int tiles_before = 0;
-    for (int s0 = 0; s0 < nseg; s0 += nt) {
+    for (int s0 = 0; s0 < nseg; s0 += nt, turn ^= 1) {
       const int s = s0 + tid;
-      int64_t a = 0;
-      int b = 0, each = 0;
+      int64_t mine = 0, sum;
       if (s < nseg) {
         if (!one) g = plan_of(s);
-        a = cost_of(g);
-        b = tiles_of(g);
-        each = g.each;
+        mine = cost_of(g);
       }
-      const int64_t mine = a;
-      const int mine_b = b;
-      int64_t ta;
-      int tb;
-      block_scan2(a, b, pl->tmp_a, pl->tmp_b, ta, tb);
+      const int64_t upto = block_scan(mine, (min(nseg - s0, nt) + 31) / 32, pl->tmp[turn], sum);
       if (pass == 1) {
-        if (one) total = ta;
-        const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-        const int64_t begin = per * blockIdx.x, first = before + a - mine;
-        const bool here = mine > 0 && begin >= first && begin < first + mine;
-        if (here) {
+        if (one) total = sum;
+        const int64_t per = div64(total + gridDim.x - 1, gridDim.x);
+        const int64_t begin = per * blockIdx.x, first = before + upto - mine;
+        if (s < nseg && mine > 0 && begin >= first && begin < first + mine) {
           pl->seg = s;
           pl->seg_begin = first;
-          pl->seg_tile = tiles_before + b - mine_b;
         }
-        if (info && blockIdx.x == 0 && s < nseg) info[s] = make_int2(tiles_before + b - mine_b, each);
         if (s0 == 0 && tid == 0) {
           pl->per = per;
           pl->begin = begin;
@@ -279,8 +256,7 @@ __device__ bool make_plan(const CacheParams& p, Plan* pl, int2* info, PlanOf pla
           if (tid == 0) pl->window = 32;
         }
       }
-      before += ta;
-      tiles_before += tb;
+      before += sum;
     }
     if (pass == 0) total = before;
   }

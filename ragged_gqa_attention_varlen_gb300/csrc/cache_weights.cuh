@@ -170,9 +170,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
 
   Plan* pl = &bars->plan;
   bool busy = make_plan(
-      p, pl, nullptr, [&](int s) { return weights_plan(p, s); },
-      [&](const SegPlan& g) -> int64_t { return weights_cost(p, g) * p.Hkv; },
-      [&](const SegPlan&) -> int { return 0; });
+      p, pl, [&](int s) { return weights_plan(p, s); },
+      [&](const SegPlan& g) -> int64_t { return weights_cost(p, g) * p.Hkv; });
   if (blockIdx.x == 0 && tid == 0) {
     if (pl->bad) report(p.status, pl->bad);
     if (smem_addr(sm) & 1023u) report(p.status, ATTN_DEV_SMEM_ALIGN);
