@@ -67,16 +67,17 @@ template <int HD>
 struct WShape {
   static constexpr uint32_t kT = HD == 160 ? 40960 : HD * 256;  // a K-major tile
   static constexpr int kChunksK = (HD + 63) / 64;
-  static constexpr int kKS = HD == 160 ? 3 : (HD == 128 ? 4 : 6);
-  static constexpr int kQS = 2;
+  static constexpr int kKS = HD == 64 ? 6 : 3;
+  static constexpr int kQS = HD == 160 ? 2 : (HD == 128 ? 3 : 4);
   static constexpr uint32_t kOffQ = kKS * kT;
+  static constexpr int kIS = 8;  // row infos: Q's place is free after the product, theirs after the sums
   static constexpr uint32_t kOffInfo = kOffQ + kQS * kT;
-  static constexpr uint32_t kOffSum = kOffInfo + kQS * sizeof(RowInfo);  // [2 pieces][128]
+  static constexpr uint32_t kOffSum = kOffInfo + kIS * sizeof(RowInfo);  // [2 pieces][128]
   static constexpr uint32_t kOffBar = (kOffSum + 2 * 128 * 4 + 15) / 16 * 16;
 };
 
 struct WBars {
-  uint64_t k_full[6], k_empty[6], q_full[2], q_empty[2], info_read[2];
+  uint64_t k_full[6], k_empty[6], q_full[4], q_empty[4], info_full[8], info_read[8];
   uint64_t s_full[4], s_read[4], pair[4], drain;
   WPieceRing ring;
   Plan plan;
@@ -138,6 +139,10 @@ __device__ __forceinline__ int64_t weights_cost(const CacheParams& p, const SegP
   return n;
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
+}
+
 __device__ __forceinline__ bool wpiece_take(WPieceRing* r, uint32_t& k, WPiece* out,
                                             volatile int* abort) {
   const int s = k & 3;
@@ -183,9 +188,12 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       mbar_init(&bars->k_full[b], 1);
       mbar_init(&bars->k_empty[b], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < S::kQS; ++b) {
       mbar_init(&bars->q_full[b], 4);
       mbar_init(&bars->q_empty[b], 1);
+    }
+    for (int b = 0; b < S::kIS; ++b) {
+      mbar_init(&bars->info_full[b], 4);
       mbar_init(&bars->info_read[b], 8);
     }
     for (int b = 0; b < 4; ++b) {
@@ -387,68 +395,93 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     if (ok) publish(last);
   } else if (warp >= 12) {
     // ------------------------------------------------------------ Q rows
+    // A Q tile that stays is fetched by the four warps together; of several that
+    // stream by, each warp fetches every fourth, so that as many are on their
+    // way as there are stages (one after the other, each took 3000 clk).
     uint32_t nt = 0, qs = 0, qph = 0, loaded = 0;
-    const int wi = warp - 12, r = wi * 32 + lane;
+    const int wi = warp - 12;
     WPiece pc;
     bool ok = true;
     while (ok && take(nt, pc)) {
       if (pc.a0 >= pc.a1) continue;
+      const bool many = pc.t1 - pc.t0 > 1;
+      const int first = many ? 0 : wi, each = many ? 1 : 4;  // this warp's runs of 32 rows
       for (int t = pc.t0; t < pc.t1; ++t) {
-        const int x0 = t * kRows, i0 = x0 / p.R, h0 = x0 - i0 * p.R;
-        const int n = min(kRows, pc.rows - x0);
-        // the row's scalars, while the stage may still be in use
-        float nlse = -INFINITY, nslope = 0.f;
-        int pos = 0;
-        if (r < n) {
-          const int dt = head_div(p, h0 + r), tok = pc.tok0 + i0 + dt;
-          const int h = pc.g * p.R + h0 + r - dt * p.R;
-          const float l = __ldg(p.lse + static_cast<int64_t>(tok) * p.Hq + h);
-          nlse = l > -INFINITY ? -l * kLog2e : -INFINITY;
-          if (POS) {
-            int b = pc.row;
-            if (!pc.own) {
-              const int b0 = __ldg(p.cu_prefix + pc.row), b1 = __ldg(p.cu_prefix + pc.row + 1);
-              b = b1 - b0 == pc.ntok && __ldg(p.cu_q + b0 + tok - pc.tok0) == tok &&
-                          __ldg(p.cu_q + b0 + tok - pc.tok0 + 1) > tok
-                      ? b0 + tok - pc.tok0
-                      : seq_of(p.cu_q, b0, b1, tok);
+        if (!many || static_cast<int>(loaded & 3) == wi) {
+          const uint32_t x0 = static_cast<uint32_t>(t) * kRows;
+          const int i0 = static_cast<int>(x0 / static_cast<uint32_t>(p.R));
+          const int h0 = static_cast<int>(x0) - i0 * p.R;
+          const int n = min(kRows, pc.rows - static_cast<int>(x0));
+          if (loaded >= S::kQS && !(ok = mbar_wait_warp(&bars->q_empty[qs], qph ^ 1, s_abort))) break;
+          uint8_t* dst = sQ + qs * S::kT;
+          copy_q_rows<HD>(p, dst, pc.g, pc.tok0 + i0, h0, n, many ? 0 : wi, many ? 1 : 4);
+          // the rows' scalars: all loads first
+          float nlse[4], nslope[4];
+          int pos[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = (first + k * each) * 32 + lane;
+            nlse[k] = -INFINITY;
+            nslope[k] = 0.f;
+            pos[k] = 0;
+            if (first + k * each < 4 && r < n) {
+              const int dt = head_div(p, h0 + r), tok = pc.tok0 + i0 + dt;
+              const int h = pc.g * p.R + h0 + r - dt * p.R;
+              nlse[k] = __ldg(p.lse + static_cast<int64_t>(tok) * p.Hq + h);
+              if (POS) {
+                int b = pc.row;
+                if (!pc.own) {
+                  const int b0 = __ldg(p.cu_prefix + pc.row), b1 = __ldg(p.cu_prefix + pc.row + 1);
+                  b = b1 - b0 == pc.ntok && __ldg(p.cu_q + b0 + tok - pc.tok0) == tok &&
+                              __ldg(p.cu_q + b0 + tok - pc.tok0 + 1) > tok
+                          ? b0 + tok - pc.tok0
+                          : seq_of(p.cu_q, b0, b1, tok);
+                }
+                if (p.slopes) nslope[k] = -__ldg(p.slopes + b * p.slopes_bs + h) * kLog2e;
+                if (p.q_pos)
+                  pos[k] = __ldg(p.q_pos + tok);
+                else if (pc.own)
+                  pos[k] = pc.plen + pc.len - pc.ntok + tok - pc.tok0;
+                else
+                  pos[k] = pc.plen + __ldg(p.own.lens + b) - (__ldg(p.cu_q + b + 1) - tok);
+              }
             }
-            if (p.slopes) nslope = -__ldg(p.slopes + b * p.slopes_bs + h) * kLog2e;
-            if (p.q_pos)
-              pos = __ldg(p.q_pos + tok);
-            else
-              pos = pc.plen + __ldg(p.own.lens + b) - (__ldg(p.cu_q + b + 1) - tok);
           }
-        }
-        if (loaded >= S::kQS) {
-          if (!(ok = mbar_wait_warp(&bars->q_empty[qs], qph ^ 1, s_abort))) break;
-          if (!(ok = mbar_wait_warp(&bars->info_read[qs], qph ^ 1, s_abort))) break;
-        }
-        uint8_t* dst = sQ + qs * S::kT;
-        copy_q_rows<HD>(p, dst, pc.g, pc.tok0 + i0, h0, n, wi, 4);
-        // rows up to the next multiple of 16 take part in the product
-        const int pad = (n + 15) / 16 * 16 - n;
-        for (int i = wi * 32 + lane; i < pad * (HD / 8); i += 128) {
-          const int q = i / (HD / 8);
-          *reinterpret_cast<uint4*>(dst + kmajor_unit(n + q, i - q * (HD / 8))) = make_uint4(0, 0, 0, 0);
-        }
-        RowInfo& info = sInfo[qs];
-        info.nlse[r] = nlse;
-        if (POS) {
-          info.nslope[r] = nslope;
-          info.pos[r] = pos;
-          info.fpos[r] = static_cast<float>(pos);
-          const int lo = __reduce_min_sync(0xffffffffu, r < n ? pos : INT32_MAX);
-          const int hi = __reduce_max_sync(0xffffffffu, r < n ? pos : INT32_MIN);
-          if (lane == 0) {
-            info.least[wi] = lo;
-            info.most[wi] = hi;
+          const int is = loaded & (S::kIS - 1);
+          if (loaded >= S::kIS &&
+              !(ok = mbar_wait_warp(&bars->info_read[is], ((loaded / S::kIS) & 1) ^ 1, s_abort)))
+            break;
+          RowInfo& info = sInfo[is];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int run = first + k * each, r = run * 32 + lane;
+            if (run >= 4) break;
+            info.nlse[r] = nlse[k] > -INFINITY ? -nlse[k] * kLog2e : -INFINITY;
+            if (POS) {
+              info.nslope[r] = nslope[k];
+              info.pos[r] = pos[k];
+              info.fpos[r] = static_cast<float>(pos[k]);
+              const int lo = __reduce_min_sync(0xffffffffu, r < n ? pos[k] : INT32_MAX);
+              const int hi = __reduce_max_sync(0xffffffffu, r < n ? pos[k] : INT32_MIN);
+              if (lane == 0) {
+                info.least[run] = lo;
+                info.most[run] = hi;
+              }
+            }
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(&bars->info_full[is], many ? 4 : 1);
+          // rows up to the next multiple of 16 take part in the product
+          const int pad = (n + 15) / 16 * 16 - n;
+          for (int i = (many ? 0 : wi * 32) + lane; i < pad * (HD / 8); i += many ? 32 : 128) {
+            const int q = i / (HD / 8);
+            *reinterpret_cast<uint4*>(dst + kmajor_unit(n + q, i - q * (HD / 8))) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(&bars->q_full[qs], many ? 4 : 1);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->q_full[qs]);
         ++loaded;
         if (++qs == S::kQS) {
           qs = 0;
@@ -463,7 +496,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     const float in_scale = CAP ? p.sigma / p.softcap : p.sigma * kLog2e;
     const float sc = CAP ? p.softcap * kLog2e : in_scale;
-    uint32_t nt = 0, step = 0, qs = 0, qph = 0, npair = 0;
+    uint32_t nt = 0, step = 0, used = 0, npair = 0;  // used: row infos
     WPiece pc;
     bool ok = true;
     while (ok && take(nt, pc)) {
@@ -494,8 +527,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           const bool last_q = many || kt == pc.a1 - 1;
           if (static_cast<int>(step & 1) == half) {
             const int cols = min(kRows, pc.rows - t * kRows);
-            const RowInfo& info = sInfo[qs];
-            if (!(ok = mbar_wait_warp(&bars->q_full[qs], qph, s_abort))) break;
+            const RowInfo& info = sInfo[used & (S::kIS - 1)];
+            if (!(ok = mbar_wait_warp(&bars->info_full[used & (S::kIS - 1)], (used / S::kIS) & 1, s_abort)))
+              break;
             if (!(ok = mbar_wait_warp(&bars->s_full[step & 3], (step >> 2) & 1, s_abort))) break;
             tc_fence_after();
             bool free = true;  // no key of this warp is masked for any row
@@ -559,16 +593,14 @@ __global__ void __launch_bounds__(kThreadsW, 1)
               else if (there)
                 out[key] = before + total;
             }
-          } else if (last_q && !(ok = mbar_wait_warp(&bars->q_full[qs], qph, s_abort))) {
-            break;  // (not ahead of the stage's filling, or two would count as one)
+          } else if (last_q && !(ok = mbar_wait_warp(&bars->info_full[used & (S::kIS - 1)],
+                                                     (used / S::kIS) & 1, s_abort))) {
+            break;  // (not ahead of the entry's filling, or two arrivals would count as one)
           }
           if (last_q) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->info_read[qs]);
-            if (++qs == S::kQS) {
-              qs = 0;
-              qph ^= 1;
-            }
+            if (lane == 0) mbar_arrive(&bars->info_read[used & (S::kIS - 1)]);
+            ++used;
           }
         }
         if (!ok || !many) continue;
