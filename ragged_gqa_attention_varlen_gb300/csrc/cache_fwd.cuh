@@ -419,6 +419,20 @@ __global__ void __launch_bounds__(kThreadsF, 1)
         int lo = g.lo, hi = g.hi;
         int64_t a = first;  // first unit of the row tile
         int gi = 0, t = 0;
+        if (varies && begin > a) {  // skip whole K/V heads before this CTA's share
+          int64_t sum = 0;
+          for (int i = lane; i < nt; i += 32) {
+            tile_keys(p, g.s, i, lo, hi);
+            sum += tile_cost(tile_steps(lo, hi));
+          }
+          const int64_t cost = warp_sum64(sum);
+          if (cost > 0) {
+            gi = static_cast<int>(min(div64(begin - a, cost), static_cast<int64_t>(p.Hkv)));
+            a += gi * cost;
+          } else {
+            gi = p.Hkv;
+          }
+        }
         if (!varies) {
           if (g.each > 0 && begin > a) {  // skip whole row tiles before this CTA's share
             const int cost = tile_cost(g.each);

@@ -165,6 +165,12 @@ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
   return a / b;
 }
 
+__device__ __forceinline__ int64_t warp_sum64(int64_t x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
 // Inclusive sums over a block of which the first `warps` warps hold values.
 __device__ __forceinline__ int64_t block_scan(int64_t a, int warps, int64_t* tmp, int64_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

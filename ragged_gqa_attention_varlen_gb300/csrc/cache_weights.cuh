@@ -102,8 +102,8 @@ __device__ __forceinline__ void key_tile_rows(const CacheParams& p, const SegPla
     if (i0 > i1) {
       t1 = 0;
     } else {
-      t0 = static_cast<int>(i0 * p.R / kRows);
-      t1 = static_cast<int>((i1 * p.R + p.R - 1) / kRows) + 1;
+      t0 = static_cast<int>(static_cast<uint32_t>(i0 * p.R) / kRows);
+      t1 = static_cast<int>(static_cast<uint32_t>(i1 * p.R + p.R - 1) / kRows) + 1;
     }
   }
 }
@@ -336,8 +336,30 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       }
       const SegPlan g = pl->segs[(s - s0) & 31];
       const int nt = g.waits;
-      for (int gi = 0; ok && gi < p.Hkv && a < end; ++gi) {
-        for (int t = 0; ok && t < g.tiles && a < end; ++t) {
+      // skip whole K/V heads, and whole tiles of the same cost, before this CTA's share
+      int g0 = 0, tile = 0;
+      if (begin > a && g.tiles > 0) {
+        int64_t cost = 0;  // of a K/V head
+        if (g.each >= 0) {
+          cost = static_cast<int64_t>(g.tiles) * (g.each + kTileCost);
+        } else {
+          int64_t sum = 0;
+          for (int kt = lane; kt < g.tiles; kt += 32) {
+            int t0, t1;
+            key_tile_rows(p, g, nt, kt, t0, t1);
+            sum += t1 - t0 + kTileCost;
+          }
+          cost = warp_sum64(sum);
+        }
+        g0 = static_cast<int>(min(div64(begin - a, cost), static_cast<int64_t>(p.Hkv)));
+        a += g0 * cost;
+        if (g.each >= 0 && g0 < p.Hkv) {
+          tile = static_cast<int>(div64(begin - a, g.each + kTileCost));
+          a += static_cast<int64_t>(tile) * (g.each + kTileCost);
+        }
+      }
+      for (int gi = g0; ok && gi < p.Hkv && a < end; ++gi, tile = 0) {
+        for (int t = tile; ok && t < g.tiles && a < end; ++t) {
           WPiece pc;
           pc.row = g.s.row;
           pc.own = g.s.own;
