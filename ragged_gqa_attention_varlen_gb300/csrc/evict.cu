@@ -10,11 +10,14 @@
 // their positions travel with them).
 //
 // select_kernel: one block per (sequence, K/V head).  The k-th largest rank is
-// found digit by digit (four 8-bit histograms in shared memory; the ranks of
-// the first kSmemKeys slots stay there), then two counting passes over
-// contiguous slot ranges per warp number the ties, the holes and the movers
-// in slot order: no atomics decide an order, so results are repeatable.
-// move_kernel: the listed K and V rows, over the whole GPU.
+// found digit by digit (8-bit histograms in shared memory, eight copies because
+// scores crowd into few exponents; the ranks of the first kSmemKeys slots stay
+// there; as soon as a digit's keys are wanted all, the rest is left out), then
+// two counting passes over contiguous slot ranges per warp number the ties, the
+// holes and the movers in slot order: no atomics decide an order, so results
+// are repeatable.  Latencies bound it: loads go out four at a time.
+// move_kernel: the listed K and V rows with their scores and positions, over
+// the whole GPU, four 16-byte units in flight per thread; copying bounds it.
 #include "../../include/attn_varlen.h"
 #include "cache.cuh"
 
@@ -26,6 +29,7 @@ constexpr int kThreadsE = 1024;
 constexpr int kWarpsE = kThreadsE / 32;
 constexpr int kSmemKeys = 48 * 1024;  // ranks held in shared memory (192 KB)
 constexpr int kThreadsM = 256;
+constexpr int kCopies = 8;  // of the histogram
 
 struct EvictWs {
   size_t newlen, counts, lists, total;
@@ -55,9 +59,10 @@ __device__ __forceinline__ uint32_t rank_key(float score, bool safe) {
 __global__ void __launch_bounds__(kThreadsE)
     select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t skey[];
-  __shared__ uint32_t hist[256];
+  __shared__ uint32_t hist[kCopies][256];
   __shared__ int s_digit, s_above;
   __shared__ int cnt[3][kWarpsE];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int s = blockIdx.x / p.Hkv, g = blockIdx.x - s * p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t slots = static_cast<int64_t>(p.width) << p.page_log2;
@@ -79,13 +84,26 @@ __global__ void __launch_bounds__(kThreadsE)
     if (g == 0) newlen[s] = bad ? n0 : k;
     if (n <= k) counts[blockIdx.x] = 0;
   }
-  if (n <= k) {  // nothing to evict
-    for (int j = tid; j < n; j += kThreadsE) {
-      if (so != sc) so[j] = sc[j];
-      if (po != kp) po[j] = kp[j];
+  // the slots below the new end (evicted ones are replaced by the moves)
+  if (so != sc || po != kp) {
+    for (int j0 = tid; j0 < k; j0 += 4 * kThreadsE) {
+      float x[4];
+      int32_t y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j0 + i * kThreadsE < k) {
+          x[i] = sc[j0 + i * kThreadsE];
+          y[i] = kp[j0 + i * kThreadsE];
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j0 + i * kThreadsE < k) {
+          if (so != sc) so[j0 + i * kThreadsE] = x[i];
+          if (po != kp) po[j0 + i * kThreadsE] = y[i];
+        }
     }
-    return;
   }
+  if (n <= k) return;  // nothing to evict
   const int from = __ldg(p.next_pos + s) - p.recent;
   auto load_key = [&](int j) { return rank_key(sc[j], kp[j] >= from); };
   auto key = [&](int j) { return j < kSmemKeys ? skey[j] : load_key(j); };
@@ -94,23 +112,47 @@ __global__ void __launch_bounds__(kThreadsE)
   uint32_t prefix = 0;
   int need = k;  // how many keys with the digits found so far are still to take
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kThreadsE) hist[i] = 0;
+    for (int i = tid; i < kCopies * 256; i += kThreadsE) hist[i >> 8][i & 255] = 0;
     __syncthreads();
-    for (int j = tid; j < n; j += kThreadsE) {
-      uint32_t x;
-      if (shift == 24) {
-        x = load_key(j);
-        if (j < kSmemKeys) skey[j] = x;
-      } else {
-        x = key(j);
+    uint32_t* mine = hist[warp & (kCopies - 1)];
+    if (shift == 24) {
+      for (int j0 = tid; j0 < n; j0 += 4 * kThreadsE) {
+        float x[4];
+        int32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j0 + i * kThreadsE < n) {
+            x[i] = sc[j0 + i * kThreadsE];
+            y[i] = kp[j0 + i * kThreadsE];
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = j0 + i * kThreadsE;
+          if (j < n) {
+            const uint32_t u = rank_key(x[i], y[i] >= from);
+            if (j < kSmemKeys) skey[j] = u;
+            atomicAdd(&mine[u >> 24], 1u);
+          }
+        }
       }
-      if (shift == 24 || ((x ^ prefix) >> (shift + 8)) == 0) atomicAdd(&hist[(x >> shift) & 255], 1u);
+    } else {
+      for (int j = tid; j < n; j += kThreadsE) {
+        const uint32_t x = key(j);
+        if (((x ^ prefix) >> (shift + 8)) == 0) atomicAdd(&mine[(x >> shift) & 255], 1u);
+      }
+    }
+    __syncthreads();
+    if (tid < 256) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) sum += hist[i][tid];
+      hist[0][tid] = sum;
     }
     __syncthreads();
     if (warp == 0) {  // lane l: digits 255 - 8l down to 248 - 8l
       int c[8], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += c[i] = static_cast<int>(hist[255 - 8 * lane - i]);
+      for (int i = 0; i < 8; ++i) sum += c[i] = static_cast<int>(hist[0][255 - 8 * lane - i]);
       int above = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -122,13 +164,17 @@ __global__ void __launch_bounds__(kThreadsE)
       for (int i = 0; i < 8; ++i) {
         if (above < need && above + c[i] >= need) {
           s_digit = 255 - 8 * lane - i;
-          s_above = above;
+          s_above = above + c[i] == need ? -1 : above;
         }
         above += c[i];
       }
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(s_digit) << shift;
+    if (s_above < 0) {  // all keys with these digits are wanted: key >= prefix
+      need = INT32_MAX;
+      break;
+    }
     need -= s_above;
     __syncthreads();
   }
@@ -179,19 +225,7 @@ __global__ void __launch_bounds__(kThreadsE)
     if (mover) movers[im + __popc(bm & below)] = j;
     ih += __popc(bh);
     im += __popc(bm);
-    if (keep && j < k) {
-      if (so != sc) so[j] = sc[j];
-      if (po != kp) po[j] = kp[j];
-    }
   });
-  __shared__ int s_moves;
-  if (tid == kThreadsE - 1) s_moves = im;
-  __syncthreads();  // the lists are complete (and visible to this block)
-  for (int i = tid; i < s_moves; i += kThreadsE) {
-    const int dst = holes[i], src = movers[i];
-    so[dst] = sc[src];
-    po[dst] = kp[src];
-  }
 }
 
 __global__ void __launch_bounds__(kThreadsM)
@@ -201,27 +235,71 @@ __global__ void __launch_bounds__(kThreadsM)
       evict_ws(p.S, p.Hkv, static_cast<int64_t>(p.width) << p.page_log2, p.budget);
   const int32_t* holes = reinterpret_cast<const int32_t*>(p.ws + w.lists) + 2 * w.list_cap * sg;
   const int32_t* movers = holes + w.list_cap;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int count = reinterpret_cast<const int32_t*>(p.ws + w.counts)[sg];
   if (g == 0 && blockIdx.y == 0 && threadIdx.x == 0)
     p.lens_out[s] = reinterpret_cast<const int32_t*>(p.ws + w.newlen)[s];
-  const int units = p.d / 8;  // 16-byte units of a row
+  const int units = p.d / 8;  // 16-byte units of a K or V row
   const int32_t* row = p.table + s * p.table_rs;
-  const int64_t all = static_cast<int64_t>(count) * 2 * units;
-  for (int64_t u = static_cast<int64_t>(blockIdx.y) * kThreadsM + threadIdx.x; u < all;
-       u += static_cast<int64_t>(gridDim.y) * kThreadsM) {
-    const int i = static_cast<int>(u / (2 * units)), x = static_cast<int>(u - i * 2ll * units);
-    const int src = movers[i], dst = holes[i];
-    const int ps = __ldg(row + (src >> p.page_log2)), pd = __ldg(row + (dst >> p.page_log2));
-    if (static_cast<unsigned>(ps) >= static_cast<unsigned>(p.num_pages) ||
-        static_cast<unsigned>(pd) >= static_cast<unsigned>(p.num_pages)) {
-      report(p.status, ATTN_DEV_BAD_CACHE);
-      continue;
+  const uint32_t per = 2 * units + 1;  // and one for the score and the position
+  const int64_t all = static_cast<int64_t>(count) * per;
+  const int64_t stride = static_cast<int64_t>(gridDim.y) * kThreadsM;
+  const float* sc = p.scores + s * p.sc_rs + g * p.sc_hs;
+  const int32_t* kp = p.key_pos + s * p.kp_rs + g * p.kp_hs;
+  float* so = p.scores_out + s * p.so_rs + g * p.so_hs;
+  int32_t* po = p.pos_out + s * p.po_rs + g * p.po_hs;
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.y) * kThreadsM + threadIdx.x; u0 < all;
+       u0 += 4 * stride) {
+    int src[4], dst[4], x[4], ps[4], pd[4];
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t u = u0 + i * stride;
+      x[i] = -1;
+      if (u < all) {
+        const int m = static_cast<int>((u >> 32) == 0 ? static_cast<uint32_t>(u) / per : u / per);
+        x[i] = static_cast<int>(u - static_cast<int64_t>(m) * per);
+        src[i] = movers[m];
+        dst[i] = holes[m];
+      }
     }
-    const Pages& pg = x < units ? p.k : p.v;
-    uint16_t* base = static_cast<uint16_t*>(const_cast<void*>(pg.base)) + g * pg.head +
-                     (x < units ? x : x - units) * 8;
-    *reinterpret_cast<uint4*>(base + pd * pg.page + (dst & (p.page_size - 1)) * pg.slot) =
-        *reinterpret_cast<const uint4*>(base + ps * pg.page + (src & (p.page_size - 1)) * pg.slot);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (x[i] >= 0 && x[i] < 2 * units) {
+        ps[i] = __ldg(row + (src[i] >> p.page_log2));
+        pd[i] = __ldg(row + (dst[i] >> p.page_log2));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (x[i] < 0) continue;
+      if (x[i] == 2 * units) {
+        v[i].x = __float_as_uint(sc[src[i]]);
+        v[i].y = kp[src[i]];
+      } else if (static_cast<unsigned>(ps[i]) >= static_cast<unsigned>(p.num_pages) ||
+                 static_cast<unsigned>(pd[i]) >= static_cast<unsigned>(p.num_pages)) {
+        report(p.status, ATTN_DEV_BAD_CACHE);
+        x[i] = -1;
+      } else {
+        const Pages& pg = x[i] < units ? p.k : p.v;
+        v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pg.base) + ps[i] * pg.page +
+                                               (src[i] & (p.page_size - 1)) * pg.slot + g * pg.head +
+                                               (x[i] < units ? x[i] : x[i] - units) * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (x[i] < 0) continue;
+      if (x[i] == 2 * units) {
+        so[dst[i]] = __uint_as_float(v[i].x);
+        po[dst[i]] = v[i].y;
+      } else {
+        const Pages& pg = x[i] < units ? p.k : p.v;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(pg.base)) + pd[i] * pg.page +
+                                  (dst[i] & (p.page_size - 1)) * pg.slot + g * pg.head +
+                                  (x[i] < units ? x[i] : x[i] - units) * 8) = v[i];
+      }
+    }
   }
 }
 
@@ -238,12 +316,20 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
   select_kernel<<<p.S * p.Hkv, kThreadsE, smem, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t units = evict_ws(p.S, p.Hkv, slots, p.budget).list_cap * 2 * (p.d / 8);
+  const int64_t units = evict_ws(p.S, p.Hkv, slots, p.budget).list_cap * (2 * (p.d / 8) + 1);
   int64_t x = (units + kThreadsM * 4 - 1) / (kThreadsM * 4);
-  const int64_t most = 152 * 8 / (p.S * p.Hkv) + 1;
+  const int64_t most = 152 * 16 / (p.S * p.Hkv) + 1;
   x = x < 1 ? 1 : (x > most ? most : x);
-  move_kernel<<<dim3(p.S * p.Hkv, static_cast<unsigned>(x)), kThreadsM, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.S * p.Hkv, static_cast<unsigned>(x));
+  cfg.blockDim = dim3(kThreadsM);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, move_kernel, p);
 }
 
 }  // namespace kv
