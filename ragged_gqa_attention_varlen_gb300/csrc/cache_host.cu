@@ -64,7 +64,7 @@ attn_status read_args(CacheParams& p, attn_dtype dtype, int B, int P, int Hq, in
   if (!dim_ok(head_dim)) return ATTN_ERR_UNSUPPORTED;
   if (B > ATTN_MAX_BATCH || P > ATTN_MAX_BATCH) return ATTN_ERR_UNSUPPORTED;
   if (total_q * Hq > INT32_MAX || Hq > 65536) return ATTN_ERR_UNSUPPORTED;
-  if (!(softcap == softcap) || !(scale_multiplier == scale_multiplier)) return ATTN_ERR_INVALID;
+  if (!std::isfinite(softcap) || !std::isfinite(scale_multiplier)) return ATTN_ERR_INVALID;
   if ((B == 0 && total_q > 0) || (B == 0 && P > 0)) return ATTN_ERR_INVALID;
   if (B == 0) return ATTN_OK;
   if (!page_ok(page_size) || num_pages < 1) return ATTN_ERR_UNSUPPORTED;

@@ -92,6 +92,13 @@ CASES = [
     case("big_cap", [600], [2], Hq=8, cap=50.0, std=12.0),
     case("huge_page", [2000, 1500], [1, 1], Hq=8, page=1024),
     case("heads_beyond_a_tile", [200], [3], Hq=200, page=16, alibi=True),
+    case("more_sequences_than_threads", ref.spread(9, 700, 1, 30), [1] * 700, Hq=4, d=64, page=16, cap=0.0),
+    case("many_prefixes", ref.spread(10, 60, 1, 40), [1, 0, 2] * 20, plens=ref.spread(11, 20, 1, 300),
+         group=[b // 3 for b in range(60)], Hq=6, Hkv=2, d=64, page=32, cap=0.0, alibi=True),
+    case("parts_beyond_a_warp", [20000], [1], Hq=8, d=64, page=256, cap=0.0),
+    case("prompt_over_many_parts", [700, 2], [300, 2], Hq=12, Hkv=4, d=64, page=64, cap=30.0, alibi=True, dtype=HF),
+    case("prompt_window_behind_prefix", [500, 90], [260, 90], plens=[150], group=[0, 0], Hq=8, Hkv=2, d=64, page=32,
+         cap=0.0, wl=70),
 ]
 
 
@@ -554,3 +561,161 @@ def test_other_stream():
     s.synchronize()
     within("out", out, want, tol)
     within("lse", lse, wl, ltol)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with what it allocates."""
+    caches = [ref.Cache([4000, 100], page=64, seed=i) for i in range(2)]
+    qs = [normal(i, 2, 48, 160) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            s.wait_stream(torch.cuda.current_stream())
+            got[i] = C.attention_varlen_cache_fwd(qs[i], caches[i].k, caches[i].v, caches[i].table, caches[i].lens,
+                                                  i32([0, 1, 2]), stream=s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        want, wl, tol, ltol = ref.attention(qs[i], caches[i], [1, 1])
+        within("out", got[i][0], want, tol)
+        within("lse", got[i][1], wl, ltol)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages behind 2^32 elements: append, attention, weights and eviction."""
+    pages, page, H, d = 70000, 64, 8, 128  # 4.6e9 elements, 9.2 GB, K and V in one pool
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    k = torch.empty(pages, page, H, d, dtype=HF, device="cuda")
+    v = torch.empty(pages, page, H, d, dtype=HF, device="cuda")
+    far = [pages - 1, pages - 3, pages - 5]
+    table = i32([far])
+    new = normal(1, 150, H, d, dtype=HF)
+    val = normal(2, 150, H, d, dtype=HF)
+    lens, st = i32([0]), status()
+    C.attention_varlen_cache_append(new, val, k, v, table, lens, i32([0, 150]), lens_out=(n := i32([0])), status=st)
+    assert n.tolist() == [150]
+    for x, src in ((k, new), (v, val)):
+        got = torch.cat([x[p] for p in far])[:150]
+        assert torch.equal(got, src)
+    q = normal(3, 1, 32, d, dtype=HF, std=2.0)
+
+    class Small:  # the same keys in a small pool
+        lens_l, plens_l, Hkv, page_ = [150], [], H, page
+
+        @staticmethod
+        def rows(pool, t, r, m):
+            return pool.cpu().double()[:m]
+
+        table = ptable = None
+
+    Small.k, Small.v, Small.d = new, val, d
+    want, wl, tol, ltol = ref.attention(q, Small, [1], cap=0.0)
+    out, lse = C.attention_varlen_cache_fwd(q, k, v, table, n, i32([0, 1]), softcap=0.0, status=st)
+    within("out", out, want, tol)
+    within("lse", lse, wl, ltol)
+    sc, _ = C.attention_varlen_cache_weights(q, k, table, n, i32([0, 1]), lse, softcap=0.0, status=st)
+    own, _, wt, _ = ref.weights(q, Small, [1], lse, cap=0.0)
+    within("weights", sc[0, :, :150], own[0], wt[0] + own[0] * 2.0 ** -22)
+    kp = torch.arange(192, dtype=torch.int32, device="cuda").expand(1, H, -1).contiguous()
+    before = sc.clone()
+    C.attention_varlen_cache_evict(k, v, table, n, sc, kp, i32([150]), 70, 8, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and n.tolist() == [70]
+    flat_k = torch.cat([k[p] for p in far])
+    for h in range(H):
+        m, moves = ref.evicted(150, before[0, h, :150].tolist(), list(range(150)), 150, 70, 8)
+        for dst, src in moves:
+            assert torch.equal(flat_k[dst, h], new[src, h]) and int(kp[0, h, dst]) == src
+
+
+def test_captured_eviction_step():
+    """Weights and eviction captured into a graph: every replay takes one key from each full cache."""
+    kc = ref.Cache([80, 80], page=16, Hkv=2, d=64, dtype=HF, poison=False)
+    q, lens, budget = normal(1, 2, 8, 64, dtype=HF), i32([80, 80]), i32([0])
+    sc = torch.rand(2, 2, kc.table.shape[1] * 16, device="cuda")
+    kp = torch.arange(sc.shape[2], dtype=torch.int32, device="cuda").expand(2, 2, -1).contiguous()
+    nxt, cu_q = i32([80, 80]), i32([0, 1, 2])
+    qp = i32([79, 79])
+
+    def step():
+        out, lse = C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, lens, cu_q, q_pos=qp, key_pos=kp, causal=True)
+        C.attention_varlen_cache_weights(q, kc.k, kc.table, lens, cu_q, lse, sc, q_pos=qp, key_pos=kp, causal=True)
+        C.attention_varlen_cache_evict(kc.k, kc.v, kc.table, lens, sc, kp, nxt, 60, 10)
+        return out, lse
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    saved = [x.clone() for x in (kc.k, kc.v, sc, kp, lens)]
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = step()
+    for a, b in zip((kc.k, kc.v, sc, kp, lens), saved):
+        a.copy_(b)
+    kc.lens_l = [80, 80]
+    for i in range(2):
+        kc.lens_l = lens.tolist()
+        want, wl, tol, ltol = ref.attention(q, kc, [1, 1], causal=True, q_pos=qp, key_pos=kp)
+        graph.replay()
+        torch.cuda.synchronize()
+        within("out", out, want, tol)
+        assert lens.tolist() == [60, 60]
+        for b in range(2):
+            for h in range(2):
+                assert set(range(70, 80)) <= set(kp[b, h, :60].tolist())
+
+
+def test_python_refusals():
+    kc = ref.Cache([20, 9], page=16, Hkv=2, d=128)
+    q, cu_q = normal(1, 2, 8, 128), i32([0, 1, 2])
+    ok = dict(q=q, k_cache=kc.k, v_cache=kc.v, table=kc.table, lens=kc.lens, cu_q=cu_q)
+    C.attention_varlen_cache_fwd(**ok)
+    for change in (dict(q=q.half()), dict(q=q[:, :7]), dict(q=q.transpose(1, 2)), dict(v_cache=kc.v[:-1]),
+                   dict(table=kc.table.long()), dict(table=kc.table.t()), dict(lens=kc.lens.float()),
+                   dict(lens=kc.lens[:1]), dict(cu_q=cu_q[:2]), dict(cu_q=cu_q.cpu()), dict(q=q.cpu()),
+                   dict(alibi_slopes=torch.zeros(2, 7, device="cuda")), dict(prefix_lens=kc.lens),
+                   dict(prefix_table=kc.table), dict(key_pos=torch.zeros(2, 2, 64, dtype=torch.int32, device="cuda")),
+                   dict(q_pos=i32([1]),), dict(out=torch.empty(2, 8, 64, dtype=BF, device="cuda")),
+                   dict(lse=torch.empty(2, 9, device="cuda")), dict(k_cache=kc.k.transpose(2, 3)),
+                   dict(status=torch.zeros(1, device="cuda")), dict(causal="x", window_left="y")):
+        with pytest.raises(ValueError):
+            C.attention_varlen_cache_fwd(**{**ok, **change})
+    with pytest.raises(C.AttnError) as e:
+        C.attention_varlen_cache_fwd(**ok, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == -4
+    with pytest.raises(C.AttnError) as e:
+        C.attention_varlen_cache_fwd(**{**ok, "softcap": math.nan})
+    assert e.value.code == -1
+    with pytest.raises(ValueError):
+        C.attention_varlen_rotary(q, None, i32([0, 1]), torch.ones(65, dtype=torch.float64, device="cuda"))
+    with pytest.raises(ValueError):
+        C.attention_varlen_rotary(q, None, i32([0, 1, 2]), torch.ones(4, dtype=torch.float64, device="cuda"))
+    with pytest.raises(ValueError):
+        C.attention_varlen_rotary(q, None, i32([0, 1]), torch.ones(4, device="cuda"))
+    k = normal(2, 2, 2, 128)
+    with pytest.raises(ValueError):
+        C.attention_varlen_cache_append(k, k, kc.k, kc.v, kc.table, kc.lens, cu_q, lens_out=kc.lens)
+    with pytest.raises(ValueError):
+        C.attention_varlen_cache_append(k, k, kc.k, kc.v, kc.table, kc.lens, cu_q,
+                                        inv_freq=torch.ones(4, dtype=torch.float64, device="cuda"))
+
+
+def test_empty_calls():
+    kc = ref.Cache([20, 9], page=16, Hkv=2, d=128)
+    none = torch.empty(0, 8, 128, dtype=BF, device="cuda")
+    out, lse = C.attention_varlen_cache_fwd(none, kc.k, kc.v, kc.table, kc.lens, i32([0, 0, 0]))
+    assert out.shape == (0, 8, 128) and lse.shape == (0, 8)
+    sc = torch.rand(2, 2, kc.table.shape[1] * 16, device="cuda")
+    got, _ = C.attention_varlen_cache_weights(none, kc.k, kc.table, kc.lens, i32([0, 0, 0]), lse, sc,
+                                              scores_out=torch.full_like(sc, 5.0))
+    assert torch.equal(got[0, :, :20], sc[0, :, :20]) and (got[0, :, 20:] == 5).all()
+    a, b = C.attention_varlen_rotary(none, None, torch.empty(1, 0, dtype=torch.int32, device="cuda"),
+                                     torch.ones(4, dtype=torch.float64, device="cuda"))
+    assert a.shape == none.shape and b is None
+    lo = torch.zeros(2, dtype=torch.int32, device="cuda")
+    C.attention_varlen_cache_append(none[:, :2], none[:, :2], kc.k, kc.v, kc.table, kc.lens, i32([0, 0, 0]), lens_out=lo)
+    assert lo.tolist() == [20, 9]
+    assert torch.isfinite(kc.k[kc.table[0, 0].long()]).all()
