@@ -48,6 +48,7 @@ struct CacheParams {
   int64_t slopes_bs;
   int wl, wr;                // window limits, < 0: none (wr = 0 when causal)
   float softcap, sigma;
+  int tile_cost;             // what a tile's start costs, in steps (cache_sched.cuh)
   void* out;                 // forward
   int64_t out_ts, out_hs;
   float* lse;                // [total_q, Hq]; the forward writes it, the weights call reads it

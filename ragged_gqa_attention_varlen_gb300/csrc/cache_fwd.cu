@@ -167,7 +167,12 @@ size_t fwd_workspace(int B, int P, int Hq, int Hkv, int d, int64_t total_q) {
   return fwd_ws(B, P, Hq, Hkv, d, total_q).total;
 }
 
-cudaError_t launch_fwd(const CacheParams& p, cudaStream_t s) {
+cudaError_t launch_fwd(const CacheParams& call, cudaStream_t s) {
+  CacheParams p = call;
+  // a piece's start takes about 7000 clk where a step takes 3600 (shared
+  // prefix without a cap), and 11000 where a step takes 3000 and the first
+  // tile is passed over twice (drafts with a cap of 3)
+  p.tile_cost = fixed_reference(p) ? 4 : 2;
   const int grid = device_ctas();
   if (grid < 1 || !encode_fn()) return cudaErrorInitializationError;
   const FwdWs w = fwd_ws(p.B, p.P, p.Hq, p.Hkv, p.d, p.total_q);

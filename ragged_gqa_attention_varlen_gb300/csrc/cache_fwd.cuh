@@ -170,13 +170,13 @@ __device__ __forceinline__ void load_pages(const CacheParams& p, FwdBars* bars, 
     const int32_t* row = t.pages + pc.row * t.rs;
     auto page_of = [&](int kt) {  // this lane's page of key tile kt, or -1: no box
       const int key = kt * kKeys + pi * box;
-      return ch < S::kChunksK && kt < pc.kt1 && key < pc.len ? tile_page(p, row, key) : -1;
+      return ch < S::kChunksK && kt >= pc.kt0 && key < pc.len ? tile_page(p, row, key) : -1;
     };
-    int page = page_of(pc.kt0);
-    for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
+    int page = page_of(pc.kt1 - 1);
+    for (int kt = pc.kt1 - 1; kt >= pc.kt0; --kt) {
       const int key0 = kt * kKeys;
       const int have = min(pieces, (pc.len - key0 + box - 1) / box);  // row blocks in use
-      const int next = page_of(kt + 1);  // read while this tile's stage is waited for
+      const int next = page_of(kt - 1);  // read while this tile's stage is waited for
       if (loaded >= kStages && !(ok = mbar_wait_warp(&empty[st], ph ^ 1, s_abort))) break;
       if (lane == 0) mbar_arrive_expect_tx(&full[st], kBytes / pieces * have);
       __syncwarp();
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           piece_done(&bars->ring, take);
           if (pc.row < 0) break;
           if (!mbar_wait(&bars->q_full, tiles & 1, s_abort)) break;
-          for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++step) {
+          for (int kt = pc.kt1 - 1; kt >= pc.kt0; --kt, ++step) {
             if (!(ok = mbar_wait(&bars->k_full[st], ph, s_abort))) break;
             // the product with the P that took the buffer's previous S (step - 2) is done
             if (step >= 2 && !(ok = mbar_wait(&bars->pv_done[step & 1], ((step - 2) >> 1) & 1, s_abort)))
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
               umma_ss(tmem + (step & 1) * 128, kmajor_desc(qb, k), kmajor_desc(kb, k), kIdS, k > 0);
             umma_commit(&bars->s_full[step & 1]);
             umma_commit(&bars->k_empty[st]);
-            if (kt == pc.kt1 - 1) umma_commit(&bars->q_empty);
+            if (kt == pc.kt0) umma_commit(&bars->q_empty);
             if (++st == S::kKS) {
               st = 0;
               ph ^= 1;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
         __syncwarp();
         if (lane == 0) piece_done(&bars->ring, take);
         if (pc.row < 0) break;
-        for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++step) {
+        for (int kt = pc.kt1 - 1; kt >= pc.kt0; --kt, ++step) {
           const int key0 = kt * kKeys;
           const int nk = min(kKeys, pc.len - key0);        // keys of the tile that exist
           const int z0 = min(max(pc.klo - key0, 0), nk);   // those [z0, z1) that some row reads
@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kThreadsF, 1)
             __syncwarp();
           }
           if (!(ok = mbar_wait_warp(&bars->p_full[step & 1], (step >> 1) & 1, s_abort))) break;
-          if (kt == pc.kt0 && tiles > 0 &&
+          const bool first = kt == pc.kt1 - 1;
+          if (first && tiles > 0 &&
               !(ok = mbar_wait_warp(&bars->o_empty, (tiles - 1) & 1, s_abort)))
             break;
           if (lane == 0) {
@@ -370,10 +371,10 @@ __global__ void __launch_bounds__(kThreadsF, 1)
             // keys 16k .. 16k + 15: pair columns 8 (k mod 4) of half k / 4
             for (int k = 0; k < ksteps; ++k)
               umma_ts(tmem + kColOv, tmem + (step & 1) * 128 + (k >> 2) * 64 + (k & 3) * 8,
-                      sdesc_sw128(vb + k * 2048, 16384, 1024), kIdO, (kt > pc.kt0 || k > 0));
+                      sdesc_sw128(vb + k * 2048, 16384, 1024), kIdO, (!first || k > 0));
             umma_commit(&bars->pv_done[step & 1]);
             umma_commit(&bars->v_empty[st]);
-            if (kt == pc.kt1 - 1) umma_commit(&bars->o_full);
+            if (kt == pc.kt0) umma_commit(&bars->o_full);
           }
           __syncwarp();
           if (++st == S::kVS) {
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           int64_t sum = 0;
           for (int i = lane; i < nt; i += 32) {
             tile_keys(p, g.s, i, lo, hi);
-            sum += tile_cost(tile_steps(lo, hi));
+            sum += tile_cost(p, tile_steps(lo, hi));
           }
           const int64_t cost = warp_sum64(sum);
           if (cost > 0) {
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
         }
         if (!varies) {
           if (g.each > 0 && begin > a) {  // skip whole row tiles before this CTA's share
-            const int cost = tile_cost(g.each);
+            const int cost = tile_cost(p, g.each);
             const int64_t skip = min(div64(begin - a, cost), static_cast<int64_t>(nt) * p.Hkv);
             a += skip * cost;
             gi = static_cast<int>(div64(skip, nt));
@@ -450,8 +451,8 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           for (; ok && t < nt && a < end; ++t) {
             if (varies) tile_keys(p, g.s, t, lo, hi);
             const int n = varies ? tile_steps(lo, hi) : g.each;
-            // units [a, a + kTileCost) carry no step
-            const int64_t at = a + kTileCost;  // of step 0
+            // units [a, a + tile_cost) carry no step
+            const int64_t at = a + p.tile_cost;  // of step 0
             const int f0 = static_cast<int>(max(begin - at, static_cast<int64_t>(0)));
             const int f1 = static_cast<int>(min(end - at, static_cast<int64_t>(n)));
             if (f0 < f1) {
@@ -475,12 +476,12 @@ __global__ void __launch_bounds__(kThreadsF, 1)
               pc.parts = f1 < n ? static_cast<int>(div64(at + n - 1, per)) - static_cast<int>(blockIdx.x) + 1 : 1;
               {  // the loads will soon ask for these
                 const int32_t* row = (pc.own ? p.own.pages + pc.row * p.own.rs : p.prefix.pages + pc.row * p.prefix.rs);
-                const int at = (pc.kt0 * kKeys >> p.page_log2) + lane;
-                if (at <= (pc.len - 1) >> p.page_log2) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + at));
+                const int at = (min(pc.kt1 * kKeys, pc.len) - 1 >> p.page_log2) - lane;
+                if (at >= pc.kt0 * kKeys >> p.page_log2) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + at));
               }
               ok = publish(pc);
             }
-            a += tile_cost(n);
+            a += tile_cost(p, n);
             x0 += kRows;
             h0 += kRows;
             if (p.R < 2 * kRows) {
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           }
         }
         if (varies && a >= end) break;
-        first = varies ? a : first + static_cast<int64_t>(tile_cost(g.each)) * nt * p.Hkv;
+        first = varies ? a : first + static_cast<int64_t>(tile_cost(p, g.each)) * nt * p.Hkv;
       }
       Piece last = {};
       last.row = -1;
@@ -574,10 +575,10 @@ __global__ void __launch_bounds__(kThreadsF, 1)
         }
       }
       // subtracted from the logits; with FIXED they come without their constant c
-      const float bref = FIXED ? m_run - out_scale : 0.f;
+      float bref = FIXED ? m_run - out_scale : 0.f;
       uint64_t l2 = f2_make(0.f, 0.f);
 
-      for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++step) {
+      for (int kt = pc.kt1 - 1; kt >= pc.kt0; --kt, ++step) {
         const int key0 = kt * kKeys + half * 64;
         const uint32_t sb = tmem + (step & 1) * 128 + half * 64 + lane_addr;
         int kpa = 0, kpb = 0;
@@ -696,6 +697,30 @@ __global__ void __launch_bounds__(kThreadsF, 1)
             l2 = f2_mul(l2, f2_make(alpha, alpha));
           }
         }
+        // With FIXED, the first tile's maximum becomes the reference (down to
+        // 2^-13 below the bound, so that no later P overflows 16 bits): the
+        // largest weight of most rows is then exactly 1.  The tile is passed
+        // over twice for that.
+        if (FIXED && kt == pc.kt1 - 1) {
+          float mx = -INFINITY;
+          if (any) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < 64; c0 += kCh) {
+              float x[kCh];
+              tmem_ld16(sb + c0, x);
+              tmem_wait_ld();
+              logits16(x, c0);
+#pragma unroll
+              for (int i = 0; i < kCh; ++i) mx = fmaxf(mx, x[i]);
+            }
+          }
+          float* mxs = sMax + (tiles & 1) * 256;
+          mxs[half * 128 + r] = mx;
+          if (!(ok = warp_exchange(&bars->mx_x[quad][tiles & 1], (tiles >> 1) & 1, s_abort))) break;
+          const float up = fmaxf(fmaxf(mx, mxs[(half ^ 1) * 128 + r]), -13.f);
+          m_run += up;
+          bref += up;
+        }
         if (any) {
           const float m_use = FIXED || m_run == -INFINITY ? 0.f : m_run;
           const float sc = keep ? 1.f : in_scale;
@@ -717,7 +742,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
             }
             tmem_st8(sb + c0 / 2, pk);
           }
-          if (!FIXED && kt > pc.kt0 && __any_sync(0xffffffffu, need)) {
+          if (!FIXED && kt < pc.kt1 - 1 && __any_sync(0xffffffffu, need)) {
             // O follows the new reference, once the previous products are in
             // it: this half's features
             if (!(ok = mbar_wait_warp(&bars->pv_done[(step - 1) & 1], ((step - 1) >> 1) & 1, s_abort)))
@@ -819,6 +844,11 @@ __global__ void __launch_bounds__(kThreadsF, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// A softcap of at most kFixedCap at default key positions.
+inline bool fixed_reference(const CacheParams& p) {
+  return p.softcap > 0.f && p.softcap <= kFixedCap && !p.own.pos && !(p.P && p.prefix.pos);
+}
+
 template <bool B, int HD>
 auto pick_fwd(const CacheParams& p) {
   const bool moved = p.own.pos || (p.P && p.prefix.pos);
@@ -826,7 +856,7 @@ auto pick_fwd(const CacheParams& p) {
   if (!(p.softcap > 0.f))
     return pos ? cache_fwd_kernel<B, HD, false, false, true>
                : cache_fwd_kernel<B, HD, false, false, false>;
-  if (p.softcap <= kFixedCap && !moved)
+  if (fixed_reference(p))
     return pos ? cache_fwd_kernel<B, HD, true, true, true>
                : cache_fwd_kernel<B, HD, true, true, false>;
   return pos ? cache_fwd_kernel<B, HD, true, false, true>

@@ -3,8 +3,9 @@
 // A row tile is 128 consecutive packed rows of one segment and K/V head: row x
 // is token x / R of the segment's tokens and head x % R of the group (R query
 // heads per K/V head).  It visits the 128-key tiles that hold a key some row
-// of it may attend to.  A tile of n steps costs n + kTileCost units (its
-// Q rows, the first step's latency and its results cost about two steps); all
+// of it may attend to.  A tile of n steps costs n + tile_cost units (its
+// Q rows, the first step's latency and its results cost as much as two to four
+// steps); all
 // tiles of a call, segment by segment, form one line of W units, and the CTA c
 // of G takes units [c * per, (c + 1) * per), per = ceil(W / G): however uneven
 // the lengths, every CTA does the same work in one go, and a long sequence of
@@ -18,7 +19,6 @@ namespace attn {
 namespace kv {
 
 constexpr int kRows = 128;
-constexpr int kTileCost = 2;
 constexpr int kMaxCtas = 160;  // CTAs of the attention and weights kernels, at most
 
 struct Seg {
@@ -121,16 +121,18 @@ __device__ __forceinline__ SegPlan seg_plan(const CacheParams& p, int s) {
 }
 
 // Cost of a tile of n steps.
-__device__ __forceinline__ int tile_cost(int n) { return n > 0 ? n + kTileCost : 0; }
+__device__ __forceinline__ int tile_cost(const CacheParams& p, int n) {
+  return n > 0 ? n + p.tile_cost : 0;
+}
 
 // Cost of one K/V head's row tiles (when they differ: one by one).
 __device__ __forceinline__ int64_t seg_cost(const CacheParams& p, const SegPlan& g) {
-  if (g.each >= 0) return static_cast<int64_t>(g.tiles) * tile_cost(g.each);
+  if (g.each >= 0) return static_cast<int64_t>(g.tiles) * tile_cost(p, g.each);
   int64_t n = 0;
   for (int t = 0; t < g.tiles; ++t) {
     int lo, hi;
     tile_keys(p, g.s, t, lo, hi);
-    n += tile_cost(tile_steps(lo, hi));
+    n += tile_cost(p, tile_steps(lo, hi));
   }
   return n;
 }

@@ -41,7 +41,9 @@ __global__ void __launch_bounds__(128)
 
 size_t weights_workspace() { return weights_ws().total; }
 
-cudaError_t launch_weights(const CacheParams& p, cudaStream_t s) {
+cudaError_t launch_weights(const CacheParams& call, cudaStream_t s) {
+  CacheParams p = call;
+  p.tile_cost = 2;
   const int grid = device_ctas();
   if (grid < 1 || !encode_fn()) return cudaErrorInitializationError;
   const WeightsWs w = weights_ws();

@@ -129,12 +129,12 @@ __device__ __forceinline__ SegPlan weights_plan(const CacheParams& p, int s) {
   return g;
 }
 __device__ __forceinline__ int64_t weights_cost(const CacheParams& p, const SegPlan& g) {
-  if (g.each >= 0) return static_cast<int64_t>(g.tiles) * (g.each + kTileCost);
+  if (g.each >= 0) return static_cast<int64_t>(g.tiles) * (g.each + p.tile_cost);
   int64_t n = 0;
   for (int kt = 0; kt < g.tiles; ++kt) {
     int t0, t1;
     key_tile_rows(p, g, g.waits, kt, t0, t1);
-    n += t1 - t0 + kTileCost;
+    n += t1 - t0 + p.tile_cost;
   }
   return n;
 }
@@ -341,21 +341,21 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       if (begin > a && g.tiles > 0) {
         int64_t cost = 0;  // of a K/V head
         if (g.each >= 0) {
-          cost = static_cast<int64_t>(g.tiles) * (g.each + kTileCost);
+          cost = static_cast<int64_t>(g.tiles) * (g.each + p.tile_cost);
         } else {
           int64_t sum = 0;
           for (int kt = lane; kt < g.tiles; kt += 32) {
             int t0, t1;
             key_tile_rows(p, g, nt, kt, t0, t1);
-            sum += t1 - t0 + kTileCost;
+            sum += t1 - t0 + p.tile_cost;
           }
           cost = warp_sum64(sum);
         }
         g0 = static_cast<int>(min(div64(begin - a, cost), static_cast<int64_t>(p.Hkv)));
         a += g0 * cost;
         if (g.each >= 0 && g0 < p.Hkv) {
-          tile = static_cast<int>(div64(begin - a, g.each + kTileCost));
-          a += static_cast<int64_t>(tile) * (g.each + kTileCost);
+          tile = static_cast<int>(div64(begin - a, g.each + p.tile_cost));
+          a += static_cast<int64_t>(tile) * (g.each + p.tile_cost);
         }
       }
       for (int gi = g0; ok && gi < p.Hkv && a < end; ++gi, tile = 0) {
@@ -379,9 +379,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
               n = pc.t1 - pc.t0;
             }
           }
-          // units [a, a + kTileCost) carry no step; a tile without any step
+          // units [a, a + p.tile_cost) carry no step; a tile without any step
           // belongs to the CTA of its first unit
-          const int64_t at = a + kTileCost;
+          const int64_t at = a + p.tile_cost;
           const int f0 = static_cast<int>(max(begin - at, static_cast<int64_t>(0)));
           const int f1 = static_cast<int>(min(end - at, static_cast<int64_t>(n)));
           if (f0 < f1 || (n == 0 && a >= begin)) {
