@@ -40,15 +40,24 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   const int tok = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.y * kHeadsJ + (lane & 7);
   const int f0 = (lane >> 3) + 4 * warp;
-  if (h >= p.Hq || tok >= __ldg(p.cu_q + p.B)) return;  // (tokens behind the last sequence)
+  if (h >= p.Hq) return;
   const int g = h / p.R, hr = h - g * p.R;
   const int2* meta = reinterpret_cast<const int2*>(p.ws + w.meta);
   const float2* stats = reinterpret_cast<const float2*>(p.ws + w.stats);
   const float4* part = reinterpret_cast<const float4*>(p.ws + w.rows);
-  const int guess = min(tok, p.B - 1);  // one token each: no search
-  const int b = __ldg(p.cu_q + guess) == tok && __ldg(p.cu_q + guess + 1) > tok
-                    ? guess
-                    : seq_of(p.cu_q, 0, p.B, tok);
+  const int64_t row = static_cast<int64_t>(tok) * p.Hq + h;
+  // The row's sequence; with one token each it is the token's own number, so
+  // its lengths are read along with the test of that.
+  int b = min(tok, p.B - 1);
+  const int end = __ldg(p.cu_q + p.B);
+  int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.own.lens + b);
+  if (tok >= end) return;  // behind the last sequence
+  if (c0 > tok || c1 <= tok) {
+    b = seq_of(p.cu_q, 0, p.B, tok);
+    c0 = __ldg(p.cu_q + b);
+    c1 = __ldg(p.cu_q + b + 1);
+    len = __ldg(p.own.lens + b);
+  }
   // whether the row's own slots and its prefix have any step, and the row's
   // place in their row tiles
   bool has_own, has_prefix = false;
@@ -57,10 +66,10 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
     Seg own;
     own.own = 1;
     own.klo = 0;
-    own.tok0 = __ldg(p.cu_q + b);
-    own.ntok = __ldg(p.cu_q + b + 1) - own.tok0;
-    own.len = __ldg(p.own.lens + b);
-    const uint32_t x = static_cast<uint32_t>(tok - own.tok0) * p.R + hr;
+    own.tok0 = c0;
+    own.ntok = c1 - c0;
+    own.len = len;
+    const uint32_t x = static_cast<uint32_t>(tok - c0) * p.R + hr;
     int lo, hi;
     tile_keys(p, own, x / kRows, lo, hi);
     has_own = hi > lo;
@@ -69,19 +78,18 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   if (p.P) {
     const int pfx = prefix_of(p, b);
     if (pfx >= 0) {
-      const int len = __ldg(p.prefix.lens + pfx);
-      has_prefix = prefix_klo(p, pfx, len) < len;
+      const int n = __ldg(p.prefix.lens + pfx);
+      has_prefix = prefix_klo(p, pfx, n) < n;
       const int tok0 = __ldg(p.cu_q + max(__ldg(p.cu_prefix + pfx), 0));
       rp = (static_cast<uint32_t>(tok - tok0) * p.R + hr) % kRows;
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int ok = reinterpret_cast<const FwdHead*>(p.ws)->ok;
   // (first CTA, parts) of the two segments
-  int2 mo = make_int2(0, 0), mp = mo;
-  const int64_t row = static_cast<int64_t>(tok) * p.Hq + h;
-  if (has_own) mo = meta[row];
-  if (has_prefix) mp = meta[p.total_q * p.Hq + row];
+  const int ok = reinterpret_cast<const FwdHead*>(p.ws)->ok;
+  int2 mo = meta[row], mp = p.P ? meta[p.total_q * p.Hq + row] : make_int2(0, 0);
+  if (!has_own) mo = make_int2(0, 0);
+  if (!has_prefix) mp = make_int2(0, 0);
   if (!ok || (mo.y == 1 && mp.y == 0)) return;
   const int parts = mo.y + mp.y;
   auto row_of = [&](int i) -> int64_t {
@@ -90,32 +98,47 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
     i -= mo.y;
     return mp.y > 1 ? cut_row(w, mp.x + i, i == 0, rp) : whole_row(w, p.total_q, p.Hq, false, tok, h);
   };
-  // the largest reference of a part that has any weight
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const float2 s = stats[row_of(i)];
-    if (s.y > 0.f) top = fmaxf(top, s.x);
-  }
-  float l = 0.f;
+  // Four parts at a time, all their loads first; the reference follows the
+  // largest met so far.
+  float top = -INFINITY, l = 0.f;
   float4 acc[kPer] = {};
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const int64_t pr = row_of(i);
-    const float2 s = stats[pr];
-    float4 v[kPer];
+  for (int i0 = 0; i0 < parts; i0 += 4) {
+    float2 s[4];
+    float4 v[4][kPer];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (f0 + 4 * kWarpsJ * k < kUnits) v[k] = part[part_at<HD>(pr, f0 + 4 * kWarpsJ * k)];
-    if (s.y > 0.f) {  // (a part without any weight may hold anything)
-      const float a = ex2_approx(s.x - top);
-      l = fmaf(a, s.y, l);
+    for (int i = 0; i < 4; ++i) {
+      s[i] = make_float2(-INFINITY, 0.f);
+      if (i0 + i < parts) {
+        const int64_t pr = row_of(i0 + i);
+        s[i] = stats[pr];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (f0 + 4 * kWarpsJ * k < kUnits) v[i][k] = part[part_at<HD>(pr, f0 + 4 * kWarpsJ * k)];
+      }
+    }
+    float up = top;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (s[i].y > 0.f) up = fmaxf(up, s[i].x);
+    if (up > top) {
+      const float a = ex2_approx(top - up);
+      top = up;
+      l *= a;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        acc[k] = make_float4(acc[k].x * a, acc[k].y * a, acc[k].z * a, acc[k].w * a);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!(s[i].y > 0.f)) continue;  // (a part without any weight may hold anything)
+      const float a = ex2_approx(s[i].x - top);
+      l = fmaf(a, s[i].y, l);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        acc[k].x = fmaf(a, v[k].x, acc[k].x);
-        acc[k].y = fmaf(a, v[k].y, acc[k].y);
-        acc[k].z = fmaf(a, v[k].z, acc[k].z);
-        acc[k].w = fmaf(a, v[k].w, acc[k].w);
+        acc[k].x = fmaf(a, v[i][k].x, acc[k].x);
+        acc[k].y = fmaf(a, v[i][k].y, acc[k].y);
+        acc[k].z = fmaf(a, v[i][k].z, acc[k].z);
+        acc[k].w = fmaf(a, v[i][k].w, acc[k].w);
       }
     }
   }
