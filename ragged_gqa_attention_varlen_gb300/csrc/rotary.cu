@@ -11,8 +11,9 @@
 // one turn and scaled to a 64-bit fraction F, and position * F modulo 2^64 is
 // the fraction of a turn with an error below |position| * 2^-53 / 2 pi * |t /
 // position| (the rounding of inv_freq / 2 pi).  In fp32, a position of 10^6
-// would leave the angle 0.06 wrong.  Its top 32 bits, as a signed fraction,
-// go to sincospif.
+// would leave the angle 0.06 wrong.  Its top 32 bits, as a signed fraction in
+// [-pi, pi), go to the fast sine and cosine, good to 2^-21.2 there: 2^-9 of a
+// rounding of the 16-bit results.
 //
 // Bound by memory: every row is read and written once.  A block takes a few
 // tokens, so that one pair's sine serves all heads.
@@ -64,10 +65,10 @@ __device__ __forceinline__ void fill_turns(const RotaryTable& r, int64_t tok0, i
   const float inv_pairs = 1.f / r.pairs;
   auto turn = [&](int t, int i, int64_t pos, uint64_t per_pos) {
     const uint64_t turns = static_cast<uint64_t>(pos) * per_pos;
-    // the top 32 bits as a signed fraction of a turn, in half turns
-    const float h = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;
+    // the top 32 bits as a signed fraction of a turn, times 2 pi
+    const float h = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 1.4629180792671596e-9f;
     float sn, cn;
-    sincospif(h, &sn, &cn);
+    __sincosf(h, &sn, &cn);
     s.cs[t][i] = make_float2(cn, r.inverse ? -sn : sn);
   };
   const int all = ntok * r.pairs;
@@ -273,34 +274,66 @@ __global__ void __launch_bounds__(kThreadsR)
     row_k[t] = rk;
     row_v[t] = rv;
   }
-  if (p.r.inv_freq) fill_turns(p.r, tok0, ntok, turns);
+  // few tokens: the turns along with the lookups; many: after the V rows
+  const bool early = p.r.inv_freq && ntok * p.r.pairs <= kThreadsR;
+  if (early) fill_turns(p.r, tok0, ntok, turns);
   __syncthreads();
+  // V rows and K rows: each thread's loads of four (two) units go out together.
+  // Of few tokens, the upper half of the threads takes V and the lower K.
+  const int step = early ? kThreadsR / 2 : kThreadsR;
+  const bool upper = static_cast<int>(threadIdx.x) >= step;
+  if (!early || upper) {
+    const int units = p.d / 8, per = p.Hkv * units, all = ntok * per;
+    const float inv_per = 1.f / per, inv_units = 1.f / units;
+    for (int u0 = threadIdx.x - (upper ? step : 0); u0 < all; u0 += 4 * step) {
+      uint4 v[4];
+      uint16_t* out[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int u = u0 + k * step, t = quotient(u, inv_per), w = u - t * per;
+        const int64_t g = quotient(w, inv_units);
+        const int f = (w - static_cast<int>(g) * units) * 8;
+        out[k] = nullptr;
+        if (u < all && row_v[t] >= 0) {
+          out[k] = static_cast<uint16_t*>(const_cast<void*>(p.v.base)) + row_v[t] + g * p.v.head + f;
+          v[k] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.vx) +
+                                                       (tok0 + t) * p.v_ts + g * p.v_hs + f));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (out[k]) *reinterpret_cast<uint4*>(out[k]) = v[k];
+    }
+  }
+  if (p.r.inv_freq && !early) {
+    fill_turns(p.r, tok0, ntok, turns);
+    __syncthreads();
+  }
+  if (early && upper) return;
   const int pairs = p.r.inv_freq ? p.r.pairs : 0;
   const RowItems it = row_items<VEC>(p.d, pairs, p.r.interleaved);
-  const RowItems iv = row_items<true>(p.d, 0, false);
-  const int per = p.Hkv * (it.total + iv.total);
-  const float inv_per = 1.f / per, inv_total = 1.f / it.total, inv_v = 1.f / iv.total;
-  for (int u = threadIdx.x; u < ntok * per; u += kThreadsR) {
-    const int t = quotient(u, inv_per);
-    int w = u - t * per;
-    if (row_k[t] < 0) continue;
-    if (w < p.Hkv * it.total) {
+  const int per = p.Hkv * it.total, all = ntok * per;
+  const float inv_per = 1.f / per, inv_total = 1.f / it.total;
+  for (int u0 = threadIdx.x; u0 < all; u0 += 2 * step) {
+    Item<BF16, VEC> item[2];
+    uint16_t* out[2];
+    int at[2], tok[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int u = u0 + k * step, t = quotient(u, inv_per), w = u - t * per;
       const int64_t g = quotient(w, inv_total);
-      w -= static_cast<int>(g) * it.total;
-      Item<BF16, VEC> item;
-      item.load(static_cast<const uint16_t*>(p.kx) + (tok0 + t) * p.k_ts + g * p.k_hs, w, it.turning,
-                pairs, p.r.interleaved);
-      item.store(static_cast<uint16_t*>(const_cast<void*>(p.k.base)) + row_k[t] + g * p.k.head, w,
-                 it.turning, pairs, p.r.interleaved, turns.cs[t]);
-    } else {
-      w -= p.Hkv * it.total;
-      const int64_t g = quotient(w, inv_v);
-      w -= static_cast<int>(g) * iv.total;
-      VecItem<BF16> item;
-      item.load(static_cast<const uint16_t*>(p.vx) + (tok0 + t) * p.v_ts + g * p.v_hs, w, 0, 0, false);
-      item.store(static_cast<uint16_t*>(const_cast<void*>(p.v.base)) + row_v[t] + g * p.v.head, w, 0, 0,
-                 false, nullptr);
+      out[k] = nullptr;
+      tok[k] = t;
+      at[k] = w - static_cast<int>(g) * it.total;
+      if (u < all && row_k[t] >= 0) {
+        out[k] = static_cast<uint16_t*>(const_cast<void*>(p.k.base)) + row_k[t] + g * p.k.head;
+        item[k].load(static_cast<const uint16_t*>(p.kx) + (tok0 + t) * p.k_ts + g * p.k_hs, at[k],
+                     it.turning, pairs, p.r.interleaved);
+      }
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (out[k]) item[k].store(out[k], at[k], it.turning, pairs, p.r.interleaved, turns.cs[tok[k]]);
   }
 }
 

@@ -386,7 +386,9 @@ EV = [pytest.param(*x, id="-".join(map(str, x[:6])) + f"-{i}") for i, x in enume
     ([500], 3, 64, 32, 77, 77, "spread"), ([400, 399], 2, 64, 16, 200, 50, "equal"),
     ([2500, 1025], 1, 128, 128, 1024, 100, "few"), ([5000], 2, 64, 1024, 1, 0, "spread"),
     ([700], 1, 160, 16, 300, 10, "odd"), ([60000, 50000], 1, 64, 64, 20000, 512, "spread"),
-    ([33, 34, 35], 2, 64, 16, 32, 1, "negative")])]
+    ([33, 34, 35], 2, 64, 16, 32, 1, "negative"), ([201, 201, 201, 201], 3, 64, 16, 200, 20, "few"),
+    ([301], 4, 64, 32, 300, 0, "odd"), ([5001, 5001], 2, 64, 64, 5000, 5000, "equal"),
+    ([2, 2, 2], 1, 128, 16, 1, 0, "negative"), ([1030, 1030], 2, 64, 16, 1029, 1000, "spread")])]
 
 
 @pytest.mark.parametrize("lens,Hkv,d,page,budget,recent,kind", EV)
