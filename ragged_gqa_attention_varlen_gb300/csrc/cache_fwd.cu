@@ -40,7 +40,12 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   const int tok = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.y * kHeadsJ + (lane & 7);
   const int f0 = (lane >> 3) + 4 * warp;
-  if (h >= p.Hq) return;
+  // Every block waits for the tile kernel before it ends, also those without
+  // rows: what follows on the stream must not overlap it.
+  if (h >= p.Hq) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int g = h / p.R, hr = h - g * p.R;
   const int2* meta = reinterpret_cast<const int2*>(p.ws + w.meta);
   const float2* stats = reinterpret_cast<const float2*>(p.ws + w.stats);
@@ -51,7 +56,10 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   int b = min(tok, p.B - 1);
   const int end = __ldg(p.cu_q + p.B);
   int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.own.lens + b);
-  if (tok >= end) return;  // behind the last sequence
+  if (tok >= end) {  // behind the last sequence
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   if (c0 > tok || c1 <= tok) {
     b = seq_of(p.cu_q, 0, p.B, tok);
     c0 = __ldg(p.cu_q + b);

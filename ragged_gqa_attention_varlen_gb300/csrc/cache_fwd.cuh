@@ -697,10 +697,12 @@ __global__ void __launch_bounds__(kThreadsF, 1)
             l2 = f2_mul(l2, f2_make(alpha, alpha));
           }
         }
-        // With FIXED, the first tile's maximum becomes the reference (down to
-        // 2^-13 below the bound, so that no later P overflows 16 bits): the
-        // largest weight of most rows is then exactly 1.  The tile is passed
-        // over twice for that.
+        // With FIXED, the first tile's maximum becomes the reference: the largest
+        // weight of most rows is then exactly 1.  The tile is passed over twice
+        // for that.  A later logit may lie as high as the cap above the ALiBi
+        // term of the nearest key, so the reference stays within 15 of that and
+        // no P passes 2^15; the row's largest is at least 2^-12.5 then (caps up to
+        // 9.5), which 16 bits hold.
         if (FIXED && kt == pc.kt1 - 1) {
           float mx = -INFINITY;
           if (any) {
@@ -717,7 +719,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           float* mxs = sMax + (tiles & 1) * 256;
           mxs[half * 128 + r] = mx;
           if (!(ok = warp_exchange(&bars->mx_x[quad][tiles & 1], (tiles >> 1) & 1, s_abort))) break;
-          const float up = fmaxf(fmaxf(mx, mxs[(half ^ 1) * 128 + r]), -13.f);
+          const float up = fmaxf(fmaxf(mx, mxs[(half ^ 1) * 128 + r]), out_scale - 15.f);
           m_run += up;
           bref += up;
         }

@@ -90,6 +90,11 @@ CASES = [
     case("steep", [600], [2], Hq=8, alibi=True, cap=0.0, std=6.0),
     case("peaked_fp16", [600, 100], [2, 1], Hq=8, cap=0.0, std=12.0, dtype=HF),
     case("big_cap", [600], [2], Hq=8, cap=50.0, std=12.0),
+    # logits at both ends of the cap, and rows that nothing of the nearest tile is left for
+    case("saturated_fp16", [300, 260], [150, 200], Hq=8, dtype=HF, cap=9.0, std=30.0),
+    case("saturated_small_cap_fp16", [300, 260], [150, 200], Hq=8, dtype=HF, cap=3.0, std=30.0, alibi=True),
+    case("saturated_window_fp16", [700], [300], Hq=8, dtype=HF, cap=9.4, std=30.0, wl=200),
+    case("saturated_uncausal", [700], [3], Hq=16, dtype=HF, cap=9.5, std=30.0, causal=False),
     case("huge_page", [2000, 1500], [1, 1], Hq=8, page=1024),
     case("heads_beyond_a_tile", [200], [3], Hq=200, page=16, alibi=True),
     case("more_sequences_than_threads", ref.spread(9, 700, 1, 30), [1] * 700, Hq=4, d=64, page=16, cap=0.0),
@@ -194,7 +199,7 @@ def test_key_weights(c):
 
 def test_weights_of_a_row_sum_to_one():
     """Every non-empty row spreads a weight of 1 over its keys."""
-    c = dict(CASES[17].values[0])
+    c = dict(next(x for x in CASES if x.id == "prefix").values[0])
     kc, q, cu_q, _, call = build(c)
     out, lse = C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, kc.lens, cu_q, **call)
     z = torch.zeros(1, c["Hkv"], kc.ptable.shape[1] * c["page"], device="cuda")
