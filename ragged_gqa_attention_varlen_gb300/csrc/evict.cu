@@ -17,9 +17,11 @@
 // holes and the movers in slot order: no atomics decide an order, so results
 // are repeatable.  Latencies bound it: loads go out four at a time.
 // move_kernel: the listed K and V rows with their scores and positions, over
-// the whole GPU, two 16-byte units in flight per thread (12 prompts of up to
-// 20000 keys, 91 MB: 55 us; with four units or one 60 and 63); a chain of three
-// scattered reads per unit bounds it.
+// the whole GPU: a row is found through three dependent scattered reads (list,
+// page table, row), so a warp takes four rows through each of them together
+// (both kernels, 12 prompts of up to 20000 keys, 91 MB: 45 us; with a thread per
+// 16-byte unit, two in flight, 55.  Eight rows: 45, and the call for one key
+// goes from 8.6 to 10.6).
 #include "../../include/attn_varlen.h"
 #include "cache.cuh"
 
@@ -32,7 +34,7 @@ constexpr int kWarpsE = kThreadsE / 32;
 constexpr int kSmemKeys = 48 * 1024;  // ranks held in shared memory (192 KB)
 constexpr int kThreadsM = 256;
 constexpr int kCopies = 8;  // of the histogram
-constexpr int kUnits = 2;   // 16-byte units in flight per thread of the moves
+constexpr int kMoves = 4;   // rows a warp moves at a time
 
 struct EvictWs {
   size_t newlen, counts, lists, total;
@@ -182,6 +184,7 @@ __global__ void __launch_bounds__(kThreadsE)
         }
       }
     } else {
+#pragma unroll 4
       for (int j = tid; j < n; j += kThreadsE) {
         const uint32_t x = key(j);
         if (((x ^ prefix) >> (shift + 8)) == 0) atomicAdd(&mine[(x >> shift) & 255], 1u);
@@ -287,63 +290,51 @@ __global__ void __launch_bounds__(kThreadsM)
     p.lens_out[s] = reinterpret_cast<const int32_t*>(p.ws + w.newlen)[s];
   const int units = p.d / 8;  // 16-byte units of a K or V row
   const int32_t* row = p.table + s * p.table_rs;
-  const uint32_t per = 2 * units + 1;  // and one for the score and the position
-  const int64_t all = static_cast<int64_t>(count) * per;
-  const int64_t stride = static_cast<int64_t>(gridDim.y) * kThreadsM;
   const float* sc = p.scores + s * p.sc_rs + g * p.sc_hs;
   const int32_t* kp = p.key_pos + s * p.kp_rs + g * p.kp_hs;
   float* so = p.scores_out + s * p.so_rs + g * p.so_hs;
   int32_t* po = p.pos_out + s * p.po_rs + g * p.po_hs;
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.y) * kThreadsM + threadIdx.x; u0 < all;
-       u0 += kUnits * stride) {
-    int src[kUnits], dst[kUnits], x[kUnits], ps[kUnits], pd[kUnits];
-    uint4 v[kUnits];
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int64_t u = u0 + i * stride;
-      x[i] = -1;
-      if (u < all) {
-        const int m = static_cast<int>((u >> 32) == 0 ? static_cast<uint32_t>(u) / per : u / per);
-        x[i] = static_cast<int>(u - static_cast<int64_t>(m) * per);
-        src[i] = movers[m];
-        dst[i] = holes[m];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      if (x[i] >= 0 && x[i] < 2 * units) {
-        ps[i] = __ldg(row + (src[i] >> p.page_log2));
-        pd[i] = __ldg(row + (dst[i] >> p.page_log2));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      if (x[i] < 0) continue;
-      if (x[i] == 2 * units) {
-        v[i].x = __float_as_uint(sc[src[i]]);
-        v[i].y = kp[src[i]];
-      } else if (static_cast<unsigned>(ps[i]) >= static_cast<unsigned>(p.num_pages) ||
-                 static_cast<unsigned>(pd[i]) >= static_cast<unsigned>(p.num_pages)) {
+  const uint16_t* kb = static_cast<const uint16_t*>(p.k.base) + g * p.k.head;
+  const uint16_t* vb = static_cast<const uint16_t*>(p.v.base) + g * p.v.head;
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.y * (kThreadsM / 32);
+  // kMoves rows a warp at a time: lanes 0 .. kMoves-1 look them up, then all
+  // lanes copy, the units of every row on their way before the first is stored
+  for (int64_t m0 = (static_cast<int64_t>(blockIdx.y) * (kThreadsM / 32) + (threadIdx.x >> 5)) * kMoves;
+       m0 < count; m0 += static_cast<int64_t>(warps) * kMoves) {
+    int ps = -1, pd = -1, src = 0, dst = 0;
+    if (lane < kMoves && m0 + lane < count) {
+      src = movers[m0 + lane];
+      dst = holes[m0 + lane];
+      ps = __ldg(row + (src >> p.page_log2));
+      pd = __ldg(row + (dst >> p.page_log2));
+      so[dst] = sc[src];
+      po[dst] = kp[src];
+      if (static_cast<unsigned>(ps) >= static_cast<unsigned>(p.num_pages) ||
+          static_cast<unsigned>(pd) >= static_cast<unsigned>(p.num_pages)) {
         report(p.status, ATTN_DEV_BAD_CACHE);
-        x[i] = -1;
-      } else {
-        const Pages& pg = x[i] < units ? p.k : p.v;
-        v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pg.base) + ps[i] * pg.page +
-                                               (src[i] & (p.page_size - 1)) * pg.slot + g * pg.head +
-                                               (x[i] < units ? x[i] : x[i] - units) * 8);
+        ps = -1;
       }
+      src &= p.page_size - 1;
+      dst &= p.page_size - 1;
     }
+    for (int u = lane; u - lane < 2 * units; u += 32) {
+      const bool k = u < units;
+      const Pages& pg = k ? p.k : p.v;
+      const uint16_t* base = (k ? kb : vb) + (k ? u : u - units) * 8;
+      uint4 v[kMoves];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      if (x[i] < 0) continue;
-      if (x[i] == 2 * units) {
-        so[dst[i]] = __uint_as_float(v[i].x);
-        po[dst[i]] = v[i].y;
-      } else {
-        const Pages& pg = x[i] < units ? p.k : p.v;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(pg.base)) + pd[i] * pg.page +
-                                  (dst[i] & (p.page_size - 1)) * pg.slot + g * pg.head +
-                                  (x[i] < units ? x[i] : x[i] - units) * 8) = v[i];
+      for (int i = 0; i < kMoves; ++i) {
+        const int page = __shfl_sync(0xffffffffu, ps, i), at = __shfl_sync(0xffffffffu, src, i);
+        if (page >= 0 && u < 2 * units)
+          v[i] = *reinterpret_cast<const uint4*>(base + page * pg.page + at * pg.slot);
+      }
+#pragma unroll
+      for (int i = 0; i < kMoves; ++i) {
+        const int ok = __shfl_sync(0xffffffffu, ps, i), page = __shfl_sync(0xffffffffu, pd, i);
+        const int at = __shfl_sync(0xffffffffu, dst, i);
+        if (ok >= 0 && u < 2 * units)
+          *reinterpret_cast<uint4*>(const_cast<uint16_t*>(base) + page * pg.page + at * pg.slot) = v[i];
       }
     }
   }
@@ -362,8 +353,8 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
   select_kernel<<<p.S * p.Hkv, kThreadsE, smem, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t units = evict_ws(p.S, p.Hkv, slots, p.budget).list_cap * (2 * (p.d / 8) + 1);
-  int64_t x = (units + kThreadsM * kUnits - 1) / (kThreadsM * kUnits);
+  constexpr int kPerBlock = kThreadsM / 32 * kMoves;
+  int64_t x = (evict_ws(p.S, p.Hkv, slots, p.budget).list_cap + kPerBlock - 1) / kPerBlock;
   const int64_t most = 152 * 32 / (p.S * p.Hkv) + 1;
   x = x < 1 ? 1 : (x > most ? most : x);
   cudaLaunchConfig_t cfg = {};
