@@ -13,15 +13,15 @@
 // found digit by digit (8-bit histograms in shared memory, eight copies because
 // scores crowd into few exponents; the ranks of the first kSmemKeys slots stay
 // there; as soon as a digit's keys are wanted all, the rest is left out), then
-// two counting passes over contiguous slot ranges per warp number the ties, the
-// holes and the movers in slot order: no atomics decide an order, so results
+// counting passes over contiguous slot ranges per warp number the ties (only if
+// some of them go), the holes and the movers in slot order: no atomics decide an order, so results
 // are repeatable.  Latencies bound it: loads go out four at a time.
 // move_kernel: the listed K and V rows with their scores and positions, over
 // the whole GPU: a row is found through three dependent scattered reads (list,
 // page table, row), so a warp takes four rows through each of them together
-// (both kernels, 12 prompts of up to 20000 keys, 91 MB: 45 us; with a thread per
-// 16-byte unit, two in flight, 55.  Eight rows: 45, and the call for one key
-// goes from 8.6 to 10.6).
+// (both kernels, 12 prompts of up to 20000 keys, 91 MB: 41 us; with a thread per
+// 16-byte unit, two in flight, 10 more.  Eight rows: the same, and the call for
+// one key goes from 8.6 to 10.6).
 #include "../../include/attn_varlen.h"
 #include "cache.cuh"
 
@@ -236,15 +236,27 @@ __global__ void __launch_bounds__(kThreadsE)
     for (int i = 0; i < warp; ++i) t += c[i];
     return t;
   };
-  int c0 = 0;
-  for (int j = j0 + lane; j - lane < j1; j += 32)
-    c0 += __popc(__ballot_sync(0xffffffffu, j < j1 && key(j) == prefix));
-  if (lane == 0) cnt[0][warp] = c0;
-  __syncthreads();
-  const int eq0 = total_before(cnt[0]);
+  const bool ties = need != INT32_MAX;  // some of the keys equal to prefix go
+  int eq0 = 0;
+  if (ties) {
+    int c0 = 0;
+    for (int j = j0 + lane; j - lane < j1; j += 32)
+      c0 += __popc(__ballot_sync(0xffffffffu, j < j1 && key(j) == prefix));
+    if (lane == 0) cnt[0][warp] = c0;
+    __syncthreads();
+    eq0 = total_before(cnt[0]);
+  }
   const uint32_t below = (1u << lane) - 1u;
   // f(slot, kept) for this warp's slots in order, whole warps at a time
   auto walk = [&](auto f) {
+    if (!ties) {
+#pragma unroll 4
+      for (int j = j0 + lane; j - lane < j1; j += 32) {
+        const bool in = j < j1;
+        f(j, in, in && key(j) >= prefix);
+      }
+      return;
+    }
     int eq = eq0;
     for (int j = j0 + lane; j - lane < j1; j += 32) {
       const bool in = j < j1;
