@@ -30,6 +30,35 @@ bool strided_ok(std::initializer_list<Strided> ts) {
   return true;
 }
 
+// Whether the rows of `row` elements that a call writes share none (an expanded
+// or overlapping output would hold whatever was written last).  Axes of one
+// may have any stride.
+struct Axis {
+  int64_t n, stride;
+};
+bool distinct(int64_t row, std::initializer_list<Axis> axes) {
+  Axis a[3];
+  int k = 0;
+  for (const Axis& x : axes) {  // in order of the strides
+    if (x.n <= 1) continue;
+    int i = k++;
+    for (; i > 0 && a[i - 1].stride > x.stride; --i) a[i] = a[i - 1];
+    a[i] = x;
+  }
+  __int128 extent = row;
+  for (int i = 0; i < k; ++i) {
+    if (a[i].stride < extent) return false;
+    extent += static_cast<__int128>(a[i].n - 1) * a[i].stride;
+  }
+  return true;
+}
+// In place means the same elements.
+bool in_place_ok(const void* in, const void* out, const Axis& in0, const Axis& in1, int64_t out0,
+                 int64_t out1) {
+  return in != out ||
+         ((in0.n <= 1 || in0.stride == out0) && (in1.n <= 1 || in1.stride == out1));
+}
+
 bool dim_ok(int d) { return d == 160 || d == 128 || d == 64; }
 bool page_ok(int ps) { return ps >= 16 && ps <= 1024 && (ps & (ps - 1)) == 0; }
 int log2_of(int x) {
@@ -140,6 +169,11 @@ extern "C" attn_status attn_varlen_rotary(
   if (!strided_ok({{q, {q_ts, q_hs}}, {q_out, {qo_ts, qo_hs}}})) return ATTN_ERR_ALIGNMENT;
   if (Hkv > 0 && !strided_ok({{k, {k_ts, k_hs}}, {k_out, {ko_ts, ko_hs}}}))
     return ATTN_ERR_ALIGNMENT;
+  if (!distinct(head_dim, {{total, qo_ts}, {Hq, qo_hs}}) ||
+      (Hkv > 0 && !distinct(head_dim, {{total, ko_ts}, {Hkv, ko_hs}})) ||
+      !in_place_ok(q, q_out, {total, q_ts}, {Hq, q_hs}, qo_ts, qo_hs) ||
+      !in_place_ok(k, k_out, {Hkv > 0 ? total : 0, k_ts}, {Hkv, k_hs}, ko_ts, ko_hs))
+    return ATTN_ERR_INVALID;
   RotaryParams p;
   std::memset(&p, 0, sizeof p);
   p.dtype = dtype;
@@ -176,6 +210,12 @@ extern "C" attn_status attn_varlen_cache_append(
   if (!strided_ok({{k_cache, {kc_ps, kc_ss, kc_hs}}, {v_cache, {vc_ps, vc_ss, vc_hs}}}))
     return ATTN_ERR_ALIGNMENT;
   if (total > 0 && !strided_ok({{k, {k_ts, k_hs}}, {v, {v_ts, v_hs}}})) return ATTN_ERR_ALIGNMENT;
+  const int64_t slots = static_cast<int64_t>(table_width) * page_size;
+  if (!distinct(head_dim, {{num_pages, kc_ps}, {page_size, kc_ss}, {Hkv, kc_hs}}) ||
+      !distinct(head_dim, {{num_pages, vc_ps}, {page_size, vc_ss}, {Hkv, vc_hs}}) ||
+      (key_pos && !distinct(slots, {{B, kp_rs}, {Hkv, kp_hs}})) ||
+      (scores && !distinct(slots, {{B, sc_rs}, {Hkv, sc_hs}})))
+    return ATTN_ERR_INVALID;
   AppendParams p;
   std::memset(&p, 0, sizeof p);
   p.dtype = dtype;
@@ -240,6 +280,7 @@ extern "C" attn_status attn_varlen_cache_fwd(
   if (st != ATTN_OK || total_q == 0) return st;
   if (!out) return ATTN_ERR_INVALID;
   if (!strided_ok({{out, {out_ts, out_hs}}})) return ATTN_ERR_ALIGNMENT;
+  if (!distinct(head_dim, {{total_q, out_ts}, {Hq, out_hs}})) return ATTN_ERR_INVALID;
   if (!workspace_ok(workspace, workspace_bytes, fwd_workspace(B, P, Hq, Hkv, head_dim, total_q)))
     return ATTN_ERR_WORKSPACE;
   p.out = out;
@@ -274,7 +315,15 @@ extern "C" attn_status attn_varlen_cache_weights(
       cu_prefix, cu_q, q_pos, alibi_slopes, slopes_bs, causal, window_left, window_right, softcap,
       scale_multiplier, const_cast<float*>(lse), device_status);
   if (st != ATTN_OK || B == 0) return st;
-  if (!scores_out) return ATTN_ERR_INVALID;
+  const int64_t slots = static_cast<int64_t>(table_width) * page_size;
+  const int64_t prefix_slots = static_cast<int64_t>(prefix_width) * page_size;
+  if (!scores_out || !distinct(slots, {{B, so_rs}, {Hkv, so_hs}}) ||
+      !in_place_ok(scores_in, scores_out, {B, si_rs}, {Hkv, si_hs}, so_rs, so_hs))
+    return ATTN_ERR_INVALID;
+  if (P > 0 && prefix_scores_out &&
+      (!distinct(prefix_slots, {{P, pso_rs}, {Hkv, pso_hs}}) ||
+       !in_place_ok(prefix_scores_in, prefix_scores_out, {P, psi_rs}, {Hkv, psi_hs}, pso_rs, pso_hs)))
+    return ATTN_ERR_INVALID;
   p.w_in[1] = scores_in;
   p.wi_rs[1] = si_rs;
   p.wi_hs[1] = si_hs;
@@ -321,12 +370,16 @@ extern "C" attn_status attn_varlen_cache_evict(
   if (!k_cache || !v_cache || !scores || !key_pos || !next_pos || !scores_out || !key_pos_out ||
       !lens_out)
     return ATTN_ERR_INVALID;
-  // in place means the same elements
   if ((scores_out == scores && (so_rs != sc_rs || so_hs != sc_hs)) ||
       (key_pos_out == key_pos && (po_rs != kp_rs || po_hs != kp_hs)))
     return ATTN_ERR_INVALID;
   if (!strided_ok({{k_cache, {kc_ps, kc_ss, kc_hs}}, {v_cache, {vc_ps, vc_ss, vc_hs}}}))
     return ATTN_ERR_ALIGNMENT;
+  if (!distinct(head_dim, {{num_pages, kc_ps}, {page_size, kc_ss}, {Hkv, kc_hs}}) ||
+      !distinct(head_dim, {{num_pages, vc_ps}, {page_size, vc_ss}, {Hkv, vc_hs}}) ||
+      !distinct(slots, {{S, so_rs}, {Hkv, so_hs}}) ||
+      !distinct(slots, {{S, po_rs}, {Hkv, po_hs}}))
+    return ATTN_ERR_INVALID;
   if (!workspace_ok(workspace, workspace_bytes, evict_workspace(S, Hkv, slots, budget)))
     return ATTN_ERR_WORKSPACE;
   EvictParams p;

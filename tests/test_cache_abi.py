@@ -162,6 +162,32 @@ def test_evict_refusals(lib):
     assert evict(lib, S=0) == 0
 
 
+def test_outputs_with_shared_elements_are_refused(lib):
+    """An expanded or overlapping output would keep whichever row came last."""
+    # rotary (its last check is not reached): heads over one another, a token's rows reaching into the next, in place with other strides
+    ok = dict(qo=0x40000, ko=0x80000, kots=160, kohs=160)
+    assert rotary(lib, **ok, qots=1280, qohs=152) == -1 and rotary(lib, **ok, qots=1272) == -1
+    assert rotary(lib, qo=0x40000, ko=0x80000, kots=152) == -1
+    assert rotary(lib, qo=FAKE, qots=2560) == -1 and rotary(lib, qo=0x40000, kots=320) == -1
+    # key positions or scores of several heads in one row, as of an expanded tensor
+    two = dict(Hkv=2, kcss=320, kcps=16 * 320, vcss=320, vcps=16 * 320)
+    assert append(lib, **two, kp=FAKE, kprs=32, kphs=0) == -1
+    assert append(lib, **two, sc=FAKE, scrs=32, schs=32) == -1
+    assert append(lib, **two, sc=FAKE, scrs=0, schs=32) == -1
+    assert append(lib, Hkv=2) == -1                # a head's rows are the next slot's
+    assert evict(lib, **two, scrs=64, sors=64, kprs=32, kphs=0, pors=32, pohs=0) == -1
+    assert evict(lib, **two, scrs=64, sors=64, kprs=64, pors=64) == -4
+    assert evict(lib, **two, scrs=32, schs=64, sors=32, sohs=64, kprs=64, pors=64) == -4   # [Hkv, S, slots]
+    assert evict(lib, Hkv=2, scrs=64, sors=64, kprs=64, pors=64) == -1
+    # key positions that are only read may be expanded
+    assert evict(lib, **two, scrs=64, sors=64, kprs=32, kphs=0, po=0x30000, pors=64) == -4
+    assert fwd(lib, ohs=152) == -1 and fwd(lib, ots=2552) == -1 and fwd(lib, ots=160, ohs=480) == -4
+    assert weights(lib, Hkv=2, sors=32, sohs=0) == -1 and weights(lib, Hkv=2, sors=64) == -4
+    assert weights(lib, si=FAKE, sirs=64) == -1 and weights(lib, si=0x30000, sirs=64) == -4
+    prefix = dict(P=2, pt=FAKE, prs=1, pw=1, pl=FAKE, cup=FAKE, pso=FAKE, Hkv=2, sors=64)
+    assert weights(lib, **prefix, psors=16, psohs=0) == -1 and weights(lib, **prefix, psors=32, psohs=16) == -4
+
+
 def test_workspace_sizes(lib):
     f = lib.attn_varlen_cache_fwd_workspace_size
     f.argtypes, f.restype = [I, I, I, I, I, L], Z

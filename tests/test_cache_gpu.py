@@ -726,3 +726,25 @@ def test_empty_calls():
     C.attention_varlen_cache_append(none[:, :2], none[:, :2], kc.k, kc.v, kc.table, kc.lens, i32([0, 0, 0]), lens_out=lo)
     assert lo.tolist() == [20, 9]
     assert torch.isfinite(kc.k[kc.table[0, 0].long()]).all()
+
+
+def test_expanded_outputs_are_refused():
+    """One row of positions or scores for all heads may be read, not written."""
+    kc = ref.Cache([40, 20], page=16, Hkv=2, d=64, dtype=HF)
+    n, nxt = kc.table.shape[1] * 16, i32([40, 20])
+    sc = torch.rand(2, 2, n, device="cuda")
+    kp = torch.arange(n, dtype=torch.int32, device="cuda").expand(2, 2, n)
+    with pytest.raises(C.AttnError):
+        C.attention_varlen_cache_evict(kc.k, kc.v, kc.table, kc.lens, sc, kp, nxt, 8)
+    po, lo = torch.empty(2, 2, n, dtype=torch.int32, device="cuda"), torch.empty_like(kc.lens)
+    C.attention_varlen_cache_evict(kc.k, kc.v, kc.table, kc.lens, sc, kp, nxt, 8, key_pos_out=po, lens_out=lo)
+    assert lo.tolist() == [8, 8]
+    q, cu = normal(3, 2, 8, 64, dtype=HF), i32([0, 1, 2])
+    out = torch.empty(1, 8, 64, dtype=HF, device="cuda").expand(2, 8, 64)
+    with pytest.raises(C.AttnError):
+        C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, lo, cu, out=out)
+    lse = C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, lo, cu)[1]
+    with pytest.raises(C.AttnError):
+        C.attention_varlen_cache_weights(q, kc.k, kc.table, lo, cu, lse, sc[:, :1].expand(2, 2, n))
+    with pytest.raises(C.AttnError):
+        C.attention_varlen_rotary(q, None, nxt, torch.ones(32, dtype=torch.float64, device="cuda"), q_out=out)
