@@ -24,9 +24,11 @@ constexpr int kWarpsJ = 4;
 constexpr int kHeadsJ = 8;  // rows (heads of a token) of a block
 
 // Joins the partial results of a row.  Its own slots were computed in one
-// part or several, and so was its prefix; part i has reference m_i, sum l_i and
-// O_i, and with weights 2^(m_i - max m) the row is sum O_i / sum l_i.  Parts are added in the order of the keys, prefix last, so the result
-// does not depend on which CTA finished first.  Rows that one part covers were
+// part or several, and so was its prefix; part i has reference m_i, sums l_i (of
+// its weights) and lr_i (of the rounded ones) and O_i, and with factors
+// 2^(m_i - max m) the row is sum O_i / sum lr_i, its lse from sum l_i.  Parts are
+// added in the order of the keys, prefix last, so the result does not depend on
+// which CTA finished first.  Rows that one part covers were
 // written by the tile kernel already; rows without any key are written here.
 // Eight heads of a token per block, eight lanes to the 128-byte line that holds
 // four features of each, the features over four lanes and four warps.  A chain
@@ -48,7 +50,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   }
   const int g = h / p.R, hr = h - g * p.R;
   const int2* meta = reinterpret_cast<const int2*>(p.ws + w.meta);
-  const float2* stats = reinterpret_cast<const float2*>(p.ws + w.stats);
+  const float4* stats = reinterpret_cast<const float4*>(p.ws + w.stats);
   const float4* part = reinterpret_cast<const float4*>(p.ws + w.rows);
   const int64_t row = static_cast<int64_t>(tok) * p.Hq + h;
   // The row's sequence; with one token each it is the token's own number, so
@@ -108,14 +110,14 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   };
   // Four parts at a time, all their loads first; the reference follows the
   // largest met so far.
-  float top = -INFINITY, l = 0.f;
+  float top = -INFINITY, l = 0.f, lr = 0.f;
   float4 acc[kPer] = {};
   for (int i0 = 0; i0 < parts; i0 += 4) {
-    float2 s[4];
+    float4 s[4];
     float4 v[4][kPer];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s[i] = make_float2(-INFINITY, 0.f);
+      s[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
       if (i0 + i < parts) {
         const int64_t pr = row_of(i0 + i);
         s[i] = stats[pr];
@@ -132,6 +134,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
       const float a = ex2_approx(top - up);
       top = up;
       l *= a;
+      lr *= a;
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
         acc[k] = make_float4(acc[k].x * a, acc[k].y * a, acc[k].z * a, acc[k].w * a);
@@ -141,6 +144,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
       if (!(s[i].y > 0.f)) continue;  // (a part without any weight may hold anything)
       const float a = ex2_approx(s[i].x - top);
       l = fmaf(a, s[i].y, l);
+      lr = fmaf(a, s[i].z, lr);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         acc[k].x = fmaf(a, v[i][k].x, acc[k].x);
@@ -150,7 +154,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = lr > 0.f ? 1.f / lr : 0.f;
   uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(tok) * p.out_ts +
                   static_cast<int64_t>(h) * p.out_hs;
 #pragma unroll

@@ -8,12 +8,10 @@
 //   P = 2^(z - m)        softmax warps, one TMEM lane per row; the 16-bit pairs
 //                        overwrite S, whose buffer is free again after P V
 //   O += P V             tcgen05.mma with P from TMEM
-// and l = sum of P in fp32 in the softmax warps, which gives lse and divides O.
-// (O holds the rounded P: dividing by the sum of those as well makes a single
-// key give exactly its V row, but as two more instructions per element it took
-// 8 % of a capped call, and as a product with a tile of ones it doubled the
-// time of P V.  Roundings of many keys average out; a single key's moves the
-// result by at most half a step of the type.)
+// and two row sums in fp32 in the softmax warps: l of P, which gives lse, and lr
+// of the rounded P that multiplies V, which divides O, so that out is a weighted
+// mean of V rows whatever the roundings: equal rows come out exactly.  (As a
+// product with a tile of ones, lr doubled the time of P V.)
 //
 // Single-token calls read every K and V row once for R <= 128 rows of a group,
 // so the copies bound them; calls with many rows behind a shared prefix are
@@ -57,7 +55,7 @@ inline FwdWs fwd_ws(int B, int P, int Hq, int Hkv, int d, int64_t total_q) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.meta = 256;
   w.stats = w.meta + up(static_cast<size_t>(all) * sizeof(int2));
-  w.rows = w.stats + up(static_cast<size_t>(rows) * sizeof(float2));
+  w.rows = w.stats + up(static_cast<size_t>(rows) * sizeof(float4));
   w.total = w.rows + up(static_cast<size_t>(rows) * d * sizeof(float));
   (void)B;
   return w;
@@ -125,8 +123,8 @@ struct FwdShape {
   static constexpr uint32_t kOffK = kQ;
   static constexpr uint32_t kOffV = kOffK + kKS * kQ;
   static constexpr uint32_t kOffMax = kOffV + kVS * kV;          // [2 steps][2 halves][128]
-  static constexpr uint32_t kOffSum = kOffMax + 2 * 2 * 128 * 4;  // [2 pieces][2 halves][128] l
-  static constexpr uint32_t kOffBar = kOffSum + 2 * 2 * 128 * 4;
+  static constexpr uint32_t kOffSum = kOffMax + 2 * 2 * 128 * 4;  // [2 pieces][2 halves][128] (l, lr)
+  static constexpr uint32_t kOffBar = kOffSum + 2 * 2 * 128 * 8;
 };
 
 struct FwdBars {
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
   uint8_t* sK = sm + S::kOffK;
   uint8_t* sV = sm + S::kOffV;
   float* sMax = reinterpret_cast<float*>(sm + S::kOffMax);
-  float* sSum = reinterpret_cast<float*>(sm + S::kOffSum);
+  float2* sSum = reinterpret_cast<float2*>(sm + S::kOffSum);
   FwdBars* bars = reinterpret_cast<FwdBars*>(sm + S::kOffBar);
   volatile int* s_abort = &bars->abort;
 
@@ -580,7 +578,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
       }
       // subtracted from the logits; with FIXED they come without their constant c
       float bref = FIXED ? m_run - out_scale : 0.f;
-      uint64_t l2 = f2_make(0.f, 0.f);
+      uint64_t l2 = f2_make(0.f, 0.f), lr2 = l2;  // of P, and of the rounded P
 
       for (int kt = pc.kt1 - 1; kt >= pc.kt0; --kt, ++step) {
         const int key0 = kt * kKeys + half * 64;
@@ -699,6 +697,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
               m_run = mx;
             }
             l2 = f2_mul(l2, f2_make(alpha, alpha));
+            lr2 = f2_mul(lr2, f2_make(alpha, alpha));
           }
         }
         // With FIXED, the first tile's maximum becomes the reference: the largest
@@ -745,6 +744,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
               const float e0 = ex2_approx(f2_lo(z)), e1 = ex2_approx(f2_hi(z));
               pk[i >> 1] = Pack<BF16>::two(e0, e1);
               l2 = f2_add(l2, f2_make(e0, e1));
+              lr2 = f2_add(lr2, Pack<BF16>::unpack(pk[i >> 1]));
             }
             tmem_st8(sb + c0 / 2, pk);
           }
@@ -774,23 +774,22 @@ __global__ void __launch_bounds__(kThreadsF, 1)
         if (lane == 0) mbar_arrive(&bars->p_full[step & 1]);
       }
       if (!ok) break;
-      // ---- the row's sum over both halves, then O
-      float l = f2_lo(l2) + f2_hi(l2);
-      float* sums = sSum + (tiles & 1) * 256;
-      sums[half * 128 + r] = l;
+      // ---- the row's sums over both halves, then O
+      float2* sums = sSum + (tiles & 1) * 256;
+      sums[half * 128 + r] = make_float2(f2_lo(l2) + f2_hi(l2), f2_lo(lr2) + f2_hi(lr2));
       if (!(ok = warp_exchange(&bars->l_x[quad], tiles & 1, s_abort))) break;
-      l = sums[r] + sums[128 + r];
+      const float l = sums[r].x + sums[128 + r].x, lr = sums[r].y + sums[128 + r].y;
       if (!(ok = mbar_wait_warp(&bars->o_full, tiles & 1, s_abort))) break;
       tc_fence_after();
       if (any) {
         constexpr int kC = HD / 2;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = lr > 0.f ? 1.f / lr : 0.f;
         int64_t pr = 0;
         if (pc.mode)
           pr = pc.mode == 1 ? cut_row(w, blockIdx.x, pc.first, r) : whole_row(w, p.total_q, p.Hq, pc.own, tok, h);
         if (valid && half == 0) {
           if (pc.mode)
-            reinterpret_cast<float2*>(p.ws + w.stats)[pr] = make_float2(m_run, l);
+            reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(m_run, l, lr, 0.f);
           else
             p.lse[static_cast<int64_t>(tok) * p.Hq + h] = l > 0.f ? (m_run + log2f(l)) * kLn2 : -INFINITY;
         }
