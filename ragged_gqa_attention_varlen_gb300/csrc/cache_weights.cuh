@@ -423,7 +423,13 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     // ------------------------------------------------------------ Q rows
     // A Q tile that stays is fetched by the four warps together; of several that
     // stream by, each warp fetches every fourth, so that as many are on their
-    // way as there are stages (one after the other, each took 3000 clk).
+    // way as there are stages (one after the other, each took 3000 clk).  A
+    // parity wait tells a phase only from the ones next to it, and with two or
+    // three places for four warps a place changes hands more often than a warp
+    // has a tile of its own.  So every warp waits for the place of every tile, in
+    // order, and arrives for every tile, its own or not: no product starts
+    // before all four have seen its place free, so none is ever a phase behind
+    // or ahead.
     uint32_t nt = 0, qs = 0, qph = 0, loaded = 0;
     const int wi = warp - 12;
     WPiece pc;
@@ -433,12 +439,12 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       const bool many = pc.t1 - pc.t0 > 1;
       const int first = many ? 0 : wi, each = many ? 1 : 4;  // this warp's runs of 32 rows
       for (int t = pc.t0; t < pc.t1; ++t) {
+        if (loaded >= S::kQS && !(ok = mbar_wait_warp(&bars->q_empty[qs], qph ^ 1, s_abort))) break;
         if (!many || static_cast<int>(loaded & 3) == wi) {
           const uint32_t x0 = static_cast<uint32_t>(t) * kRows;
           const int i0 = static_cast<int>(x0 / static_cast<uint32_t>(p.R));
           const int h0 = static_cast<int>(x0) - i0 * p.R;
           const int n = min(kRows, pc.rows - static_cast<int>(x0));
-          if (loaded >= S::kQS && !(ok = mbar_wait_warp(&bars->q_empty[qs], qph ^ 1, s_abort))) break;
           uint8_t* dst = sQ + qs * S::kT;
           copy_q_rows<HD>(p, dst, pc.g, pc.tok0 + i0, h0, n, many ? 0 : wi, many ? 1 : 4);
           // the rows' scalars: all loads first
@@ -473,6 +479,11 @@ __global__ void __launch_bounds__(kThreadsW, 1)
               }
             }
           }
+          // The scalars' place, once the sums have read those of kIS tiles before.  A
+          // warp may pass over places here: the product kQS tiles before is done,
+          // which needed the step four before it summed, and the groups take steps
+          // in turn, so both have read all tiles up to kQS + 6 before.
+          static_assert(2 * S::kIS >= S::kQS + 6, "a wait for row scalars could be a phase behind");
           const int is = loaded & (S::kIS - 1);
           if (loaded >= S::kIS &&
               !(ok = mbar_wait_warp(&bars->info_read[is], ((loaded / S::kIS) & 1) ^ 1, s_abort)))
@@ -506,8 +517,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_n(&bars->q_full[qs], many ? 4 : 1);
         }
+        if (lane == 0) mbar_arrive(&bars->q_full[qs]);
         ++loaded;
         if (++qs == S::kQS) {
           qs = 0;

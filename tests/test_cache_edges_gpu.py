@@ -47,3 +47,55 @@ def test_equal_values_come_out_exactly(lens, plens, counts, Hq, Hkv, d, page, dt
     out, _ = C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, kc.lens, i32(ref.cu(counts)), softcap=cap, **call)
     want = row.repeat_interleave(Hq // Hkv, 0).expand_as(out)
     assert torch.equal(out, want), (out != want).float().mean()
+
+
+# ---------------------------------------------------------------- key weights of many Q tiles
+
+# Q tiles that a CTA streams, at least 12 of them, so that they go round the ring several times
+STREAMS = [
+    dict(lens=[700], counts=[600], Hq=96, Hkv=1, d=160, dtype=BF, cap=3.0, causal=False),
+    dict(lens=[1000], counts=[800], Hq=96, Hkv=1, d=160, dtype=HF, cap=0.0, causal=True, alibi=True),
+    dict(lens=[400] * 16, counts=[40] * 16, Hq=96, Hkv=1, d=160, dtype=BF, cap=3.0, causal=True, alibi=True),
+    dict(lens=[20] * 64, counts=[1] * 64, plens=[5000], Hq=96, Hkv=1, d=160, dtype=BF, cap=3.0, causal=True),
+    dict(lens=[30, 900, 5, 300], counts=[1, 500, 1, 300], plens=[300], Hq=48, Hkv=1, d=160, dtype=HF, cap=30.0, causal=False),
+    dict(lens=[1500], counts=[1500], Hq=32, Hkv=8, d=128, dtype=HF, cap=0.0, causal=True),
+    dict(lens=[900, 2, 1300], counts=[900, 1, 1300], plens=[], Hq=32, Hkv=4, d=128, dtype=BF, cap=3.0, causal=True,
+         alibi=True),
+    dict(lens=[64] * 128, counts=[1] * 128, plens=[4000], Hq=64, Hkv=2, d=128, dtype=HF, cap=0.0, causal=False),
+    dict(lens=[1200], counts=[1200], Hq=32, Hkv=4, d=64, dtype=HF, cap=3.0, causal=True, alibi=True)]
+
+
+@pytest.mark.parametrize("c", STREAMS, ids=lambda c: f"d{c['d']}-{c['Hq']}-{len(c['lens'])}-{max(c['counts'])}-{c['cap']:g}")
+def test_key_weights_of_many_tiles(c):
+    plens, d, Hq, Hkv, dt = c.get("plens", []), c["d"], c["Hq"], c["Hkv"], c["dtype"]
+    B, T = len(c["lens"]), sum(c["counts"])
+    kc = ref.Cache(c["lens"], plens, Hkv, d, 64, dt)
+    q = normal(3, T, Hq, d, dtype=dt, std=2.0)
+    opt = dict(causal=c["causal"], cap=c["cap"], group=[0] * B if plens else None)
+    call = dict(causal=c["causal"], softcap=c["cap"])
+    if c.get("alibi"):
+        opt["slopes"] = torch.rand(B, Hq, generator=torch.Generator().manual_seed(2)) * 0.05
+        call["alibi_slopes"] = opt["slopes"].cuda()
+    pre0 = None
+    if plens:
+        call.update(prefix_table=kc.ptable, prefix_lens=kc.plens, cu_prefix=i32([0, B]))
+        pre0 = torch.zeros(1, Hkv, kc.ptable.shape[1] * 64, device="cuda")
+    st, cu_q = status(), i32(ref.cu(c["counts"]))
+    _, lse = C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, kc.lens, cu_q, status=st, **call)
+
+    def weights():
+        own, pre = C.attention_varlen_cache_weights(q, kc.k, kc.table, kc.lens, cu_q, lse, status=st,
+                                                    prefix_scores=None if pre0 is None else pre0.clone(), **call)
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        return own, pre
+
+    own, pre = weights()
+    want, pwant, tol, ptol = ref.weights(q, kc, c["counts"], lse, **opt)
+    for b, n in enumerate(c["lens"]):
+        within(f"own {b}", own[b, :, :n], want[b], tol[b] + want[b] * 2.0 ** -22)
+    for b, n in enumerate(plens):
+        within(f"prefix {b}", pre[b, :, :n], pwant[b], ptol[b] + pwant[b] * 2.0 ** -22)
+    for _ in range(3):
+        again, pagain = weights()
+        assert torch.equal(again, own) and (pre is None or torch.equal(pagain, pre))
