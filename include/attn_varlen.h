@@ -633,7 +633,11 @@ attn_status attn_varlen_rotary(
  * every K/V head, positions[0][token] or, without positions, the slot number;
  * scores (may be NULL; fp32, laid out like key_pos) receives 0.  lens_out (may
  * be NULL, not `lens` itself) receives lens[b] plus the number of new tokens.
- * The other slots are not touched.  No two rows of the table may share a page
+ * A sequence whose length is negative or whose tokens do not all fit its table
+ * takes none of them and keeps its length (ATTN_DEV_BAD_CACHE); a token whose
+ * page is out of the pool is left out alone.  With an inconsistent cu_new
+ * (ATTN_DEV_BAD_CU) nothing is appended and every length is kept.  The other
+ * slots are not touched.  No two rows of the table may share a page
  * that is written here. */
 attn_status attn_varlen_cache_append(
     attn_dtype dtype, int B, int Hkv, int head_dim, int64_t total,

@@ -92,7 +92,9 @@ def attention_varlen_cache_append(k, v, k_cache, v_cache, table, lens, cu_new, p
     in the table already).  With ``inv_freq`` the K rows are turned on the way
     (see attention_varlen_rotary).  ``key_pos`` ``[B, Hkv, slots]`` receives the
     tokens' ``positions[0]`` (or slot numbers), ``scores`` zeros, ``lens_out``
-    the new lengths (not ``lens`` itself)."""
+    the new lengths (not ``lens`` itself).  A sequence whose tokens do not all fit
+    its table takes none and keeps its length; with an inconsistent ``cu_new``
+    nothing is appended."""
     _run("append", stream, k, (k, v, k_cache, v_cache, table, lens, cu_new, positions, inv_freq, pair_axis,
                                interleaved, key_pos, scores, lens_out, status))
 

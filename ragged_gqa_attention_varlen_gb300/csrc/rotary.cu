@@ -32,6 +32,7 @@ constexpr int kThreadsR = 256;
 constexpr int kItemsR = 4096;   // 16-byte units (pairs of them for halves) a block turns, at most
 constexpr int kItemsA = 2048;   // ... and appends
 constexpr int kMaxTokensR = 32;
+static_assert(kMaxTokensR <= kThreadsR, "a thread looks one token up");
 constexpr int kMaxPairs = kHeadDim / 2;
 
 // Fraction of a turn per position, as a 64-bit binary fraction.
@@ -233,9 +234,19 @@ __global__ void __launch_bounds__(kThreadsR)
   }
 }
 
+// The slots that sequence b's tokens take start here, or -1 when its length is
+// negative or they do not all fit its table: none of them is taken then.
+__device__ __forceinline__ int append_at(const AppendParams& p, int b, int n) {
+  const int len = __ldg(p.lens + b);
+  const int64_t slots = static_cast<int64_t>(p.width) << p.page_log2;
+  return len >= 0 && static_cast<int64_t>(len) + n <= slots ? len : -1;
+}
+
 // New tokens into their pages: K rows turned (when the call has rotary
-// positions), V rows copied.  A token whose slot has no valid page is skipped
-// and reported.
+// positions), V rows copied.  Every block checks the whole of cu_new (along
+// with its lookups): a call whose runs of tokens contradict one another writes
+// nothing.  A sequence that does not fit its table is left out, and so is a token
+// whose page is out of the pool.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreadsR)
     append_kernel(const __grid_constant__ AppendParams p, int ntok) {
@@ -243,34 +254,33 @@ __global__ void __launch_bounds__(kThreadsR)
   __shared__ int64_t row_k[kMaxTokensR], row_v[kMaxTokensR];  // first element, or -1
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * ntok;
   ntok = static_cast<int>(min(static_cast<int64_t>(ntok), p.T - tok0));
-  if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b < p.B; b += kThreadsR) {
-      const int c0 = __ldg(p.cu_new + b), c1 = __ldg(p.cu_new + b + 1);
-      if (c0 < 0 || c1 < c0 || c1 > p.T || (b == 0 && c0 != 0)) report(p.status, ATTN_DEV_BAD_CU);
-      if (p.lens_out) p.lens_out[b] = __ldg(p.lens + b) + c1 - c0;
-    }
+  int bad = 0;
+  for (int b = threadIdx.x; b < p.B; b += kThreadsR) {
+    const int c0 = __ldg(p.cu_new + b), c1 = __ldg(p.cu_new + b + 1);
+    bad |= c0 < 0 || c1 < c0 || c1 > p.T || (b == 0 && c0 != 0);
   }
-  for (int t = threadIdx.x; t < ntok; t += kThreadsR) {
-    const int tok = static_cast<int>(tok0) + t;
+  // kMaxTokensR <= kThreadsR: a token is one thread's
+  int seq = -1, slot = 0;  // of this thread's token, if it is taken
+  if (static_cast<int>(threadIdx.x) < ntok) {
+    const int t = threadIdx.x, tok = static_cast<int>(tok0) + t;
     int64_t rk = -1, rv = -1;
     if (tok < __ldg(p.cu_new + p.B)) {  // tokens behind the last sequence are left out
       const int b = seq_of(p.cu_new, 0, p.B, tok);
-      const int64_t slot = static_cast<int64_t>(__ldg(p.lens + b)) + tok - __ldg(p.cu_new + b);
+      const int c0 = __ldg(p.cu_new + b), c1 = __ldg(p.cu_new + b + 1);
       int page = -1;
-      if (slot >= 0 && (slot >> p.page_log2) < p.width)
+      // (cu_new may be anything still: only a token of its own run is looked up)
+      const int at = c0 >= 0 && c0 <= tok && tok < c1 ? append_at(p, b, c1 - c0) : -1;
+      if (at >= 0) {
+        slot = at + tok - c0;
         page = __ldg(p.table + b * p.table_rs + (slot >> p.page_log2));
+      }
       if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {
-        const int in = static_cast<int>(slot) & (p.page_size - 1);
+        const int in = slot & (p.page_size - 1);
         rk = page * p.k.page + in * p.k.slot;
         rv = page * p.v.page + in * p.v.slot;
-        for (int g = 0; g < p.Hkv; ++g) {
-          if (p.key_pos)
-            p.key_pos[b * p.kp_rs + g * p.kp_hs + slot] =
-                p.r.positions ? __ldg(p.r.positions + tok) : static_cast<int32_t>(slot);
-          if (p.scores) p.scores[b * p.sc_rs + g * p.sc_hs + slot] = 0.f;
-        }
+        seq = b;
       } else {
-        report(p.status, ATTN_DEV_BAD_CACHE);
+        seq = -2;
       }
     }
     row_k[t] = rk;
@@ -279,7 +289,27 @@ __global__ void __launch_bounds__(kThreadsR)
   // few tokens: the turns along with the lookups; many: after the V rows
   const bool early = p.r.inv_freq && ntok * p.r.pairs <= kThreadsR;
   if (early) fill_turns(p.r, tok0, ntok, turns);
-  __syncthreads();
+  bad = __syncthreads_or(bad);
+  if (blockIdx.x == 0) {
+    if (bad && threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_CU);
+    for (int b = threadIdx.x; b < p.B && (p.lens_out || !bad); b += kThreadsR) {
+      const int n = bad ? 0 : __ldg(p.cu_new + b + 1) - __ldg(p.cu_new + b);
+      const int at = append_at(p, b, n);
+      if (!bad && at < 0) report(p.status, ATTN_DEV_BAD_CACHE);
+      if (p.lens_out) p.lens_out[b] = at < 0 ? __ldg(p.lens + b) : at + n;
+    }
+  }
+  if (bad) return;
+  if (seq >= 0) {
+    const int tok = static_cast<int>(tok0) + threadIdx.x;
+    for (int g = 0; g < p.Hkv; ++g) {
+      if (p.key_pos)
+        p.key_pos[seq * p.kp_rs + g * p.kp_hs + slot] = p.r.positions ? __ldg(p.r.positions + tok) : slot;
+      if (p.scores) p.scores[seq * p.sc_rs + g * p.sc_hs + slot] = 0.f;
+    }
+  } else if (seq == -2) {
+    report(p.status, ATTN_DEV_BAD_CACHE);
+  }
   // V rows and K rows: each thread's loads of four (two) units go out together.
   // Of few tokens, the upper half of the threads takes V and the lower K.
   const int step = early ? kThreadsR / 2 : kThreadsR;

@@ -99,3 +99,42 @@ def test_key_weights_of_many_tiles(c):
     for _ in range(3):
         again, pagain = weights()
         assert torch.equal(again, own) and (pre is None or torch.equal(pagain, pre))
+
+
+# ---------------------------------------------------------------- append: metadata that does not fit
+
+@pytest.mark.parametrize("cu,lens,written", [
+    ([2, 3, 6], [20, 9], []),             # does not start at 0
+    ([0, 4, 2], [20, 9], []),             # decreases
+    ([0, -1, 6], [20, 9], []),
+    ([0, 3, 7], [20, 9], []),             # more tokens than there are
+    ([0, 3, 6], [-2, 9], [1]),            # a negative length: the other sequence's tokens are taken
+    ([0, 3, 6], [20, 10 ** 6], [0]),
+    ([0, 3, 6], [46, 9], [1]),            # two of three tokens would fit: none is taken
+    ([0, 3, 6], [20, 2 ** 31 - 1], [0])])
+@pytest.mark.parametrize("rot", [False, True])
+def test_append_leaves_out_what_does_not_fit(cu, lens, written, rot):
+    kc = ref.Cache([48, 48], page=16, extra_width=0, poison=False)
+    k0, v0 = kc.k.clone(), kc.v.clone()
+    k, v = normal(1, 6, 1, 160), normal(2, 6, 1, 160)
+    kp = torch.full((2, 1, 48), -5, dtype=torch.int32, device="cuda")
+    sc, out, st = torch.full((2, 1, 48), 3.0, device="cuda"), i32([-7, -7]), status()
+    kw = {}
+    if rot:
+        kw = dict(positions=i32([9] * 6), inv_freq=torch.zeros(80, dtype=torch.float64, device="cuda"))  # angle 0
+    C.attention_varlen_cache_append(k, v, kc.k, kc.v, kc.table, i32(lens), i32(cu), key_pos=kp, scores=sc, lens_out=out,
+                                    status=st, **kw)
+    torch.cuda.synchronize()
+    bad_cu = not written
+    assert int(st) == (1 if bad_cu else C.DEV_BAD_CACHE)
+    wl, wk, wv, wp, ws = list(lens), k0.clone(), v0.clone(), torch.full_like(kp, -5), torch.full_like(sc, 3.0)
+    for b in written:
+        n = cu[b + 1] - cu[b]
+        wl[b] += n
+        for i in range(n):
+            j = lens[b] + i
+            pg = int(kc.table[b, j // 16])
+            wk[pg, j % 16], wv[pg, j % 16] = k[cu[b] + i], v[cu[b] + i]
+            wp[b, :, j], ws[b, :, j] = 9 if rot else j, 0.0
+    assert out.tolist() == wl
+    assert torch.equal(kc.k, wk) and torch.equal(kc.v, wv) and torch.equal(kp, wp) and torch.equal(sc, ws)
