@@ -660,11 +660,11 @@ attn_status attn_varlen_cache_append(
  * inside [0, B]).  The queries of all sequences of a prefix are put together,
  * so its keys are read once.  With Lk = prefix length + own length, query i of
  * Lq stands at position Lk - Lq + i, or at q_pos[token] when q_pos is given
- * (required with key_pos).  Logits, softcap, ALiBi (fp32 slopes [B, Hq] times
- * the distance of the positions), masks (on the positions), out and lse are
- * those of attn_varlen_fwd (a slope batch stride of 0 gives every sequence the
- * same slopes); rows without an admissible key get out = 0, lse =
- * -inf.  lse is dense fp32 [total_q, Hq].  P = 0: no prefixes. */
+ * (required with key_pos when there are query tokens).  Logits, softcap, ALiBi
+ * (fp32 slopes [B, Hq] times the distance of the positions), masks (on the
+ * positions), out and lse are those of attn_varlen_fwd (a slope batch stride of
+ * 0 gives every sequence the same slopes); rows without an admissible key get
+ * out = 0, lse = -inf.  lse is dense fp32 [total_q, Hq].  P = 0: no prefixes. */
 size_t attn_varlen_cache_fwd_workspace_size(int B, int P, int Hq, int Hkv, int head_dim,
                                             int64_t total_q);
 attn_status attn_varlen_cache_fwd(

@@ -103,7 +103,7 @@ attn_status read_args(CacheParams& p, attn_dtype dtype, int B, int P, int Hq, in
   if (static_cast<int64_t>(own.width) * page_size > INT32_MAX / 2 ||
       static_cast<int64_t>(prefix.width) * page_size > INT32_MAX / 2)
     return ATTN_ERR_UNSUPPORTED;
-  if ((own.pos || (P > 0 && prefix.pos)) && !q_pos) return ATTN_ERR_INVALID;
+  if (total_q > 0 && (own.pos || (P > 0 && prefix.pos)) && !q_pos) return ATTN_ERR_INVALID;
   if (slopes && B > 1 && slopes_bs != 0 && slopes_bs < Hq) return ATTN_ERR_INVALID;
   if (!k.base || (with_v && !v.base) || (total_q > 0 && (!q || !lse))) return ATTN_ERR_INVALID;
   if (total_q > 0 && !strided_ok({{q, {q_ts, q_hs}}})) return ATTN_ERR_ALIGNMENT;

@@ -219,3 +219,12 @@ def test_python_calls_refuse_host_tensors(lib):
         C.attention_varlen_cache_evict(pool, pool, t, i, s, s.int(), i, 4)
     with pytest.raises(ValueError, match="tensor"):
         C.attention_varlen_cache_fwd(None, pool, pool, t, i, i)
+
+
+@pytest.mark.parametrize("f", [fwd, weights])
+def test_key_positions_without_tokens(lib, f):
+    """Without query tokens there are no positions of theirs to give."""
+    prefix = dict(P=1, pt=FAKE, prs=1, pw=1, pl=FAKE, cup=FAKE)
+    assert f(lib, kp=FAKE) == -1 and f(lib, **prefix, pkp=FAKE) == -1
+    nothing = 0 if f is fwd else -4                # attention has nothing to do, weights has scores to copy
+    assert f(lib, kp=FAKE, total=0, q=None) == nothing and f(lib, **prefix, pkp=FAKE, total=0) == nothing

@@ -138,3 +138,26 @@ def test_append_leaves_out_what_does_not_fit(cu, lens, written, rot):
             wp[b, :, j], ws[b, :, j] = 9 if rot else j, 0.0
     assert out.tolist() == wl
     assert torch.equal(kc.k, wk) and torch.equal(kc.v, wv) and torch.equal(kp, wp) and torch.equal(sc, ws)
+
+
+# ---------------------------------------------------------------- calls without tokens
+
+def test_no_tokens_with_key_positions():
+    """After an eviction (key positions) a step without query tokens is as good as one before it."""
+    kc = ref.Cache([20, 9], [30], page=16, Hkv=2, d=128)
+    none = torch.empty(0, 8, 128, dtype=BF, device="cuda")
+    kp = torch.zeros(2, 2, kc.table.shape[1] * 16, dtype=torch.int32, device="cuda")
+    call = dict(key_pos=kp, prefix_table=kc.ptable, prefix_lens=kc.plens, cu_prefix=i32([0, 2]),
+                prefix_key_pos=torch.zeros(1, 2, kc.ptable.shape[1] * 16, dtype=torch.int32, device="cuda"), causal=True)
+    for qp in (None, torch.empty(0, dtype=torch.int32, device="cuda")):
+        st = status()
+        out, lse = C.attention_varlen_cache_fwd(none, kc.k, kc.v, kc.table, kc.lens, i32([0, 0, 0]), q_pos=qp, status=st,
+                                                **call)
+        assert out.shape == (0, 8, 128) and lse.shape == (0, 8)
+        sc = torch.rand(2, 2, kc.table.shape[1] * 16, device="cuda")
+        got, _ = C.attention_varlen_cache_weights(none, kc.k, kc.table, kc.lens, i32([0, 0, 0]), lse, sc, q_pos=qp,
+                                                  scores_out=torch.full_like(sc, 5.0), status=st, **call)
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        for b, n in enumerate([20, 9]):
+            assert torch.equal(got[b, :, :n], sc[b, :, :n]) and (got[b, :, n:] == 5).all()
