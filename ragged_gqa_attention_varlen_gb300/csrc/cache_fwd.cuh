@@ -455,8 +455,8 @@ __global__ void __launch_bounds__(kThreadsF, 1)
             const int n = varies ? tile_steps(lo, hi) : g.each;
             // units [a, a + tile_cost) carry no step
             const int64_t at = a + p.tile_cost;  // of step 0
-            const int f0 = static_cast<int>(max(begin - at, static_cast<int64_t>(0)));
-            const int f1 = static_cast<int>(min(end - at, static_cast<int64_t>(n)));
+            const Steps mine = share_steps(begin, end, at, n);
+            const int f0 = mine.from, f1 = mine.to;
             if (f0 < f1) {
               Piece pc;
               pc.row = g.s.row;

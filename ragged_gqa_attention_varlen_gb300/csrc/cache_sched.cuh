@@ -14,6 +14,7 @@
 // derives its share from the lengths itself, so nothing is launched before.
 #pragma once
 #include "cache.cuh"
+#include "cache_share.h"
 
 namespace attn {
 namespace kv {

@@ -386,8 +386,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           // units [a, a + p.tile_cost) carry no step; a tile without any step
           // belongs to the CTA of its first unit
           const int64_t at = a + p.tile_cost;
-          const int f0 = static_cast<int>(max(begin - at, static_cast<int64_t>(0)));
-          const int f1 = static_cast<int>(min(end - at, static_cast<int64_t>(n)));
+          const Steps mine = share_steps(begin, end, at, n);
+          const int f0 = mine.from, f1 = mine.to;
           if (f0 < f1 || (n == 0 && a >= begin)) {
             if (nt <= 1) {
               pc.kt0 = f0;
