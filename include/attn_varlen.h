@@ -594,7 +594,8 @@ attn_status attn_varlen_fvjp_fwd_bwd_noalloc(
  * the device, or NULL), and never clear it: a caller zeroes it once and reads
  * it when it likes.  Lengths that exceed the table or page numbers outside of
  * the pool set ATTN_DEV_BAD_CACHE, inconsistent cu arrays ATTN_DEV_BAD_CU;
- * the call then leaves out what they concern and never reads or writes out of
+ * the call then leaves out what they concern (the slots of a page out of the
+ * pool count as if they were not there) and never reads or writes out of
  * range.  Query tokens at or behind cu_q[B] (a batch padded to the size of a
  * captured graph) are left as they are in every output.  Workspaces belong to
  * one call at a time: calls that may overlap need one each.  An array that a

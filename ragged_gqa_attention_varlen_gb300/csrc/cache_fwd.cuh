@@ -131,6 +131,7 @@ struct FwdBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t s_full[2], p_full[2], pv_done[2];
+  uint32_t gone[8];  // of a step's key tile: load boxes whose page is out of the pool
   uint64_t o_full, o_empty, drain;
   uint64_t mx_x[4][2], l_x[4];
   PieceRing ring;
@@ -180,6 +181,14 @@ __device__ __forceinline__ void load_pages(const CacheParams& p, FwdBars* bars, 
       const int have = min(pieces, (pc.len - key0 + box - 1) / box);  // row blocks in use
       const int next = page_of(kt - 1);  // read while this tile's stage is waited for
       if (loaded >= kStages && !(ok = mbar_wait_warp(&empty[st], ph ^ 1, s_abort))) break;
+      if (K) {
+        // Pages out of the pool are loaded as zeros; their keys are masked by this.
+        // Eight entries: the load of a step waits for the product at most six before,
+        // which waited for the softmax two before that.
+        static_assert(!K || kStages + 2 <= 8, "an entry could still be read");
+        const uint32_t gone = __ballot_sync(0xffffffffu, ch == 0 && page == p.num_pages);
+        if (lane == 0) bars->gone[loaded & 7] = gone;
+      }
       if (lane == 0) mbar_arrive_expect_tx(&full[st], kBytes / pieces * have);
       __syncwarp();
       if (page >= 0) {
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
       mbar_init(&bars->v_empty[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->s_full[b], 2);  // the products, and the issuer (which has seen `gone`)
       mbar_init(&bars->p_full[b], 8);
       mbar_init(&bars->pv_done[b], 1);
     }
@@ -289,7 +298,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
     return;
   }
-  const int box = min(p.page_size, kKeys);  // rows of a load box
+  const int box = min(p.page_size, kKeys), box_log2 = min(p.page_log2, 7);  // rows of a load box
 
   if (warp < 4) {
     warpgroup_reg_dealloc<kRegsPlan>();
@@ -318,6 +327,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
             for (int k = 0; k < HD / 16; ++k)
               umma_ss(tmem + (step & 1) * 128, kmajor_desc(qb, k), kmajor_desc(kb, k), kIdS, k > 0);
             umma_commit(&bars->s_full[step & 1]);
+            mbar_arrive(&bars->s_full[step & 1]);
             umma_commit(&bars->k_empty[st]);
             if (kt == pc.kt0) umma_commit(&bars->q_empty);
             if (++st == S::kKS) {
@@ -565,14 +575,22 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           if (p.wr >= 0) jhi = min(jhi, pos + p.wr);
         }
       }
+      const int32_t* pages = pc.own ? p.own.pages + pc.row * p.own.rs : p.prefix.pages + pc.row * p.prefix.rs;
+      auto no_page = [&](int j) {
+        return static_cast<unsigned>(__ldg(pages + (j >> p.page_log2))) >= static_cast<unsigned>(p.num_pages);
+      };
       float m_run = -INFINITY;
       if (FIXED) {
         m_run = 0.f;
-        if (POS && jlo <= jhi) {
-          // the ALiBi term of the nearest (or, rising, the farthest) key: every
-          // logit lies within the cap of it
-          const int d = slope2 >= 0.f ? (pos < jlo ? jlo - pos : (pos > jhi ? pos - jhi : 0))
-                                      : max(abs(pos - jlo), abs(pos - jhi));
+        if (POS && p.slopes && jlo <= jhi) {
+          // the ALiBi term of the nearest (or, rising, the farthest) key that has a
+          // page: every logit lies within the cap of it
+          const bool near = slope2 >= 0.f;
+          int a = near ? min(pos, jhi) : jhi, b = near ? max(pos, jlo) : jlo;
+          while (a >= jlo && no_page(a)) a = (a >> p.page_log2 << p.page_log2) - 1;
+          while (b <= jhi && no_page(b)) b = ((b >> p.page_log2) + 1) << p.page_log2;
+          const int da = a >= jlo ? abs(pos - a) : -1, db = b <= jhi ? abs(pos - b) : -1;
+          const int d = near && da >= 0 && db >= 0 ? min(da, db) : max(max(da, db), 0);
           m_run = -slope2 * static_cast<float>(d);
         }
       }
@@ -589,12 +607,14 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           kpb = __ldg(kp + min(key0 + 32 + lane, pc.len - 1));
         }
         // the bounds are applied per key only where they cut some row's keys
-        const bool edge = __any_sync(0xffffffffu, valid && (key0 < jlo || key0 + 63 > jhi));
+        bool edge = __any_sync(0xffffffffu, valid && (key0 < jlo || key0 + 63 > jhi));
+        uint32_t gone = 0;  // a bit per load box of keys without a page
         const bool behind = POS && __all_sync(0xffffffffu, !valid || pos >= key0 + 63);
         // without logits to keep, both passes read the products and scale themselves
         const bool keep = CAP || (POS && (kpos || p.slopes)) || !(in_scale > 0.f);
+        auto no_box = [&](int c0) { return gone >> ((half * 64 + c0) >> box_log2) & 1; };
         auto mask = [&](auto& x, int c0, int n) {
-          const int lo = jlo - key0 - c0, hi = jhi - key0 - c0;
+          const int lo = no_box(c0) ? n : jlo - key0 - c0, hi = jhi - key0 - c0;
 #pragma unroll
           for (int i = 0; i < n; ++i) x[i] = i >= lo && i <= hi ? x[i] : -INFINITY;
         };
@@ -620,10 +640,11 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           }
           const float sc = FIXED ? -2.f * out_scale : (CAP ? out_scale : in_scale);
           if (POS && kpos) {
+            const int len = no_box(c0) ? 0 : pc.len;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int kq = __shfl_sync(0xffffffffu, c0 < 32 ? kpa : kpb, (c0 & 31) + i);
-              const bool adm = key0 + c0 + i < pc.len && (p.wl < 0 || kq >= pos - p.wl) &&
+              const bool adm = key0 + c0 + i < len && (p.wl < 0 || kq >= pos - p.wl) &&
                                (p.wr < 0 || kq <= pos + p.wr);
               x[i] = adm ? fmaf(x[i], sc, -slope2 * static_cast<float>(abs(pos - kq))) : -INFINITY;
             }
@@ -661,6 +682,8 @@ __global__ void __launch_bounds__(kThreadsF, 1)
         };
         if (!(ok = mbar_wait_warp(&bars->s_full[step & 1], (step >> 1) & 1, s_abort))) break;
         tc_fence_after();
+        gone = bars->gone[step & 7];
+        edge = edge || gone;
         float alpha = 1.f;
         bool need = false;
         if (!FIXED) {

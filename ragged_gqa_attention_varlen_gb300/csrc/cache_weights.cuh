@@ -553,9 +553,12 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         const bool there = key < pc.len;
         float before = 0.f;  // read while the products run
         if (there && in && !pc.cut) before = in[key];
+        const Table& t = pc.own ? p.own : p.prefix;
+        // a key whose page is out of the pool receives nothing
+        const bool gone = there && static_cast<unsigned>(__ldg(t.pages + pc.row * t.rs + (key >> p.page_log2))) >=
+                                       static_cast<unsigned>(p.num_pages);
         int kpos = 0;
         if (POS) {
-          const Table& t = pc.own ? p.own : p.prefix;
           kpos = t.pos ? __ldg(t.pos + pc.row * t.pos_rs + pc.g * t.pos_hs + min(key, pc.len - 1))
                        : (pc.own ? pc.plen : 0) + key;
         }
@@ -625,6 +628,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
             if (lane == 0) mbar_arrive(&bars->s_read[step & 3]);
             total += f2_lo(sum) + f2_hi(sum);
             if (!many) {  // one row tile
+              if (gone) total = 0.f;
               if (pc.cut)
                 parts[(2 * blockIdx.x + (pc.cut == 2)) * 128 + r] = total;
               else if (there)
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         if (!(ok = warp_exchange(&bars->pair[quad], npair & 1, s_abort))) break;
         ++npair;
         if (!half) {
-          total += mine[r];
+          total = gone ? 0.f : total + mine[r];
           if (pc.cut)
             parts[(2 * blockIdx.x + (pc.cut == 2)) * 128 + r] = total;
           else if (there)

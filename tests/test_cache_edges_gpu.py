@@ -161,3 +161,87 @@ def test_no_tokens_with_key_positions():
         assert int(st) == 0
         for b, n in enumerate([20, 9]):
             assert torch.equal(got[b, :, :n], sc[b, :, :n]) and (got[b, :, n:] == 5).all()
+
+
+# ---------------------------------------------------------------- pages out of the pool, lengths beyond the table
+
+class Without:
+    """A cache as its calls are to read it: slots of pages out of the pool do not exist."""
+
+    def __init__(self, kc, lens, plens, own_gone, pre_gone):
+        self.Hkv, self.d, self.k, self.v, self.kc = kc.Hkv, kc.d, kc.k, kc.v, kc
+        self.table, self.ptable = "own", "prefix"
+        self.keep = {"own": [[j for j in range(n) if (b, j // kc.page) not in own_gone] for b, n in enumerate(lens)],
+                     "prefix": [[j for j in range(n) if (b, j // kc.page) not in pre_gone] for b, n in enumerate(plens)]}
+        self.lens_l, self.plens_l = ([len(x) for x in self.keep[t]] for t in ("own", "prefix"))
+
+    def rows(self, pool, table, r, n):
+        keep = self.keep[table][r]
+        whole = self.kc.rows(pool, self.kc.table if table == "own" else self.kc.ptable, r, max(keep, default=-1) + 1)
+        return whole[torch.tensor(keep, dtype=torch.long)] if keep else whole[:0]
+
+    def positions(self, table, offset):
+        width = max([1] + [len(x) for x in self.keep[table]])
+        kp = torch.zeros(len(self.keep[table]), self.Hkv, width, dtype=torch.int32)
+        for b, x in enumerate(self.keep[table]):
+            kp[b, :, :len(x)] = torch.tensor([offset + j for j in x], dtype=torch.int32)
+        return kp
+
+
+@pytest.mark.parametrize("cap,alibi,causal,moved", [(3.0, True, True, False), (0.0, False, False, False),
+                                                    (30.0, True, True, False), (3.0, True, True, True),
+                                                    (0.0, False, True, True)])
+@pytest.mark.parametrize("lens,plens,counts,Hq,Hkv,d,page,own_gone,pre_gone", [
+    ([70, 40, 200], (), [1, 3, 2], 16, 1, 160, 16, [(0, 1), (2, 0), (2, 12)], []),
+    ([300, 129], (), [1, 40], 8, 2, 128, 64, [(0, 0), (0, 4), (1, 1)], []),
+    ([2000, 700], (), [1, 1], 8, 1, 64, 256, [(0, 3), (0, 7)], []),
+    ([40, 90], [500], [2, 1], 48, 1, 160, 32, [(1, 2)], [(0, 0), (0, 9), (0, 10)]),
+    ([33], (), [2], 8, 1, 64, 64, [(0, 0)], [])])  # nothing is left
+def test_pages_out_of_the_pool_are_left_out(lens, plens, counts, Hq, Hkv, d, page, own_gone, pre_gone, cap, alibi, causal,
+                                           moved):
+    kc = ref.Cache(lens, plens, Hkv, d, page, HF)
+    bad, pbad = kc.table.clone(), kc.ptable.clone()
+    for i, (b, j) in enumerate(own_gone):
+        bad[b, j] = -1 if i % 2 else kc.num_pages
+    for i, (b, j) in enumerate(pre_gone):
+        pbad[b, j] = 2 ** 31 - 1 if i % 2 else -2 ** 31
+    left = Without(kc, lens, plens, own_gone, pre_gone)
+    B, P, T = len(lens), len(plens), sum(counts)
+    plen = plens[0] if P else 0
+    group = [0] * B if P else None
+    qp = [plen + n - c + i for n, c in zip(lens, counts) for i in range(c)]
+    slopes = torch.rand(B, Hq, generator=torch.Generator().manual_seed(3)) * 0.05 if alibi else None
+    q = normal(5, T, Hq, d, dtype=HF, std=2.0)
+    opt = dict(group=group, slopes=slopes, causal=causal, cap=cap, q_pos=torch.tensor(qp),
+               key_pos=left.positions("own", plen), pkey_pos=left.positions("prefix", 0) if P else None)
+    call = dict(causal=causal, softcap=cap)
+    if alibi:
+        call["alibi_slopes"] = slopes.cuda()
+    if P:
+        call.update(prefix_table=pbad, prefix_lens=kc.plens, cu_prefix=i32([0, B]))
+    if moved:  # the same positions, given explicitly
+        call["q_pos"] = i32(qp)
+        call["key_pos"] = (plen + torch.arange(bad.shape[1] * page, dtype=torch.int32, device="cuda")).expand(B, Hkv, -1)
+    st, cu_q = status(), i32(ref.cu(counts))
+    want, wl, otol, ltol = ref.attention(q, left, counts, **opt)
+    out, lse = C.attention_varlen_cache_fwd(q, kc.k, kc.v, bad, kc.lens, cu_q, status=st, **call)
+    torch.cuda.synchronize()
+    assert int(st) == C.DEV_BAD_CACHE
+    within("lse", lse, wl, ltol)
+    within("out", out, want, otol)
+    start = torch.rand(B, Hkv, bad.shape[1] * page, device="cuda")
+    pstart = torch.rand(P, Hkv, pbad.shape[1] * page, device="cuda") if P else None
+    st = status()
+    own, pre, wtol, ptol = ref.weights(q, left, counts, lse, **opt)
+    sc, psc = C.attention_varlen_cache_weights(q, kc.k, bad, kc.lens, cu_q, lse, start.clone(), status=st,
+                                               prefix_scores=None if pstart is None else pstart.clone(), **call)
+    torch.cuda.synchronize()
+    assert int(st) == C.DEV_BAD_CACHE
+    for got, x0, w, tol, table in ((sc, start, own, wtol, "own"), (psc, pstart, pre, ptol, "prefix")):
+        for b, keep in enumerate(left.keep[table] if got is not None else []):
+            j = torch.tensor(keep, dtype=torch.long)
+            target = x0[b].cpu().double()[:, j] + w[b]
+            within(f"{table} {b}", got[b][:, j.cuda()], target, tol[b] + target.abs() * 2.0 ** -22)
+            gone = torch.ones(got.shape[2], dtype=torch.bool)
+            gone[j] = False
+            assert torch.equal(got[b][:, gone.cuda()], x0[b][:, gone.cuda()])  # keep what they had
