@@ -718,11 +718,12 @@ attn_status attn_varlen_cache_weights(
  * next_pos[s] - recent (the most recent; 0 <= recent <= budget), then by
  * scores descending (NaN last), equal scores by lowest slot.  In the K and V
  * pages the i-th evicted slot below the new length takes the row of the i-th
- * kept slot at or above it; other rows are not touched.  scores_out and
- * key_pos_out receive the kept slots' values at their new places, lens_out the
- * new lengths; each may be its input array (in place) or apart from it.  The
- * rows may be sequences or shared prefixes (with their own tables); no two
- * may share a page that holds slots. */
+ * kept slot at or above it; other rows are not touched.  A move from or to a
+ * page out of the pool is left out (ATTN_DEV_BAD_CACHE): its slot keeps its key,
+ * score and position.  scores_out and key_pos_out receive the kept slots' values
+ * at their new places, lens_out the new lengths; each may be its input array (in
+ * place) or apart from it.  The rows may be sequences or shared prefixes (with
+ * their own tables); no two may share a page that holds slots. */
 size_t attn_varlen_cache_evict_workspace_size(int S, int Hkv, int table_width, int page_size,
                                               int budget);
 attn_status attn_varlen_cache_evict(

@@ -320,12 +320,16 @@ __global__ void __launch_bounds__(kThreadsM)
       dst = holes[m0 + lane];
       ps = __ldg(row + (src >> p.page_log2));
       pd = __ldg(row + (dst >> p.page_log2));
-      so[dst] = sc[src];
-      po[dst] = kp[src];
+      const float score = sc[src];
+      const int32_t pos = kp[src];
       if (static_cast<unsigned>(ps) >= static_cast<unsigned>(p.num_pages) ||
           static_cast<unsigned>(pd) >= static_cast<unsigned>(p.num_pages)) {
+        // nothing of this move: the slot keeps its key, score and position
         report(p.status, ATTN_DEV_BAD_CACHE);
         ps = -1;
+      } else {
+        so[dst] = score;
+        po[dst] = pos;
       }
       src &= p.page_size - 1;
       dst &= p.page_size - 1;

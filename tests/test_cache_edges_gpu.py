@@ -245,3 +245,27 @@ def test_pages_out_of_the_pool_are_left_out(lens, plens, counts, Hq, Hkv, d, pag
             gone = torch.ones(got.shape[2], dtype=torch.bool)
             gone[j] = False
             assert torch.equal(got[b][:, gone.cuda()], x0[b][:, gone.cuda()])  # keep what they had
+
+
+def test_evict_keeps_rows_scores_and_positions_together():
+    """Where a move's page is out of the pool nothing of it moves: the slot keeps its key, score
+    and position."""
+    kc = ref.Cache([64], page=16, extra_width=0, dtype=HF, poison=False)
+    k0, v0, table = kc.k.clone(), kc.v.clone(), kc.table.clone()
+    table[0, 3] = 1000  # sources 48 .. 63
+    sc = torch.arange(64, dtype=torch.float32, device="cuda").view(1, 1, 64)
+    kp = torch.arange(64, dtype=torch.int32, device="cuda").view(1, 1, 64)
+    for in_place in (True, False):
+        s, p, lens, st = sc.clone(), kp.clone(), i32([64]), status()
+        kc.k.copy_(k0), kc.v.copy_(v0)
+        kw = {} if in_place else dict(scores_out=torch.full_like(sc, -1.0), key_pos_out=torch.full_like(kp, -1))
+        _, so, po = C.attention_varlen_cache_evict(kc.k, kc.v, table, lens, s, p, i32([64]), 20, 0, status=st, **kw)
+        torch.cuda.synchronize()
+        assert int(st) == C.DEV_BAD_CACHE and lens.tolist() == [20]
+        # kept: scores 44 .. 63; the movers 44 .. 47 go into the first evicted slots, 0 .. 3
+        want = [44, 45, 46, 47] + list(range(4, 20))
+        assert po[0, 0, :20].tolist() == want and so[0, 0, :20].tolist() == [float(x) for x in want]
+        t = kc.table[0].tolist()
+        for slot, src in enumerate(want):
+            for x, x0 in ((kc.k, k0), (kc.v, v0)):
+                assert torch.equal(x[t[slot // 16], slot % 16], x0[t[src // 16], src % 16]), (slot, src)
