@@ -594,14 +594,16 @@ attn_status attn_varlen_fvjp_fwd_bwd_noalloc(
  * the device, or NULL), and never clear it: a caller zeroes it once and reads
  * it when it likes.  Lengths that exceed the table or page numbers outside of
  * the pool set ATTN_DEV_BAD_CACHE, inconsistent cu arrays ATTN_DEV_BAD_CU;
- * the call then leaves out what they concern (the slots of a page out of the
- * pool count as if they were not there) and never reads or writes out of
- * range.  Query tokens at or behind cu_q[B] (a batch padded to the size of a
- * captured graph) are left as they are in every output.  Workspaces belong to
- * one call at a time: calls that may overlap need one each.  An array that a
- * call writes holds every element once: strides that let its rows share
- * elements (an expanded tensor), or an output at its input's address with other
- * strides, are ATTN_ERR_INVALID.  Arrays that are only read may be expanded. */
+ * the call then leaves out what they concern and never reads or writes out of
+ * range: a row of a table whose length does not fit counts as empty, the slots
+ * of a page out of the pool as if they were not there, and with inconsistent cu
+ * arrays nothing is written.  Query tokens at or behind cu_q[B] (a batch padded
+ * to the size of a captured graph) are left as they are in every output.
+ * Workspaces belong to one call at a time: calls that may overlap need one each.
+ * An array that a call writes holds every element once: strides that let its
+ * rows share elements (an expanded tensor), or an output at its input's address
+ * with other strides, are ATTN_ERR_INVALID.  Arrays that are
+ * only read may be expanded. */
 
 /* Rotary positions with several axes, in place or into other tensors.  Pair i
  * of a row's first 2*pairs features -- (i, i + pairs), or (2i, 2i + 1) when

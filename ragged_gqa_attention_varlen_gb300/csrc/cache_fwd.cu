@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   // its lengths are read along with the test of that.
   int b = min(tok, p.B - 1);
   const int end = __ldg(p.cu_q + p.B);
-  int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.own.lens + b);
+  int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = seg_len(p, true, b);
   if (tok >= end) {  // behind the last sequence
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
     b = seq_of(p.cu_q, 0, p.B, tok);
     c0 = __ldg(p.cu_q + b);
     c1 = __ldg(p.cu_q + b + 1);
-    len = __ldg(p.own.lens + b);
+    len = seg_len(p, true, b);
   }
   // whether the row's own slots and its prefix have any step, and the row's
   // place in their row tiles
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   if (p.P) {
     const int pfx = prefix_of(p, b);
     if (pfx >= 0) {
-      const int n = __ldg(p.prefix.lens + pfx);
+      const int n = seg_len(p, false, pfx);
       has_prefix = prefix_klo(p, pfx, n) < n;
       const int tok0 = __ldg(p.cu_q + max(__ldg(p.cu_prefix + pfx), 0));
       rp = (static_cast<uint32_t>(tok - tok0) * p.R + hr) % kRows;

@@ -291,7 +291,6 @@ __global__ void __launch_bounds__(kThreadsF, 1)
       report(p.status, ATTN_DEV_SMEM_ALIGN);
       ok = 0;
     }
-    if (pl->bad) report(p.status, pl->bad);
     head->ok = ok;
   }
   if (!busy || (smem_addr(sm) & 1023u)) {  // uniform
@@ -568,7 +567,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           else if (pc.own)
             pos = pc.len - pc.ntok + tok - pc.tok0;
           else
-            pos = pc.plen + __ldg(p.own.lens + b) - (__ldg(p.cu_q + b + 1) - tok);
+            pos = pc.plen + seg_len(p, true, b) - (__ldg(p.cu_q + b + 1) - tok);
         }
         if (!kpos) {
           if (p.wl >= 0) jlo = max(jlo, pos - p.wl);

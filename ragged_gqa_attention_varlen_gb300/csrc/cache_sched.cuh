@@ -61,6 +61,14 @@ __device__ __forceinline__ int seg_tiles(const CacheParams& p, const Seg& s) {
 }
 
 
+// Keys of row `row` of the prefixes' table or the sequences' own.  A length that
+// does not fit the table counts as 0 (seg_check reports it).
+__device__ __forceinline__ int seg_len(const CacheParams& p, bool own, int row) {
+  const Table& t = own ? p.own : p.prefix;
+  const int n = __ldg(t.lens + row);
+  return static_cast<unsigned>(n) <= static_cast<unsigned>(t.width) << p.page_log2 ? n : 0;
+}
+
 // The first slot of prefix pfx that some sequence's window reaches: at default
 // positions query 0 of sequence b stands at prefix_len + own_len - Lq.
 __device__ __forceinline__ int prefix_klo(const CacheParams& p, int pfx, int len) {
@@ -70,7 +78,7 @@ __device__ __forceinline__ int prefix_klo(const CacheParams& p, int pfx, int len
   int64_t lo = len;
   for (int b = b0; b < b1 && lo > 0; ++b) {
     const int nq = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b);
-    if (nq > 0) lo = min(lo, static_cast<int64_t>(len) + __ldg(p.own.lens + b) - nq - p.wl);
+    if (nq > 0) lo = min(lo, static_cast<int64_t>(len) + seg_len(p, true, b) - nq - p.wl);
   }
   return static_cast<int>(max(lo, static_cast<int64_t>(0)));
 }
@@ -84,7 +92,7 @@ __device__ __forceinline__ Seg seg_load(const CacheParams& p, int s) {
   const int b1 = g.own ? g.row + 1 : __ldg(p.cu_prefix + g.row + 1);
   g.tok0 = __ldg(p.cu_q + b0);
   g.ntok = __ldg(p.cu_q + b1) - g.tok0;
-  g.len = __ldg((g.own ? p.own.lens : p.prefix.lens) + g.row);
+  g.len = seg_len(p, g.own, g.row);
   g.klo = g.own ? 0 : prefix_klo(p, g.row, g.len);
   return g;
 }
@@ -107,7 +115,7 @@ __device__ __forceinline__ SegPlan seg_plan(const CacheParams& p, int s) {
   if (g.s.own && p.P) {
     const int pfx = prefix_of(p, g.s.row);
     if (pfx >= 0) {
-      g.plen = __ldg(p.prefix.lens + pfx);
+      g.plen = seg_len(p, false, pfx);
       g.waits = prefix_klo(p, pfx, g.plen) < g.plen;
     }
   }
@@ -144,7 +152,8 @@ __device__ __forceinline__ int head_div(const CacheParams& p, int x) {
   return static_cast<int>((static_cast<float>(x) + 0.5f) * p.inv_R);
 }
 
-// What is wrong with segment s's metadata, as status bits.
+// What is wrong with segment s's metadata, as status bits: with ATTN_DEV_BAD_CU
+// the call does nothing, a bad length leaves out its segment's keys.
 __device__ __forceinline__ int seg_check(const CacheParams& p, int s) {
   int bad = 0;
   if (s >= p.P) {
@@ -201,7 +210,7 @@ struct Plan {
   int64_t seg_begin;        // the first unit of that segment
   int seg;                  // the segment that holds unit `begin`
   int window;               // segments [seg, seg + window) of this array are filled
-  int bad, pad;
+  int bad, pad;             // whether the cu arrays are inconsistent
   SegPlan segs[32];
   int64_t tmp[2][32];
 };
@@ -219,17 +228,18 @@ __device__ bool make_plan(const CacheParams& p, Plan* pl, PlanOf plan_of, CostOf
   if (one) {
     if (tid < nseg) {
       bad = seg_check(p, tid);
-      if (!bad) g = plan_of(tid);
+      if (!(bad & ATTN_DEV_BAD_CU)) g = plan_of(tid);
     }
   } else {
     for (int s = tid; s < nseg; s += nt) bad |= seg_check(p, s);
   }
+  if (bad && blockIdx.x == 0) report(p.status, bad);
   if (tid == 0) {
     pl->bad = 0;
     pl->window = 0;
   }
-  if (__syncthreads_or(bad)) {
-    if (bad) atomicOr(&pl->bad, bad);
+  if (__syncthreads_or(bad & ATTN_DEV_BAD_CU)) {
+    if (tid == 0) pl->bad = 1;
     __syncthreads();
     return false;
   }

@@ -182,7 +182,6 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       p, pl, [&](int s) { return weights_plan(p, s); },
       [&](const SegPlan& g) -> int64_t { return weights_cost(p, g) * p.Hkv; });
   if (blockIdx.x == 0 && tid == 0) {
-    if (pl->bad) report(p.status, pl->bad);
     if (smem_addr(sm) & 1023u) report(p.status, ATTN_DEV_SMEM_ALIGN);
   }
   if (!busy || (smem_addr(sm) & 1023u)) return;  // uniform
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                 else if (pc.own)
                   pos[k] = pc.plen + pc.len - pc.ntok + tok - pc.tok0;
                 else
-                  pos[k] = pc.plen + __ldg(p.own.lens + b) - (__ldg(p.cu_q + b + 1) - tok);
+                  pos[k] = pc.plen + seg_len(p, true, b) - (__ldg(p.cu_q + b + 1) - tok);
               }
             }
           }

@@ -247,6 +247,43 @@ def test_pages_out_of_the_pool_are_left_out(lens, plens, counts, Hq, Hkv, d, pag
             assert torch.equal(got[b][:, gone.cuda()], x0[b][:, gone.cuda()])  # keep what they had
 
 
+def test_a_bad_length_concerns_its_keys_only():
+    """The other sequences' results are what they are without it; the sequence itself has its
+    prefix left, or nothing."""
+    lens, counts = [300, 40, 90, 20], [1, 2, 1, 1]
+    kc = ref.Cache(lens, [50], page=16)
+    q, cu_q = normal(3, 5, 8, 160), i32(ref.cu(counts))
+    group = dict(prefix_table=kc.ptable, prefix_lens=kc.plens, cu_prefix=i32([2, 4]))
+    sc0 = torch.rand(4, 1, kc.table.shape[1] * 16, device="cuda")
+    for bad in (-1, 10 ** 6, -2 ** 31):
+        for at in (1, 2):
+            ln, st = list(lens), status()
+            ln[at] = bad
+            out, lse = C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, i32(ln), cu_q, status=st, softcap=3.0, **group)
+            torch.cuda.synchronize()
+            assert int(st) == C.DEV_BAD_CACHE
+            left = Without(kc, [0 if b == at else n for b, n in enumerate(lens)], [50], [], [])
+            want, wl, otol, ltol = ref.attention(q, left, counts, group=[-1, -1, 0, 0])
+            within("lse", lse, wl, ltol)
+            within("out", out, want, otol)
+            st = status()
+            sc, _ = C.attention_varlen_cache_weights(q, kc.k, kc.table, i32(ln), cu_q, lse, sc0.clone(), status=st, **group)
+            torch.cuda.synchronize()
+            assert int(st) == C.DEV_BAD_CACHE and torch.equal(sc[at], sc0[at])
+            own, _, wtol, _ = ref.weights(q, left, counts, lse, group=[-1, -1, 0, 0])
+            for b, n in enumerate(left.lens_l):
+                target = sc0[b, :, :n].cpu().double() + own[b]
+                within("w", sc[b, :, :n], target, wtol[b] + target.abs() * 2.0 ** -22)
+                assert torch.equal(sc[b, :, n:], sc0[b, :, n:])
+    st = status()
+    out, lse = C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, kc.lens, cu_q, status=st,
+                                            **{**group, "prefix_lens": i32([10 ** 6])})
+    torch.cuda.synchronize()
+    assert int(st) == C.DEV_BAD_CACHE
+    want, wl, otol, ltol = ref.attention(q, kc, counts)
+    within("out", out, want, otol)
+
+
 def test_evict_keeps_rows_scores_and_positions_together():
     """Where a move's page is out of the pool nothing of it moves: the slot keeps its key, score
     and position."""
