@@ -602,8 +602,9 @@ attn_status attn_varlen_fvjp_fwd_bwd_noalloc(
  * Workspaces belong to one call at a time: calls that may overlap need one each.
  * An array that a call writes holds every element once: strides that let its
  * rows share elements (an expanded tensor), or an output at its input's address
- * with other strides, are ATTN_ERR_INVALID.  Arrays that are
- * only read may be expanded. */
+ * with other strides, are ATTN_ERR_INVALID.  Arrays that are only read may be
+ * expanded (strides of 0), the page pools and lse apart; so may a table's rows
+ * where its pages are only read. */
 
 /* Rotary positions with several axes, in place or into other tensors.  Pair i
  * of a row's first 2*pairs features -- (i, i + pairs), or (2i, 2i + 1) when

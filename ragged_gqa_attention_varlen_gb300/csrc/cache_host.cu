@@ -16,19 +16,22 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Base alignment and strides of the 16-bit tensors a call reads or writes.
+// Base alignment and strides of the 16-bit tensors a call reads or writes.  Rows
+// that are only read may be expanded (a stride of 0).
 struct Strided {
   const void* base;
   std::initializer_list<int64_t> strides;
 };
-bool strided_ok(std::initializer_list<Strided> ts) {
+bool strided_from(int64_t least, std::initializer_list<Strided> ts) {
   for (const Strided& t : ts) {
     if (!aligned16(t.base)) return false;
     for (int64_t s : t.strides)
-      if (s <= 0 || s % 8) return false;
+      if (s < least || s % 8) return false;
   }
   return true;
 }
+bool strided_ok(std::initializer_list<Strided> ts) { return strided_from(8, ts); }
+bool readable(std::initializer_list<Strided> ts) { return strided_from(0, ts); }
 
 // Whether the rows of `row` elements that a call writes share none (an expanded
 // or overlapping output would hold whatever was written last).  Axes of one
@@ -76,8 +79,12 @@ attn_status rotary_args(const int32_t* positions, int axes, const double* inv_fr
 
 attn_status done(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
+bool table_readable(int rows, const int32_t* table, int64_t rs, int width, const int32_t* lens) {
+  return rows == 0 || (table && lens && width >= 1 && (rs >= 0 || rows == 1));
+}
+// The table of a call that writes to its pages: its rows are apart.
 bool table_ok(int rows, const int32_t* table, int64_t rs, int width, const int32_t* lens) {
-  return rows == 0 || (table && lens && width >= 1 && (rs >= width || rows == 1));
+  return table_readable(rows, table, rs, width, lens) && (rs >= width || rows <= 1);
 }
 
 // What attention and the key weights share.
@@ -97,8 +104,8 @@ attn_status read_args(CacheParams& p, attn_dtype dtype, int B, int P, int Hq, in
   if ((B == 0 && total_q > 0) || (B == 0 && P > 0)) return ATTN_ERR_INVALID;
   if (B == 0) return ATTN_OK;
   if (!page_ok(page_size) || num_pages < 1) return ATTN_ERR_UNSUPPORTED;
-  if (!cu_q || !table_ok(B, own.pages, own.rs, own.width, own.lens)) return ATTN_ERR_INVALID;
-  if (P > 0 && (!cu_prefix || !table_ok(P, prefix.pages, prefix.rs, prefix.width, prefix.lens)))
+  if (!cu_q || !table_readable(B, own.pages, own.rs, own.width, own.lens)) return ATTN_ERR_INVALID;
+  if (P > 0 && (!cu_prefix || !table_readable(P, prefix.pages, prefix.rs, prefix.width, prefix.lens)))
     return ATTN_ERR_INVALID;
   if (static_cast<int64_t>(own.width) * page_size > INT32_MAX / 2 ||
       static_cast<int64_t>(prefix.width) * page_size > INT32_MAX / 2)
@@ -106,7 +113,7 @@ attn_status read_args(CacheParams& p, attn_dtype dtype, int B, int P, int Hq, in
   if (total_q > 0 && (own.pos || (P > 0 && prefix.pos)) && !q_pos) return ATTN_ERR_INVALID;
   if (slopes && B > 1 && slopes_bs != 0 && slopes_bs < Hq) return ATTN_ERR_INVALID;
   if (!k.base || (with_v && !v.base) || (total_q > 0 && (!q || !lse))) return ATTN_ERR_INVALID;
-  if (total_q > 0 && !strided_ok({{q, {q_ts, q_hs}}})) return ATTN_ERR_ALIGNMENT;
+  if (total_q > 0 && !readable({{q, {q_ts, q_hs}}})) return ATTN_ERR_ALIGNMENT;
   if (!strided_ok({{k.base, {k.page, k.slot, k.head}}})) return ATTN_ERR_ALIGNMENT;
   if (with_v && !strided_ok({{v.base, {v.page, v.slot, v.head}}})) return ATTN_ERR_ALIGNMENT;
   p.dtype = dtype;
@@ -166,8 +173,9 @@ extern "C" attn_status attn_varlen_rotary(
   if (st != ATTN_OK) return st;
   if (total == 0) return ATTN_OK;
   if (!q || !q_out || (Hkv > 0 && (!k || !k_out))) return ATTN_ERR_INVALID;
-  if (!strided_ok({{q, {q_ts, q_hs}}, {q_out, {qo_ts, qo_hs}}})) return ATTN_ERR_ALIGNMENT;
-  if (Hkv > 0 && !strided_ok({{k, {k_ts, k_hs}}, {k_out, {ko_ts, ko_hs}}}))
+  if (!readable({{q, {q_ts, q_hs}}}) || !strided_ok({{q_out, {qo_ts, qo_hs}}}))
+    return ATTN_ERR_ALIGNMENT;
+  if (Hkv > 0 && (!readable({{k, {k_ts, k_hs}}}) || !strided_ok({{k_out, {ko_ts, ko_hs}}})))
     return ATTN_ERR_ALIGNMENT;
   if (!distinct(head_dim, {{total, qo_ts}, {Hq, qo_hs}}) ||
       (Hkv > 0 && !distinct(head_dim, {{total, ko_ts}, {Hkv, ko_hs}})) ||
@@ -209,7 +217,7 @@ extern "C" attn_status attn_varlen_cache_append(
   if (!k_cache || !v_cache || (total > 0 && (!k || !v))) return ATTN_ERR_INVALID;
   if (!strided_ok({{k_cache, {kc_ps, kc_ss, kc_hs}}, {v_cache, {vc_ps, vc_ss, vc_hs}}}))
     return ATTN_ERR_ALIGNMENT;
-  if (total > 0 && !strided_ok({{k, {k_ts, k_hs}}, {v, {v_ts, v_hs}}})) return ATTN_ERR_ALIGNMENT;
+  if (total > 0 && !readable({{k, {k_ts, k_hs}}, {v, {v_ts, v_hs}}})) return ATTN_ERR_ALIGNMENT;
   const int64_t slots = static_cast<int64_t>(table_width) * page_size;
   if (!distinct(head_dim, {{num_pages, kc_ps}, {page_size, kc_ss}, {Hkv, kc_hs}}) ||
       !distinct(head_dim, {{num_pages, vc_ps}, {page_size, vc_ss}, {Hkv, vc_hs}}) ||

@@ -228,3 +228,15 @@ def test_key_positions_without_tokens(lib, f):
     assert f(lib, kp=FAKE) == -1 and f(lib, **prefix, pkp=FAKE) == -1
     nothing = 0 if f is fwd else -4                # attention has nothing to do, weights has scores to copy
     assert f(lib, kp=FAKE, total=0, q=None) == nothing and f(lib, **prefix, pkp=FAKE, total=0) == nothing
+
+
+def test_expanded_inputs_are_taken(lib):
+    """Strides of 0 where rows are only read: q, k, v, and the tables of calls that read the pages."""
+    for f in (fwd, weights):
+        assert f(lib, trs=0) == -4 and f(lib, qts=0, qhs=0) == -4 and f(lib, trs=-1) == -1 and f(lib, qts=-8) == -3
+        assert f(lib, P=2, pt=FAKE, prs=0, pw=4, pl=FAKE, cup=FAKE) == -4
+        assert f(lib, kcss=0) == -3                # (a pool has its rows)
+    shared = dict(qts=0, khs=0, qo=0x40000, ko=0x80000)
+    assert rotary(lib, **shared, kots=152) == -1 and rotary(lib, **shared, qohs=0) == -3
+    assert append(lib, trs=0) == -1 and evict(lib, trs=0) == -1   # pages that are written belong to one row
+    assert append(lib, kts=0, vhs=0, sc=FAKE, scrs=0, schs=0) == -1 and append(lib, kts=-160) == -3

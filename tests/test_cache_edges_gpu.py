@@ -306,3 +306,37 @@ def test_evict_keeps_rows_scores_and_positions_together():
         for slot, src in enumerate(want):
             for x, x0 in ((kc.k, k0), (kc.v, v0)):
                 assert torch.equal(x[t[slot // 16], slot % 16], x0[t[src // 16], src % 16]), (slot, src)
+
+
+# ---------------------------------------------------------------- arguments
+
+def test_read_only_arrays_may_be_expanded():
+    """One page table for several readers of the same keys, one row of q for several tokens."""
+    kc = ref.Cache([100], [40], page=16, Hkv=2, d=128)
+    B = 3
+    q = normal(1, 1, 8, 128).expand(B, 8, 128)
+    cu_q, lens, plens = i32([0, 1, 2, 3]), i32([100, 7, 64]), i32([40, 33])
+    one = dict(prefix_table=kc.ptable.expand(2, -1), prefix_lens=plens, cu_prefix=i32([0, 1, 3]))
+    each = dict(one, prefix_table=kc.ptable.repeat(2, 1))
+    st = status()
+    a, la = C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table.expand(B, -1), lens, cu_q, status=st, **one)
+    b, lb = C.attention_varlen_cache_fwd(q.contiguous(), kc.k, kc.v, kc.table.repeat(B, 1), lens, cu_q, status=st, **each)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    w, _ = C.attention_varlen_cache_weights(q, kc.k, kc.table.expand(B, -1), lens, cu_q, la, status=st, **one)
+    x, _ = C.attention_varlen_cache_weights(q.contiguous(), kc.k, kc.table.repeat(B, 1), lens, cu_q, la, status=st, **each)
+    assert torch.equal(w, x)
+    k = normal(2, 3, 1, 128).expand(3, 2, 128)  # one K row for both heads
+    inv = torch.ones(64, dtype=torch.float64, device="cuda")
+    u = C.attention_varlen_rotary(q, k, i32([1, 2, 3]), inv)
+    v = C.attention_varlen_rotary(q.contiguous(), k.contiguous(), i32([1, 2, 3]), inv)
+    assert torch.equal(u[0], v[0]) and torch.equal(u[1], v[1])
+    big = ref.Cache([20, 20, 20], page=16, Hkv=2, d=128, poison=False)
+    k0 = big.k.clone()
+    C.attention_varlen_cache_append(k, k, big.k, big.v, big.table, i32([3, 4, 5]), cu_q, status=st)
+    for b in range(B):
+        pg = int(big.table[b, 0])
+        assert torch.equal(big.k[pg, 3 + b], k[b]) and torch.equal(big.v[pg, 3 + b], k[b])
+        k0[pg, 3 + b] = k[b]
+    assert torch.equal(big.k, k0) and int(st) == 0
+    with pytest.raises(C.AttnError):  # one page written by several sequences
+        C.attention_varlen_cache_append(k, k, big.k, big.v, big.table[:1].expand(3, -1), i32([3, 4, 5]), cu_q)
