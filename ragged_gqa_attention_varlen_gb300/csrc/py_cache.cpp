@@ -75,7 +75,12 @@ double real(PyObject* o) {
   }
   return v;
 }
-int truth(PyObject* o) { return PyObject_IsTrue(o) > 0; }
+struct Raised {};  // a Python error is set
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v;
+}
 
 // A call's device, made current for its duration, and its stream.
 struct Call {
@@ -268,6 +273,7 @@ PyObject* guarded(Py_ssize_t nargs, Py_ssize_t want, F f) {
     }
   } catch (const std::invalid_argument& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const Raised&) {
   } catch (const python_error&) {
     // (its Python error is set)
   } catch (const c10::OutOfMemoryError& e) {

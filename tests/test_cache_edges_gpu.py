@@ -340,3 +340,20 @@ def test_read_only_arrays_may_be_expanded():
     assert torch.equal(big.k, k0) and int(st) == 0
     with pytest.raises(C.AttnError):  # one page written by several sequences
         C.attention_varlen_cache_append(k, k, big.k, big.v, big.table[:1].expand(3, -1), i32([3, 4, 5]), cu_q)
+
+
+def test_an_option_without_a_truth_value_is_refused():
+    class Neither:
+        def __bool__(self):
+            raise KeyError("neither")
+
+    kc = ref.Cache([20, 9], page=16, Hkv=2, d=128)
+    q, cu_q = normal(1, 2, 8, 128), i32([0, 1, 2])
+    out = torch.full_like(q, 5.0)
+    with pytest.raises(KeyError, match="neither"):
+        C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, kc.lens, cu_q, out=out, causal=Neither())
+    with pytest.raises(KeyError, match="neither"):
+        C.attention_varlen_rotary(q, None, i32([0, 1]), torch.ones(4, dtype=torch.float64, device="cuda"),
+                                  inverse=Neither(), q_out=out)
+    torch.cuda.synchronize()
+    assert (out == 5).all()
