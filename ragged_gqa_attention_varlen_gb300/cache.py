@@ -4,13 +4,22 @@ weights and eviction (argument marshalling only, by a native module).
 A cache is two tensors of pages ``[num_pages, page_size, Hkv, d]`` (K and V;
 ``page_size`` a power of two from 16 to 1024), a table ``[B, width]`` (int32)
 with the pages of each sequence, and its lengths ``lens`` ``[B]`` (int32), all
-on the device.  One generation step:
+on the device.  One generation step, with the tokens' ``positions`` ``[T]``, the
+keys' ``key_pos`` and accumulated ``scores`` ``[B, Hkv, slots]``, and ``next_pos``
+``[B]``, the position that each sequence's next token will have:
 
-    q, k = attention_varlen_rotary(q, k, positions, inv_freq)
-    attention_varlen_cache_append(k, v, k_cache, v_cache, table, lens, cu_q, lens_out=new_lens)
-    out, lse = attention_varlen_cache_fwd(q, k_cache, v_cache, table, new_lens, cu_q)
-    attention_varlen_cache_weights(q, k_cache, table, new_lens, cu_q, lse, scores)
+    q, _ = attention_varlen_rotary(q, None, positions, inv_freq)
+    attention_varlen_cache_append(k, v, k_cache, v_cache, table, lens, cu_q, positions=positions,
+                                  inv_freq=inv_freq, key_pos=key_pos, scores=scores, lens_out=new_lens)
+    out, lse = attention_varlen_cache_fwd(q, k_cache, v_cache, table, new_lens, cu_q,
+                                          q_pos=positions, key_pos=key_pos, causal=True)
+    attention_varlen_cache_weights(q, k_cache, table, new_lens, cu_q, lse, scores,
+                                   q_pos=positions, key_pos=key_pos, causal=True)
     attention_varlen_cache_evict(k_cache, v_cache, table, new_lens, scores, key_pos, next_pos, budget)
+
+An eviction leaves the slots in another order: from then on the positions say
+which key is which, and the next step's ``lens`` are ``new_lens``, which the
+eviction has shortened.
 
 Every call is asynchronous on ``stream`` (default: the current stream of the
 tensors' device).  Problems that only the device can see (lengths beyond the

@@ -357,3 +357,64 @@ def test_an_option_without_a_truth_value_is_refused():
                                   inverse=Neither(), q_out=out)
     torch.cuda.synchronize()
     assert (out == 5).all()
+
+
+# ---------------------------------------------------------------- the documented step
+
+def documented_steps():
+    """The lines of code of a generation step in the module's docstring and in README.md."""
+    import os
+    import re
+
+    from conftest import ROOT
+
+    doc = re.search(r"One generation step(?:.|\n)*?:\n\n((?:    .*\n)+)\n", C.__doc__).group(1)
+    block = next(x for x in re.findall(r"```python\n(.*?)```", open(os.path.join(ROOT, "README.md")).read(), re.S)
+                 if "cache_evict" in x)
+    return re.sub(r"(?m)^    ", "", doc), block
+
+
+@pytest.mark.parametrize("which", [0, 1], ids=["docstring", "readme"])
+def test_the_documented_step(which):
+    """Steps as the documents write them, over evictions: every new token's key has its position
+    and its weight, and attention is that over the keys that are left."""
+    code = documented_steps()[which]
+    B, Hq, d, page, width, budget = 2, 8, 64, 16, 4, 20
+    kc = ref.Cache([width * page] * B, (), 1, d, page, HF, extra_width=0)
+    lens, cu_q = i32([0, 0]), i32([0, 1, 2])
+    key_pos = torch.full((B, 1, width * page), -1, dtype=torch.int32, device="cuda")
+    scores = torch.full((B, 1, width * page), math.nan, device="cuda")
+    inv_freq = (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).cuda()
+    slopes = torch.zeros(B, Hq, device="cuda")
+    for t in range(30):
+        q, k, v = (normal(3 * t + i, B, h, d, dtype=HF, std=2.0) for i, h in ((0, Hq), (1, 1), (2, 1)))
+        new = torch.zeros_like(lens)
+        before = {}
+
+        def evict(*a, **kw):  # what stood before the eviction
+            before.update(key_pos=key_pos.clone(), scores=scores.clone(), lens=new.tolist(), k=kc.k.clone(), v=kc.v.clone())
+            return C.attention_varlen_cache_evict(*a, **kw)
+
+        space = {x: getattr(C, x) for x in dir(C) if x.startswith("attention_varlen")}
+        space.update(q=q, k=k, v=v, k_cache=kc.k, v_cache=kc.v, table=kc.table, lens=lens, new_lens=new, lens1=new, cu_q=cu_q,
+                     positions=i32([t] * B), inv_freq=inv_freq, key_pos=key_pos, scores=scores, slopes=slopes,
+                     next_pos=i32([t + 1] * B), budget=budget, attention_varlen_cache_evict=evict)
+        fake = type("module", (), {x: staticmethod(f) for x, f in space.items() if x.startswith("attention_varlen")})
+        exec(code.replace("from ragged_gqa_attention_varlen_gb300 import cache as C\n", ""), {**space, "C": fake}, space)
+        n = min(t, budget) + 1
+        assert before["lens"] == [n, n] and new.tolist() == [min(t + 1, budget)] * B
+        kc.lens_l = [n, n]
+        after = kc.k.clone(), kc.v.clone()
+        kc.k.copy_(before["k"]), kc.v.copy_(before["v"])
+        want, wl, tol, ltol = ref.attention(space["q"], kc, [1, 1], causal=True, q_pos=torch.tensor([t, t]),
+                                            key_pos=before["key_pos"])
+        kc.k.copy_(after[0]), kc.v.copy_(after[1])
+        within("out", space["out"], want, tol)
+        for b in range(B):
+            assert t in key_pos[b, 0, :new.tolist()[b]].tolist() or n > budget
+            assert t in before["key_pos"][b, 0, :n].tolist()
+            # each of the 8 rows has spread a weight of 1 over the keys in every step so far, and what
+            # an evicted key had is gone with it: no more than 8 (t + 1), and finite
+            total = float(before["scores"][b, 0, :n].double().sum())
+            assert 8 * (1 - 2 ** -10) <= total <= 8 * (t + 1) * (1 + 2 ** -10)
+        lens = new
