@@ -25,8 +25,9 @@ constexpr int kHeadsJ = 8;  // rows (heads of a token) of a block
 
 // Joins the partial results of a row.  Its own slots were computed in one
 // part or several, and so was its prefix; part i has reference m_i, sums l_i (of
-// its weights) and lr_i (of the rounded ones) and O_i, and with factors
-// 2^(m_i - max m) the row is sum O_i / sum lr_i, its lse from sum l_i.  Parts are
+// its weights) and lr_i (of the rounded ones) and O_i (m_i in two terms, of
+// which the parts of a segment share one: far rows' parts are weighed by the other
+// without its roundings), and with factors 2^(m_i - max m) the row is sum O_i / sum lr_i, its lse from sum l_i.  Parts are
 // added in the order of the keys, prefix last, so the result does not depend on
 // which CTA finished first.  Rows that one part covers were
 // written by the tile kernel already; rows without any key are written here.
@@ -110,14 +111,14 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   };
   // Four parts at a time, all their loads first; the reference follows the
   // largest met so far.
-  float top = -INFINITY, l = 0.f, lr = 0.f;
+  float top = -INFINITY, top0 = 0.f, l = 0.f, lr = 0.f;  // the reference: top + top0
   float4 acc[kPer] = {};
   for (int i0 = 0; i0 < parts; i0 += 4) {
     float4 s[4];
     float4 v[4][kPer];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      s[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);  // m, l, lr, m0
       if (i0 + i < parts) {
         const int64_t pr = row_of(i0 + i);
         s[i] = stats[pr];
@@ -126,13 +127,14 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
           if (f0 + 4 * kWarpsJ * k < kUnits) v[i][k] = part[part_at<HD>(pr, f0 + 4 * kWarpsJ * k)];
       }
     }
-    float up = top;
+    float up = top, up0 = top0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (s[i].y > 0.f) up = fmaxf(up, s[i].x);
-    if (up > top) {
-      const float a = ex2_approx(top - up);
+      if (s[i].y > 0.f && (s[i].x - up) + (s[i].w - up0) > 0.f) up = s[i].x, up0 = s[i].w;
+    if (up != top || up0 != top0) {
+      const float a = ex2_approx((top - up) + (top0 - up0));
       top = up;
+      top0 = up0;
       l *= a;
       lr *= a;
 #pragma unroll
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (!(s[i].y > 0.f)) continue;  // (a part without any weight may hold anything)
-      const float a = ex2_approx(s[i].x - top);
+      const float a = ex2_approx((s[i].x - top) + (s[i].w - top0));
       l = fmaf(a, s[i].y, l);
       lr = fmaf(a, s[i].z, lr);
 #pragma unroll
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
           make_uint2(Pack<BF16>::two(acc[k].x * inv, acc[k].y * inv),
                      Pack<BF16>::two(acc[k].z * inv, acc[k].w * inv));
   if (f0 == 0)
-    p.lse[row] = l > 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
+    p.lse[row] = l > 0.f ? (top + log2f(l) + top0) * kLn2 : -INFINITY;
 }
 
 template <int HD>

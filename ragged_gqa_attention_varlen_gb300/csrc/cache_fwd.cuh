@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
         meta[(static_cast<int64_t>(pc.own ? 0 : p.total_q) + tok) * p.Hq + h] = make_int2(blockIdx.x, pc.parts);
       // the row's own slope, and the keys [jlo, jhi] it may attend to; default
       // positions are counted from the segment's slot 0
-      float slope2 = 0.f;
+      float slope2 = 0.f, m0 = 0.f;  // m0: ALiBi term common to all keys
       int jlo = 0, jhi = pc.len - 1, pos = 0;
       bool kpos = false;
       const int32_t* kp = nullptr;
@@ -572,6 +572,15 @@ __global__ void __launch_bounds__(kThreadsF, 1)
         if (!kpos) {
           if (p.wl >= 0) jlo = max(jlo, pos - p.wl);
           if (p.wr >= 0) jhi = min(jhi, pos + p.wr);
+          // A row that stands beyond its keys is moved up to them (their tile's
+          // end), and what that takes off every distance is added to the result: the
+          // distances of far positions would lose their last bits in fp32, and
+          // logits near 2^24 the reference's.
+          if (p.slopes && jlo <= jhi) {
+            const int to = min(max(pos, jlo), jhi | (kKeys - 1));
+            m0 = -slope2 * static_cast<float>(abs(pos - to));
+            pos = to;
+          }
         }
       }
       const int32_t* pages = pc.own ? p.own.pages + pc.row * p.own.rs : p.prefix.pages + pc.row * p.prefix.rs;
@@ -811,9 +820,9 @@ __global__ void __launch_bounds__(kThreadsF, 1)
           pr = pc.mode == 1 ? cut_row(w, blockIdx.x, pc.first, r) : whole_row(w, p.total_q, p.Hq, pc.own, tok, h);
         if (valid && half == 0) {
           if (pc.mode)
-            reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(m_run, l, lr, 0.f);
+            reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(m_run, l, lr, m0);
           else
-            p.lse[static_cast<int64_t>(tok) * p.Hq + h] = l > 0.f ? (m_run + log2f(l)) * kLn2 : -INFINITY;
+            p.lse[static_cast<int64_t>(tok) * p.Hq + h] = l > 0.f ? (m_run + log2f(l) + m0) * kLn2 : -INFINITY;
         }
         uint16_t* orow = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(tok) * p.out_ts +
                          static_cast<int64_t>(h) * p.out_hs + half * kC;

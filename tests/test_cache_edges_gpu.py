@@ -418,3 +418,39 @@ def test_the_documented_step(which):
             total = float(before["scores"][b, 0, :n].double().sum())
             assert 8 * (1 - 2 ** -10) <= total <= 8 * (t + 1) * (1 + 2 ** -10)
         lens = new
+
+
+# ---------------------------------------------------------------- rows far from their keys
+
+@pytest.mark.parametrize("cap", [0.0, 3.0, 30.0])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("far", [1000, 1 << 20, (1 << 24) + 1, (1 << 30) - 700])
+def test_alibi_of_rows_far_from_their_keys(far, dtype, cap):
+    """ALiBi's weights depend on how the keys' distances differ: a row at any distance behind its
+    keys gives what it gives next to them, and lse is less by slope times the way between."""
+    lens, counts, Hq = [300, 40, 5000], [1, 20, 2], 16
+    kc = ref.Cache(lens, [260], d=160, page=64, dtype=dtype)
+    q = normal(2, sum(counts), Hq, 160, dtype=dtype)
+    g = torch.Generator().manual_seed(4)
+    slopes = torch.rand(3, Hq, generator=g) + 0.01
+    slopes[:, ::4] = 0.0
+    group = [0, -1, -1]
+    end = [260 + 300, 40, 5000]
+    near = [end[b] + i for b, n in enumerate(counts) for i in range(n)]
+    call = dict(softcap=cap, alibi_slopes=slopes.cuda(), prefix_table=kc.ptable, prefix_lens=kc.plens,
+                cu_prefix=i32([0, 1]), causal=True)
+    want, wl, otol, ltol = ref.attention(q, kc, counts, group=group, slopes=slopes, causal=True, cap=cap,
+                                         q_pos=torch.tensor(near))
+    st = status()
+    out, lse = C.attention_varlen_cache_fwd(q, kc.k, kc.v, kc.table, kc.lens, i32(ref.cu(counts)), status=st,
+                                            q_pos=i32([x + far for x in near]), **call)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    less = far * torch.repeat_interleave(slopes.double(), torch.tensor(counts), 0)
+    within("lse", lse, wl - less, ltol + less * 2.0 ** -22)
+    flat = slopes[0] == 0  # without ALiBi every row is what it was
+    within("out", out[:, flat.cuda()], want[:, flat], otol[:, flat])
+    within("out", out[1:], want[1:], otol[1:])
+    # the first sequence's prefix and own keys are weighed against one another by two terms, each off by
+    # half a step: 2^-24 of twice its size
+    within("out", out[:1], want[:1], otol[:1] + torch.expm1((4 * less[:1, :, None] * 2.0 ** -24).clamp(max=20)) * 4)
