@@ -10,8 +10,12 @@
 //   O += P V             tcgen05.mma with P from TMEM
 // and two row sums in fp32 in the softmax warps: l of P, which gives lse, and lr
 // of the rounded P that multiplies V, which divides O, so that out is a weighted
-// mean of V rows whatever the roundings: equal rows come out exactly.  (As a
-// product with a tile of ones, lr doubled the time of P V.)
+// mean of V rows whatever the roundings: equal rows come out exactly.  (lr takes 8
+// % of a capped call of drafts, nothing of one with short steps; as a product
+// with a tile of ones it doubled the time of P V.)  P has V's 16-bit type because
+// the tensor core takes one type for both: out's error against 64 bits is 0.0023
+// of its size with bf16 weights all alike (0.0019 where few are large), of which
+// 0.0017 are the rounding of out itself.
 //
 // Single-token calls read every K and V row once for R <= 128 rows of a group,
 // so the copies bound them; calls with many rows behind a shared prefix are
@@ -29,9 +33,9 @@
 // first step and slowed the rest; four warps per quadrant with 32 keys each
 // gained nothing.
 //
-// Measured with the join: 64 single tokens over 270000 keys in 16-row pages 54 us
-// (3.2 TB/s; 26 us would be the copy's rate), 128 behind an 8200-key prefix 94 us,
-// 144 drafted tokens behind two prefixes of 12001 keys 158 us (780 TFLOP/s).
+// Measured with the join: 64 single tokens over 270000 keys in 16-row pages 54.5
+// us (3.2 TB/s; 26 us would be the copy's rate), 128 behind an 8200-key prefix 101
+// us, 144 drafted tokens behind two prefixes of 12001 keys 178 us (691 TFLOP/s).
 #pragma once
 #include "../../include/attn_varlen.h"
 #include "cache_tile.cuh"

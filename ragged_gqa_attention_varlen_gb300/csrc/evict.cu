@@ -19,9 +19,9 @@
 // move_kernel: the listed K and V rows with their scores and positions, over
 // the whole GPU: a row is found through three dependent scattered reads (list,
 // page table, row), so a warp takes four rows through each of them together
-// (both kernels, 12 prompts of up to 20000 keys, 91 MB: 41 us; with a thread per
-// 16-byte unit, two in flight, 10 more.  Eight rows: the same, and the call for
-// one key goes from 8.6 to 10.6).
+// (both kernels, 12 prompts of up to 20000 keys, 91 MB: 46 to 48 us; with a thread
+// per 16-byte unit, two in flight, 10 more.  Eight rows: the same, and the call
+// for one key goes from 8.6 to 10.6).
 #include "../../include/attn_varlen.h"
 #include "cache.cuh"
 
