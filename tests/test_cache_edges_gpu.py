@@ -362,7 +362,7 @@ def test_an_option_without_a_truth_value_is_refused():
 # ---------------------------------------------------------------- the documented step
 
 def documented_steps():
-    """The lines of code of a generation step in the module's docstring and in README.md."""
+    """The lines of code of a generation step in the module's docstring and in the readme."""
     import os
     import re
 
