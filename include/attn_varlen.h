@@ -97,6 +97,7 @@ typedef enum {
 #define ATTN_DEV_SMEM_ALIGN 0x10     /* dynamic shared memory base not 1024-byte aligned */
 #define ATTN_DEV_MASK_SPACE 0x20     /* keep-mask buffer smaller than the lengths need */
 #define ATTN_DEV_BAD_CACHE 0x40      /* a cache length or page number outside of its table or pool */
+#define ATTN_DEV_NO_PAGES 0x80       /* a fork needs more free pages, or more room in its table, than there are */
 
 /* Largest batch (number of sequences) accepted. */
 #define ATTN_MAX_BATCH 16384
@@ -570,9 +571,10 @@ attn_status attn_varlen_fvjp_fwd_bwd_noalloc(
     float *lse, int32_t *device_status, void *stream);
 
 /* ---------------------------------------------------------------------------
- * Generation: rotary positions, a paged K/V cache, attention over it with
- * prefixes that sequences share, the attention weight each cached key has
- * received, and eviction by it.
+ * Generation: rotary positions (also with norms of the rows, and its gradients), a
+ * paged K/V cache in 16 or in 8 bits, attention over it with prefixes that
+ * sequences share, the attention weight each cached key has received, and eviction
+ * by it; forking, packing and copying its pages.
  *
  * The cache.  k_cache and v_cache are pools of pages [num_pages, page_size,
  * Hkv, head_dim] of 16-bit elements with page, slot and head strides in
@@ -741,6 +743,168 @@ attn_status attn_varlen_cache_evict(
     int32_t *key_pos_out, int64_t po_row_stride, int64_t po_head_stride,
     int32_t *lens_out, void *workspace, size_t workspace_bytes, int32_t *device_status,
     void *stream);
+
+/* Norms of the rows of q and k, one for each head of each token, with the rotary
+ * turn of attn_varlen_rotary in the same pass:
+ *   r = (mean_i x_i^2 + eps)^(-1/2),  y = turn(x_i r weight_i).
+ * q_weight, k_weight are fp32 [head_dim], shared by the heads (NULL: ones).
+ * inv_freq NULL: no turn (positions, axes, pair_axis and pairs are not looked at
+ * then).  k may be NULL (Hkv = 0).  eps >= 0.  The arithmetic is fp32; an output
+ * is rounded once.  q_out = q, k_out = k work in place. */
+attn_status attn_varlen_norm_rotary(
+    attn_dtype dtype, int64_t total, int Hq, int Hkv, int head_dim,
+    const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+    const void *k, int64_t k_tok_stride, int64_t k_head_stride,
+    const float *q_weight, const float *k_weight, float eps,
+    const int32_t *positions, int64_t axis_stride, int axes,
+    const double *inv_freq, const int32_t *pair_axis, int pairs, int interleaved,
+    void *q_out, int64_t qo_tok_stride, int64_t qo_head_stride,
+    void *k_out, int64_t ko_tok_stride, int64_t ko_head_stride, void *stream);
+
+/* Its vector-Jacobian product: from the gradients dq_out, dk_out of the outputs
+ * and the call's inputs q, k to dq, dk and, in fp32 [head_dim] and summed over all
+ * rows in a fixed order, dq_weight, dk_weight (NULL: not wanted; with total = 0
+ * they are zeros).  dq and dk may be dq_out and dk_out, or q and k.  The workspace
+ * is needed for the weights' gradients only. */
+size_t attn_varlen_norm_rotary_bwd_workspace_size(int64_t total, int Hq, int Hkv, int head_dim);
+attn_status attn_varlen_norm_rotary_bwd(
+    attn_dtype dtype, int64_t total, int Hq, int Hkv, int head_dim,
+    const void *dq_out, int64_t dqo_tok_stride, int64_t dqo_head_stride,
+    const void *dk_out, int64_t dko_tok_stride, int64_t dko_head_stride,
+    const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+    const void *k, int64_t k_tok_stride, int64_t k_head_stride,
+    const float *q_weight, const float *k_weight, float eps,
+    const int32_t *positions, int64_t axis_stride, int axes,
+    const double *inv_freq, const int32_t *pair_axis, int pairs, int interleaved,
+    void *dq, int64_t dq_tok_stride, int64_t dq_head_stride,
+    void *dk, int64_t dk_tok_stride, int64_t dk_head_stride,
+    float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* A cache held in 8 bits.  k_cache and v_cache are pools as above of e4m3 values
+ * (OCP FP8 without infinities: 1 sign, 4 exponent and 3 fraction bits, at most
+ * 448), strides multiples of 16.  k_scale and v_scale are fp32 [num_pages,
+ * page_size / scale_block, Hkv] with page, block and head strides (of elements),
+ * scale_block a power of two, 16 to min(page_size, 128): slot j of a page holds
+ * scale[page][j / scale_block][head] times its e4m3 values.  Scales of blocks that
+ * hold a slot are finite and not negative; the others may be anything.
+ *
+ * Append as attn_varlen_cache_append does (without scores), quantising.  With
+ * `norm` the K rows are first normed as in attn_varlen_norm_rotary with k_weight
+ * and eps, then turned.  For each block, head and tensor, with top the largest
+ * |value| of the block's new slots and was its scale if it holds slots already
+ * (else 0):
+ *   now = was if top <= 448 was, else the smallest power of two >= 2^-126 with
+ *         top <= 448 now; 0 if there is nothing but zeros;
+ * the new slots become the nearest e4m3 (ties to even) of value / now, computed as
+ * value * (1 / now), and held ones, when now != was, that of held * (was / now).
+ * K and V rows must be finite. */
+attn_status attn_varlen_cache8_append(
+    attn_dtype dtype, int B, int Hkv, int head_dim, int64_t total,
+    const void *k, int64_t k_tok_stride, int64_t k_head_stride,
+    const void *v, int64_t v_tok_stride, int64_t v_head_stride,
+    void *k_cache, int64_t kc_page_stride, int64_t kc_slot_stride, int64_t kc_head_stride,
+    void *v_cache, int64_t vc_page_stride, int64_t vc_slot_stride, int64_t vc_head_stride,
+    float *k_scale, int64_t ks_page_stride, int64_t ks_block_stride, int64_t ks_head_stride,
+    float *v_scale, int64_t vs_page_stride, int64_t vs_block_stride, int64_t vs_head_stride,
+    int num_pages, int page_size, int scale_block,
+    const int32_t *table, int64_t table_row_stride, int table_width,
+    const int32_t *lens, const int32_t *cu_new,
+    const int32_t *positions, int64_t axis_stride, int axes,
+    const double *inv_freq, const int32_t *pair_axis, int pairs, int interleaved,
+    int norm, const float *k_weight, float eps,
+    int32_t *key_pos, int64_t kp_row_stride, int64_t kp_head_stride,
+    int32_t *lens_out, int32_t *device_status, void *stream);
+
+/* Attention over it: attn_varlen_cache_fwd with the values that the pages stand
+ * for (all other arguments, outputs and errors are that call's). */
+size_t attn_varlen_cache8_fwd_workspace_size(int B, int P, int Hq, int Hkv, int head_dim,
+                                             int64_t total_q);
+attn_status attn_varlen_cache8_fwd(
+    attn_dtype dtype, int B, int P, int Hq, int Hkv, int head_dim, int64_t total_q,
+    const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+    const void *k_cache, int64_t kc_page_stride, int64_t kc_slot_stride, int64_t kc_head_stride,
+    const void *v_cache, int64_t vc_page_stride, int64_t vc_slot_stride, int64_t vc_head_stride,
+    const float *k_scale, int64_t ks_page_stride, int64_t ks_block_stride, int64_t ks_head_stride,
+    const float *v_scale, int64_t vs_page_stride, int64_t vs_block_stride, int64_t vs_head_stride,
+    int num_pages, int page_size, int scale_block,
+    const int32_t *table, int64_t table_row_stride, int table_width, const int32_t *lens,
+    const int32_t *prefix_table, int64_t prefix_row_stride, int prefix_width,
+    const int32_t *prefix_lens, const int32_t *cu_prefix, const int32_t *cu_q,
+    const int32_t *q_pos, const int32_t *key_pos, int64_t kp_row_stride, int64_t kp_head_stride,
+    const int32_t *prefix_key_pos, int64_t pkp_row_stride, int64_t pkp_head_stride,
+    const float *alibi_slopes, int64_t slopes_batch_stride, int causal, int window_left,
+    int window_right, float softcap, float scale_multiplier,
+    void *out, int64_t out_tok_stride, int64_t out_head_stride, float *lse,
+    void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream);
+
+/* Pages as wholes.  The calls below move what pages hold in any number of pools at
+ * once -- K and V of every layer, scales too: all pools that one table's page
+ * numbers index.  Strides and bytes are multiples of 4 (of 16, with 16-byte
+ * aligned bases, they move fastest). */
+typedef struct {
+  void *base;
+  int64_t page_stride, row_stride, piece_stride; /* in BYTES */
+  int32_t rows;    /* of a page: page_size, or a power of two below it (scales of blocks) */
+  int32_t pieces;  /* contiguous runs of a row (heads) */
+  int32_t bytes;   /* of a run */
+} attn_pool;
+
+/* Fork, free and reserve: row r of the table goes on from what row parents[r] held
+ * (-1: it is empty).  Rows that go on from the same one share its full pages; the
+ * first of them (lowest r) keeps its other pages, the others get a copy of the
+ * partly filled one (its used slots).  Rows that nobody goes on from give their
+ * pages back.  Every row that goes on then gets pages for room[r] more slots (room
+ * NULL: none).  parents[r] = r for all r with some room reserves pages for new
+ * tokens; leaving a row out frees it.
+ *
+ * lens [rows] are the slots in use, held [rows] the pages in a row's table (the
+ * entries from held[r] on are not looked at; lens[r] <= held[r] * page_size).
+ * refs [num_pages] counts the table rows that hold a page, 0 means free; other
+ * holders (prefix tables) count too and keep a page from being given away.  Partly
+ * filled pages have one holder (this call keeps it so).  New pages are the lowest
+ * free ones, in the order of the rows, pages given back in this call among them.
+ * The outputs may be the inputs (in place; table_out with the same stride) or
+ * apart; entries of table_out from held_out[r] on are not written.
+ *
+ * All or nothing: a length, count, parent, room or page number out of range
+ * (ATTN_DEV_BAD_CACHE), more pages than are free or than the table is wide
+ * (ATTN_DEV_NO_PAGES) leave the outputs equal to the inputs (whole rows of the
+ * table then) and the pools as they were. */
+size_t attn_varlen_cache_fork_workspace_size(int rows, int table_width, int num_pages);
+attn_status attn_varlen_cache_fork(
+    int rows, int num_pages, int page_size, const attn_pool *pools, int npools,
+    const int32_t *table, int64_t table_row_stride, int table_width,
+    const int32_t *lens, const int32_t *held, const int32_t *refs,
+    const int32_t *parents, const int32_t *room,
+    int32_t *table_out, int64_t table_out_row_stride,
+    int32_t *lens_out, int32_t *held_out, int32_t *refs_out,
+    void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream);
+
+/* Pack the live pages (refs > 0) into the first *live ones: the i-th free page
+ * below that number takes the i-th live page at or above it, in all pools; the
+ * tables' first held[r] entries and refs follow (pages from *live on get 0).  The
+ * sequences' table and one of prefixes (prefix_rows = 0: none) take part.  Outputs
+ * may be the inputs.  Entries out of the pool, or of pages that nobody counts, are
+ * left as they are (ATTN_DEV_BAD_CACHE). */
+size_t attn_varlen_cache_compact_workspace_size(int num_pages);
+attn_status attn_varlen_cache_compact(
+    int num_pages, int page_size, const attn_pool *pools, int npools,
+    int rows, const int32_t *table, int64_t table_row_stride, int table_width, const int32_t *held,
+    int32_t *table_out, int64_t table_out_row_stride,
+    int prefix_rows, const int32_t *prefix_table, int64_t prefix_row_stride, int prefix_width,
+    const int32_t *prefix_held, int32_t *prefix_table_out, int64_t prefix_out_row_stride,
+    const int32_t *refs, int32_t *refs_out, int32_t *live,
+    void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream);
+
+/* Copy pages: page dst_pages[i] of every pool in dst_pools takes page src_pages[i]
+ * of the pool at its place in src_pools (the same rows, pieces and bytes; they may
+ * be the same pools), for i < count (lists on the device).  No page may be written
+ * twice, or written and read.  A pair with a page out of its pool is left out
+ * (ATTN_DEV_BAD_CACHE). */
+attn_status attn_varlen_cache_copy(int count, const int32_t *src_pages, const int32_t *dst_pages,
+                                   int num_src_pages, int num_dst_pages, int page_size,
+                                   const attn_pool *src_pools, const attn_pool *dst_pools, int npools,
+                                   int32_t *device_status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -37,12 +37,17 @@ from . import binding
 from .binding import AttnError
 
 DEV_BAD_CACHE = 0x40
+DEV_NO_PAGES = 0x80
 
 # in the order in which the native module takes their addresses
 EXPORTS = ("attn_varlen_rotary", "attn_varlen_cache_append", "attn_varlen_cache_fwd",
            "attn_varlen_cache_fwd_workspace_size", "attn_varlen_cache_weights",
            "attn_varlen_cache_weights_workspace_size", "attn_varlen_cache_evict",
-           "attn_varlen_cache_evict_workspace_size")
+           "attn_varlen_cache_evict_workspace_size", "attn_varlen_norm_rotary", "attn_varlen_norm_rotary_bwd",
+           "attn_varlen_norm_rotary_bwd_workspace_size", "attn_varlen_cache8_append", "attn_varlen_cache8_fwd",
+           "attn_varlen_cache8_fwd_workspace_size", "attn_varlen_cache_fork",
+           "attn_varlen_cache_fork_workspace_size", "attn_varlen_cache_compact",
+           "attn_varlen_cache_compact_workspace_size", "attn_varlen_cache_copy")
 
 _native = None
 
@@ -165,3 +170,100 @@ def attention_varlen_cache_evict(k_cache, v_cache, table, lens, scores, key_pos,
     return _run("evict", stream, k_cache, (
         k_cache, v_cache, table, lens, scores, key_pos, next_pos, budget, recent, scores_out, key_pos_out,
         lens_out, workspace, status))
+
+
+def attention_varlen_norm_rotary(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None,
+                                 pair_axis=None, interleaved=False, eps=1e-6, q_out=None, k_out=None,
+                                 stream=None):
+    """Norm every row (one head of one token) of packed q ``[T, Hq, d]`` and k
+    ``[T, Hkv, d]`` (or None) -- x / sqrt(mean(x^2) + eps) times fp32 weights
+    ``[d]`` (None: ones) -- and turn it by rotary positions in the same pass
+    (``inv_freq`` None: no turn; otherwise as attention_varlen_rotary).  Returns
+    (q_out, k_out); ``q_out = q`` and ``k_out = k`` work in place."""
+    return _run("norm", stream, q, (q, k, q_weight, k_weight, positions, inv_freq, pair_axis, interleaved, eps,
+                                    q_out, k_out))
+
+
+def attention_varlen_norm_rotary_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positions=None,
+                                     inv_freq=None, pair_axis=None, interleaved=False, eps=1e-6, dq=None,
+                                     dk=None, dq_weight=None, dk_weight=None, workspace=None, stream=None):
+    """The vector-Jacobian product of attention_varlen_norm_rotary: from the
+    gradients of its outputs and its inputs to (dq, dk, dq_weight, dk_weight); the
+    weights' gradients are fp32, summed over all rows in a fixed order (None for a
+    weight that is None).  ``dq`` may be ``dq_out``, ``dk`` ``dk_out``."""
+    return _run("norm_bwd", stream, q, (dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, pair_axis,
+                                        interleaved, eps, dq, dk, dq_weight, dk_weight, workspace))
+
+
+def attention_varlen_cache8_append(k, v, k_cache, v_cache, k_scale, v_scale, table, lens, cu_new,
+                                   positions=None, inv_freq=None, pair_axis=None, interleaved=False,
+                                   k_weight=None, eps=1e-6, norm=None, key_pos=None, lens_out=None,
+                                   status=None, stream=None):
+    """Write packed new tokens into a cache held in 8 bits.
+
+    Its pools are ``float8_e4m3fn`` tensors of pages, and ``k_scale``, ``v_scale``
+    fp32 ``[num_pages, page_size / block, Hkv]`` hold a factor for each block of
+    slots and head (blocks of 16 to 128 slots, a power of two).  As
+    attention_varlen_cache_append (without scores); with ``k_weight`` (or ``norm =
+    True``) the K rows are normed first (attention_varlen_norm_rotary), then
+    turned.  A block's scale is the smallest power of two that its largest value
+    needs; it grows with the block's new tokens, and what the block holds is
+    rounded again then.  K and V must be finite."""
+    _run("append8", stream, k, (k, v, k_cache, v_cache, k_scale, v_scale, table, lens, cu_new, positions, inv_freq,
+                                pair_axis, interleaved, norm, k_weight, eps, key_pos, lens_out, status))
+
+
+def attention_varlen_cache8_fwd(q, k_cache, v_cache, k_scale, v_scale, table, lens, cu_q, alibi_slopes=None,
+                                prefix_table=None, prefix_lens=None, cu_prefix=None, q_pos=None,
+                                key_pos=None, prefix_key_pos=None, causal=False, window_left=-1,
+                                window_right=-1, softcap=3.0, scale_multiplier=0.75, out=None, lse=None,
+                                workspace=None, status=None, stream=None):
+    """attention_varlen_cache_fwd over a cache held in 8 bits (see
+    attention_varlen_cache8_append): the keys and values are its e4m3 values times
+    their block's scale (finite, not negative), everything else is as there."""
+    return _run("fwd8", stream, q, (
+        q, k_cache, table, lens, cu_q, alibi_slopes, prefix_table, prefix_lens, cu_prefix, q_pos, key_pos,
+        prefix_key_pos, causal, window_left, window_right, softcap, scale_multiplier, v_cache, k_scale, v_scale,
+        out, lse, workspace, status))
+
+
+def attention_varlen_cache_fork(pools, table, lens, held, refs, parents, room=None, table_out=None,
+                                lens_out=None, held_out=None, refs_out=None, page_size=None, workspace=None,
+                                status=None, stream=None):
+    """Fork, free and reserve rows of a cache's table: row r goes on from what row
+    ``parents[r]`` held (-1: empty).
+
+    Rows that go on from the same one share its full pages (``refs`` ``[num_pages]``
+    counts the holders of a page, 0: free); the first of them keeps its other
+    pages, the others get a copy of the partly filled one, in all ``pools`` (a list:
+    K and V of every layer, scales too).  Rows that nobody goes on from give their
+    pages back, and every row gets pages for ``room[r]`` more slots, the lowest free
+    ones first.  ``held`` ``[rows]`` counts the pages in each row of the table.
+    ``parents[r] = r`` with some room reserves pages for an append, leaving a row
+    out frees it.
+
+    Returns (table_out, lens_out, held_out, refs_out), by default in place.  Too few
+    pages or too narrow a table (DEV_NO_PAGES in ``status``), or anything out of
+    range (DEV_BAD_CACHE), and nothing is changed at all."""
+    return _run("fork", stream, table, (pools, table, lens, held, refs, parents, room, table_out, lens_out, held_out,
+                                        refs_out, page_size, workspace, status))
+
+
+def attention_varlen_cache_compact(pools, table, held, refs, prefix_table=None, prefix_held=None,
+                                   table_out=None, refs_out=None, prefix_table_out=None, live=None,
+                                   page_size=None, workspace=None, status=None, stream=None):
+    """Pack the pages with ``refs > 0`` into the first ``live`` (int32 ``[1]``) ones:
+    the i-th free page below that number takes the i-th live page at or above it, in
+    all ``pools``; the tables' first ``held[r]`` entries and ``refs`` follow.  Returns
+    (live, table_out, refs_out, prefix_table_out), by default in place."""
+    return _run("compact", stream, table, (pools, table, held, refs, prefix_table, prefix_held, table_out, refs_out,
+                                           prefix_table_out, live, page_size, workspace, status))
+
+
+def attention_varlen_cache_copy(src_pools, src_pages, dst_pages, dst_pools=None, page_size=None, status=None,
+                                stream=None):
+    """Copy page ``src_pages[i]`` of every pool in ``src_pools`` to page
+    ``dst_pages[i]`` of the pool at its place in ``dst_pools`` (default: the same
+    pools).  No page may be written twice, or written and read; pairs with a page
+    out of its pool are left out."""
+    _run("copy", stream, src_pages, (src_pools, src_pages, dst_pages, dst_pools, page_size, status))

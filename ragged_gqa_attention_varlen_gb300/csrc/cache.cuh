@@ -130,6 +130,20 @@ size_t weights_workspace();
 cudaError_t launch_fwd(const CacheParams& p, cudaStream_t s);
 cudaError_t launch_weights(const CacheParams& p, cudaStream_t s);
 
+// Scales of a pool held in 8 bits: [num_pages, page_size / block, Hkv].
+struct Scales {
+  float* base;
+  int64_t page, block, head;
+};
+
+// Attention over a cache held in 8 bits (k, v of `c`: pages of e4m3 values).
+struct Cache8Params {
+  CacheParams c;
+  Scales ks, vs;
+  int block_log2;
+};
+cudaError_t launch_fwd8(const Cache8Params& p, cudaStream_t s);
+
 // Rotary positions: x[H][d] rows of up to two tensors, or new K rows on their
 // way into the cache.
 struct RotaryTable {
@@ -155,6 +169,28 @@ struct RotaryParams {
   RotaryTensor t[2];  // t[1].H = 0: only one
 };
 
+// Norms of the rows of up to two tensors, with the turn in the same pass.
+struct NormTensor {
+  const void* x;
+  int64_t ts, hs;
+  const void* dy;        // backward: the gradient of the output
+  int64_t dts, dhs;
+  const float* weight;   // [d], or null: ones
+  void* out;             // the output, or (backward) the gradient of x
+  int64_t ots, ohs;
+  float* dweight;        // backward: [d], or null
+  int H;
+};
+
+struct NormParams {
+  int dtype, d;
+  int64_t T;
+  float eps;
+  RotaryTable r;  // r.inv_freq null: no turn
+  NormTensor t[2];
+  float* partial;  // backward: sums of a block [blocks, d]
+};
+
 struct AppendParams {
   int dtype, B, Hkv, d;
   int64_t T;
@@ -174,6 +210,15 @@ struct AppendParams {
   int64_t sc_rs, sc_hs;
   int32_t* lens_out;
   int32_t* status;
+};
+
+struct Append8Params {
+  AppendParams a;  // (k, v: pages of e4m3 values; strides in elements)
+  Scales ks, vs;
+  int block, block_log2;
+  const float* k_weight;  // [d]: K rows are normed first; null: not, unless `norm`
+  int norm;
+  float eps;
 };
 
 struct EvictParams {
@@ -199,9 +244,76 @@ struct EvictParams {
   int32_t* status;
 };
 
+// A pool of pages as the kernels that move whole pages see it: `rows` rows a
+// page, each of `pieces` runs of `bytes` contiguous bytes; strides in bytes.
+struct MovedPool {
+  const void* src;
+  void* dst;
+  int64_t src_page, src_row, src_piece, dst_page, dst_row, dst_piece;
+  int rows, pieces, bytes;
+  int flat;  // a page is one run of bytes in both
+  int wide;  // everything is a multiple of 16 bytes (of 4 otherwise)
+};
+constexpr int kPoolsPerLaunch = 32;
+struct MovedPools {
+  MovedPool pool[kPoolsPerLaunch];
+  int n;
+};
+
+// One move of the list in a workspace: page dst takes the first `used` of the
+// page_size slots of page src.
+struct Move {
+  int src, dst, used, pad;
+};
+
+struct ForkParams {
+  int R, W, N;  // rows and width of the table, pages
+  int page_log2;
+  const int32_t* table;
+  int64_t table_rs;
+  const int32_t *lens, *held, *refs, *parents, *room;
+  int32_t* table_out;
+  int64_t to_rs;
+  int32_t *lens_out, *held_out, *refs_out;
+  uint8_t* ws;
+  int32_t* status;
+};
+
+// Tables whose pages a compaction renumbers.
+struct CompactTable {
+  int R, W;
+  const int32_t* table;
+  int64_t rs;
+  const int32_t* held;
+  int32_t* out;
+  int64_t out_rs;
+};
+struct CompactParams {
+  int N, page_log2;
+  const int32_t* refs;
+  int32_t* refs_out;
+  int32_t* live;
+  CompactTable t[2];  // t[1].R = 0: only one
+  uint8_t* ws;
+  int32_t* status;
+};
+
+size_t fork_workspace(int R, int W, int N);
+size_t compact_workspace(int N);
+// pools: n of them in host memory, moved within themselves (src = dst)
+cudaError_t launch_fork(const ForkParams& p, const MovedPool* pools, int n, cudaStream_t s);
+cudaError_t launch_compact(const CompactParams& p, const MovedPool* pools, int n, cudaStream_t s);
+// count pairs (src[i], dst[i]) on the device
+cudaError_t launch_copy_pages(const int32_t* src, const int32_t* dst, int count, int src_pages,
+                              int dst_pages, const MovedPool* pools, int n, int32_t* status,
+                              cudaStream_t s);
 size_t evict_workspace(int S, int Hkv, int64_t slots, int budget);
 cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t s);
+size_t norm_bwd_workspace(int64_t T, int Hq, int Hkv, int d);
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_append8(const Append8Params& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 
 }  // namespace kv

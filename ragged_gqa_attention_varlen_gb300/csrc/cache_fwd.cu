@@ -204,6 +204,22 @@ size_t fwd_workspace(int B, int P, int Hq, int Hkv, int d, int64_t total_q) {
   return fwd_ws(B, P, Hq, Hkv, d, total_q).total;
 }
 
+// A programmatic dependent of the tile kernel: its blocks are placed early and
+// wait for the results.
+cudaError_t launch_join(const CacheParams& p, const FwdWs& w, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.total_q), (p.Hq + kHeadsJ - 1) / kHeadsJ);
+  cfg.blockDim = dim3(kWarpsJ * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto k = p.d == 160 ? join_for<160>(p) : (p.d == 128 ? join_for<128>(p) : join_for<64>(p));
+  return cudaLaunchKernelEx(&cfg, k, p, w);
+}
+
 cudaError_t launch_fwd(const CacheParams& call, cudaStream_t s) {
   CacheParams p = call;
   // a piece's start takes about 7000 clk where a step takes 3600 (shared
@@ -222,19 +238,7 @@ cudaError_t launch_fwd(const CacheParams& call, cudaStream_t s) {
                   : p.d == 128 ? launch_fwd_d<128>(p, w, tk, tkt, tv, grid, s)
                                : launch_fwd_d<64>(p, w, tk, tkt, tv, grid, s);
   if (e != cudaSuccess) return e;
-  // a programmatic dependent of the tile kernel: its blocks are placed early
-  // and wait for the results
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.total_q), (p.Hq + kHeadsJ - 1) / kHeadsJ);
-  cfg.blockDim = dim3(kWarpsJ * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  auto k = p.d == 160 ? join_for<160>(p) : (p.d == 128 ? join_for<128>(p) : join_for<64>(p));
-  return cudaLaunchKernelEx(&cfg, k, p, w);
+  return launch_join(p, w, s);
 }
 
 }  // namespace kv

@@ -1,0 +1,384 @@
+// norm.cu -- norms of the rows of q and k with the turn by rotary positions in
+// the same pass, and the gradients.
+//
+// A row x of d features (one head of one token) with weights w:
+//   r = (mean(x^2) + eps)^(-1/2),  n_i = x_i r w_i,  y = turn(n)
+// and with g = turn^-1(dy), h_i = g_i w_i:
+//   dx_i = r (h_i - x_i r^2 mean(h x)),  dw_i = sum over the rows of g_i x_i r.
+// Everything between the load and the store is fp32; a row is rounded once.
+//
+// Bound by memory: the forward reads and writes each row once, the backward
+// reads x and dy and writes dx.  A row lies in the registers of four to ten
+// lanes (rowfrag.cuh), so its sums take a few shuffles and nothing is read
+// twice; a block takes runs of tokens with all their heads, so one pair's sine
+// serves them all.  The weights' gradients are summed per lane over the rows of a
+// block, then over the lanes and warps, and a second kernel adds the blocks in
+// their order: no atomics, the same bits every time.
+#include "../../include/attn_varlen.h"
+#include "rowfrag.cuh"
+
+namespace attn {
+namespace kv {
+namespace {
+
+constexpr int kSms = 152;
+// Warps of a block: rows that are turned through shared memory (VEC false) need
+// a buffer each.
+template <bool VEC>
+constexpr int warps_n() { return VEC ? 8 : 4; }
+
+// How one tensor's rows are cut into jobs: runs of ntok tokens x hs heads.
+struct Jobs {
+  int ntok, hs, splits;  // splits: head ranges of a run
+  int64_t count;
+};
+Jobs jobs_of(int64_t T, int H, int rows_min) {
+  Jobs j = {1, 1, 1, 0};
+  if (H < 1) return j;
+  // rows of a job: enough jobs for four rounds of the SMs, or as few rows as one
+  // pass of a block takes
+  int64_t rows = T * H / (4 * kSms);
+  rows = rows < rows_min ? rows_min : (rows > 512 ? 512 : rows);
+  if (H <= rows) {
+    const int64_t n = rows / H;
+    j.ntok = static_cast<int>(n > kMaxTokensR ? kMaxTokensR : n);
+    j.hs = H;
+  } else {
+    j.splits = static_cast<int>((H + rows - 1) / rows);
+    j.hs = (H + j.splits - 1) / j.splits;
+    j.splits = (H + j.hs - 1) / j.hs;
+  }
+  j.count = (T + j.ntok - 1) / j.ntok * j.splits;
+  return j;
+}
+
+struct NormPlan {
+  Jobs job[2];
+  int blocks[2];  // backward: blocks of each tensor
+};
+
+// A lane's part of a row.
+template <bool BF16, bool VEC>
+struct RowOps {
+  uint4 raw[2];
+  __device__ __forceinline__ void load(const uint16_t* x, const Units& u) {
+    raw[0] = __ldcs(reinterpret_cast<const uint4*>(x + u.a));
+    raw[1] = __ldcs(reinterpret_cast<const uint4*>(x + u.b));
+  }
+  __device__ __forceinline__ void zero() { raw[0] = raw[1] = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void unpack(float (&v)[2][8]) const {
+    unpack8<BF16>(raw[0], v[0]);
+    unpack8<BF16>(raw[1], v[1]);
+  }
+  __device__ __forceinline__ static void store(uint16_t* y, const float (&v)[2][8], const Units& u) {
+    __stcs(reinterpret_cast<uint4*>(y + u.a), pack8<BF16>(v[0]));
+    __stcs(reinterpret_cast<uint4*>(y + u.b), pack8<BF16>(v[1]));
+  }
+  __device__ __forceinline__ static void weights(const float* w, float (&v)[2][8], const Units& u) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[0][e] = w ? __ldg(w + u.a + e) : 1.f;
+      v[1][e] = w ? __ldg(w + u.b + e) : 1.f;
+    }
+  }
+  __device__ __forceinline__ static void turn(float (&v)[2][8], float* row, int j, int pairs, bool interleaved,
+                                              const float2* cs) {
+    auto at = [&](int i) { return cs[i]; };
+    if (VEC)
+      turn_item(v[0], v[1], j, pairs, interleaved, at);
+    else
+      turn_row(v, row, j, pairs, interleaved, at);
+  }
+};
+
+struct Run {
+  int64_t tok0;
+  int ntok, h0, nh;
+};
+__device__ __forceinline__ Run run_of(const Jobs& j, int64_t T, int H, int64_t i) {
+  Run r;
+  const int64_t run = j.splits > 1 ? i / j.splits : i;
+  r.tok0 = run * j.ntok;
+  r.ntok = static_cast<int>(min(static_cast<int64_t>(j.ntok), T - r.tok0));
+  r.h0 = static_cast<int>(i - run * j.splits) * j.hs;
+  r.nh = min(j.hs, H - r.h0);
+  return r;
+}
+
+// The lane's row of a run, by passes of the block: token in the run, head.
+struct RowAt {
+  int tok, h;
+  bool valid;
+};
+template <int D>
+__device__ __forceinline__ RowAt row_at(const Run& run, int r0, float inv_nh) {
+  using S = RowShape<D>;
+  const int g = (threadIdx.x & 31) / S::kLanes, row = r0 + g;
+  RowAt r;
+  r.valid = g < S::kRowsWarp && row < run.ntok * run.nh;
+  r.tok = r.valid ? quotient(row, inv_nh) : 0;
+  r.h = run.h0 + (r.valid ? row - r.tok * run.nh : 0);
+  return r;
+}
+
+template <int D, bool VEC>
+struct NormSmem {
+  Turns turns;
+  // rows that are turned through shared memory (one more a warp for idle lanes)
+  float rows[VEC ? 1 : warps_n<VEC>() * (RowShape<D>::kRowsWarp + 1)][VEC ? 1 : D + 4];
+  __device__ __forceinline__ float* row() {
+    using S = RowShape<D>;
+    if (VEC) return nullptr;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    return rows[warp * (S::kRowsWarp + 1) + lane / S::kLanes];
+  }
+};
+
+template <bool BF16, int D, bool VEC>
+__global__ void __launch_bounds__(warps_n<VEC>() * 32)
+    norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormPlan plan) {
+  using S = RowShape<D>;
+  using Ops = RowOps<BF16, VEC>;
+  constexpr int kStep = warps_n<VEC>() * S::kRowsWarp;
+  __shared__ NormSmem<D, VEC> sm;
+  const int j = (threadIdx.x & 31) % S::kLanes;
+  const bool inter = p.r.interleaved;
+  const int pairs = p.r.inv_freq ? p.r.pairs : 0;
+  const Units at = item_units<VEC>(j, pairs, inter);
+  for (int64_t i = blockIdx.x; i < plan.job[0].count + plan.job[1].count; i += gridDim.x) {
+    const int which = i >= plan.job[0].count;
+    const NormTensor& t = p.t[which];
+    const Run run = run_of(plan.job[which], p.T, t.H, which ? i - plan.job[0].count : i);
+    const uint16_t* x0 = static_cast<const uint16_t*>(t.x) + run.tok0 * t.ts;
+    uint16_t* y0 = static_cast<uint16_t*>(t.out) + run.tok0 * t.ots;
+    const float inv_nh = 1.f / run.nh;
+    const int all = run.ntok * run.nh;
+    int r0 = (threadIdx.x >> 5) * S::kRowsWarp;
+    Ops next;
+    RowAt row = row_at<D>(run, r0, inv_nh);
+    next.zero();
+    if (row.valid) next.load(x0 + row.tok * t.ts + row.h * t.hs, at);
+    if (pairs) {
+      __syncthreads();
+      fill_turns(p.r, run.tok0, run.ntok, sm.turns);
+    }
+    float w[2][8];
+    Ops::weights(t.weight, w, at);
+    if (pairs) __syncthreads();
+    while (r0 < all) {
+      float v[2][8];
+      next.unpack(v);
+      const RowAt now = row;
+      r0 += kStep;
+      row = row_at<D>(run, r0, inv_nh);
+      if (row.valid) next.load(x0 + row.tok * t.ts + row.h * t.hs, at);
+      float sq = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq = fmaf(v[0][e], v[0][e], fmaf(v[1][e], v[1][e], sq));
+      const float r = 1.f / sqrtf(row_sum<D>(sq) * (1.f / D) + p.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[0][e] *= r * w[0][e];
+        v[1][e] *= r * w[1][e];
+      }
+      if (pairs) Ops::turn(v, sm.row(), j, pairs, inter, sm.turns.cs[now.tok]);
+      if (now.valid) Ops::store(y0 + now.tok * t.ots + now.h * t.ohs, v, at);
+    }
+  }
+}
+
+// Blocks [0, blocks[0]) take q, the others k.
+template <bool BF16, int D, bool VEC>
+__global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 2 : 1)
+    norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormPlan plan) {
+  using S = RowShape<D>;
+  using Ops = RowOps<BF16, VEC>;
+  constexpr int kWarps = warps_n<VEC>(), kStep = kWarps * S::kRowsWarp;
+  __shared__ NormSmem<D, VEC> sm;
+  __shared__ float sums[kWarps][D];
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = lane % S::kLanes;
+  const bool inter = p.r.interleaved;
+  const int pairs = p.r.inv_freq ? p.r.pairs : 0;
+  const Units at = item_units<VEC>(j, pairs, inter);
+  const int which = static_cast<int>(blockIdx.x) >= plan.blocks[0];
+  const NormTensor& t = p.t[which];
+  const Jobs& jobs = plan.job[which];
+  float w[2][8], dw[2][8];
+  Ops::weights(t.weight, w, at);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
+  for (int64_t i = blockIdx.x - (which ? plan.blocks[0] : 0); i < jobs.count; i += plan.blocks[which]) {
+    const Run run = run_of(jobs, p.T, t.H, i);
+    const uint16_t* x0 = static_cast<const uint16_t*>(t.x) + run.tok0 * t.ts;
+    const uint16_t* d0 = static_cast<const uint16_t*>(t.dy) + run.tok0 * t.dts;
+    uint16_t* y0 = static_cast<uint16_t*>(t.out) + run.tok0 * t.ots;
+    const float inv_nh = 1.f / run.nh;
+    const int all = run.ntok * run.nh;
+    int r0 = warp * S::kRowsWarp;
+    Ops next, dnext;
+    RowAt row = row_at<D>(run, r0, inv_nh);
+    next.zero();
+    dnext.zero();
+    auto load = [&] {
+      if (row.valid) {
+        next.load(x0 + row.tok * t.ts + row.h * t.hs, at);
+        dnext.load(d0 + row.tok * t.dts + row.h * t.dhs, at);
+      } else {  // (nothing of it may reach the sums)
+        dnext.zero();
+      }
+    };
+    load();
+    if (pairs) {
+      __syncthreads();
+      fill_turns(p.r, run.tok0, run.ntok, sm.turns);
+      __syncthreads();
+    }
+    while (r0 < all) {
+      float x[2][8], g[2][8];
+      next.unpack(x);
+      dnext.unpack(g);
+      const RowAt now = row;
+      r0 += kStep;
+      row = row_at<D>(run, r0, inv_nh);
+      load();
+      if (pairs) Ops::turn(g, sm.row(), j, pairs, inter, sm.turns.cs[now.tok]);
+      float sq = 0.f, hx = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sq = fmaf(x[u][e], x[u][e], sq);
+          hx = fmaf(g[u][e] * w[u][e], x[u][e], hx);
+        }
+      const float r = 1.f / sqrtf(row_sum<D>(sq) * (1.f / D) + p.eps);
+      const float c = row_sum<D>(hx) * (1.f / D) * r * r;  // r^2 mean(h x)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float gr = g[u][e] * r;
+          dw[u][e] = fmaf(now.valid ? gr : 0.f, x[u][e], dw[u][e]);
+          g[u][e] = fmaf(gr, w[u][e], -x[u][e] * (r * c));
+        }
+      if (now.valid) Ops::store(y0 + now.tok * t.ots + now.h * t.ohs, g, at);
+    }
+  }
+  if (!t.dweight) return;
+  // over the warp's rows, then over the warps, each in a fixed order
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float s = 0.f;
+#pragma unroll
+      for (int g = 0; g < S::kRowsWarp; ++g) s += __shfl_sync(0xffffffffu, dw[u][e], g * S::kLanes + j);
+      if (lane < S::kLanes) sums[warp][(u ? at.b : at.a) + e] = s;
+    }
+  __syncthreads();
+  for (int f = threadIdx.x; f < D; f += kWarps * 32) {
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) s += sums[q][f];
+    p.partial[static_cast<int64_t>(blockIdx.x) * D + f] = s;
+  }
+}
+
+// dweight of tensor blockIdx.y, features 32 blockIdx.x and up: 32 warps add a
+// part of the blocks each, then one adds the warps.
+__global__ void __launch_bounds__(1024)
+    norm_join_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormPlan plan) {
+  __shared__ float sums[32][33];
+  const int which = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int f = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float* out = p.t[which].dweight;
+  if (!out) return;
+  const float* part = p.partial + static_cast<int64_t>(which ? plan.blocks[0] : 0) * p.d + f;
+  float s = 0.f;
+  for (int b = warp; b < plan.blocks[which]; b += 32) s += part[static_cast<int64_t>(b) * p.d];
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp) return;
+  s = 0.f;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) s += sums[q][lane];
+  out[f] = s;
+}
+
+template <template <bool, int, bool> class F, class... A>
+void pick(const NormParams& p, bool vec, A... a, unsigned grid, cudaStream_t s) {
+  const bool b = p.dtype == 1;
+#define ATTN_PICK(D)                                      \
+  if (p.d == D)                                           \
+    b ? (vec ? F<true, D, true>::go(a..., grid, s) : F<true, D, false>::go(a..., grid, s)) \
+      : (vec ? F<false, D, true>::go(a..., grid, s) : F<false, D, false>::go(a..., grid, s));
+  ATTN_PICK(64)
+  ATTN_PICK(128)
+  ATTN_PICK(160)
+#undef ATTN_PICK
+}
+template <bool B, int D, bool V>
+struct Fwd {
+  static void go(const NormParams& p, const NormPlan& n, unsigned grid, cudaStream_t s) {
+    norm_kernel<B, D, V><<<grid, warps_n<V>() * 32, 0, s>>>(p, n);
+  }
+};
+template <bool B, int D, bool V>
+struct Bwd {
+  static void go(const NormParams& p, const NormPlan& n, unsigned grid, cudaStream_t s) {
+    norm_bwd_kernel<B, D, V><<<grid, warps_n<V>() * 32, 0, s>>>(p, n);
+  }
+};
+
+NormPlan plan_of(int64_t T, int Hq, int Hkv, int d) {
+  NormPlan n;
+  const int rows = 8 * (32 / (d / 16));  // of a pass
+  n.job[0] = jobs_of(T, Hq, rows);
+  n.job[1] = jobs_of(T, Hkv, rows);
+  // backward: the blocks in proportion to the rows, one at least
+  const int most = 2 * kSms;  // as many as are resident
+  int64_t k = Hkv > 0 ? (static_cast<int64_t>(most) * Hkv + Hq + Hkv - 1) / (Hq + Hkv) : 0;
+  const int64_t q = most - k < 1 ? 1 : most - k;
+  n.blocks[0] = static_cast<int>(n.job[0].count < q ? n.job[0].count : q);
+  n.blocks[1] = static_cast<int>(n.job[1].count < k ? n.job[1].count : k);
+  return n;
+}
+
+}  // namespace
+
+size_t norm_bwd_workspace(int64_t T, int Hq, int Hkv, int d) {
+  const NormPlan n = plan_of(T, Hq, Hkv, d);
+  const size_t bytes = static_cast<size_t>(n.blocks[0] + n.blocks[1]) * d * sizeof(float);
+  return bytes < 256 ? 256 : bytes;
+}
+
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
+  const NormPlan n = plan_of(p.T, p.t[0].H, p.t[1].H, p.d);
+  const int64_t all = n.job[0].count + n.job[1].count, most = 16 * kSms;
+  pick<Fwd, const NormParams&, const NormPlan&>(p, vector_pairs(p.r.inv_freq ? p.r.pairs : 0, p.r.interleaved), p, n,
+                                                static_cast<unsigned>(all < most ? all : most), s);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s) {
+  const NormPlan n = plan_of(p.T, p.t[0].H, p.t[1].H, p.d);
+  if (p.T > 0) pick<Bwd, const NormParams&, const NormPlan&>(p, vector_pairs(p.r.inv_freq ? p.r.pairs : 0, p.r.interleaved), p, n,
+                                                static_cast<unsigned>(n.blocks[0] + n.blocks[1]), s);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || (!p.t[0].dweight && !p.t[1].dweight)) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.d / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_join_kernel, p, n);
+}
+
+}  // namespace kv
+}  // namespace attn

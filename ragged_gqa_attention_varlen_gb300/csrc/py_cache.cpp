@@ -16,6 +16,7 @@
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "../../include/attn_varlen.h"
 
@@ -30,6 +31,17 @@ struct Fns {
   decltype(&attn_varlen_cache_weights_workspace_size) weights_ws;
   decltype(&attn_varlen_cache_evict) evict;
   decltype(&attn_varlen_cache_evict_workspace_size) evict_ws;
+  decltype(&attn_varlen_norm_rotary) norm;
+  decltype(&attn_varlen_norm_rotary_bwd) norm_bwd;
+  decltype(&attn_varlen_norm_rotary_bwd_workspace_size) norm_bwd_ws;
+  decltype(&attn_varlen_cache8_append) append8;
+  decltype(&attn_varlen_cache8_fwd) fwd8;
+  decltype(&attn_varlen_cache8_fwd_workspace_size) fwd8_ws;
+  decltype(&attn_varlen_cache_fork) fork;
+  decltype(&attn_varlen_cache_fork_workspace_size) fork_ws;
+  decltype(&attn_varlen_cache_compact) compact;
+  decltype(&attn_varlen_cache_compact_workspace_size) compact_ws;
+  decltype(&attn_varlen_cache_copy) copy;
   decltype(&attn_status_string) status_string;
 } fn;
 PyObject* attn_error = nullptr;  // the exception of a negative status
@@ -132,8 +144,9 @@ Pool pool(const Call& c, const Tensor& t, const char* name, at::ScalarType type)
   c.here(t, name);
   if (t.scalar_type() != type || t.dim() != 4 || t.stride(3) != 1 || t.size(0) > INT32_MAX ||
       t.size(1) > 1024)
-    bad(std::string(name) + " must be [num_pages, page_size, Hkv, d] of the call's 16-bit type with a "
-        "contiguous feature axis and at most 1024 rows a page");
+    bad(std::string(name) + " must be [num_pages, page_size, Hkv, d] of " +
+        (type == at::kFloat8_e4m3fn ? "float8_e4m3fn" : "the call's 16-bit type") +
+        " with a contiguous feature axis and at most 1024 rows a page");
   const int64_t ps = t.size(1), h = t.size(2), d = t.size(3);
   return {t.data_ptr(), used(t.stride(0), t.size(0), ps * h * d), used(t.stride(1), ps, h * d),
           used(t.stride(2), h, d)};
@@ -369,13 +382,13 @@ struct Read {
   int causal, wl, wr;
   float cap_value, scale;
 };
-Read read_args(const Call& c, const Tensor& q, PyObject* const* a) {
+Read read_args(const Call& c, const Tensor& q, PyObject* const* a, bool bytes = false) {
   Read r;
   r.dt = dtype_of(q);
   r.type = q.scalar_type();
   if (q.dim() != 3 || !head_dim(q.size(2))) bad("q must be [tokens, heads, d] with d 64, 128 or 160");
   const Tensor& kc = tensor(a[0], "k_cache");
-  r.k = pool(c, kc, "k_cache", r.type);
+  r.k = pool(c, kc, "k_cache", bytes ? at::kFloat8_e4m3fn : r.type);
   r.T = q.size(0);
   const int64_t Hq = q.size(1), Hkv = kc.size(2), d = q.size(2);
   if (Hkv < 1 || Hq < 1 || Hq % Hkv || kc.size(3) != d || Hq > INT32_MAX)
@@ -520,6 +533,333 @@ PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+const float* weight(const Call& c, Maybe t, const char* name, int64_t d) {
+  if (!t) return nullptr;
+  c.here(*t, name);
+  if (t->scalar_type() != at::kFloat || t->dim() != 1 || t->size(0) != d || !t->is_contiguous())
+    bad(std::string(name) + " must be a contiguous fp32 CUDA vector of " + std::to_string(d));
+  return t->data_ptr<float>();
+}
+
+// (q, k, q_weight, k_weight, positions, inv_freq, pair_axis, interleaved, eps, q_out, k_out)
+PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    const Tensor& q = tensor(a[0], "q");
+    Maybe k = maybe(a[1], "k");
+    const Call c(q);
+    const attn_dtype dt = dtype_of(q);
+    if (q.dim() != 3 || !head_dim(q.size(2))) bad("q must be [tokens, heads, d] with d 64, 128 or 160");
+    const int64_t T = q.size(0), Hq = q.size(1), d = q.size(2), Hkv = k && k->dim() == 3 ? k->size(1) : 0;
+    const auto type = q.scalar_type();
+    const Rows x = rows16(c, q, "q", type, Hq, d, T);
+    const Rows y = k ? rows16(c, *k, "k", type, Hkv, d, T) : Rows();
+    const float *qw = weight(c, maybe(a[2], "q_weight"), "q_weight", d), *kw = weight(c, maybe(a[3], "k_weight"), "k_weight", d);
+    const Rotary r = rotary(c, maybe(a[4], "positions"), maybe(a[5], "inv_freq"), maybe(a[6], "pair_axis"), d, T);
+    Maybe qo = maybe(a[9], "q_out"), ko = maybe(a[10], "k_out");
+    if (ko && !k) bad("k_out without k");
+    const Tensor nq = qo ? *qo : c.make({T, Hq, d}, type);
+    const Tensor nk = !k ? Tensor() : (ko ? *ko : c.make({T, Hkv, d}, type));
+    const Rows u = rows16(c, nq, "q_out", type, Hq, d, T);
+    const Rows v = k ? rows16(c, nk, "k_out", type, Hkv, d, T) : Rows();
+    const int inter = truth(a[7]);
+    const float eps = static_cast<float>(real(a[8]));
+    if (T > 0)
+      check(fn.norm(dt, T, static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d), x.p, x.ts, x.hs, y.p,
+                    y.ts, y.hs, qw, kw, eps, r.pos, r.axis_stride, r.axes, r.freq, r.axis, r.pairs, inter, u.p, u.ts,
+                    u.hs, v.p, v.ts, v.hs, c.stream()));
+    return Py_BuildValue("(NN)", result(a[9], nq), k ? result(a[10], nk) : kept(Py_None));
+  });
+}
+
+// (dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, pair_axis, interleaved,
+//  eps, dq, dk, dq_weight, dk_weight, workspace)
+PyObject* py_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&]() -> PyObject* {
+    const Tensor& q = tensor(a[2], "q");
+    Maybe k = maybe(a[3], "k"), dko = maybe(a[1], "dk_out");
+    const Call c(q);
+    const attn_dtype dt = dtype_of(q);
+    if (q.dim() != 3 || !head_dim(q.size(2))) bad("q must be [tokens, heads, d] with d 64, 128 or 160");
+    if ((k != nullptr) != (dko != nullptr)) bad("k and dk_out belong together");
+    const int64_t T = q.size(0), Hq = q.size(1), d = q.size(2), Hkv = k && k->dim() == 3 ? k->size(1) : 0;
+    const auto type = q.scalar_type();
+    const Rows x = rows16(c, q, "q", type, Hq, d, T), dx = rows16(c, tensor(a[0], "dq_out"), "dq_out", type, Hq, d, T);
+    const Rows y = k ? rows16(c, *k, "k", type, Hkv, d, T) : Rows();
+    const Rows dy = k ? rows16(c, *dko, "dk_out", type, Hkv, d, T) : Rows();
+    const float *qw = weight(c, maybe(a[4], "q_weight"), "q_weight", d), *kw = weight(c, maybe(a[5], "k_weight"), "k_weight", d);
+    if (kw && !k) bad("k_weight without k");
+    const Rotary r = rotary(c, maybe(a[6], "positions"), maybe(a[7], "inv_freq"), maybe(a[8], "pair_axis"), d, T);
+    Maybe oq = maybe(a[11], "dq"), ok = maybe(a[12], "dk"), wq = maybe(a[13], "dq_weight"), wk = maybe(a[14], "dk_weight");
+    if (ok && !k) bad("dk without k");
+    if ((wq && !qw) || (wk && !kw)) bad("the gradient of a weight that the call does not have");
+    const Tensor nq = oq ? *oq : c.make({T, Hq, d}, type);
+    const Tensor nk = !k ? Tensor() : (ok ? *ok : c.make({T, Hkv, d}, type));
+    const Tensor nwq = !qw ? Tensor() : (wq ? *wq : c.make({d}, at::kFloat));
+    const Tensor nwk = !kw ? Tensor() : (wk ? *wk : c.make({d}, at::kFloat));
+    const Rows u = rows16(c, nq, "dq", type, Hq, d, T);
+    const Rows v = k ? rows16(c, nk, "dk", type, Hkv, d, T) : Rows();
+    float* gq = const_cast<float*>(weight(c, qw ? &nwq : nullptr, "dq_weight", d));
+    float* gk = const_cast<float*>(weight(c, kw ? &nwk : nullptr, "dk_weight", d));
+    const int inter = truth(a[9]);
+    const float eps = static_cast<float>(real(a[10]));
+    const Workspace w = workspace(c, maybe(a[15], "workspace"),
+                                  fn.norm_bwd_ws(T, static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d)));
+    check(fn.norm_bwd(dt, T, static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d), dx.p, dx.ts, dx.hs, dy.p,
+                      dy.ts, dy.hs, x.p, x.ts, x.hs, y.p, y.ts, y.hs, qw, kw, eps, r.pos, r.axis_stride, r.axes, r.freq,
+                      r.axis, r.pairs, inter, u.p, u.ts, u.hs, v.p, v.ts, v.hs, gq, gk, w.p, w.bytes, c.stream()));
+    return Py_BuildValue("(NNNN)", result(a[11], nq), k ? result(a[12], nk) : kept(Py_None),
+                         qw ? result(a[13], nwq) : kept(Py_None), kw ? result(a[14], nwk) : kept(Py_None));
+  });
+}
+
+struct BlockScales {  // [num_pages, page_size / block, Hkv]
+  float* p;
+  int64_t ps, bs, hs;
+  int block;
+};
+BlockScales block_scales(const Call& c, const Tensor& t, const char* name, const Tensor& cache) {
+  c.here(t, name);
+  if (t.scalar_type() != at::kFloat || t.dim() != 3 || t.size(0) != cache.size(0) || t.size(1) < 1 ||
+      cache.size(1) % t.size(1) || t.size(2) != cache.size(2))
+    bad(std::string(name) + " must be fp32 [" + std::to_string(cache.size(0)) + ", page_size / block, " +
+        std::to_string(cache.size(2)) + "] on the device");
+  return {t.data_ptr<float>(), t.stride(0), t.stride(1), t.stride(2), static_cast<int>(cache.size(1) / t.size(1))};
+}
+
+// (k, v, k_cache, v_cache, k_scale, v_scale, table, lens, cu_new, positions, inv_freq,
+//  pair_axis, interleaved, norm, k_weight, eps, key_pos, lens_out, status)
+PyObject* py_append8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 19, [&]() -> PyObject* {
+    const Tensor& k = tensor(a[0], "k");
+    const Tensor& v = tensor(a[1], "v");
+    const Call c(k);
+    const attn_dtype dt = dtype_of(k);
+    if (k.dim() != 3 || !head_dim(k.size(2))) bad("k must be [tokens, heads, d] with d 64, 128 or 160");
+    const int64_t T = k.size(0), H = k.size(1), d = k.size(2);
+    const auto type = k.scalar_type();
+    const Tensor &kc = tensor(a[2], "k_cache"), &vc = tensor(a[3], "v_cache"), &lens = tensor(a[7], "lens");
+    const Pool kp = pool(c, kc, "k_cache", at::kFloat8_e4m3fn), vp = pool(c, vc, "v_cache", at::kFloat8_e4m3fn);
+    if (kc.sizes() != vc.sizes() || kc.size(2) != H || kc.size(3) != d)
+      bad("k_cache and v_cache must both be [num_pages, page_size, " + std::to_string(H) + ", " + std::to_string(d) + "]");
+    const BlockScales ks = block_scales(c, tensor(a[4], "k_scale"), "k_scale", kc);
+    const BlockScales vs = block_scales(c, tensor(a[5], "v_scale"), "v_scale", vc);
+    if (ks.block != vs.block) bad("k_scale and v_scale must have the same blocks");
+    const Tab t = table(c, tensor(a[6], "table"), lens, "table");
+    const int64_t cap = t.width * kc.size(1);
+    const Rows x = rows16(c, k, "k", type, H, d, T), y = rows16(c, v, "v", type, H, d, T);
+    const Rotary r = rotary(c, maybe(a[9], "positions"), maybe(a[10], "inv_freq"), maybe(a[11], "pair_axis"), d, T);
+    const float* kw = weight(c, maybe(a[14], "k_weight"), "k_weight", d);
+    const auto pos = slots<int32_t>(c, maybe(a[16], "key_pos"), "key_pos", t.rows, H, cap);
+    Maybe lo = maybe(a[17], "lens_out");
+    int32_t* lens_out = lo ? const_cast<int32_t*>(vec(c, *lo, "lens_out", t.rows)) : nullptr;
+    if (lens_out && lens_out == t.lens) bad("lens_out must not be lens");
+    const int inter = truth(a[12]), norm = a[13] == Py_None ? kw != nullptr : truth(a[13]);
+    if (kw && !norm) bad("k_weight without the norm");
+    check(fn.append8(dt, static_cast<int>(t.rows), static_cast<int>(H), static_cast<int>(d), T, x.p, x.ts, x.hs, y.p,
+                     y.ts, y.hs, kp.p, kp.ps, kp.ss, kp.hs, vp.p, vp.ps, vp.ss, vp.hs, ks.p, ks.ps, ks.bs, ks.hs, vs.p,
+                     vs.ps, vs.bs, vs.hs, static_cast<int>(kc.size(0)), static_cast<int>(kc.size(1)), ks.block, t.p,
+                     t.rs, t.width, t.lens, vec(c, tensor(a[8], "cu_new"), "cu_new", t.rows + 1), r.pos, r.axis_stride,
+                     r.axes, r.freq, r.axis, r.pairs, inter, norm, kw, static_cast<float>(real(a[15])), pos.p, pos.rs,
+                     pos.hs, lens_out, status_of(c, maybe(a[18], "status")), c.stream()));
+    Py_RETURN_NONE;
+  });
+}
+
+// (q, the 16 of read_args, v_cache, k_scale, v_scale, out, lse, workspace, status)
+PyObject* py_fwd8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 24, [&]() -> PyObject* {
+    const Tensor& q = tensor(a[0], "q");
+    const Call c(q);
+    const Read r = read_args(c, q, a + 1, true);
+    const Tensor &kc = tensor(a[1], "k_cache"), &vc = tensor(a[17], "v_cache");
+    const Pool v = pool(c, vc, "v_cache", at::kFloat8_e4m3fn);
+    if (vc.sizes() != kc.sizes()) bad("k_cache and v_cache must have the same shape");
+    const BlockScales ks = block_scales(c, tensor(a[18], "k_scale"), "k_scale", kc);
+    const BlockScales vs = block_scales(c, tensor(a[19], "v_scale"), "v_scale", vc);
+    if (ks.block != vs.block) bad("k_scale and v_scale must have the same blocks");
+    Maybe go = maybe(a[20], "out"), gl = maybe(a[21], "lse");
+    const Tensor out = go ? *go : c.make({r.T, r.Hq, r.d}, r.type);
+    const Tensor lse = gl ? *gl : c.make({r.T, r.Hq}, at::kFloat);
+    const Rows o = rows16(c, out, "out", r.type, r.Hq, r.d, r.T);
+    const float* l = lse_of(c, lse, r);
+    const Workspace w = workspace(c, maybe(a[22], "workspace"), fn.fwd8_ws(r.B, r.P, r.Hq, r.Hkv, r.d, r.T));
+    check(fn.fwd8(r.dt, r.B, r.P, r.Hq, r.Hkv, r.d, r.T, r.q.p, r.q.ts, r.q.hs, r.k.p, r.k.ps, r.k.ss, r.k.hs, v.p,
+                  v.ps, v.ss, v.hs, ks.p, ks.ps, ks.bs, ks.hs, vs.p, vs.ps, vs.bs, vs.hs, r.pages, r.page, ks.block,
+                  r.own.p, r.own.rs, r.own.width, r.own.lens, r.prefix.p, r.prefix.rs, r.prefix.width, r.prefix.lens,
+                  r.cu_prefix, r.cu_q, r.q_pos, r.pos.p, r.pos.rs, r.pos.hs, r.ppos.p, r.ppos.rs, r.ppos.hs, r.slopes,
+                  r.slopes_bs, r.causal, r.wl, r.wr, r.cap_value, r.scale, o.p, o.ts, o.hs, const_cast<float*>(l), w.p,
+                  w.bytes, status_of(c, maybe(a[23], "status")), c.stream()));
+    return Py_BuildValue("(NN)", result(a[20], out), result(a[21], lse));
+  });
+}
+
+// A sequence of pools, each [num_pages, rows, heads, d] or [num_pages, rows, heads].
+struct Pools {
+  PyObject* seq;
+  std::vector<attn_pool> pool;
+  std::vector<const Tensor*> t;
+  int64_t pages = -1, page_size = 0;
+  explicit Pools(PyObject* o, const char* name) : seq(PySequence_Fast(o, "pools must be a list of tensors")) {
+    if (!seq) throw Raised{};
+    try {
+      const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+      for (Py_ssize_t i = 0; i < n; ++i) add(tensor(PySequence_Fast_GET_ITEM(seq, i), name), name);
+    } catch (...) {
+      Py_DECREF(seq);
+      throw;
+    }
+  }
+  ~Pools() { Py_DECREF(seq); }
+  Pools(const Pools&) = delete;
+  Pools& operator=(const Pools&) = delete;
+  void add(const Tensor& x, const char* name) {
+    const int64_t dims = x.dim(), e = static_cast<int64_t>(x.element_size());
+    if ((dims != 4 && dims != 3) || (dims == 4 && x.size(3) > 1 && x.stride(3) != 1) || x.numel() == 0 || x.size(0) > INT32_MAX ||
+        x.size(1) > 1024 || x.size(2) > INT32_MAX || (dims == 4 && x.size(3) * e > INT32_MAX))
+      bad(std::string(name) + " must be tensors [num_pages, rows, heads, d] or [num_pages, rows, heads], not empty, "
+          "at most 1024 rows a page, with a contiguous feature axis");
+    if (pages >= 0 && x.size(0) != pages) bad(std::string(name) + " must have the same number of pages");
+    pages = x.size(0);
+    page_size = std::max(page_size, x.size(1));
+    attn_pool p;
+    p.base = x.data_ptr();
+    p.rows = static_cast<int32_t>(x.size(1));
+    if (dims == 4) {
+      p.pieces = static_cast<int32_t>(x.size(2));
+      p.bytes = static_cast<int32_t>(x.size(3) * e);
+      p.piece_stride = used(x.stride(2), x.size(2), x.size(3)) * e;
+    } else if (x.size(2) == 1 || x.stride(2) == 1) {
+      p.pieces = 1;
+      p.bytes = static_cast<int32_t>(x.size(2) * e);
+      p.piece_stride = p.bytes;
+    } else {
+      p.pieces = static_cast<int32_t>(x.size(2));
+      p.bytes = static_cast<int32_t>(e);
+      p.piece_stride = x.stride(2) * e;
+    }
+    const int64_t row = static_cast<int64_t>(p.pieces) * p.bytes;
+    p.row_stride = x.size(1) > 1 ? x.stride(1) * e : row;
+    p.page_stride = x.size(0) > 1 ? x.stride(0) * e : row * p.rows;
+    pool.push_back(p);
+    t.push_back(&x);
+  }
+  void here(const Call& c, const char* name) const {
+    for (const Tensor* x : t) c.here(*x, name);
+  }
+};
+int page_size_of(PyObject* given, const Pools& p) {
+  if (given != Py_None) return small(given);
+  if (p.pool.empty()) bad("page_size is needed without pools");
+  return static_cast<int>(p.page_size);
+}
+struct Cells {  // an int32 table [rows, width]
+  int32_t* p = nullptr;
+  int64_t rs = 0;
+  int rows = 0, width = 1;
+};
+Cells cells(const Call& c, const Tensor& t, const char* name, int64_t rows, int64_t width) {
+  c.here(t, name);
+  if (t.scalar_type() != at::kInt || t.dim() != 2 || (rows >= 0 && t.size(0) != rows) || (width >= 0 && t.size(1) != width) ||
+      t.size(1) < 1 || t.size(0) > INT32_MAX || t.size(1) > INT32_MAX || (t.size(1) > 1 && t.stride(1) != 1))
+    bad(std::string(name) + " must be an int32 CUDA tensor [rows, width] with contiguous rows, of one shape with its output");
+  return {t.data_ptr<int32_t>(), used(t.stride(0), t.size(0), t.size(1)), static_cast<int>(t.size(0)), static_cast<int>(t.size(1))};
+}
+
+// (pools, table, lens, held, refs, parents, room, table_out, lens_out, held_out, refs_out, page_size, workspace, status)
+PyObject* py_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject* {
+    const Tensor &tab = tensor(a[1], "table"), &refs = tensor(a[4], "refs");
+    const Call c(tab);
+    const Pools pools(a[0], "pools");
+    pools.here(c, "pools");
+    const int64_t N = refs.numel();
+    if (pools.pages >= 0 && N != pools.pages) bad("refs must have an entry for every page of the pools");
+    const Cells t = cells(c, tab, "table", -1, -1);
+    PyObject *to = a[7] != Py_None ? a[7] : a[1], *lo = a[8] != Py_None ? a[8] : a[2];
+    PyObject *ho = a[9] != Py_None ? a[9] : a[3], *ro = a[10] != Py_None ? a[10] : a[4];
+    const Cells u = cells(c, tensor(to, "table_out"), "table_out", t.rows, t.width);
+    auto ints = [&](PyObject* o, const char* name, int64_t count) {
+      return const_cast<int32_t*>(vec(c, tensor(o, name), name, count));
+    };
+    if (N > INT32_MAX) bad("refs has too many entries");
+    const int32_t* room = a[6] == Py_None ? nullptr : ints(a[6], "room", t.rows);
+    const Workspace w = workspace(c, maybe(a[12], "workspace"), fn.fork_ws(t.rows, t.width, static_cast<int>(N)));
+    check(fn.fork(t.rows, static_cast<int>(N), page_size_of(a[11], pools), pools.pool.data(), static_cast<int>(pools.pool.size()),
+                  t.p, t.rs, t.width, ints(a[2], "lens", t.rows), ints(a[3], "held", t.rows), ints(a[4], "refs", N),
+                  ints(a[5], "parents", t.rows), room, u.p, u.rs, ints(lo, "lens_out", t.rows), ints(ho, "held_out", t.rows),
+                  ints(ro, "refs_out", N), w.p, w.bytes, status_of(c, maybe(a[13], "status")), c.stream()));
+    return Py_BuildValue("(NNNN)", kept(to), kept(lo), kept(ho), kept(ro));
+  });
+}
+
+// (pools, table, held, refs, prefix_table, prefix_held, table_out, refs_out, prefix_table_out, live, page_size, workspace, status)
+PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* {
+    const Tensor &tab = tensor(a[1], "table"), &refs = tensor(a[3], "refs");
+    const Call c(tab);
+    const Pools pools(a[0], "pools");
+    pools.here(c, "pools");
+    const int64_t N = refs.numel();
+    if (N > INT32_MAX || (pools.pages >= 0 && N != pools.pages)) bad("refs must have an entry for every page of the pools");
+    auto ints = [&](PyObject* o, const char* name, int64_t count) {
+      return const_cast<int32_t*>(vec(c, tensor(o, name), name, count));
+    };
+    PyObject *to = a[6] != Py_None ? a[6] : a[1], *ro = a[7] != Py_None ? a[7] : a[3], *po = a[8] != Py_None ? a[8] : a[4];
+    const Cells t = cells(c, tab, "table", -1, -1), u = cells(c, tensor(to, "table_out"), "table_out", t.rows, t.width);
+    Cells pt, pu;
+    const int32_t* ph = nullptr;
+    if (a[4] != Py_None) {
+      pt = cells(c, tensor(a[4], "prefix_table"), "prefix_table", -1, -1);
+      pu = cells(c, tensor(po, "prefix_table_out"), "prefix_table_out", pt.rows, pt.width);
+      ph = ints(a[5], "prefix_held", pt.rows);
+    } else if (a[5] != Py_None || a[8] != Py_None) {
+      bad("prefix_held and prefix_table_out need prefix_table");
+    }
+    Maybe gl = maybe(a[9], "live");
+    const Tensor live = gl ? *gl : c.make({1}, at::kInt);
+    int32_t* lp = const_cast<int32_t*>(vec(c, live, "live", 1));
+    const Workspace w = workspace(c, maybe(a[11], "workspace"), fn.compact_ws(static_cast<int>(N)));
+    check(fn.compact(static_cast<int>(N), page_size_of(a[10], pools), pools.pool.data(), static_cast<int>(pools.pool.size()), t.rows,
+                     t.p, t.rs, t.width, ints(a[2], "held", t.rows), u.p, u.rs, pt.rows, pt.p, pt.rs, pt.width, ph, pu.p, pu.rs,
+                     ints(a[3], "refs", N), ints(ro, "refs_out", N), lp, w.p, w.bytes, status_of(c, maybe(a[12], "status")),
+                     c.stream()));
+    return Py_BuildValue("(NNNN)", result(a[9], live), kept(to), kept(ro), kept(po));
+  });
+}
+
+// (src_pools, src_pages, dst_pages, dst_pools, page_size, status)
+PyObject* py_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const Tensor& from = tensor(a[1], "src_pages");
+    const Call c(from);
+    const Pools src(a[0], "src_pools"), dst(a[3] != Py_None ? a[3] : a[0], "dst_pools");
+    src.here(c, "src_pools");
+    dst.here(c, "dst_pools");
+    if (src.pool.size() != dst.pool.size()) bad("src_pools and dst_pools must have the same number of pools");
+    const int64_t count = from.numel();
+    if (count > INT32_MAX) bad("too many pages");
+    const int32_t* f = vec(c, from, "src_pages", count);
+    const int32_t* t = vec(c, tensor(a[2], "dst_pages"), "dst_pages", count);
+    if (src.pool.empty()) Py_RETURN_NONE;
+    for (size_t i = 0; i < src.t.size(); ++i)
+      if (src.t[i]->scalar_type() != dst.t[i]->scalar_type() || src.t[i]->sizes().slice(1) != dst.t[i]->sizes().slice(1))
+        bad("pools at the same place must have the same type and pages");
+    std::vector<attn_pool> sp = src.pool, dp = dst.pool;
+    for (size_t i = 0; i < sp.size(); ++i) {  // (rows of heads may be one run in one of them only)
+      if (sp[i].pieces == dp[i].pieces) continue;
+      attn_pool& one = sp[i].pieces == 1 ? sp[i] : dp[i];
+      const attn_pool& many = sp[i].pieces == 1 ? dp[i] : sp[i];
+      one.pieces = many.pieces;
+      one.bytes = many.bytes;
+      one.piece_stride = many.bytes;
+    }
+    check(fn.copy(static_cast<int>(count), f, t, static_cast<int>(src.pages), static_cast<int>(dst.pages),
+                  page_size_of(a[4], src), sp.data(), dp.data(), static_cast<int>(sp.size()),
+                  status_of(c, maybe(a[5], "status")), c.stream()));
+    Py_RETURN_NONE;
+  });
+}
+
 // bind(error class, addresses in the order of Fns)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   constexpr Py_ssize_t count = sizeof(Fns) / sizeof(void*);
@@ -540,6 +880,9 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD("bind", py_bind),       METHOD("rotary", py_rotary), METHOD("append", py_append),
                          METHOD("fwd", py_fwd),         METHOD("weights", py_weights), METHOD("evict", py_evict),
+                         METHOD("norm", py_norm),       METHOD("norm_bwd", py_norm_bwd), METHOD("append8", py_append8),
+                         METHOD("fwd8", py_fwd8),       METHOD("fork", py_fork),       METHOD("compact", py_compact),
+                         METHOD("copy", py_copy),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -22,7 +22,7 @@
 #include <type_traits>
 
 #include "../../include/attn_varlen.h"
-#include "cache.cuh"
+#include "rowfrag.cuh"
 
 namespace attn {
 namespace kv {
@@ -31,92 +31,7 @@ namespace {
 constexpr int kThreadsR = 256;
 constexpr int kItemsR = 4096;   // 16-byte units (pairs of them for halves) a block turns, at most
 constexpr int kItemsA = 2048;   // ... and appends
-constexpr int kMaxTokensR = 32;
 static_assert(kMaxTokensR <= kThreadsR, "a thread looks one token up");
-constexpr int kMaxPairs = kHeadDim / 2;
-
-// Fraction of a turn per position, as a 64-bit binary fraction.
-__device__ __forceinline__ uint64_t turn_fraction(double inv_freq) {
-  const double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  const double f = t - floor(t);                       // [0, 1]
-  return f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0ull;
-}
-
-// x / n for 0 <= x < 2^20, as in head_div (n is fixed for a launch).
-__device__ __forceinline__ int quotient(int x, float inv_n) {
-  return static_cast<int>((static_cast<float>(x) + 0.5f) * inv_n);
-}
-
-struct Turns {
-  float2 cs[kMaxTokensR][kMaxPairs];  // cos, sin
-  uint64_t per_pos[kMaxPairs];        // turn_fraction of each pair
-  int64_t row[kMaxPairs];             // its axis' row of the positions
-};
-
-// cos and sin of every pair for ntok tokens from tok0 on (whole block; the
-// caller synchronises).  The 64-bit arithmetic is done once per pair and
-// block: it runs at 1/50 of the fp32 rate here, and once per (pair, token) it
-// took most of the time of calls with one head.
-__device__ __forceinline__ void fill_turns(const RotaryTable& r, int64_t tok0, int ntok, Turns& s) {
-  const bool once = ntok * r.pairs <= static_cast<int>(blockDim.x);  // no pair is met twice
-  for (int i = threadIdx.x; i < r.pairs && !once; i += blockDim.x) {
-    int ax = r.pair_axis ? __ldg(r.pair_axis + i) : 0;
-    ax = min(max(ax, 0), r.axes - 1);
-    s.per_pos[i] = turn_fraction(__ldg(r.inv_freq + i));
-    s.row[i] = ax * r.axis_stride;
-  }
-  const float inv_pairs = 1.f / r.pairs;
-  auto turn = [&](int t, int i, int64_t pos, uint64_t per_pos) {
-    const uint64_t turns = static_cast<uint64_t>(pos) * per_pos;
-    // the top 32 bits as a signed fraction of a turn, times 2 pi
-    const float h = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 1.4629180792671596e-9f;
-    float sn, cn;
-    __sincosf(h, &sn, &cn);
-    s.cs[t][i] = make_float2(cn, r.inverse ? -sn : sn);
-  };
-  const int all = ntok * r.pairs;
-  if (once) {
-    const int u = threadIdx.x, t = quotient(u, inv_pairs), i = u - t * r.pairs;
-    if (u < all) {
-      const int ax = r.pair_axis ? __ldg(r.pair_axis + i) : 0;
-      const int64_t row = min(max(ax, 0), r.axes - 1) * r.axis_stride;
-      turn(t, i, __ldg(r.positions + row + tok0 + t), turn_fraction(__ldg(r.inv_freq + i)));
-    }
-    return;
-  }
-  __syncthreads();
-  for (int u0 = threadIdx.x; u0 < all; u0 += 4 * blockDim.x) {
-    int pos[4];  // four positions in flight
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = u0 + k * blockDim.x, t = quotient(u, inv_pairs);
-      if (u < all) pos[k] = __ldg(r.positions + s.row[u - t * r.pairs] + tok0 + t);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = u0 + k * blockDim.x, t = quotient(u, inv_pairs), i = u - t * r.pairs;
-      if (u < all) turn(t, i, pos[k], s.per_pos[i]);
-    }
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void turn2(float2 c, float& a, float& b) {
-  const float x = a;
-  a = x * c.x - b * c.y;
-  b = b * c.x + x * c.y;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint64_t f = Pack<BF16>::unpack(w[i]);
-    v[2 * i] = f2_lo(f);
-    v[2 * i + 1] = f2_hi(f);
-  }
-}
 
 // 16-byte units of a row: with VEC, `rot_units` items that turn (a pair of
 // units for halves, one for interleaved) and then units that are copied.
@@ -232,14 +147,6 @@ __global__ void __launch_bounds__(kThreadsR)
       if (u0 + k * kThreadsR < all)
         item[k].store(out[k], at[k], it.turning, p.r.pairs, p.r.interleaved, turns.cs[tok[k]]);
   }
-}
-
-// The slots that sequence b's tokens take start here, or -1 when its length is
-// negative or they do not all fit its table: none of them is taken then.
-__device__ __forceinline__ int append_at(const AppendParams& p, int b, int n) {
-  const int len = __ldg(p.lens + b);
-  const int64_t slots = static_cast<int64_t>(p.width) << p.page_log2;
-  return len >= 0 && static_cast<int64_t>(len) + n <= slots ? len : -1;
 }
 
 // New tokens into their pages: K rows turned (when the call has rotary
@@ -377,8 +284,6 @@ int block_tokens(int64_t T, int64_t items_per_token, int most) {
   n = n < spread ? n : spread;
   return static_cast<int>(n < 1 ? 1 : (n > kMaxTokensR ? kMaxTokensR : n));
 }
-
-bool vector_pairs(int pairs, bool interleaved) { return pairs % (interleaved ? 4 : 8) == 0; }
 
 }  // namespace
 
