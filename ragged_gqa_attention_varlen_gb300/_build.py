@@ -24,7 +24,7 @@ SOURCES = ["host.cu", "sched.cu", "fwd.cu", "bwd_dq.cu", "bwd_dkdv.cu", "bwd_dkd
            "cache_host.cu", "rotary.cu", "cache_fwd.cu", "cache_d160.cu", "cache_d128.cu",
            "cache_d64.cu", "cache_weights.cu", "evict.cu",
            "cache_more_host.cu", "norm.cu", "append8.cu", "cache8_fwd.cu", "cache8_d160.cu", "cache8_d128.cu",
-           "cache8_d64.cu", "pages.cu"]
+           "cache8_d64.cu", "cache8_few_d160.cu", "cache8_few_d128.cu", "cache8_few_d64.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-Wall"]

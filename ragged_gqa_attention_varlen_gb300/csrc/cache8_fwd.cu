@@ -18,42 +18,77 @@ extern template cudaError_t launch_fwd8_d<128>(const Cache8Params&, const FwdWs&
 extern template cudaError_t launch_fwd8_d<64>(const Cache8Params&, const FwdWs&, const CUtensorMap&,
                                               const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 
+template <int HD>
+cudaError_t launch_few_d(const Cache8Params&, const FwdWs&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                         const CUtensorMap&, int, cudaStream_t);
+extern template cudaError_t launch_few_d<160>(const Cache8Params&, const FwdWs&, const CUtensorMap&, const CUtensorMap&,
+                                              const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+extern template cudaError_t launch_few_d<128>(const Cache8Params&, const FwdWs&, const CUtensorMap&, const CUtensorMap&,
+                                              const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+extern template cudaError_t launch_few_d<64>(const Cache8Params&, const FwdWs&, const CUtensorMap&, const CUtensorMap&,
+                                             const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+
 namespace {
 
-// Boxes of `width` features of min(page_size, 128) rows of a page.
-bool encode_bytes(CUtensorMap* m, const CacheParams& p, const Pages& pg, int width, CUtensorMapSwizzle swizzle) {
+// Boxes of `width` features of min(page_size, rows) rows of a page.  Lines of 128
+// bytes: a row of one head is no longer, and with 256 the neighbouring head's bytes
+// came along and were gone when they were wanted (96 sequences of 8 heads: 697 MB
+// read for 490, 120 us instead of 104).
+bool encode_bytes(CUtensorMap* m, const CacheParams& p, const Pages& pg, int width, int rows, CUtensorMapSwizzle swizzle) {
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(p.Hkv),
                         static_cast<cuuint64_t>(p.page_size), static_cast<cuuint64_t>(p.num_pages)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(pg.head), static_cast<cuuint64_t>(pg.slot),
                            static_cast<cuuint64_t>(pg.page)};
   cuuint32_t box[4] = {static_cast<cuuint32_t>(width), 1,
-                       static_cast<cuuint32_t>(p.page_size < kKeys ? p.page_size : kKeys), 1};
+                       static_cast<cuuint32_t>(p.page_size < rows ? p.page_size : rows), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pg.base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Few rows a key: a sequence's tokens, on average, have at most 8 rows in a K/V
+// head.  (The kernel for few rows is right for any number; a longer run of tokens
+// reads its keys once for each 8 rows.)  Prefixes bring the rows of many sequences
+// together and stay with the tiles of 128 rows.
+bool few_rows(const CacheParams& p) {
+  return p.P == 0 && (p.total_q + p.B - 1) / p.B * p.R <= 8;
 }
 
 }  // namespace
 
 cudaError_t launch_fwd8(const Cache8Params& call, cudaStream_t s) {
   Cache8Params p = call;
-  // what a piece's start costs in steps, as in cache_fwd.cu
-  p.c.tile_cost = p.c.softcap > 0.f ? 4 : 2;
   const int grid = device_ctas();
   if (grid < 1 || !encode_fn()) return cudaErrorInitializationError;
   const FwdWs w = fwd_ws(p.c.B, p.c.P, p.c.Hq, p.c.Hkv, p.c.d, p.c.total_q);
-  CUtensorMap tk, tkt, tv;
+  CUtensorMap tk, tkt, tv, tvt;
   std::memset(&tkt, 0, sizeof tkt);
-  const int d = p.c.d;
-  if (!encode_bytes(&tk, p.c, p.c.k, d == 64 ? 64 : 128, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
-      (d == 160 && !encode_bytes(&tkt, p.c, p.c.k, 32, CU_TENSOR_MAP_SWIZZLE_32B)) ||
-      !encode_bytes(&tv, p.c, p.c.v, d, CU_TENSOR_MAP_SWIZZLE_NONE))
+  std::memset(&tvt, 0, sizeof tvt);
+  const int d = p.c.d, wide = d == 64 ? 64 : 128;
+  const CUtensorMapSwizzle swizzle = d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (few_rows(p.c)) {
+    p.c.tile_cost = 2;  // the joins of a piece's warps and its first loads
+    constexpr int kRowsBox = 64;
+    if (!encode_bytes(&tk, p.c, p.c.k, wide, kRowsBox, swizzle) || !encode_bytes(&tv, p.c, p.c.v, wide, kRowsBox, swizzle) ||
+        (d == 160 && (!encode_bytes(&tkt, p.c, p.c.k, 32, kRowsBox, CU_TENSOR_MAP_SWIZZLE_32B) ||
+                      !encode_bytes(&tvt, p.c, p.c.v, 32, kRowsBox, CU_TENSOR_MAP_SWIZZLE_32B))))
+      return cudaErrorInvalidValue;
+    const cudaError_t e = d == 160   ? launch_few_d<160>(p, w, tk, tkt, tv, tvt, grid, s)
+                          : d == 128 ? launch_few_d<128>(p, w, tk, tkt, tv, tvt, grid, s)
+                                     : launch_few_d<64>(p, w, tk, tkt, tv, tvt, grid, s);
+    return e != cudaSuccess ? e : launch_join(p.c, w, 8, s);
+  }
+  // what a piece's start costs in steps, as in cache_fwd.cu
+  p.c.tile_cost = p.c.softcap > 0.f ? 4 : 2;
+  if (!encode_bytes(&tk, p.c, p.c.k, wide, kKeys, swizzle) ||
+      (d == 160 && !encode_bytes(&tkt, p.c, p.c.k, 32, kKeys, CU_TENSOR_MAP_SWIZZLE_32B)) ||
+      !encode_bytes(&tv, p.c, p.c.v, d, kKeys, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   const cudaError_t e = d == 160   ? launch_fwd8_d<160>(p, w, tk, tkt, tv, grid, s)
                         : d == 128 ? launch_fwd8_d<128>(p, w, tk, tkt, tv, grid, s)
                                    : launch_fwd8_d<64>(p, w, tk, tkt, tv, grid, s);
-  return e != cudaSuccess ? e : launch_join(p.c, w, s);
+  return e != cudaSuccess ? e : launch_join(p.c, w, kRows, s);
 }
 
 }  // namespace kv

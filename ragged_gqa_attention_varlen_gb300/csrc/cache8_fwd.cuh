@@ -41,7 +41,7 @@
 #pragma once
 #include <cuda_fp8.h>
 
-#include "cache_piece.cuh"
+#include "cache8_wait.cuh"
 
 namespace attn {
 namespace kv {
@@ -96,55 +96,11 @@ struct Fwd8Bars {
   int abort;
 };
 
-// Waits as in sm103.cuh, by a try that may suspend the warp for longer: twenty warps
-// that poll took a third of the issue slots.
-__device__ __forceinline__ bool mbar_try_long(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool mbar_wait8(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_long(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_long(bar, parity)) {
-    if (*abort) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool mbar_wait8_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait8(bar, parity, abort));
-}
-__device__ __forceinline__ bool warp_exchange8(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  __threadfence_block();
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-  return mbar_wait8_warp(bar, parity, abort);
-}
-__device__ __forceinline__ bool piece_take8(PieceRing* r, uint32_t& k, Piece* out, volatile int* abort) {
-  const int s = k & 3;
-  if (!mbar_wait8(&r->full[s], (k >> 2) & 1, abort)) return false;
-  *out = r->piece[s];
-  ++k;
-  return true;
-}
-
 constexpr int kThreads8 = 640;
 // registers per thread of warps 0-3, 4-11, 12-15 and 16-19 (launched at 96)
 constexpr int kRegsPlan8 = 88, kRegsSoft8 = 128, kRegsConv8 = 64, kRegsQ8 = 72;
 static_assert(kRegsPlan8 + 2 * kRegsSoft8 + kRegsConv8 + kRegsQ8 <= 5 * 96, "register split exceeds the launch");
 constexpr uint32_t kColO8 = 256;  // TMEM: S0 / P0 [0,128), S1 / P1 [128,256), O [256, 256 + d)
-constexpr float kLazy8 = 8.f;     // rescale when the maximum grows by more (base 2)
-constexpr float kShift8 = 7.f;    // P of a row's maximum, as an exponent
 constexpr float kFixedCap8 = 9.5f;
 
 // The reference of the V scales, as every warp that needs it follows it.
@@ -172,15 +128,6 @@ struct VRef {
   __device__ __forceinline__ float of_p(float scale) const { return fminf(scale * inv * (1.f / kLeastV), 1.f); }
   static constexpr float kLeastV = 1.f / 32768.f;
 };
-
-__device__ __forceinline__ void cp_async4_or_zero(float* dst, const float* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 4 : 0)
-               : "memory");
-}
-// Arrives on `bar` (which counts this thread) when the thread's copies have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
 
 // One warp: the bytes of every key tile of the pieces into the stages, a box per
 // lane, and the scales: V's with both, since the warps that convert V and those

@@ -35,7 +35,7 @@ constexpr int kHeadsJ = 8;  // rows (heads of a token) of a block
 // four features of each, the features over four lanes and four warps.  A chain
 // of dependent loads bounds it (sequence, plan, first part, parts); what does
 // not depend on the tile kernel is read before the wait for it.
-template <bool BF16, int HD>
+template <bool BF16, int HD, int TR>
 __global__ void __launch_bounds__(kWarpsJ * 32)
     join_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ FwdWs w) {
   constexpr int kUnits = HD / 4;                            // float4 of a row
@@ -82,9 +82,9 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
     own.len = len;
     const uint32_t x = static_cast<uint32_t>(tok - c0) * p.R + hr;
     int lo, hi;
-    tile_keys(p, own, x / kRows, lo, hi);
+    tile_keys<TR>(p, own, x / TR, lo, hi);
     has_own = hi > lo;
-    ro = x % kRows;
+    ro = x % TR;
   }
   if (p.P) {
     const int pfx = prefix_of(p, b);
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
       const int n = seg_len(p, false, pfx);
       has_prefix = prefix_klo(p, pfx, n) < n;
       const int tok0 = __ldg(p.cu_q + max(__ldg(p.cu_prefix + pfx), 0));
-      rp = (static_cast<uint32_t>(tok - tok0) * p.R + hr) % kRows;
+      rp = (static_cast<uint32_t>(tok - tok0) * p.R + hr) % TR;
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -170,8 +170,9 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
 }
 
 template <int HD>
-auto join_for(const CacheParams& p) {
-  return p.dtype == 1 ? join_kernel<true, HD> : join_kernel<false, HD>;
+auto join_for(const CacheParams& p, int tile_rows) {
+  if (tile_rows == 8) return p.dtype == 1 ? join_kernel<true, HD, 8> : join_kernel<false, HD, 8>;
+  return p.dtype == 1 ? join_kernel<true, HD, kRows> : join_kernel<false, HD, kRows>;
 }
 
 }  // namespace
@@ -206,7 +207,7 @@ size_t fwd_workspace(int B, int P, int Hq, int Hkv, int d, int64_t total_q) {
 
 // A programmatic dependent of the tile kernel: its blocks are placed early and
 // wait for the results.
-cudaError_t launch_join(const CacheParams& p, const FwdWs& w, cudaStream_t s) {
+cudaError_t launch_join(const CacheParams& p, const FwdWs& w, int tile_rows, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.total_q), (p.Hq + kHeadsJ - 1) / kHeadsJ);
   cfg.blockDim = dim3(kWarpsJ * 32);
@@ -216,7 +217,9 @@ cudaError_t launch_join(const CacheParams& p, const FwdWs& w, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto k = p.d == 160 ? join_for<160>(p) : (p.d == 128 ? join_for<128>(p) : join_for<64>(p));
+  auto k = p.d == 160   ? join_for<160>(p, tile_rows)
+           : p.d == 128 ? join_for<128>(p, tile_rows)
+                        : join_for<64>(p, tile_rows);
   return cudaLaunchKernelEx(&cfg, k, p, w);
 }
 
@@ -238,7 +241,7 @@ cudaError_t launch_fwd(const CacheParams& call, cudaStream_t s) {
                   : p.d == 128 ? launch_fwd_d<128>(p, w, tk, tkt, tv, grid, s)
                                : launch_fwd_d<64>(p, w, tk, tkt, tv, grid, s);
   if (e != cudaSuccess) return e;
-  return launch_join(p, w, s);
+  return launch_join(p, w, kRows, s);
 }
 
 }  // namespace kv

@@ -83,9 +83,11 @@ __device__ __forceinline__ void piece_done(PieceRing* r, uint32_t k_taken) {
 }
 
 // Joins the partial results behind the tile kernel (cache_fwd.cu).
-cudaError_t launch_join(const CacheParams& p, const FwdWs& w, cudaStream_t s);
+// (tile_rows: rows of its tiles, 128 or 8)
+cudaError_t launch_join(const CacheParams& p, const FwdWs& w, int tile_rows, cudaStream_t s);
 
 // One warp: this CTA's share as pieces, in the order of the segments.
+template <int TR = kRows>
 __device__ __forceinline__ void plan_pieces(const CacheParams& p, Plan* pl, PieceRing* ring,
                                             volatile int* s_abort) {
   const int lane = threadIdx.x & 31;
@@ -110,7 +112,7 @@ __device__ __forceinline__ void plan_pieces(const CacheParams& p, Plan* pl, Piec
   for (int s = s0; ok && first < end && s < p.P + p.B; ++s) {
     if (s - s0 >= known && ((s - s0) & 31) == 0) {  // the next 32 segments
       __syncwarp();
-      if (s + lane < p.P + p.B) pl->segs[lane] = seg_plan(p, s + lane);
+      if (s + lane < p.P + p.B) pl->segs[lane] = seg_plan<TR>(p, s + lane);
       __syncwarp();
     }
     const SegPlan g = pl->segs[(s - s0) & 31];
@@ -122,7 +124,7 @@ __device__ __forceinline__ void plan_pieces(const CacheParams& p, Plan* pl, Piec
     if (varies && begin > a) {  // skip whole K/V heads before this CTA's share
       int64_t sum = 0;
       for (int i = lane; i < nt; i += 32) {
-        tile_keys(p, g.s, i, lo, hi);
+        tile_keys<TR>(p, g.s, i, lo, hi);
         sum += tile_cost(p, tile_steps(lo, hi));
       }
       const int64_t cost = warp_sum64(sum);
@@ -144,11 +146,11 @@ __device__ __forceinline__ void plan_pieces(const CacheParams& p, Plan* pl, Piec
       if (g.each == 0) gi = p.Hkv;
     }
     for (; ok && gi < p.Hkv && a < end; ++gi, t = 0) {
-      int64_t x0 = static_cast<int64_t>(t) * kRows;  // the tile's first row
+      int64_t x0 = static_cast<int64_t>(t) * TR;  // the tile's first row
       int i0 = static_cast<int>(static_cast<uint32_t>(x0) / static_cast<uint32_t>(p.R));
       int h0 = static_cast<int>(x0 - static_cast<int64_t>(i0) * p.R);
       for (; ok && t < nt && a < end; ++t) {
-        if (varies) tile_keys(p, g.s, t, lo, hi);
+        if (varies) tile_keys<TR>(p, g.s, t, lo, hi);
         const int n = varies ? tile_steps(lo, hi) : g.each;
         // units [a, a + tile_cost) carry no step
         const int64_t at = a + p.tile_cost;  // of step 0
@@ -161,7 +163,7 @@ __device__ __forceinline__ void plan_pieces(const CacheParams& p, Plan* pl, Piec
           pc.g = gi;
           pc.tok = g.s.tok0 + i0;
           pc.head = h0;
-          pc.rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(g.s.ntok) * p.R - x0));
+          pc.rows = static_cast<int>(min(static_cast<int64_t>(TR), static_cast<int64_t>(g.s.ntok) * p.R - x0));
           pc.tok0 = g.s.tok0;
           pc.ntok = g.s.ntok;
           pc.len = g.s.len;
@@ -181,9 +183,9 @@ __device__ __forceinline__ void plan_pieces(const CacheParams& p, Plan* pl, Piec
           ok = publish(pc);
         }
         a += tile_cost(p, n);
-        x0 += kRows;
-        h0 += kRows;
-        if (p.R < 2 * kRows) {
+        x0 += TR;
+        h0 += TR;
+        if (p.R < 2 * TR) {
           const int dt = head_div(p, h0);
           i0 += dt;
           h0 -= dt * p.R;

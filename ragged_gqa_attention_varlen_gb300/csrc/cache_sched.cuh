@@ -1,6 +1,6 @@
 // cache_sched.cuh -- how attention over the paged cache is cut into pieces.
 //
-// A row tile is 128 consecutive packed rows of one segment and K/V head: row x
+// A row tile is 128 (TR) consecutive packed rows of one segment and K/V head: row x
 // is token x / R of the segment's tokens and head x % R of the group (R query
 // heads per K/V head).  It visits the 128-key tiles that hold a key some row
 // of it may attend to.  A tile of n steps costs n + tile_cost units (its
@@ -38,14 +38,15 @@ __device__ __forceinline__ bool seg_varies(const CacheParams& p, const Seg& s) {
 // Keys [lo, hi) of which some row of row tile t may attend to one: exact
 // bounds for own slots at default positions, where slot j stands at prefix_len
 // + j and query i at prefix_len + len - ntok + i.
+template <int TR = kRows>
 __device__ __forceinline__ void tile_keys(const CacheParams& p, const Seg& s, int t, int& lo,
                                           int& hi) {
   lo = s.klo;
   hi = s.len;
   if (s.own && !p.q_pos) {
-    const uint32_t x0 = static_cast<uint32_t>(t) * kRows, R = p.R;
+    const uint32_t x0 = static_cast<uint32_t>(t) * TR, R = p.R;
     const int i0 = static_cast<int>(x0 / R);
-    const int i1 = min(s.ntok - 1, static_cast<int>((x0 + kRows - 1) / R));
+    const int i1 = min(s.ntok - 1, static_cast<int>((x0 + TR - 1) / R));
     const int64_t k0 = static_cast<int64_t>(s.len) - s.ntok;
     if (p.wl >= 0) lo = static_cast<int>(min(static_cast<int64_t>(s.len), max(static_cast<int64_t>(0), k0 + i0 - p.wl)));
     if (p.wr >= 0) hi = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(s.len), k0 + i1 + p.wr + 1)));
@@ -56,8 +57,9 @@ __device__ __forceinline__ int tile_steps(int lo, int hi) {
   return hi > lo ? (hi + kKeys - 1) / kKeys - lo / kKeys : 0;
 }
 
+template <int TR = kRows>
 __device__ __forceinline__ int seg_tiles(const CacheParams& p, const Seg& s) {
-  return static_cast<int>((static_cast<int64_t>(s.ntok) * p.R + kRows - 1) / kRows);
+  return static_cast<int>((static_cast<int64_t>(s.ntok) * p.R + TR - 1) / TR);
 }
 
 
@@ -107,6 +109,7 @@ struct SegPlan {
   int lo, hi;  // keys of the row tiles when they are all the same
 };
 
+template <int TR = kRows>
 __device__ __forceinline__ SegPlan seg_plan(const CacheParams& p, int s) {
   SegPlan g;
   g.s = seg_load(p, s);
@@ -119,11 +122,11 @@ __device__ __forceinline__ SegPlan seg_plan(const CacheParams& p, int s) {
       g.waits = prefix_klo(p, pfx, g.plen) < g.plen;
     }
   }
-  g.tiles = seg_tiles(p, g.s);
+  g.tiles = seg_tiles<TR>(p, g.s);
   g.each = seg_varies(p, g.s) ? -1 : 0;
   g.lo = g.hi = 0;
   if (g.each == 0 && g.tiles > 0) {
-    tile_keys(p, g.s, 0, g.lo, g.hi);
+    tile_keys<TR>(p, g.s, 0, g.lo, g.hi);
     g.each = tile_steps(g.lo, g.hi);
   }
   return g;
@@ -135,12 +138,13 @@ __device__ __forceinline__ int tile_cost(const CacheParams& p, int n) {
 }
 
 // Cost of one K/V head's row tiles (when they differ: one by one).
+template <int TR = kRows>
 __device__ __forceinline__ int64_t seg_cost(const CacheParams& p, const SegPlan& g) {
   if (g.each >= 0) return static_cast<int64_t>(g.tiles) * tile_cost(p, g.each);
   int64_t n = 0;
   for (int t = 0; t < g.tiles; ++t) {
     int lo, hi;
-    tile_keys(p, g.s, t, lo, hi);
+    tile_keys<TR>(p, g.s, t, lo, hi);
     n += tile_cost(p, tile_steps(lo, hi));
   }
   return n;

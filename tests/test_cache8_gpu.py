@@ -8,13 +8,31 @@ import torch
 import cache8_ref as ref8
 import cache_ref as ref
 from ragged_gqa_attention_varlen_gb300 import cache as C
-from test_cache_gpu import BF, CASES, HF, i32, lib, normal, status, within  # noqa: F401
+from test_cache_gpu import BF, CASES, HF, case, i32, lib, normal, status, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 F8 = torch.float8_e4m3fn
 
 
 # ---------------------------------------------------------------- attention
+
+# calls whose sequences have few rows a K/V head, which have a kernel of their own: many
+# pieces for each CTA, stages that wrap, rows of several tokens, tiles that 8 rows cut
+FEW = [
+    case("few_many_pieces", ref.spread(21, 60, 1, 1500), [1] * 60, Hq=32, Hkv=8, d=128, page=64, cap=0.0),
+    case("few_long", [20000, 9000, 1], [1, 1, 1], Hq=8, Hkv=2, d=128, page=16, cap=0.0, alibi=True, dtype=HF),
+    case("few_wide_head", ref.spread(22, 20, 1, 900), [1] * 20, Hq=10, Hkv=5, d=160, page=32, alibi=True),
+    case("few_wide_head_small_pages", [4000, 33, 64, 65], [1] * 4, Hq=8, Hkv=8, d=160, page=16, cap=30.0, dtype=HF),
+    case("few_narrow_head", ref.spread(23, 70, 1, 700), [1] * 70, Hq=5, Hkv=5, d=64, page=128, cap=0.0, wl=100),
+    case("few_tokens", [300, 20, 513, 64], [2, 3, 1, 1], Hq=6, Hkv=3, d=128, page=64, alibi=True, dtype=HF),
+    case("few_but_one_prompt", [300] + [40] * 30, [60] + [1] * 30, Hq=4, Hkv=2, d=64, page=16, cap=3.0),
+    case("few_uncausal_window", [700, 31], [2, 2], Hq=4, Hkv=2, d=128, page=16, causal=False, wl=90, wr=0, cap=0.0),
+    case("few_shuffled", [400, 33], [1, 2], Hq=4, Hkv=2, d=160, page=64, alibi=True, shuffled=True, cap=0.0),
+    case("few_without_keys", [0, 5, 0], [1, 0, 2], Hq=4, Hkv=2, d=64, cap=0.0),
+    case("few_peaked", [600, 100], [1, 1], Hq=8, Hkv=4, d=128, cap=0.0, std=12.0, dtype=HF),
+    case("few_strided", [200, 31], [1, 2], Hq=6, Hkv=2, d=160, page=32, strided=True),
+]
+
 
 def odd_scales(top, g):
     """Scales that are no powers of two, four times apart, some larger than needed."""
@@ -63,7 +81,7 @@ def attend(q, kc, cu_q, call, **more):
     return C.attention_varlen_cache8_fwd(q, kc.k8, kc.v8, kc.k_scale, kc.v_scale, kc.table, kc.lens, cu_q, **call, **more)
 
 
-@pytest.mark.parametrize("c", CASES)
+@pytest.mark.parametrize("c", CASES + FEW)
 def test_attention(c):
     block = min(c["page"], (16, 32, 64, 128)[len(c["lens"]) % 4])
     kc, q, cu_q, opt, call = build(c, block)
@@ -81,7 +99,7 @@ def test_attention(c):
 
 
 PICKED = [x for x in CASES if x.id in ("wide_group", "long_split", "three_groups", "drafts", "window_both", "prefixes_some_without",
-                                       "shuffled_prefix", "odd_heads", "prompt", "peaked_fp16", "saturated_fp16")]
+                                       "shuffled_prefix", "odd_heads", "prompt", "peaked_fp16", "saturated_fp16")] + FEW
 
 
 @pytest.mark.parametrize("scales", [odd_scales, steep_scales])
@@ -176,9 +194,10 @@ def test_pages_out_of_the_pool_count_for_nothing():
         assert int(st) & bit
 
 
-def test_captured_and_on_two_streams():
+@pytest.mark.parametrize("Hq", [48, 6])
+def test_captured_and_on_two_streams(Hq):
     kc = ref8.Cache8([700, 90], page=64, block=64, Hkv=1)
-    q = normal(3, 2, 48, 160)
+    q = normal(3, 2, Hq, 160)
     cu_q = i32([0, 1, 2])
     want = attend(q, kc, cu_q, dict(causal=True))
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
@@ -186,7 +205,7 @@ def test_captured_and_on_two_streams():
     a, b = attend(q, kc, cu_q, dict(causal=True), stream=s1), attend(q, kc, cu_q, dict(causal=True), stream=s2)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for r in (a, b) for x, y in zip(r, want))
-    out, lse, ws = torch.empty_like(q), torch.empty(2, 48, device="cuda"), torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    out, lse, ws = torch.empty_like(q), torch.empty(2, Hq, device="cuda"), torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         attend(q, kc, cu_q, dict(causal=True), out=out, lse=lse, workspace=ws)
@@ -194,6 +213,16 @@ def test_captured_and_on_two_streams():
         out.zero_()
         g.replay()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_the_same_call_many_times():
+    """One answer, whatever the order in which the CTAs' loads land."""
+    kc = ref8.Cache8(ref.spread(31, 90, 100, 1500), Hkv=4, d=128, page=64, block=32)
+    q, cu_q = normal(3, 90, 8, 128), i32(range(91))
+    want = attend(q, kc, cu_q, dict(causal=True, softcap=0.0))
+    for _ in range(300):
+        got = attend(q, kc, cu_q, dict(causal=True, softcap=0.0))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 # ---------------------------------------------------------------- append
