@@ -33,15 +33,22 @@ __device__ __forceinline__ float2 turn_of(int64_t pos, uint64_t per_pos) {
 }
 
 struct Turns {
-  float2 cs[kMaxTokensR][kMaxPairs];  // cos, sin
+  alignas(16) float2 cs[kMaxTokensR][kMaxPairs];  // cos, sin
   uint64_t per_pos[kMaxPairs];        // turn_fraction of each pair
   int64_t row[kMaxPairs];             // its axis' row of the positions
 };
 
-// cos and sin of every pair for ntok tokens from tok0 on (whole block; the
-// caller synchronises).  The 64-bit arithmetic is done once per pair and
+// Where a token's row of `cs` holds pair i when a lane reads its eight pairs as
+// four 16-byte units: unit c of lane l at c ^ (l / 2) % 4 of the lane's four, so
+// the eight lanes of a shared memory pass meet every bank once (in order they
+// met two groups of four banks, and a load took four times its passes).
+__device__ __forceinline__ int spread_pair(int i) { return i ^ (((i >> 4) & 3) << 1); }
+
+// cos and sin of every pair for ntok tokens from tok0 on, SPREAD: at spread_pair
+// (whole block; the caller synchronises).  The 64-bit arithmetic is done once per pair and
 // block: it runs at 1/50 of the fp32 rate here, and once per (pair, token) it
 // took most of the time of calls with one head.
+template <bool SPREAD = false>
 __device__ __forceinline__ void fill_turns(const RotaryTable& r, int64_t tok0, int ntok, Turns& s) {
   const bool once = ntok * r.pairs <= static_cast<int>(blockDim.x);  // no pair is met twice
   for (int i = threadIdx.x; i < r.pairs && !once; i += blockDim.x) {
@@ -53,7 +60,7 @@ __device__ __forceinline__ void fill_turns(const RotaryTable& r, int64_t tok0, i
   const float inv_pairs = 1.f / r.pairs;
   auto turn = [&](int t, int i, int64_t pos, uint64_t per_pos) {
     const float2 c = turn_of(pos, per_pos);
-    s.cs[t][i] = make_float2(c.x, r.inverse ? -c.y : c.y);
+    s.cs[t][SPREAD ? spread_pair(i) : i] = make_float2(c.x, r.inverse ? -c.y : c.y);
   };
   const int all = ntok * r.pairs;
   if (once) {

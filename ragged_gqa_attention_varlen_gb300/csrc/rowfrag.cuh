@@ -62,24 +62,38 @@ __device__ __forceinline__ float row_max(float v) {
   return row_all<D>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// Turn the two units of item i; turn(pair) gives (cos, sin).
+// Turn the two units of item i; turn(pair, a, b) gives (cos, sin) of a pair, which
+// is an even one, and of the next.
 template <class Turn>
 __device__ __forceinline__ void turn_item(float (&a)[8], float (&b)[8], int i, int pairs,
                                           bool interleaved, Turn turn) {
+  float2 c0, c1;
   if (!interleaved) {
     if (i < pairs / 8) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) turn2<true>(turn(i * 8 + e), a[e], b[e]);
+      for (int e = 0; e < 8; e += 2) {
+        turn(i * 8 + e, c0, c1);
+        turn2<true>(c0, a[e], b[e]);
+        turn2<true>(c1, a[e + 1], b[e + 1]);
+      }
     }
     return;
   }
   if (2 * i < pairs / 4) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) turn2<true>(turn(i * 8 + e), a[2 * e], a[2 * e + 1]);
+    for (int e = 0; e < 4; e += 2) {
+      turn(i * 8 + e, c0, c1);
+      turn2<true>(c0, a[2 * e], a[2 * e + 1]);
+      turn2<true>(c1, a[2 * e + 2], a[2 * e + 3]);
+    }
   }
   if (2 * i + 1 < pairs / 4) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) turn2<true>(turn(i * 8 + 4 + e), b[2 * e], b[2 * e + 1]);
+    for (int e = 0; e < 4; e += 2) {
+      turn(i * 8 + 4 + e, c0, c1);
+      turn2<true>(c0, b[2 * e], b[2 * e + 1]);
+      turn2<true>(c1, b[2 * e + 2], b[2 * e + 3]);
+    }
   }
 }
 
