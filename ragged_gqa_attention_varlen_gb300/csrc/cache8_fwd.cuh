@@ -678,14 +678,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
             for (int i = 0; i < 16; i += 2) {
               if (FIXED) {
                 // c - 2c / (1 + e^2x): the cap is small, so its absolute error of
-                // c 2^-22 is that of the logit itself; the constant c is in bref
+                // c 2^-22 is that of the logit itself; the constant c is in bref.  (One
+                // reciprocal for two needs clamps and four products: 244 against 242 us.)
                 const uint64_t y = f2_mul(f2_make(x[i], x[i + 1]), f2_make(exp_scale, exp_scale));
-                const uint64_t d = f2_add(f2_make(ex2_approx(fminf(f2_lo(y), 60.f)), ex2_approx(fminf(f2_hi(y), 60.f))),
-                                          f2_make(1.f, 1.f));
-                const float rc = rcp_approx(f2_lo(d) * f2_hi(d));
-                const uint64_t t = f2_mul(f2_make(f2_hi(d), f2_lo(d)), f2_make(rc, rc));
-                x[i] = f2_lo(t);
-                x[i + 1] = f2_hi(t);
+                const uint64_t d = f2_add(f2_make(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y))), f2_make(1.f, 1.f));
+                x[i] = rcp_approx(f2_lo(d));
+                x[i + 1] = rcp_approx(f2_hi(d));
                 continue;
               }
               const uint64_t th = tanh2_fp32(f2_mul(f2_make(x[i], x[i + 1]), f2_make(in, in)));
