@@ -35,9 +35,20 @@
 //
 // Warps (640 threads): 0 loads K (TMA boxes of min(page_size, 128) rows per lane)
 // and the scales, 16 loads V, 1 issues S, 2 issues O, 3 plans the CTA's pieces,
-// 17-19 bring in Q rows, 12-15 convert V, 64 keys at a time (rows that no row of the
+// 17-19 bring in Q rows (the first tile's with 4-11), 12-15 convert V, 64 keys at a time (rows that no row of the
 // tile reads become zeros: the pages may hold anything there, and 0 * NaN would
 // reach O), 4-11 softmax as in cache_fwd.cuh.
+//
+// Measured with the join: 144 drafted tokens of 96 heads behind two prefixes of 12001
+// keys 214 us (575 TFLOP/s of the logits' and outputs' products), 64 single tokens of
+// 80 heads over 277000 keys in 16-row pages 58.5 us (1.5 TB/s), one token of 96 heads
+// over 700 keys 18.9 us.  A step takes about 4000 clk: 3600 of softmax (four passes of
+// 16 columns, two warps in each sub-partition, at half of the issue slots; the fetch
+// of instructions is the largest stall that is not a dependency), the rest the
+// hand-offs to the products (1300 clk of tensor work) and back.  Loading the next
+// pass's products ahead (254 us), passes of 32 columns (281), descriptors kept as
+// halves and sleeping waits (no change) were tried.  A CTA's first product stands
+// 20000 clk behind its start: plan, page and row lookups, first instructions.
 #pragma once
 #include <cuda_fp8.h>
 
@@ -81,7 +92,7 @@ __device__ __forceinline__ uint64_t byte_desc(uint32_t base, int k) {
 constexpr int kStepsHeld = 16;  // steps whose scales are kept
 
 struct Fwd8Bars {
-  uint64_t q_full, q_empty;
+  uint64_t q_full, q_empty, q_more;
   uint64_t rk_full[6], rk_empty[6], rv_full[6], rv_empty[6];
   uint64_t v_full[6], v_empty[6];
   uint64_t s_full[2], p_full[2], pv_done[2];
@@ -229,6 +240,18 @@ __device__ __forceinline__ uint32_t mul2_f16(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t sub2_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t narrow2(uint32_t h) {  // to e4m3, in the low half
+  __half2_raw x;
+  x.x = static_cast<unsigned short>(h & 0xffff);
+  x.y = static_cast<unsigned short>(h >> 16);
+  return __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+}
+
 // Four warps: V's bytes to fp16 tiles of 64 keys in the swizzled layout of the
 // product, times scale / vref; 16 keys (a scale) each.  A lane's units of 8 values
 // lie at the same places of every 16 keys, so their offsets are worked out once,
@@ -310,67 +333,74 @@ __device__ __forceinline__ void convert_v(Fwd8Bars* bars, const uint8_t* raw0, u
 }
 
 // Rows of Q as pieces of e4m3 (above); the inverse of the row's factor goes to
-// `qs`.  Warp wi of three; four lanes a row, two rows of a lane in flight.
+// `qs`.  Warp wi of nw; four lanes a row, the next row of a lane in flight.
+// Scaled values and what the pieces leave are exact in fp16 but for what lies below
+// its smallest numbers, 2^-33 of the row's largest.  The units are a rolled loop:
+// this code is short because its fetch is what a CTA's first product waits for and
+// what the softmax loops lose from the instruction cache (drafts / ragged batch /
+// one user: remainders in fp32, all unrolled 242 / 66 / 19.5 us; in fp16, unrolled
+// 236 / 60 / 18.3; rolled 214 / 58 / 18.7).
 template <bool BF16, int HD>
-__device__ __forceinline__ void split_q_rows(const CacheParams& p, uint8_t* dst, float* qs, const Piece& pc, int wi) {
+__device__ __forceinline__ void split_q_rows(const CacheParams& p, uint8_t* dst, float* qs, const Piece& pc, int wi,
+                                             int nw) {
   using S = Fwd8Shape<BF16, HD>;
   constexpr int kPer = HD / 32;  // 16-byte units of q of a lane
   const int lane = threadIdx.x & 31, u0 = lane & 3;
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(pc.g) * p.R * p.q_hs;
-  for (int r0 = wi * 16 + (lane >> 2); r0 - (lane >> 2) < pc.rows; r0 += 48) {
-    uint4 x[2][kPer];
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(pc.g) * p.R * p.q_hs + u0 * 8;
+  auto row_at = [&](int r) {
+    const int hh = pc.head + r, dt = head_div(p, hh);
+    return q + static_cast<int64_t>(pc.tok + dt) * p.q_ts + static_cast<int64_t>(hh - dt * p.R) * p.q_hs;
+  };
+  uint4 next[kPer];
+  auto load = [&](int r) {
+    const uint16_t* src = row_at(r);
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int r = r0 + 8 * n, hh = pc.head + r, dt = head_div(p, hh);
-      const uint16_t* src = q + static_cast<int64_t>(pc.tok + dt) * p.q_ts + static_cast<int64_t>(hh - dt * p.R) * p.q_hs;
+    for (int k = 0; k < kPer; ++k)
+      next[k] = r < pc.rows ? __ldg(reinterpret_cast<const uint4*>(src + k * 32)) : make_uint4(0, 0, 0, 0);
+  };
+  int r = wi * 8 + (lane >> 2);
+  load(r);
+#pragma unroll 1
+  for (; r - (lane >> 2) < pc.rows; r += nw * 8) {
+    uint4 x[kPer];
 #pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        x[n][k] = r < pc.rows ? __ldg(reinterpret_cast<const uint4*>(src + (u0 + 4 * k) * 8)) : make_uint4(0, 0, 0, 0);
-    }
+    for (int k = 0; k < kPer; ++k) x[k] = next[k];
+    load(r + nw * 8);
+    uint32_t top = 0;  // the largest magnitude's bits, in both halves
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int r = r0 + 8 * n;
-      uint32_t top = 0;  // the largest magnitude's bits, in both halves
+    for (int k = 0; k < kPer; ++k)
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
+                                   __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (r >= pc.rows) continue;
+    const int bits = __float_as_int(to_float<BF16>(static_cast<uint16_t>(max(top >> 16, top & 0xffffu))));
+    // 1.m 2^e times 2^(8 - e), or 2^(7 - e) above 1.75
+    const int up = min(max(262 - (bits >> 23) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0), 1), 253);
+    const uint64_t by = f2_make(__int_as_float(up << 23), __int_as_float(up << 23));
+    if (u0 == 0) qs[r] = __int_as_float((254 - up) << 23);
+#pragma unroll 1
+    for (int k = 0; k < kPer; ++k) {
+      const uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const uint32_t w[4] = {x[n][k].x, x[n][k].y, x[n][k].z, x[n][k].w};
+      for (int j = 1; j < kPer; ++j) x[j - 1] = x[j];
+      const int u = u0 + 4 * k;  // 8 values: half of a 16-byte unit of bytes
+      uint8_t* y = dst + byte_unit<HD>(r, u >> 1) + (u & 1) * 8;
+      uint32_t left[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t z = f2_mul(Pack<BF16>::unpack(w[i]), by);
+        left[i] = Pack<false>::two(f2_lo(z), f2_hi(z));
       }
-      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if (r >= pc.rows) continue;
-      const int bits = __float_as_int(to_float<BF16>(static_cast<uint16_t>(max(top >> 16, top & 0xffffu))));
-      // 1.m 2^e times 2^(8 - e), or 2^(7 - e) above 1.75
-      const int up = min(max(262 - (bits >> 23) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0), 1), 253);
-      const float by = __int_as_float(up << 23);
-      if (u0 == 0) qs[r] = __int_as_float((254 - up) << 23);
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        float v[8];
-        const uint32_t w[4] = {x[n][k].x, x[n][k].y, x[n][k].z, x[n][k].w};
+      for (int piece = 0; piece < S::kPieces; ++piece) {
+        uint32_t b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint64_t two = Pack<BF16>::unpack(w[i]);
-          v[2 * i] = f2_lo(two) * by;
-          v[2 * i + 1] = f2_hi(two) * by;
+          b[i] = narrow2(left[i]);
+          if (piece + 1 < S::kPieces) left[i] = sub2_f16(left[i], widen2(b[i]));
         }
-        const int u = u0 + 4 * k;  // 8 values: half of a 16-byte unit of bytes
-        uint8_t* y = dst + byte_unit<HD>(r, u >> 1) + (u & 1) * 8;
-#pragma unroll
-        for (int piece = 0; piece < S::kPieces; ++piece) {
-          uint32_t b[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            b[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-            if (piece + 1 < S::kPieces) {  // what is left
-              const uint64_t back = Pack<false>::unpack(widen2(b[i]));
-              v[2 * i] -= f2_lo(back);
-              v[2 * i + 1] -= f2_hi(back);
-            }
-          }
-          *reinterpret_cast<uint2*>(y + piece * S::kTile) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-        }
+        *reinterpret_cast<uint2*>(y + piece * S::kTile) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
       }
     }
   }
@@ -403,6 +433,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     mbar_init(&bars->q_full, 3);
     mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_more, 8);  // the first tile: the softmax warps' rows
     for (int b = 0; b < S::kRK; ++b) {
       mbar_init(&bars->rk_full[b], 1 + 32);  // the boxes' bytes, and each lane's scales
       mbar_init(&bars->rk_empty[b], 1);
@@ -484,6 +515,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
           piece_done(&bars->ring, take);
           if (pc.row < 0) break;
           if (!mbar_wait8(&bars->q_full, tiles & 1, s_abort)) break;
+          if (tiles == 0 && !mbar_wait8(&bars->q_more, 0, s_abort)) break;
           for (int kt = pc.kt1 - 1; kt >= pc.kt0; --kt, ++step) {
             if (!(ok = mbar_wait8(&bars->rk_full[st], ph, s_abort))) break;
             // the product with the P that took the buffer's previous S (step - 2) is done
@@ -571,6 +603,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
       __syncwarp();
       if (lane == 0) piece_done(&bars->ring, take);
       if (pc.row < 0) break;
+      // the first tile's rows: nothing to do but wait for them (three warps had them
+      // ready 24000 clk after the kernel's start, eleven 18000)
+      if (tiles == 0) {
+        split_q_rows<BF16, HD>(p, sQ, sQs, pc, warp - 1, 11);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_more);
+      }
       const bool valid = r < pc.rows;
       const bool any = quad * 32 < pc.rows;  // some row of this warp
       int tok = pc.tok, h = pc.head + r;     // packed token, head
@@ -929,7 +969,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         if (tiles > 0 && !mbar_wait8_warp(&bars->q_empty, (tiles - 1) & 1, s_abort)) break;
         // (the factors of four tiles ago are not read any more: S of the last tile
         // is done, so P of two steps before it has been multiplied)
-        split_q_rows<BF16, HD>(p, sQ, sQs + (tiles & 3) * 128, pc, warp - 17);
+        split_q_rows<BF16, HD>(p, sQ, sQs + (tiles & 3) * 128, pc, warp - 17, tiles ? 3 : 11);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->q_full);
