@@ -21,6 +21,20 @@ An eviction leaves the slots in another order: from then on the positions say
 which key is which, and the next step's ``lens`` are ``new_lens``, which the
 eviction has shortened.
 
+A cache held in 8 bits has e4m3 pages of the same shape and fp32 factors per
+block of slots and head beside them; its step, with norms of q and k, and beams
+that go on from others:
+
+    q, _ = attention_varlen_norm_rotary(q, None, q_weight, None, positions, inv_freq)
+    attention_varlen_cache_fork(pools, table, lens, held, refs, parents, room)
+    attention_varlen_cache8_append(k, v, k_cache, v_cache, k_scale, v_scale, table, lens, cu_q,
+                                   positions=positions, inv_freq=inv_freq, k_weight=k_weight, lens_out=new_lens)
+    out, lse = attention_varlen_cache8_fwd(q, k_cache, v_cache, k_scale, v_scale, table, new_lens, cu_q, causal=True)
+
+attention_varlen_norm_rotary_bwd trains the norms, attention_varlen_cache_compact
+packs the live pages of a pool together, attention_varlen_cache_copy moves pages
+between pools; these two and the fork take pools of either kind.
+
 Every call is asynchronous on ``stream`` (default: the current stream of the
 tensors' device).  Problems that only the device can see (lengths beyond the
 table, page numbers outside of the pool, inconsistent cu arrays) set bits of

@@ -47,12 +47,15 @@ __device__ __forceinline__ float pow2_scale(float top) {
 }
 
 // turn_of (rotary.cuh) to fp32's accuracy: what is off here moves values across e4m3's
-// borders, where a whole step is the least that one can be wrong by.
+// borders, where a whole step is the least that one can be wrong by.  The angle goes
+// to fp32 as its distance from the nearest quarter turn (off by 2^-27 of a half turn).
 __device__ __forceinline__ float2 exact_turn(int64_t pos, uint64_t per_pos) {
-  const uint64_t turns = static_cast<uint64_t>(pos) * per_pos;
+  const uint32_t u = static_cast<uint32_t>((static_cast<uint64_t>(pos) * per_pos) >> 32);
+  const uint32_t quarter = (u + 0x20000000u) >> 30;
   float sn, cn;
-  sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f, &sn, &cn);
-  return make_float2(cn, sn);
+  sincospif(static_cast<float>(static_cast<int32_t>(u - (quarter << 30))) * 4.656612873077393e-10f, &sn, &cn);
+  const float a = quarter & 1 ? sn : cn, b = quarter & 1 ? cn : sn;
+  return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
 __device__ __forceinline__ uint2 pack_e4m3(const float (&v)[8], float inv) {

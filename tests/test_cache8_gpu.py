@@ -399,3 +399,42 @@ def test_steps_of_generation():
             mine = kn[at[b]:at[b + 1]].cpu().double()
             scale = max(float(s) for s in kc.k_scale[kc.table[b, :2].long()].nan_to_num(0).flatten())
             assert ((held - mine).abs() <= mine.abs() * (2.0 ** -4 + 2.0 ** -7) + scale * 2.0 ** -9).all()
+
+
+def test_a_captured_step_is_the_step():
+    """Norm, fork, append and attend in a graph, replayed: the same bits as the calls one by one,
+    with lengths and tables that move on the device."""
+    R, Hq, Hkv, d, page, block, N = 6, 8, 2, 64, 16, 16, 40
+    inv = (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).cuda()
+    q, k, v = (normal(50 + i, R, h, d, dtype=BF, std=2.0) for i, h in enumerate((Hq, Hkv, Hkv)))
+    cu, parents, room, pos = i32(range(R + 1)), i32([0, 0, 2, 2, 5, 4]), i32([1] * R), i32([9] * R)
+    kw = torch.full((d,), 1.5, device="cuda")
+
+    def state():
+        pools = [torch.zeros(N, page, Hkv, d, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2)]
+        pools += [torch.zeros(N, page // block, Hkv, device="cuda") for _ in range(2)]
+        table, lens, held = torch.full((R, 5), -1, dtype=torch.int32, device="cuda"), i32([0] * R), i32([0] * R)
+        return pools, table, lens, held, torch.zeros(N, dtype=torch.int32, device="cuda"), torch.zeros_like(lens), status(), \
+            torch.empty_like(q), torch.empty(R, Hq, device="cuda")
+
+    def step(pools, table, lens, held, refs, new, st, out, lse):
+        C.attention_varlen_cache_fork(pools, table, lens, held, refs, parents, room, status=st)
+        qn, _ = C.attention_varlen_norm_rotary(q, None, kw, None, pos, inv)
+        C.attention_varlen_cache8_append(k, v, *pools, table, lens, cu, positions=pos, inv_freq=inv, k_weight=kw, lens_out=new,
+                                         status=st)
+        C.attention_varlen_cache8_fwd(qn, *pools, table, new, cu, causal=True, out=out, lse=lse, status=st)
+        lens.copy_(new)
+
+    one, two = state(), state()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step(*two)
+    for n in range(40):
+        step(*one)
+        g.replay()
+        torch.cuda.synchronize()
+        flat = lambda x: [t.view(torch.uint8) for t in (*x[0], *x[1:])]
+        assert all(torch.equal(a, b) for a, b in zip(flat(one), flat(two))), n
+    assert int(one[6]) == 0 and one[2].tolist() == [40] * R
