@@ -1,7 +1,7 @@
 // cache8_few.cuh -- attention over the 8-bit cache for few query rows a key: the
 // single tokens of grouped heads.
 //
-// With at most 8 rows a key, the tiles of cache8_fwd.cuh are nearly empty, and
+// With up to 16 rows a key, the tiles of cache8_fwd.cuh are nearly empty, and
 // their hand-offs between loads, tensor core, softmax and conversion, not the
 // pages' bytes, are what a step waits for (3700 clk a step of 128 keys where the
 // copy's rate would take 1400).  Here a warp does everything for 32 keys at a time,
@@ -30,6 +30,9 @@
 //
 // Warps: 8 compute, four load in turn (one takes 1900 clk for 64 keys), one joins and
 // one plans the pieces.
+//
+// Measured with the join: 96 single tokens of 32 heads over 8 (d = 128, bf16, 490 MB)
+// 102 us, 4.8 TB/s; by the tiles of 128 rows 268 us.  One loading warp 249, three 151.
 #pragma once
 #include <cuda_fp8.h>
 

@@ -47,12 +47,15 @@ bool encode_bytes(CUtensorMap* m, const CacheParams& p, const Pages& pg, int wid
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Few rows a key: a sequence's tokens, on average, have at most 8 rows in a K/V
-// head.  (The kernel for few rows is right for any number; a longer run of tokens
-// reads its keys once for each 8 rows.)  Prefixes bring the rows of many sequences
-// together and stay with the tiles of 128 rows.
+// Few rows a key: a sequence's tokens, on average, have at most 16 rows in a K/V
+// head.  (The kernel for few rows is right for any number; it takes 8 rows at a time
+// and reads the keys once for each 8.)  96 sequences over 425000 keys of 8 heads, d =
+// 128, its time and that of the tiles of 128 rows: 4 rows 166 and 371 us, 8 rows 173
+// and 372, 16 rows 323 and 373 (capped 333 and 419), 24 rows 471 and 373; 16 rows of
+// one head of 160: 74 and 74.  Prefixes bring the rows of many sequences together and
+// stay with the tiles.
 bool few_rows(const CacheParams& p) {
-  return p.P == 0 && (p.total_q + p.B - 1) / p.B * p.R <= 8;
+  return p.P == 0 && (p.total_q + p.B - 1) / p.B * p.R <= 16;
 }
 
 }  // namespace

@@ -30,6 +30,8 @@ FEW = [
     case("few_shuffled", [400, 33], [1, 2], Hq=4, Hkv=2, d=160, page=64, alibi=True, shuffled=True, cap=0.0),
     case("few_without_keys", [0, 5, 0], [1, 0, 2], Hq=4, Hkv=2, d=64, cap=0.0),
     case("few_peaked", [600, 100], [1, 1], Hq=8, Hkv=4, d=128, cap=0.0, std=12.0, dtype=HF),
+    case("few_in_two_tiles", ref.spread(24, 30, 1, 1200), [1] * 30, Hq=32, Hkv=2, d=128, page=64, cap=0.0),
+    case("few_in_tiles_of_eight_and_four", [900, 65, 1, 31], [1] * 4, Hq=24, Hkv=2, d=160, page=32, alibi=True, dtype=HF),
     case("few_strided", [200, 31], [1, 2], Hq=6, Hkv=2, d=160, page=32, strided=True),
 ]
 
