@@ -863,8 +863,8 @@ typedef struct {
  * holders (prefix tables) count too and keep a page from being given away.  Partly
  * filled pages have one holder (this call keeps it so).  New pages are the lowest
  * free ones, in the order of the rows, pages given back in this call among them.
- * The outputs may be the inputs (in place; table_out with the same stride) or
- * apart; entries of table_out from held_out[r] on are not written.
+ * Each output may be its input (in place; table_out with the same stride) or lies
+ * apart from all inputs; entries of table_out from held_out[r] on are not written.
  *
  * All or nothing: a length, count, parent, room or page number out of range
  * (ATTN_DEV_BAD_CACHE), more pages than are free or than the table is wide
@@ -883,8 +883,8 @@ attn_status attn_varlen_cache_fork(
 /* Pack the live pages (refs > 0) into the first *live ones: the i-th free page
  * below that number takes the i-th live page at or above it, in all pools; the
  * tables' first held[r] entries and refs follow (pages from *live on get 0).  The
- * sequences' table and one of prefixes (prefix_rows = 0: none) take part.  Outputs
- * may be the inputs.  Entries out of the pool, or of pages that nobody counts, are
+ * sequences' table and one of prefixes (prefix_rows = 0: none) take part.  Each output
+ * may be its input, or lies apart from all inputs.  Entries out of the pool, or of pages that nobody counts, are
  * left as they are (ATTN_DEV_BAD_CACHE). */
 size_t attn_varlen_cache_compact_workspace_size(int num_pages);
 attn_status attn_varlen_cache_compact(

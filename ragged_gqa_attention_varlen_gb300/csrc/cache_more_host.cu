@@ -45,6 +45,36 @@ bool block_ok(int block, int page_size) { return block >= 16 && block <= 128 && 
 bool scale_strides(const Scales& s) { return s.page >= 0 && s.block >= 0 && s.head >= 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Entries of an int32 array, and a table's.
+struct Span {
+  const void* base;
+  __int128 n;
+};
+Span span(const void* p, int64_t n) { return {p, n}; }
+Span span(const void* p, int rows, int64_t stride, int width) {
+  return {p, rows > 0 ? static_cast<__int128>(rows - 1) * stride + width : 0};
+}
+bool meet(const Span& a, const Span& b) {
+  if (!a.base || !b.base || a.n < 1 || b.n < 1) return false;
+  const __int128 x = reinterpret_cast<uintptr_t>(a.base), y = reinterpret_cast<uintptr_t>(b.base);
+  return x < y + 4 * b.n && y < x + 4 * a.n;
+}
+// Whether the outputs are apart from one another and from the inputs; the first `own`
+// of them may be the inputs at their places instead.
+bool outputs_apart(std::initializer_list<Span> in, std::initializer_list<Span> out, int own) {
+  for (size_t i = 0; i < out.size(); ++i) {
+    const Span& o = out.begin()[i];
+    for (size_t j = 0; j < in.size(); ++j) {
+      const Span& x = in.begin()[j];
+      const bool same = i == j && static_cast<int>(i) < own && o.base == x.base;
+      if (!same && meet(o, x)) return false;
+    }
+    for (size_t j = 0; j < i; ++j)
+      if (meet(o, out.begin()[j])) return false;
+  }
+  return true;
+}
+
 // The pools that a call moves, as its kernels see them.
 attn_status moved_pools(const attn_pool* src, const attn_pool* dst, int n, int page_size, int src_pages, int dst_pages,
                         std::vector<MovedPool>& out) {
@@ -293,8 +323,11 @@ extern "C" attn_status attn_varlen_cache_fork(
   if (rows > 0 && (!table || !lens || !held || !parents || !table_out || !lens_out || !held_out)) return ATTN_ERR_INVALID;
   if (rows > 1 && (table_rs < table_width || table_out_rs < table_width)) return ATTN_ERR_INVALID;
   if (rows > 1 && table_out == table && table_out_rs != table_rs) return ATTN_ERR_INVALID;
-  if (rows > 0 && (lens_out == held_out || lens_out == parents || held_out == parents || lens_out == held || held_out == lens ||
-                   (room && (room == lens_out || room == held_out))))
+  if (!outputs_apart({span(table, rows, table_rs, table_width), span(lens, rows), span(held, rows), span(refs, num_pages),
+                      span(parents, rows), span(room, rows)},
+                     {span(table_out, rows, table_out_rs, table_width), span(lens_out, rows), span(held_out, rows),
+                      span(refs_out, num_pages)},
+                     4))
     return ATTN_ERR_INVALID;
   std::vector<MovedPool> m;
   attn_status st;
@@ -334,6 +367,11 @@ extern "C" attn_status attn_varlen_cache_compact(
     if (static_cast<int64_t>(t.R) * t.W > (1 << 28)) return ATTN_ERR_UNSUPPORTED;
     if (t.R > 1 && (t.rs < t.W || t.out_rs < t.W || (t.out == t.table && t.out_rs != t.rs))) return ATTN_ERR_INVALID;
   }
+  const CompactTable &s = p.t[0], &f = p.t[1];
+  if (!outputs_apart({span(s.table, s.R, s.rs, s.W), span(f.table, f.R, f.rs, f.W), span(refs, num_pages), span(s.held, s.R),
+                      span(f.held, f.R)},
+                     {span(s.out, s.R, s.out_rs, s.W), span(f.out, f.R, f.out_rs, f.W), span(refs_out, num_pages), span(live, 1)}, 3))
+    return ATTN_ERR_INVALID;
   std::vector<MovedPool> m;
   attn_status st;
   try {

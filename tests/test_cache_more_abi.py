@@ -160,6 +160,14 @@ def test_fork_refusals(lib):
     assert size(I(3), I(4), I(9)) > 0 and size(I(-1), I(4), I(9)) == 0 and size(I(16384), I(1 << 20), I(9)) == 0
 
 
+def test_fork_refuses_outputs_that_meet_other_arrays(lib):
+    for out, at in (("ro", 0x14000), ("ro", 0x15000), ("ro", 0x11000 - 4), ("lo", 0x14000 + 8), ("ho", 0x15000), ("to", 0x14000),
+                    ("lo", 0x13000 + 32), ("to", 0x10004), ("to", 0x12000 - 44), ("ho", 0x11000 + 8)):
+        assert fork(lib, **{out: at}) == -1, (out, hex(at))
+    for out, at in (("ro", 0x14000 + 12), ("ro", 0x14000 - 36), ("to", 0x12000 - 48), ("lo", 0x13000 + 36), ("to", 0x70000)):
+        assert fork(lib, **{out: at}) == -4, (out, hex(at))      # side by side
+
+
 def compact(lib, pools=None, **over):
     pools = [pool()] if pools is None else pools
     arr = (Pool * max(1, len(pools)))(*pools)
@@ -177,6 +185,11 @@ def test_compact_and_copy_refusals(lib):
         assert compact(lib, **{name: None}) == -1, name
     assert compact(lib, trs=3) == -1 and compact(lib, tors=6) == -1 and compact(lib, ptors=3) == -1
     assert compact(lib, pools=[pool(row=0)]) == -1
+    for out, at in (("pto", 0x10000), ("to", 0x30000), ("ro", 0x12000), ("live", 0x13000 + 32), ("live", 0x12000), ("ro", 0x31000 - 8),
+                    ("to", 0x13000), ("live", 0x10000 + 44)):
+        assert compact(lib, **{out: at}) == -1, (out, hex(at))
+    assert compact(lib, live=0x13000 + 36) == -4 and compact(lib, pto=0x30000 + 32) == -4
+    assert compact(lib, ptable=0x10000, pto=0x50000, to=0x60000) == -4      # one table twice, read
 
     def copy(src=None, dst=None, **over):
         src, dst = (Pool * 1)(src or pool()), (Pool * 1)(dst or pool(base=0x50000))
