@@ -35,9 +35,9 @@
 //
 // Warps (640 threads): 0 loads K (TMA boxes of min(page_size, 128) rows per lane)
 // and the scales, 16 loads V, 1 issues S, 2 issues O, 3 plans the CTA's pieces,
-// 17-19 bring in Q rows (the first tile's with 4-11), 12-15 convert V, 64 keys at a time (rows that no row of the
-// tile reads become zeros: the pages may hold anything there, and 0 * NaN would
-// reach O), 4-11 softmax as in cache_fwd.cuh.
+// 17-19 bring in Q rows (with 4-11 the first tile's), 12-15 convert V, 64 keys at a
+// time (rows that no row of the tile reads become zeros: the pages may hold anything
+// there, and 0 * NaN would reach O), 4-11 softmax as in cache_fwd.cuh.
 //
 // Measured with the join: 144 drafted tokens of 96 heads behind two prefixes of 12001
 // keys 214 us (575 TFLOP/s of the logits' and outputs' products), 64 single tokens of

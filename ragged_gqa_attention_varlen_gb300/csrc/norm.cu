@@ -15,12 +15,11 @@
 // block, then over the lanes and warps, and a second kernel adds the blocks in
 // their order: no atomics, the same bits every time.
 //
-// Measured (bf16, turned): forward, 16000 tokens x 97 heads of 160: 197 us, 5.05
-// TB/s of its 0.99 GB; backward, 9999 tokens x 40 heads of 128: 71 us, 4.3 TB/s; 64
-// tokens x 81 heads of 160: 4.4 us, one launch.  The forward spends 0.6 of its
-// issue slots, most on the values themselves, and three resident blocks (80
-// registers) beat two (85: 228 against 209 us); rows kept as running offsets instead
-// of products spill at that count (204 us), two rows in flight a lane too (244 us).
+// Measured (bf16, turned): forward, 16000 tokens x 97 heads of 160: 190 us, 5.2 TB/s
+// of its 0.99 GB; backward, 9999 tokens x 40 heads of 128: 71 us, 4.3 TB/s; 64 tokens
+// x 81 heads of 160: 4.2 us, one launch.  The forward spends 0.6 of its issue slots,
+// most on the values themselves, and three resident blocks (80 registers) beat two
+// (85: 228 against 209 us); two rows in flight a lane took 244 us.
 #include "../../include/attn_varlen.h"
 #include "rowfrag.cuh"
 
@@ -117,37 +116,47 @@ __device__ __forceinline__ Run run_of(const Jobs& j, int64_t T, int H, int64_t i
   return r;
 }
 
-// The lane's row of a run, by passes of the block: token in the run, head, and
-// the row's place in up to three tensors.  Steps are additions: a division and the
-// products of the strides for every row took a fifth of the forward's instructions.
-struct RowAt {
-  int tok, h, left;  // left: rows from this one to the run's end
-  __device__ __forceinline__ bool valid() const { return left > 0; }
-};
-template <int D, int STEP>
+// The lane's row of a run, by passes of the block: its token in the run, its head,
+// and its place in N tensors, in elements from the run's first row.  Steps are
+// additions: a division and the products of the strides for every row took a fifth
+// of the forward's instructions.  Off: uint32_t where a run spans less than 2^31
+// elements of every tensor (short_runs): 190 us for the forward above, 64-bit ones
+// spill and take 204, the products 197.
+template <int D, int STEP, class Off, int N>
 struct Rows {
-  RowAt at;
+  int tok, h, left;  // left: rows from this one to the run's end
+  Off off[N];
   int nh, dtok, dh;
+  Off by[N], wrap[N];
   __device__ __forceinline__ Rows(const Run& run, int r0) {
     using S = RowShape<D>;
     const int g = (threadIdx.x & 31) / S::kLanes, row = r0 + g;
     nh = run.nh;
-    at.left = g < S::kRowsWarp ? run.ntok * run.nh - row : 0;
-    at.tok = at.left > 0 ? quotient(row, 1.f / nh) : 0;
-    at.h = row - at.tok * nh;
+    left = g < S::kRowsWarp ? run.ntok * run.nh - row : 0;
+    tok = left > 0 ? quotient(row, 1.f / nh) : 0;
+    h = left > 0 ? row - tok * nh : 0;
     dtok = quotient(STEP, 1.f / nh);
     dh = STEP - dtok * nh;
   }
+  __device__ __forceinline__ void tensor(int n, int h0, int64_t ts, int64_t hs) {
+    off[n] = static_cast<Off>(tok * ts + (h0 + h) * hs);
+    by[n] = static_cast<Off>(dtok * ts + dh * hs);
+    wrap[n] = static_cast<Off>(ts - nh * hs);
+  }
+  __device__ __forceinline__ bool valid() const { return left > 0; }
   __device__ __forceinline__ void step() {
-    at.left -= STEP;
-    at.tok += dtok;
-    at.h += dh;
-    if (at.h >= nh) {
-      at.h -= nh;
-      ++at.tok;
+    left -= STEP;
+    tok += dtok;
+    h += dh;
+#pragma unroll
+    for (int n = 0; n < N; ++n) off[n] += by[n];
+    if (h >= nh) {
+      h -= nh;
+      ++tok;
+#pragma unroll
+      for (int n = 0; n < N; ++n) off[n] += wrap[n];
     }
   }
-  __device__ __forceinline__ int64_t place(int h0, int64_t ts, int64_t hs) const { return at.tok * ts + (h0 + at.h) * hs; }
 };
 
 template <int D, bool VEC>
@@ -163,7 +172,7 @@ struct NormSmem {
   }
 };
 
-template <bool BF16, int D, bool VEC>
+template <bool BF16, int D, bool VEC, class Off>
 __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 3 : 1)
     norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormPlan plan) {
   using S = RowShape<D>;
@@ -183,9 +192,11 @@ __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 3 : 1)
     const int all = run.ntok * run.nh;
     int r0 = (threadIdx.x >> 5) * S::kRowsWarp;
     Ops next;
-    Rows<D, kStep> row(run, r0);
+    Rows<D, kStep, Off, 2> row(run, r0);
+    row.tensor(0, run.h0, t.ts, t.hs);
+    row.tensor(1, run.h0, t.ots, t.ohs);
     next.zero();
-    if (row.at.valid()) next.load(x0 + row.place(run.h0, t.ts, t.hs), at);
+    if (row.valid()) next.load(x0 + row.off[0], at);
     if (pairs) {
       __syncthreads();
       fill_turns<VEC>(p.r, run.tok0, run.ntok, sm.turns);
@@ -196,10 +207,11 @@ __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 3 : 1)
     for (; r0 < all; r0 += kStep) {
       uint64_t x[8];
       next.unpack(x);
-      const RowAt now = row.at;
-      uint16_t* y = y0 + row.place(run.h0, t.ots, t.ohs);
+      const bool valid = row.valid();
+      const int tok = valid ? row.tok : 0;
+      uint16_t* y = y0 + row.off[1];
       row.step();
-      if (row.at.valid()) next.load(x0 + row.place(run.h0, t.ts, t.hs), at);
+      if (row.valid()) next.load(x0 + row.off[0], at);
       uint64_t sq = f2_mul(x[0], x[0]);
 #pragma unroll
       for (int e = 1; e < 8; ++e) sq = f2_fma(x[e], x[e], sq);
@@ -211,14 +223,14 @@ __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 3 : 1)
         v[e >> 2][(e & 3) * 2] = f2_lo(z);
         v[e >> 2][(e & 3) * 2 + 1] = f2_hi(z);
       }
-      if (pairs) Ops::turn(v, sm.row(), j, pairs, inter, sm.turns.cs[now.valid() ? now.tok : 0]);
-      if (now.valid()) Ops::store(y, v, at);
+      if (pairs) Ops::turn(v, sm.row(), j, pairs, inter, sm.turns.cs[tok]);
+      if (valid) Ops::store(y, v, at);
     }
   }
 }
 
 // Blocks [0, blocks[0]) take q, the others k.
-template <bool BF16, int D, bool VEC>
+template <bool BF16, int D, bool VEC, class Off>
 __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 2 : 1)
     norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormPlan plan) {
   using S = RowShape<D>;
@@ -247,12 +259,14 @@ __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 2 : 1)
     const int all = run.ntok * run.nh;
     int r0 = warp * S::kRowsWarp;
     Ops next, dnext;
-    Rows<D, kStep> row(run, r0);
-    next.zero();
+    Rows<D, kStep, Off, 3> row(run, r0);
+    row.tensor(0, run.h0, t.ts, t.hs);
+    row.tensor(1, run.h0, t.ots, t.ohs);
+    row.tensor(2, run.h0, t.dts, t.dhs);
     auto load = [&] {
-      if (row.at.valid()) {
-        next.load(x0 + row.place(run.h0, t.ts, t.hs), at);
-        dnext.load(d0 + row.place(run.h0, t.dts, t.dhs), at);
+      if (row.valid()) {
+        next.load(x0 + row.off[0], at);
+        dnext.load(d0 + row.off[2], at);
       } else {  // (nothing of it may reach the sums)
         next.zero();
         dnext.zero();
@@ -267,15 +281,16 @@ __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 2 : 1)
     for (; r0 < all; r0 += kStep) {
       uint64_t x[8], g[8];
       next.unpack(x);
-      const RowAt now = row.at;
-      uint16_t* y = y0 + row.place(run.h0, t.ots, t.ohs);
+      const bool valid = row.valid();
+      const int tok = valid ? row.tok : 0;
+      uint16_t* y = y0 + row.off[1];
       if (pairs) {
         float v[2][8];
         unpack8<BF16>(dnext.raw[0], v[0]);
         unpack8<BF16>(dnext.raw[1], v[1]);
         row.step();
         load();
-        Ops::turn(v, sm.row(), j, pairs, inter, sm.turns.cs[now.valid() ? now.tok : 0]);
+        Ops::turn(v, sm.row(), j, pairs, inter, sm.turns.cs[tok]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = f2_make(v[e >> 2][(e & 3) * 2], v[e >> 2][(e & 3) * 2 + 1]);
       } else {
@@ -300,7 +315,7 @@ __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 2 : 1)
         v[e >> 2][(e & 3) * 2] = f2_lo(z);
         v[e >> 2][(e & 3) * 2 + 1] = f2_hi(z);
       }
-      if (now.valid()) Ops::store(y, v, at);
+      if (valid) Ops::store(y, v, at);
     }
   }
   if (!t.dweight) return;
@@ -346,30 +361,44 @@ __global__ void __launch_bounds__(1024)
   out[f] = s;
 }
 
-template <template <bool, int, bool> class F, class... A>
-void pick(const NormParams& p, bool vec, A... a, unsigned grid, cudaStream_t s) {
+// (rows that are turned through shared memory have the one form)
+template <template <bool, int, bool, class> class F, class... A>
+void pick(const NormParams& p, bool vec, bool near, A... a, unsigned grid, cudaStream_t s) {
   const bool b = p.dtype == 1;
-#define ATTN_PICK(D)                                      \
-  if (p.d == D)                                           \
-    b ? (vec ? F<true, D, true>::go(a..., grid, s) : F<true, D, false>::go(a..., grid, s)) \
-      : (vec ? F<false, D, true>::go(a..., grid, s) : F<false, D, false>::go(a..., grid, s));
+#define ATTN_GO(B, D)                                            \
+  vec ? (near ? F<B, D, true, uint32_t>::go(a..., grid, s) : F<B, D, true, int64_t>::go(a..., grid, s)) \
+      : F<B, D, false, int64_t>::go(a..., grid, s)
+#define ATTN_PICK(D) \
+  if (p.d == D) b ? (ATTN_GO(true, D)) : (ATTN_GO(false, D));
   ATTN_PICK(64)
   ATTN_PICK(128)
   ATTN_PICK(160)
 #undef ATTN_PICK
+#undef ATTN_GO
 }
-template <bool B, int D, bool V>
+template <bool B, int D, bool V, class Off>
 struct Fwd {
   static void go(const NormParams& p, const NormPlan& n, unsigned grid, cudaStream_t s) {
-    norm_kernel<B, D, V><<<grid, warps_n<V>() * 32, 0, s>>>(p, n);
+    norm_kernel<B, D, V, Off><<<grid, warps_n<V>() * 32, 0, s>>>(p, n);
   }
 };
-template <bool B, int D, bool V>
+template <bool B, int D, bool V, class Off>
 struct Bwd {
   static void go(const NormParams& p, const NormPlan& n, unsigned grid, cudaStream_t s) {
-    norm_bwd_kernel<B, D, V><<<grid, warps_n<V>() * 32, 0, s>>>(p, n);
+    norm_bwd_kernel<B, D, V, Off><<<grid, warps_n<V>() * 32, 0, s>>>(p, n);
   }
 };
+
+// Whether offsets within a run fit 32 bits (rows of heads far apart do not: one head
+// behind the other's tokens).
+bool short_runs(const NormParams& p) {
+  for (const NormTensor& t : p.t) {
+    const __int128 H = t.H > 1 ? t.H - 1 : 0, T = p.T > 1 ? kMaxTokensR : 0;
+    auto far = [&](int64_t ts, int64_t hs) { return T * ts + H * hs + p.d >= (1ll << 31); };
+    if (t.H > 0 && (far(t.ts, t.hs) || far(t.ots, t.ohs) || far(t.dts, t.dhs))) return false;
+  }
+  return true;
+}
 
 NormPlan plan_of(int64_t T, int Hq, int Hkv, int d) {
   NormPlan n;
@@ -396,14 +425,14 @@ size_t norm_bwd_workspace(int64_t T, int Hq, int Hkv, int d) {
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   const NormPlan n = plan_of(p.T, p.t[0].H, p.t[1].H, p.d);
   const int64_t all = n.job[0].count + n.job[1].count, most = 16 * kSms;
-  pick<Fwd, const NormParams&, const NormPlan&>(p, vector_pairs(p.r.inv_freq ? p.r.pairs : 0, p.r.interleaved), p, n,
+  pick<Fwd, const NormParams&, const NormPlan&>(p, vector_pairs(p.r.inv_freq ? p.r.pairs : 0, p.r.interleaved), short_runs(p), p, n,
                                                 static_cast<unsigned>(all < most ? all : most), s);
   return cudaGetLastError();
 }
 
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s) {
   const NormPlan n = plan_of(p.T, p.t[0].H, p.t[1].H, p.d);
-  if (p.T > 0) pick<Bwd, const NormParams&, const NormPlan&>(p, vector_pairs(p.r.inv_freq ? p.r.pairs : 0, p.r.interleaved), p, n,
+  if (p.T > 0) pick<Bwd, const NormParams&, const NormPlan&>(p, vector_pairs(p.r.inv_freq ? p.r.pairs : 0, p.r.interleaved), short_runs(p), p, n,
                                                 static_cast<unsigned>(n.blocks[0] + n.blocks[1]), s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!p.t[0].dweight && !p.t[1].dweight)) return e;

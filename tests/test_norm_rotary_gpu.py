@@ -160,3 +160,21 @@ def test_expanded_inputs():
     assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
     with pytest.raises(C.AttnError):
         C.attention_varlen_norm_rotary(q, None, q_out=torch.empty(1, 6, 128, dtype=BF, device="cuda").expand(70, 6, 128))
+
+
+def test_heads_far_apart():
+    """Head-major rows more than 2^32 elements apart, in place: the bits of packed ones."""
+    T, H, d, far = 70, 2, 64, 2 ** 32 + 64
+    pos, inv = torch.arange(T, dtype=torch.int32, device="cuda") * 37, (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).cuda()
+    q, dy = (torch.randn(T, H, d, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in (1, 2))
+    w = torch.linspace(0.5, 1.5, d, device="cuda")
+    want, _ = C.attention_varlen_norm_rotary(q, None, w, None, pos, inv)
+    dq, _, dw, _ = C.attention_varlen_norm_rotary_bwd(dy, None, q, None, w, None, pos, inv)
+    store = torch.empty(far + T * d, dtype=torch.bfloat16, device="cuda")
+    x = store.as_strided((T, H, d), (d, far, 1))
+    x.copy_(q)
+    C.attention_varlen_norm_rotary(x, None, w, None, pos, inv, q_out=x)
+    assert torch.equal(x, want)
+    x.copy_(dy)
+    got, _, gw, _ = C.attention_varlen_norm_rotary_bwd(x, None, q, None, w, None, pos, inv, dq=x)
+    assert torch.equal(got, dq) and torch.equal(gw, dw)
