@@ -749,8 +749,10 @@ attn_status attn_varlen_cache_evict(
  *   r = (mean_i x_i^2 + eps)^(-1/2),  y = turn(x_i r weight_i).
  * q_weight, k_weight are fp32 [head_dim], shared by the heads (NULL: ones).
  * inv_freq NULL: no turn (positions, axes, pair_axis and pairs are not looked at
- * then).  k may be NULL (Hkv = 0).  eps >= 0.  The arithmetic is fp32; an output
- * is rounded once.  q_out = q, k_out = k work in place. */
+ * then).  k may be NULL (Hkv = 0).  eps >= 0; with eps = 0 a row of zeros has no
+ * norm (NaN, in its gradients and the weights' too).  The arithmetic is fp32, so
+ * are a row's squares (sizes of 2^-60 to 2^60); an output is rounded once.  q_out =
+ * q, k_out = k work in place. */
 attn_status attn_varlen_norm_rotary(
     attn_dtype dtype, int64_t total, int Hq, int Hkv, int head_dim,
     const void *q, int64_t q_tok_stride, int64_t q_head_stride,

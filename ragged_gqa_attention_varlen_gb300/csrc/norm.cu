@@ -4,7 +4,7 @@
 // A row x of d features (one head of one token) with weights w:
 //   r = (mean(x^2) + eps)^(-1/2),  n_i = x_i r w_i,  y = turn(n)
 // and with g = turn^-1(dy), h_i = g_i w_i:
-//   dx_i = r (h_i - x_i r^2 mean(h x)),  dw_i = sum over the rows of g_i x_i r.
+//   dx_i = r (h_i - x_i r mean(h x r)),  dw_i = sum over the rows of g_i x_i r.
 // Everything between the load and the store is fp32; a row is rounded once.
 //
 // Bound by memory: the forward reads and writes each row once, the backward
@@ -16,7 +16,7 @@
 // their order: no atomics, the same bits every time.
 //
 // Measured (bf16, turned): forward, 16000 tokens x 97 heads of 160: 190 us, 5.2 TB/s
-// of its 0.99 GB; backward, 9999 tokens x 40 heads of 128: 71 us, 4.3 TB/s; 64 tokens
+// of its 0.99 GB; backward, 9999 tokens x 40 heads of 128: 72 us, 4.3 TB/s; 64 tokens
 // x 81 heads of 160: 4.2 us, one launch.  The forward spends 0.6 of its issue slots,
 // most on the values themselves, and three resident blocks (80 registers) beat two
 // (85: 228 against 209 us); two rows in flight a lane took 244 us.
@@ -71,7 +71,7 @@ struct RowOps {
     raw[0] = __ldcs(reinterpret_cast<const uint4*>(x + u.a));
     raw[1] = __ldcs(reinterpret_cast<const uint4*>(x + u.b));
   }
-  __device__ __forceinline__ void zero() { raw[0] = raw[1] = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void fill(uint32_t v) { raw[0] = raw[1] = make_uint4(v, v, v, v); }
   // The 16 values as pairs.
   __device__ __forceinline__ void unpack(uint64_t (&v)[8]) const {
     const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 3 : 1)
     Rows<D, kStep, Off, 2> row(run, r0);
     row.tensor(0, run.h0, t.ts, t.hs);
     row.tensor(1, run.h0, t.ots, t.ohs);
-    next.zero();
+    next.fill(0);
     if (row.valid()) next.load(x0 + row.off[0], at);
     if (pairs) {
       __syncthreads();
@@ -267,9 +267,9 @@ __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 2 : 1)
       if (row.valid()) {
         next.load(x0 + row.off[0], at);
         dnext.load(d0 + row.off[2], at);
-      } else {  // (nothing of it may reach the sums)
-        next.zero();
-        dnext.zero();
+      } else {  // nothing of it may reach the sums: ones, whose r is finite with eps = 0 too, times zeros
+        next.fill(BF16 ? 0x3f803f80u : 0x3c003c00u);
+        dnext.fill(0);
       }
     };
     load();
@@ -305,13 +305,15 @@ __global__ void __launch_bounds__(warps_n<VEC>() * 32, VEC ? 2 : 1)
         hx = f2_fma(f2_mul(g[e], w[e]), x[e], hx);
       }
       const float r = rsqrtf(row_sum<D>(f2_lo(sq) + f2_hi(sq)) * (1.f / D) + p.eps);
-      const float rc = -row_sum<D>(f2_lo(hx) + f2_hi(hx)) * (1.f / D) * r * r * r;  // -r^3 mean(h x)
+      // dx = r h - x^ (r mean(h x^)), x^ = x r: r^3 in one factor would pass fp32's range
+      // for rows below 2^-42 with eps = 0
+      const float rc = -row_sum<D>(f2_lo(hx) + f2_hi(hx)) * (1.f / D) * r * r;  // -r mean(h x^)
       float v[2][8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint64_t gr = f2_mul(g[e], f2_make(r, r));
         dw[e] = f2_fma(gr, x[e], dw[e]);
-        const uint64_t z = f2_fma(gr, w[e], f2_mul(x[e], f2_make(rc, rc)));
+        const uint64_t z = f2_fma(gr, w[e], f2_mul(f2_mul(x[e], f2_make(r, r)), f2_make(rc, rc)));
         v[e >> 2][(e & 3) * 2] = f2_lo(z);
         v[e >> 2][(e & 3) * 2 + 1] = f2_hi(z);
       }
