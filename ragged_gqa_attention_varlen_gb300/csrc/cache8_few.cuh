@@ -68,7 +68,7 @@ struct FewBars {
   uint64_t done, taken;            // O of a piece's warps: left, added up
   alignas(16) float scale[16][8];  // of a stage: K scales of its four 16 keys, V scales
   uint32_t gone[16];               // of a stage: bit i: its i-th 16 keys have no page
-  float2 stat[kFewWarps][8];             // (reference, sum) of a row in each warp
+  alignas(16) float4 stat[kFewWarps][8];  // (reference, sum, sum of the rounded weights, -) of a row in each warp
   float m0[8];                     // ALiBi term common to a row's keys
   PieceRing ring;
   Plan plan;
@@ -183,15 +183,18 @@ __device__ __forceinline__ void few_join(const CacheParams& p, const FwdWs& w, F
     if (!mbar_wait8_warp(&bars->done, round++ & 1, s_abort)) return;
     {
       for (int r8 = 0; r8 < pc.rows; ++r8) {
-        const float2 mine = lane < kFewWarps ? bars->stat[lane][r8] : make_float2(-INFINITY, 0.f);
+        const float4 mine = lane < kFewWarps ? bars->stat[lane][r8] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         float top = mine.x;
 #pragma unroll
         for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
         if (top == -INFINITY) top = 0.f;
         const float f = mine.x == -INFINITY ? 0.f : ex2_approx(mine.x - top);
-        float sum = mine.y * f;
+        float sum = mine.y * f, rounded = mine.z * f;
 #pragma unroll
-        for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        for (int x = 16; x; x >>= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          rounded += __shfl_xor_sync(0xffffffffu, rounded, x);
+        }
         int h = pc.head + r8;
         const int dt = head_div(p, h);
         const int64_t tok = pc.tok + dt;
@@ -200,7 +203,7 @@ __device__ __forceinline__ void few_join(const CacheParams& p, const FwdWs& w, F
         int64_t pr = 0;
         if (pc.mode)
           pr = pc.mode == 1 ? cut_row(w, blockIdx.x, pc.first, r8) : whole_row(w, p.total_q, p.Hq, pc.own, tok, h);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = rounded > 0.f ? 1.f / rounded : 0.f;
 #pragma unroll
         for (int u = 0; u < (HD / 4 + 31) / 32; ++u) {
           const int f4 = lane + 32 * u;
@@ -225,7 +228,7 @@ __device__ __forceinline__ void few_join(const CacheParams& p, const FwdWs& w, F
         }
         if (lane == 0) {
           if (pc.mode)
-            reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(top, sum, sum, m0);
+            reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(top, sum, rounded, m0);
           else
             p.lse[tok * p.Hq + h] = sum > 0.f ? (top + log2f(sum) + m0) * kLn2 : -INFINITY;
         }
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       float o[S::kCols][4];
 #pragma unroll
       for (int j = 0; j < S::kCols; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      float m_run[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float m_run[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
       float vref = 0.f, vinv = 0.f;
 
       // Chunks from the last keys back, each stage's upper half first.  A stage whose
@@ -510,6 +513,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             move = true;
           }
           l[n] *= alpha[n];
+          lr[n] *= alpha[n];
         }
         const float vtop = fmaxf(vs.x, vs.y);
         if (vtop > vref) {  // the power of two at or above it, within [2^-126, 2^126]
@@ -547,13 +551,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
               for (int n = 0; n < 4; ++n) o[j][n] *= up;
           }
+          // The rounded weights count as what they stand for (out is a weighted mean then),
+          // unless a far block's lose bits that its own keys do not need and the sum does.
+          const float back = by >= 1.f / 64 && down == 1.f ? rcp_approx(by) : 0.f;
           uint32_t pb[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float e0 = ex2_approx(s[mt][2 * e] - m_use[0]), e1 = ex2_approx(s[mt][2 * e + 1] - m_use[1]);
+            pb[e] = Pack<false>::two(e0 * by, e1 * by);
+            const uint64_t seen = Pack<false>::unpack(pb[e]);
             l[0] += e0;
             l[1] += e1;
-            pb[e] = turn8x8(Pack<false>::two(e0 * by, e1 * by));
+            lr[0] += back > 0.f ? f2_lo(seen) * back : e0;
+            lr[1] += back > 0.f ? f2_hi(seen) * back : e1;
+            pb[e] = turn8x8(pb[e]);
           }
           constexpr int kWords = HD == 64 ? 2 : (HD == 128 ? 4 : 5);  // of four features a lane holds of a row
           uint32_t v[4][kWords];
@@ -608,8 +619,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // ---- leave O and the sums to the joining warp
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) {
-        l[0] += __shfl_xor_sync(0xffffffffu, l[0], x);
-        l[1] += __shfl_xor_sync(0xffffffffu, l[1], x);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          l[n] += __shfl_xor_sync(0xffffffffu, l[n], x);
+          lr[n] += __shfl_xor_sync(0xffffffffu, lr[n], x);
+        }
       }
       if (round > 0 && !(ok = mbar_wait8_warp(&bars->taken, (round - 1) & 1, s_abort))) break;
       ++round;
@@ -617,7 +631,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int n = 0; n < 2; ++n) {
         const int r = 2 * t + n;
         if (g == 0) {
-          bars->stat[warp][r] = make_float2(m_run[n] == -INFINITY ? -INFINITY : m_run[n] - kShift8, l[n]);
+          bars->stat[warp][r] = make_float4(m_run[n] == -INFINITY ? -INFINITY : m_run[n] - kShift8, l[n], lr[n], 0.f);
           if (warp == 0) bars->m0[r] = m0[n];
         }
         if (r >= pc.rows) continue;

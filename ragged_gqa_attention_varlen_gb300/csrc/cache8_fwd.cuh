@@ -24,11 +24,14 @@
 // vref, a power of two, is a sixteenth of the largest V scale met when it was set:
 // while a block's scale is at most 64 vref, V16 stays below 2^15; beyond that vref
 // moves and O with it.  Every warp that needs it follows the scales by itself.  A
-// block whose scale is less than 2^-15 vref enters V16 with that, and its weights
-// with the rest: e4m3 times a power of two from 2^-15 to 2^6 is exact in fp16, so
-// blocks lose nothing however far their scales lie apart, until the weights do.  P
-// lies up to 2^15 (a shift of 7 above the usual 1, and 8 for the lazy reference),
-// so the smallest weights that fp16 still holds are 2^-31 of the largest.
+// block enters V16 with the power of two at or above scale / vref, 2^-15 at least,
+// and its weights take the rest: e4m3 times a power of two from 2^-15 to 2^6 is exact
+// in fp16, so V is never rounded, whatever the scales are, and blocks lose nothing
+// however far their scales lie apart, until the weights do.  P lies up to 2^15 (a
+// shift of 7 above the usual 1, and 8 for the lazy reference), so the smallest weights
+// that fp16 still holds are 2^-31 of the largest.
+// out divides by the sum of the rounded weights (as in cache_fwd.cuh, so it is a
+// weighted mean of V rows whatever the roundings), lse by that of the unrounded ones.
 //
 // The pages' bytes bound calls of few rows a key; the softmax's MUFU work, the
 // conversion and the hand-offs bound those of many.
@@ -70,7 +73,7 @@ struct Fwd8Shape {
   static constexpr uint32_t kOffRV = kOffRK + kRK * kTile;
   static constexpr uint32_t kOffMax = kOffRV + kRV * kTile;       // [2 steps][2 halves][128]
   static constexpr uint32_t kOffSum = kOffMax + 2 * 2 * 128 * 4;  // [2 pieces][2 halves][128]
-  static constexpr uint32_t kOffQs = kOffSum + 2 * 2 * 128 * 4;   // [4 pieces][128] row factors of Q
+  static constexpr uint32_t kOffQs = kOffSum + 2 * 2 * 128 * 8;   // [4 pieces][128] row factors of Q
   static constexpr uint32_t kOffBar = kOffQs + 4 * 128 * 4;
 };
 
@@ -134,9 +137,16 @@ struct VRef {
   // What of a block's scale V16 takes, and the weights.
   __device__ __forceinline__ float of_v(float scale) const {
     const float by = scale * inv;
-    return by > 0.f ? fmaxf(by, kLeastV) : 0.f;
+    return by > 0.f ? above(by) : 0.f;
   }
-  __device__ __forceinline__ float of_p(float scale) const { return fminf(scale * inv * (1.f / kLeastV), 1.f); }
+  __device__ __forceinline__ float of_p(float scale) const {
+    const float by = scale * inv;
+    return by * __int_as_float(0x7f000000 - __float_as_int(above(by)));
+  }
+  // The power of two at or above it, kLeastV at least.
+  __device__ __forceinline__ static float above(float by) {
+    return fmaxf(__int_as_float((__float_as_int(by) + 0x7fffff) & 0x7f800000), kLeastV);
+  }
   static constexpr float kLeastV = 1.f / 32768.f;
 };
 
@@ -422,7 +432,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   uint8_t* sV = sm + S::kOffV;
   uint8_t* sK = sm + S::kOffRK;
   float* sMax = reinterpret_cast<float*>(sm + S::kOffMax);
-  float* sSum = reinterpret_cast<float*>(sm + S::kOffSum);
+  float2* sSum = reinterpret_cast<float2*>(sm + S::kOffSum);
   float* sQs = reinterpret_cast<float*>(sm + S::kOffQs);
   Fwd8Bars* bars = reinterpret_cast<Fwd8Bars*>(sm + S::kOffBar);
   volatile int* s_abort = &bars->abort;
@@ -684,7 +694,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
       // subtracted from the logits; with FIXED they come without their constant c
       float bref = FIXED ? m_run - out_scale : 0.f;
       float in_scale = call_scale;
-      uint64_t l2 = f2_make(0.f, 0.f);  // of P
+      uint64_t l2 = f2_make(0.f, 0.f), lr2 = l2;  // of P, and of P as V sees it
       vref.start();
 
       for (int kt = pc.kt1 - 1; kt >= pc.kt0; --kt, ++step) {
@@ -815,6 +825,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
               m_run = mx;
             }
             l2 = f2_mul(l2, f2_make(alpha, alpha));
+            lr2 = f2_mul(lr2, f2_make(alpha, alpha));
           }
         }
         // With FIXED, the first tile's maximum becomes the reference.  The tile is
@@ -861,17 +872,27 @@ __global__ void __launch_bounds__(kThreads8, 1)
               if (!keep && edge) mask(x, c0, kCh);
             }
             uint32_t pk[kCh / 2];
+            const uint64_t l_was = l2, lr_was = lr2;
 #pragma unroll
             for (int i = 0; i < kCh; i += 2) {
               x[i] = ex2_approx(x[i]);
               x[i + 1] = ex2_approx(x[i + 1]);
               pk[i >> 1] = Pack<false>::two(x[i], x[i + 1]);
               l2 = f2_add(l2, f2_make(x[i], x[i + 1]));
+              lr2 = f2_add(lr2, Pack<false>::unpack(pk[i >> 1]));
             }
             const float rest = vref.of_p(vs[c0 >> 4]);
-            if (rest < 1.f) {  // (rare: a scale far below the others)
+            if (rest < 1.f) {  // (a scale that is no power of two, or far below the others)
+              // The rounded weights count as what they stand for, unless a far block's lose
+              // bits that its own keys do not need and the sum does.
+              uint64_t rb = f2_make(0.f, 0.f);
 #pragma unroll
-              for (int i = 0; i < kCh; i += 2) pk[i >> 1] = Pack<false>::two(x[i] * rest, x[i + 1] * rest);
+              for (int i = 0; i < kCh; i += 2) {
+                pk[i >> 1] = Pack<false>::two(x[i] * rest, x[i + 1] * rest);
+                rb = f2_add(rb, Pack<false>::unpack(pk[i >> 1]));
+              }
+              const float back = rcp_approx(rest);
+              lr2 = rest < 0.5f ? f2_add(lr_was, f2_add(l2, f2_mul(l_was, f2_make(-1.f, -1.f)))) : f2_fma(rb, f2_make(back, back), lr_was);
             }
             tmem_st8(sb + c0 / 2, pk);
           }
@@ -902,23 +923,23 @@ __global__ void __launch_bounds__(kThreads8, 1)
         if (lane == 0) mbar_arrive(&bars->p_full[step & 1]);
       }
       if (!ok) break;
-      // ---- the row's sum over both halves, then O
-      float* sums = sSum + (tiles & 1) * 256;
-      sums[half * 128 + r] = f2_lo(l2) + f2_hi(l2);
+      // ---- the row's sums over both halves, then O
+      float2* sums = sSum + (tiles & 1) * 256;
+      sums[half * 128 + r] = make_float2(f2_lo(l2) + f2_hi(l2), f2_lo(lr2) + f2_hi(lr2));
       if (!(ok = warp_exchange8(&bars->l_x[quad], tiles & 1, s_abort))) break;
-      const float l = sums[r] + sums[128 + r];
+      const float l = sums[r].x + sums[128 + r].x, lr = sums[r].y + sums[128 + r].y;
       if (!(ok = mbar_wait8_warp(&bars->o_full, tiles & 1, s_abort))) break;
       tc_fence_after();
       if (any) {
         constexpr int kC = HD / 2;
         const float m_ref = FIXED ? m_run : (m_run == -INFINITY ? 0.f : m_run - kShift8);
-        const float inv = pc.mode ? vref.ref : (l > 0.f ? vref.ref / l : 0.f);
+        const float inv = pc.mode ? vref.ref : (lr > 0.f ? vref.ref / lr : 0.f);
         int64_t pr = 0;
         if (pc.mode)
           pr = pc.mode == 1 ? cut_row(w, blockIdx.x, pc.first, r) : whole_row(w, p.total_q, p.Hq, pc.own, tok, h);
         if (valid && half == 0) {
           if (pc.mode)
-            reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(m_ref, l, l, m0);
+            reinterpret_cast<float4*>(p.ws + w.stats)[pr] = make_float4(m_ref, l, lr, m0);
           else
             p.lse[static_cast<int64_t>(tok) * p.Hq + h] = l > 0.f ? (m_ref + log2f(l) + m0) * kLn2 : -INFINITY;
         }
