@@ -1,12 +1,16 @@
-"""The cache held in 8 bits at its edges, for both of its attention kernels: exact means."""
+"""The cache held in 8 bits at its edges, for both of its attention kernels: exact means, rows bounded by
+their own weights, factors far apart, missing pages, rows far from their keys."""
+import math
+
 import pytest
 import torch
 
 import cache8_ref as ref8
+import cache8_rows as rows8
 import cache_ref as ref
 from ragged_gqa_attention_varlen_gb300 import cache as C
-from test_cache8_gpu import F8, attend
-from test_cache_gpu import HF, i32, lib, normal, status  # noqa: F401
+from test_cache8_gpu import F8, PICKED, attend, build, odd_scales, steep_scales
+from test_cache_gpu import BF, HF, case, i32, lib, normal, status, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -17,6 +21,11 @@ def run(q, kc, counts, call, want_status=0, **more):
     torch.cuda.synchronize()
     assert int(st) == want_status
     return got
+
+
+def check(got, want, where=slice(None)):
+    within("lse", got[1][where], want[1][where], want[3][where])
+    within("out", got[0][where], want[0][where], want[2][where])
 
 
 # ---------------------------------------------------------------- sums of the weights
@@ -42,3 +51,146 @@ def test_equal_values_come_out_exactly(lens, plens, counts, Hq, Hkv, d, page, sc
     out, _ = run(q, kc, counts, dict(softcap=cap, **call))
     want = (row * scale).to(HF).repeat_interleave(Hq // Hkv, 0).expand_as(out)
     assert torch.equal(out, want), (out != want).float().mean()
+
+
+# ---------------------------------------------------------------- each row by its own size
+
+# single tokens, a few and prompts in one batch, on both sides of the rule for few rows; keys enough to be cut
+MIXED = [
+    case("mixed_one_prompt", [900] + ref.spread(41, 60, 1, 900), [130] + [1] * 60, Hq=4, Hkv=2, d=64, page=32, cap=0.0),
+    case("mixed_prompt_in_the_middle", ref.spread(42, 30, 1, 600) + [1500] + [40] * 30, [1] * 30 + [60] + [0, 2] * 15, Hq=4, Hkv=1, d=160, page=64, alibi=True),
+    case("mixed_long", [9000, 7000, 33, 2500], [1, 5, 1, 1], Hq=16, Hkv=2, d=128, page=64, cap=0.0, dtype=HF, alibi=True),
+    case("mixed_window", ref.spread(43, 20, 1, 900), [1, 3] * 10, Hq=16, Hkv=2, d=128, page=16, wl=100, cap=30.0),
+    case("mixed_at_the_border", [300, 301, 302, 303] * 5, [1, 2, 3, 1] * 5, Hq=16, Hkv=2, d=64, page=16, cap=9.0, dtype=HF),
+    case("mixed_shuffled", [400, 33, 250, 600], [1, 30, 2, 1], Hq=2, Hkv=1, d=160, page=64, alibi=True, shuffled=True),
+    case("mixed_no_keys", [0, 5, 0, 400], [30, 0, 1, 1], Hq=2, Hkv=2, d=64, cap=0.0),
+    case("fewer_tokens_than_sequences", [700, 20, 30, 500, 5, 6, 7, 8] * 8, ([40] + [0] * 7) + [0, 0, 0, 1, 0, 0, 0, 0] * 7, Hq=8, Hkv=2, d=128, page=64, cap=0.0),
+]
+
+
+@pytest.mark.parametrize("scales", [None, odd_scales, steep_scales])
+@pytest.mark.parametrize("c", PICKED + MIXED)
+def test_rows_by_their_own_size(c, scales):
+    kc, q, cu_q, opt, call = build(c, 16, seed=5, scales=scales, std=0.05 if scales is steep_scales else None)
+    got = run(q, kc, c["counts"], call)
+    check(got, rows8.attention(q, kc, c["counts"], **opt))
+    again = run(q, kc, c["counts"], call)
+    assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+
+
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("apart", [20, 30, 40])
+@pytest.mark.parametrize("Hq,cap", [(8, 0.0), (48, 0.0), (48, 3.0)])
+def test_small_blocks_beside_huge_ones(Hq, cap, apart, odd):
+    """The window holds blocks 2^20 to 2^40 below the others of its key tiles, which no row reads."""
+    kc = ref8.Cache8([300, 1000], Hkv=1, d=160, page=64, block=16, scales=odd_scales if odd else None)
+    for b, n in enumerate(kc.lens_l):
+        for first in range(0, (n - 51) // 16 * 16, 16):
+            kc.v_scale[int(kc.table[b, first // 64]), first % 64 // 16] *= 2.0 ** apart
+    kc.v = kc._values(kc.v8, kc.v_scale)
+    q = normal(4, 2, Hq, 160, dtype=HF)
+    got = run(q, kc, [1, 1], dict(causal=True, window_left=50, softcap=cap))
+    check(got, rows8.attention(q, kc, [1, 1], causal=True, wl=50, cap=cap))
+
+
+# ---------------------------------------------------------------- what the pages hold
+
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("cap", [0.0, 3.0, 30.0])
+@pytest.mark.parametrize("Hq", [8, 48])
+def test_missing_pages_in_both_kernels(Hq, cap, alibi):
+    """As if their slots were not there: single pages, a whole key tile, the nearest and the farthest."""
+    kc = ref8.Cache8([300, 700, 40], Hkv=1, page=16, block=16)
+    gone = {0: [2, 4, 18], 1: list(range(8, 16)) + [0, 43], 2: [0, 1, 2]}
+    good = kc.table.clone()
+    for b, pages in gone.items():
+        for i, p in enumerate(pages):
+            kc.table[b, p] = 10 ** 6 if i % 2 else -3
+    q = normal(3, 3, Hq, 160)
+    slopes = torch.rand(3, Hq, generator=torch.Generator().manual_seed(2)) * 0.2
+    slopes[:, 1::3] *= -1
+    call = dict(causal=True, softcap=cap, **(dict(alibi_slopes=slopes.cuda()) if alibi else {}))
+    got = run(q, kc, [1] * 3, call, C.DEV_BAD_CACHE)
+    kc.table = good
+    keep = lambda b, p, pl, n: torch.tensor([j // 16 not in gone[b] for j in range(n)])
+    want = rows8.attention(q, kc, [1] * 3, causal=True, cap=cap, slopes=slopes if alibi else None, keep=keep)
+    check(got, want)
+    assert (got[0][2] == 0).all()
+
+
+@pytest.mark.parametrize("cap", [0.0, 3.0])
+def test_missing_page_of_a_prefix(cap):
+    kc = ref8.Cache8([30, 1, 200], [400], Hkv=2, d=128, page=64, block=32)
+    good = kc.ptable.clone()
+    kc.ptable[0, 3] = -1
+    q = normal(3, 4, 8, 128)
+    call = dict(causal=True, softcap=cap, prefix_table=kc.ptable, prefix_lens=kc.plens, cu_prefix=i32([0, 3]))
+    got = run(q, kc, [1, 2, 1], call, C.DEV_BAD_CACHE)
+    kc.ptable = good
+    keep = lambda b, p, pl, n: torch.tensor([not 192 <= j < 256 for j in range(pl)] + [True] * n)
+    check(got, rows8.attention(q, kc, [1, 2, 1], causal=True, cap=cap, group=[0, 0, 0], keep=keep))
+
+
+@pytest.mark.parametrize("cap", [0.0, 3.0])
+@pytest.mark.parametrize("Hq", [8, 96])
+def test_zero_factors_in_both_kernels(Hq, cap):
+    """Blocks of zeros among others, and all the keys that are met first."""
+    kc = ref8.Cache8([700, 400], Hkv=2, d=128, page=64, block=16, scales=lambda top, g: torch.where(
+        torch.rand(top.shape, generator=g) < 0.5, 0.0, ref8.pow2_scale(top)))
+    for p in kc.table[0, 4:11].tolist():
+        kc.v_scale[p] = torch.where(torch.isnan(kc.v_scale[p]), math.nan, 0.0)
+    kc.v = kc._values(kc.v8, kc.v_scale)
+    q = normal(2, 2, Hq, 128, dtype=HF)
+    check(run(q, kc, [1, 1], dict(softcap=cap)), rows8.attention(q, kc, [1, 1], cap=cap))
+
+
+def test_pages_beyond_4_gb_in_the_tiles():
+    kc = ref8.Cache8([200, 700], Hkv=1, d=128, page=64, block=16)
+    q = normal(2, 2, 48, 128, dtype=HF)
+    want = run(q, kc, [1, 1], dict(softcap=0.0))
+    far = (5 << 30) // (64 * 128)
+    n = kc.k8.shape[0]
+    for x in ("k", "v"):
+        big = torch.empty(far + n, 64, 1, 128, dtype=torch.uint8, device="cuda")
+        big[far:] = getattr(kc, x + "8").view(torch.uint8)
+        scale = torch.full((far + n, 4, 1), math.nan, device="cuda")
+        scale[far:] = getattr(kc, x + "_scale")
+        setattr(kc, x + "8", big.view(F8))
+        setattr(kc, x + "_scale", scale)
+    kc.table = (kc.table + far).int()
+    got = run(q, kc, [1, 1], dict(softcap=0.0))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("counts", [[1, 1, 0, 0], [1, 2, 0, 0], [20, 1, 0, 0]])
+def test_padded_batch_of_few_rows(counts):
+    kc = ref8.Cache8([40, 20, 0, 0], page=16, Hkv=1)
+    T = sum(counts)
+    q = normal(3, T + 5, 2, 160)
+    q[T:] = math.nan
+    out, lse = torch.full_like(q, 5.0), torch.full((T + 5, 2), 5.0, device="cuda")
+    run(q, kc, counts, dict(causal=True), out=out, lse=lse)
+    assert (out[T:] == 5).all() and (lse[T:] == 5).all()
+    check((out[:T], lse[:T]), rows8.attention(q[:T], kc, counts, causal=True))
+
+
+# ---------------------------------------------------------------- rows far from their keys
+
+@pytest.mark.parametrize("cap", [0.0, 3.0, 30.0])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("far", [1000, 1 << 20, (1 << 24) + 1, (1 << 30) - 6000])
+@pytest.mark.parametrize("Hq", [4, 32])
+def test_alibi_of_rows_far_from_their_keys(Hq, far, dtype, cap):
+    """A row at any distance behind its keys weighs them as one next to them does; lse is less by
+    slope times the way between."""
+    lens, counts = [300, 40, 5000], [1, 2, 1]
+    kc = ref8.Cache8(lens, Hkv=2, d=160, page=64, block=32)
+    q = normal(2, sum(counts), Hq, 160, dtype=dtype)
+    slopes = torch.rand(3, Hq, generator=torch.Generator().manual_seed(4)) + 0.01
+    slopes[:, ::4] = 0.0
+    near = [lens[b] + i for b, n in enumerate(counts) for i in range(n)]
+    want = rows8.attention(q, kc, counts, slopes=slopes, causal=True, cap=cap, q_pos=torch.tensor(near))
+    out, lse = run(q, kc, counts, dict(softcap=cap, alibi_slopes=slopes.cuda(), causal=True, q_pos=i32([x + far for x in near])))
+    less = far * torch.repeat_interleave(slopes.double(), torch.tensor(counts), 0)
+    within("lse", lse, want[1] - less, want[3] + less * 2.0 ** -22)
+    within("out", out, want[0], want[2])
