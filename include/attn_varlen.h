@@ -862,7 +862,8 @@ typedef struct {
  * lens [rows] are the slots in use, held [rows] the pages in a row's table (the
  * entries from held[r] on are not looked at; lens[r] <= held[r] * page_size).
  * refs [num_pages] counts the table rows that hold a page, 0 means free; other
- * holders (prefix tables) count too and keep a page from being given away.  Partly
+ * holders (prefix tables) count too and keep a page from being given away (a page
+ * held by more rows than it counts is a count out of range).  Partly
  * filled pages have one holder (this call keeps it so).  New pages are the lowest
  * free ones, in the order of the rows, pages given back in this call among them.
  * Each output may be its input (in place; table_out with the same stride) or lies

@@ -22,7 +22,7 @@ constexpr int kThreadsP = 1024;
 constexpr int kCtasP = 8;  // of the cluster, at most
 
 struct PagesHead {  // of both workspaces, at offset 0
-  int bad, lacking, moves;  // (status bits of the inputs; of the pages)
+  int bad, lacking, moves;  // (status bits of the inputs; of the pages and their counts)
   int count[kCtasP][3];  // of each block: sums of its part
 };
 
@@ -67,7 +67,7 @@ __device__ __forceinline__ Part part_of(int n) {
 }
 
 struct ForkWs {
-  size_t delta, times, lowest, lens, held, fresh, start, free, table, moves, total;
+  size_t delta, uses, times, lowest, lens, held, fresh, start, free, table, moves, total;
 };
 ForkWs fork_ws(int R, int W, int N) {
   ForkWs w;
@@ -78,6 +78,7 @@ ForkWs fork_ws(int R, int W, int N) {
     return here;
   };
   w.delta = take(N, 4);
+  w.uses = take(N, 4);
   w.times = take(R, 4);
   w.lowest = take(R, 4);
   w.lens = take(R, 4);
@@ -107,6 +108,7 @@ __global__ void __launch_bounds__(kThreadsP)
   const int ps = 1 << p.page_log2;
   PagesHead* head = reinterpret_cast<PagesHead*>(p.ws);
   int* delta = reinterpret_cast<int*>(p.ws + w.delta);
+  int* uses = reinterpret_cast<int*>(p.ws + w.uses);
   int* times = reinterpret_cast<int*>(p.ws + w.times);
   int* lowest = reinterpret_cast<int*>(p.ws + w.lowest);
   int* lens = reinterpret_cast<int*>(p.ws + w.lens);
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(kThreadsP)
     head->lacking = 0;
     head->moves = 0;
   }
-  for (int i = at; i < p.N; i += nt) delta[i] = 0;
+  for (int i = at; i < p.N; i += nt) delta[i] = uses[i] = 0;
   for (int r = at; r < p.R; r += nt) {
     times[r] = 0;
     lowest[r] = p.R;
@@ -146,7 +148,11 @@ __global__ void __launch_bounds__(kThreadsP)
     const int r = static_cast<int>(i / p.W), c = static_cast<int>(i - static_cast<int64_t>(r) * p.W);
     const int page = p.table[r * p.table_rs + c];
     table[i] = page;
-    if (c < p.held[r] && static_cast<unsigned>(page) >= static_cast<unsigned>(p.N)) bad |= ATTN_DEV_BAD_CACHE;
+    if (c >= p.held[r]) continue;
+    if (static_cast<unsigned>(page) < static_cast<unsigned>(p.N))
+      atomicAdd(uses + page, 1);
+    else
+      bad |= ATTN_DEV_BAD_CACHE;
   }
   if (bad) atomicOr(&head->bad, bad);
   cluster_sync();
@@ -188,13 +194,16 @@ __global__ void __launch_bounds__(kThreadsP)
   cluster_sync();
   // ---- the free pages, lowest first
   const Part pages = part_of(p.N);
-  int free_here = 0, first_free = 0;
+  int free_here = 0, first_free = 0, wrong = 0;
   if (sound) {
     for (int i0 = pages.lo; i0 < pages.hi; i0 += kThreadsP) {
       const int i = i0 + tid;
-      const int is = i < pages.hi && p.refs[i] + delta[i] == 0;
-      free_here += __syncthreads_count(is);
+      const int n = i < pages.hi ? p.refs[i] : 0;
+      // held by more rows than it counts: it could pass for free while a row keeps it
+      if (i < pages.hi && uses[i] > 0 && n < uses[i]) wrong = 1;
+      free_here += __syncthreads_count(i < pages.hi && n + delta[i] == 0);
     }
+    if (wrong) atomicOr(&head->lacking, ATTN_DEV_BAD_CACHE);
     if (tid == 0) {
       head->count[blockIdx.x][0] = need;
       head->count[blockIdx.x][1] = free_here;
