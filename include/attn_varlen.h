@@ -639,6 +639,7 @@ attn_status attn_varlen_rotary(
  * every K/V head, positions[0][token] or, without positions, the slot number;
  * scores (may be NULL; fp32, laid out like key_pos) receives 0.  lens_out (may
  * be NULL, not `lens` itself) receives lens[b] plus the number of new tokens.
+ * These three lie apart from what the call reads and from one another.
  * A sequence whose length is negative or whose tokens do not all fit its table
  * takes none of them and keeps its length (ATTN_DEV_BAD_CACHE); a token whose
  * page is out of the pool is left out alone.  With an inconsistent cu_new

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstring>
 #include <initializer_list>
+#include <utility>
 
 #include "../../include/attn_varlen.h"
 #include "cache.cuh"
@@ -61,6 +62,51 @@ inline bool in_place_ok(const void* in, const void* out, const Axis& in0, const 
          ((in0.n <= 1 || in0.stride == out0) && (in1.n <= 1 || in1.stride == out1));
 }
 
+// Elements of an array in memory: runs of `run` bytes on up to two axes (strides in
+// bytes; negative ones are refused elsewhere).
+struct Area {
+  const void* base;
+  __int128 run;
+  Axis outer, inner;
+  Area(const void* p, __int128 bytes, Axis a = {1, 0}, Axis b = {1, 0}) : base(p), run(bytes), outer(a), inner(b) {
+    if (inner.stride > outer.stride && inner.n > 1) std::swap(outer, inner);
+    for (Axis* x : {&outer, &inner})
+      if (x->n <= 1 || x->stride <= 0) *x = {x->n < 1 ? 0 : 1, 0};
+  }
+  bool empty() const { return !base || run < 1 || outer.n < 1 || inner.n < 1; }
+  __int128 at() const { return reinterpret_cast<uintptr_t>(base); }
+  __int128 length() const { return (outer.n - 1) * static_cast<__int128>(outer.stride) + row(); }
+  __int128 row() const { return (inner.n - 1) * static_cast<__int128>(inner.stride) + run; }
+};
+// Which of n pieces of `piece` bytes, `stride` apart, may meet [lo, hi) (relative to the first).
+inline bool pieces_that_meet(const Axis& x, __int128 piece, __int128 lo, __int128 hi, __int128& from, __int128& to) {
+  if (hi <= 0 || lo >= (x.n - 1) * static_cast<__int128>(x.stride) + piece) return false;
+  from = x.stride && lo >= piece ? (lo - piece) / x.stride + 1 : 0;
+  to = x.stride ? (hi - 1) / x.stride : 0;
+  if (to > x.n - 1) to = x.n - 1;
+  return from <= to;
+}
+inline bool meets(const Area& a, __int128 lo, __int128 hi) {
+  __int128 i0, i1, j0, j1;
+  if (!pieces_that_meet(a.outer, a.row(), lo, hi, i0, i1)) return false;
+  for (__int128 i = i0; i <= i1; ++i)
+    if (pieces_that_meet(a.inner, a.run, lo - i * a.outer.stride, hi - i * a.outer.stride, j0, j1)) return true;
+  return false;
+}
+// Whether two arrays share a byte.  Runs of the one with fewer are looked for in the
+// other, but only where the ranges that the arrays span meet at all.
+inline bool share_memory(const Area& x, const Area& y) {
+  if (x.empty() || y.empty() || x.at() >= y.at() + y.length() || y.at() >= x.at() + x.length()) return false;
+  const bool swap = x.outer.n * x.inner.n > y.outer.n * y.inner.n;
+  const Area &a = swap ? y : x, &b = swap ? x : y;
+  for (int64_t i = 0; i < a.outer.n; ++i)
+    for (int64_t j = 0; j < a.inner.n; ++j) {
+      const __int128 lo = a.at() + i * static_cast<__int128>(a.outer.stride) + j * static_cast<__int128>(a.inner.stride) - b.at();
+      if (meets(b, lo, lo + a.run)) return true;
+    }
+  return false;
+}
+
 inline bool dim_ok(int d) { return d == 160 || d == 128 || d == 64; }
 inline bool page_ok(int ps) { return ps >= 16 && ps <= 1024 && (ps & (ps - 1)) == 0; }
 inline int log2_of(int x) {
@@ -84,6 +130,33 @@ inline bool table_readable(int rows, const int32_t* table, int64_t rs, int width
 // The table of a call that writes to its pages: its rows are apart.
 inline bool table_ok(int rows, const int32_t* table, int64_t rs, int width, const int32_t* lens) {
   return table_readable(rows, table, rs, width, lens) && (rs >= width || rows <= 1);
+}
+
+// Whether what an append writes beside the pages is apart from what its other blocks
+// of threads still read, and from one another.
+inline bool append_outputs_apart(int B, int Hkv, int64_t total, int page_size, const int32_t* table, int64_t table_rs,
+                                 int width, const int32_t* lens, const int32_t* cu_new, const int32_t* positions,
+                                 int64_t axis_stride, int axes, const double* inv_freq, const int32_t* pair_axis,
+                                 int pairs, const int32_t* key_pos, int64_t kp_rs, int64_t kp_hs, const float* scores,
+                                 int64_t sc_rs, int64_t sc_hs, const int32_t* lens_out) {
+  const int64_t slots = static_cast<int64_t>(width) * page_size;
+  const bool turned = inv_freq != nullptr;
+  const Area in[] = {{lens, 4 * static_cast<__int128>(B)},
+                     {cu_new, 4 * (static_cast<__int128>(B) + 1)},
+                     {table, 4 * static_cast<__int128>(width), {B, 4 * table_rs}},
+                     {positions, 4 * static_cast<__int128>(total), {turned ? axes : 1, 4 * axis_stride}},
+                     {inv_freq, 8 * static_cast<__int128>(turned ? pairs : 0)},
+                     {pair_axis, 4 * static_cast<__int128>(turned ? pairs : 0)}};
+  const Area out[] = {{lens_out, 4 * static_cast<__int128>(B)},
+                      {key_pos, 4 * static_cast<__int128>(slots), {B, 4 * kp_rs}, {Hkv, 4 * kp_hs}},
+                      {scores, 4 * static_cast<__int128>(slots), {B, 4 * sc_rs}, {Hkv, 4 * sc_hs}}};
+  for (const Area& o : out) {
+    for (const Area& i : in)
+      if (share_memory(o, i)) return false;
+    for (const Area& x : out)
+      if (&x != &o && share_memory(o, x)) return false;
+  }
+  return true;
 }
 
 // What attention and the key weights share.  `unit`: the pages' elements in 16

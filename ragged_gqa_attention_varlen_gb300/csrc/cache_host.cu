@@ -60,6 +60,9 @@ extern "C" attn_status attn_varlen_cache_append(
     const attn_status st = rotary_args(positions, axes, inv_freq, pairs, head_dim, total);
     if (st != ATTN_OK) return st;
   }
+  if (!append_outputs_apart(B, Hkv, total, page_size, table, table_rs, table_width, lens, cu_new, positions, axis_stride, axes,
+                            inv_freq, pair_axis, pairs, key_pos, kp_rs, kp_hs, scores, sc_rs, sc_hs, lens_out))
+    return ATTN_ERR_INVALID;
   if (!k_cache || !v_cache || (total > 0 && (!k || !v))) return ATTN_ERR_INVALID;
   if (!strided_ok({{k_cache, {kc_ps, kc_ss, kc_hs}}, {v_cache, {vc_ps, vc_ss, vc_hs}}}))
     return ATTN_ERR_ALIGNMENT;

@@ -203,6 +203,9 @@ extern "C" attn_status attn_varlen_cache8_append(
     const attn_status st = rotary_args(positions, axes, inv_freq, pairs, head_dim, total);
     if (st != ATTN_OK) return st;
   }
+  if (!append_outputs_apart(B, Hkv, total, page_size, table, table_rs, table_width, lens, cu_new, positions, axis_stride, axes,
+                            inv_freq, pair_axis, pairs, key_pos, kp_rs, kp_hs, nullptr, 0, 0, lens_out))
+    return ATTN_ERR_INVALID;
   if (norm && (!(eps >= 0.f) || !std::isfinite(eps))) return ATTN_ERR_INVALID;
   if (!k_cache || !v_cache || !k_scale || !v_scale || (total > 0 && (!k || !v))) return ATTN_ERR_INVALID;
   if (!strided_from(16, {{k_cache, {kc_ps, kc_ss, kc_hs}}, {v_cache, {vc_ps, vc_ss, vc_hs}}}, 16)) return ATTN_ERR_ALIGNMENT;
