@@ -34,6 +34,8 @@ namespace {
 constexpr int kWarpsQ = 16, kThreadsQ = kWarpsQ * 32;
 constexpr int kMaxTokensQ = 64;  // of a block: two for each lane of a warp
 constexpr int kCuQ = 256;        // entries of cu_new that a block keeps
+constexpr float kLeastScale = 1.1754943508222875e-38f;  // 2^-126
+constexpr float kFarUp = 18446744073709551616.f;        // 2^64
 
 template <int D>
 constexpr int pass_rows() { return kWarpsQ * RowShape<D>::kRowsWarp; }
@@ -70,7 +72,7 @@ struct Job {         // a block of slots with new tokens
   int tok, start;    // its first new token, and that token's row here
   int held;          // slots it holds already
   int64_t at, scale; // its first slot's place in the pool (elements), its scale's
-  float was, now, inv;
+  float was, now, up, inv;  // inv: 1 / (now up)
   int top;           // bits of the largest |value|
 };
 
@@ -278,7 +280,9 @@ __global__ void __launch_bounds__(kThreadsQ)
     Job& job = sm.job[tid];
     const float top = __int_as_float(job.top);
     job.now = top <= 448.f * job.was ? job.was : pow2_scale(top);
-    job.inv = job.now > 0.f ? 1.f / job.now : 0.f;
+    // (another quantiser's factor may be too small for its reciprocal: value 2^64 / (now 2^64))
+    job.up = job.now < kLeastScale ? kFarUp : 1.f;
+    job.inv = job.now > 0.f ? 1.f / (job.now * job.up) : 0.f;
     sc.base[job.scale] = job.now;
   }
   __syncthreads();
@@ -290,6 +294,13 @@ __global__ void __launch_bounds__(kThreadsQ)
     if (of[it] < 0) continue;
     const Job& job = sm.job[of[it]];
     uint8_t* y = dst + job.at + static_cast<int64_t>(job.held + tok[it] - job.tok) * pool.slot;
+    if (job.up != 1.f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[it][0][e] *= job.up;
+        v[it][1][e] *= job.up;
+      }
+    }
     *reinterpret_cast<uint2*>(y + u.a) = pack_e4m3(v[it][0], job.inv);
     *reinterpret_cast<uint2*>(y + u.b) = pack_e4m3(v[it][1], job.inv);
   }

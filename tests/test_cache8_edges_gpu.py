@@ -1,5 +1,6 @@
 """The cache held in 8 bits at its edges, for both of its attention kernels: exact means, rows bounded by
-their own weights, factors far apart, missing pages, rows far from their keys."""
+their own weights, factors far apart, missing pages, rows far from their keys; and the append's
+smallest factors."""
 import math
 
 import pytest
@@ -194,3 +195,28 @@ def test_alibi_of_rows_far_from_their_keys(Hq, far, dtype, cap):
     less = far * torch.repeat_interleave(slopes.double(), torch.tensor(counts), 0)
     within("lse", lse, want[1] - less, want[3] + less * 2.0 ** -22)
     within("out", out, want[0], want[2])
+
+
+# ---------------------------------------------------------------- append
+
+def test_append_to_blocks_with_the_smallest_factors():
+    """Factors below 2^-126 (another quantiser's) are factors all the same: zeros stay zeros beside
+    them, and small values are value / factor."""
+    kc = ref8.Cache8([16] * 4, Hkv=1, d=64, page=16, block=16)
+    tiny = [2.0 ** -127, 2.0 ** -130, 3 * 2.0 ** -149, 2.0 ** -128]
+    k = torch.zeros(4, 1, 64)
+    k[1, 0, :3] = torch.tensor([2.0 ** -126, -(2.0 ** -128), 2.0 ** -133])
+    k[3, 0, 5] = 1.0
+    k = k.to(BF).cuda()
+    pages = [int(p) for p in kc.table[:, 0]]
+    for p, s in zip(pages, tiny):
+        kc.k_scale[p] = kc.v_scale[p] = s
+    held = [x.view(torch.uint8).clone() for x in (kc.k8, kc.v8)]
+    C.attention_varlen_cache8_append(k, k, kc.k8, kc.v8, kc.k_scale, kc.v_scale, kc.table, i32([8] * 4), i32(range(5)))
+    for x, s, old in ((kc.k8, kc.k_scale, held[0]), (kc.v8, kc.v_scale, held[1])):
+        assert [float(s[p, 0, 0]) for p in pages] == tiny[:3] + [2.0 ** -8]
+        for b in (0, 1, 2):
+            got = x[pages[b], 8, 0].float().cpu().double()
+            assert torch.equal(got, ref8.e4m3(k[b, 0].cpu().double() / tiny[b])), b
+            assert torch.equal(x[pages[b], :8].view(torch.uint8), old[pages[b], :8])
+        assert float(x[pages[3], 8, 0, 5].float()) == 256.0
