@@ -49,6 +49,7 @@ struct CacheParams {
   int wl, wr;                // window limits, < 0: none (wr = 0 when causal)
   float softcap, sigma;
   int tile_cost;             // what a tile's start costs, in steps (cache_sched.cuh)
+  int least_rows, most_rows; // the sequences that this kernel takes, by their rows of a K/V head (most 0: all)
   void* out;                 // forward
   int64_t out_ts, out_hs;
   float* lse;                // [total_q, Hq]; the forward writes it, the weights call reads it
@@ -126,6 +127,7 @@ bool encode_pages(CUtensorMap* m, const CacheParams& p, const Pages& pg, bool ta
 int device_ctas();  // CTAs of a persistent kernel on the current device
 
 size_t fwd_workspace(int B, int P, int Hq, int Hkv, int d, int64_t total_q);
+size_t fwd8_workspace(int B, int P, int Hq, int Hkv, int d, int64_t total_q);
 size_t weights_workspace();
 cudaError_t launch_fwd(const CacheParams& p, cudaStream_t s);
 cudaError_t launch_weights(const CacheParams& p, cudaStream_t s);

@@ -503,8 +503,15 @@ __global__ void __launch_bounds__(kThreads8, 1)
     }
     head->ok = ok;
   }
+  // Where the kernel for few rows took a part of the sequences, this one starts beside
+  // its last CTAs and reads nothing of it, but ends behind it: the join waits for this
+  // one alone.
+  auto behind_few = [&] {
+    if (p.most_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   if (!busy || (smem_addr(sm) & 1023u)) {  // uniform
     if (warp == 1) tmem_dealloc(tmem, 512);
+    behind_few();
     return;
   }
   const int box = min(p.page_size, kKeys), box_log2 = min(p.page_log2, 7);  // rows of a load box
@@ -1002,6 +1009,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   if (tid == 0 && *s_abort) report(p.status, ATTN_DEV_TIMEOUT_FWD);
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  behind_few();
 }
 
 // A softcap of at most kFixedCap8 at default key positions.
@@ -1033,8 +1041,17 @@ cudaError_t launch_fwd8_d(const Cache8Params& p, const FwdWs& w, const CUtensorM
   auto k = p.c.dtype == 1 ? pick_fwd8<true, HD>(p.c) : pick_fwd8<false, HD>(p.c);
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k<<<grid, kThreads8, smem, s>>>(p, w, tk, tkt, tv);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads8);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.c.most_rows ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k, p, w, tk, tkt, tv);
 }
 
 }  // namespace kv

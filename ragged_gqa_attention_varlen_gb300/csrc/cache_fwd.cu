@@ -37,7 +37,7 @@ constexpr int kHeadsJ = 8;  // rows (heads of a token) of a block
 // not depend on the tile kernel is read before the wait for it.
 template <bool BF16, int HD, int TR>
 __global__ void __launch_bounds__(kWarpsJ * 32)
-    join_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ FwdWs w) {
+    join_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ FwdWs tiles, const __grid_constant__ FwdWs few) {
   constexpr int kUnits = HD / 4;                            // float4 of a row
   constexpr int kPer = (kUnits + 4 * kWarpsJ - 1) / (4 * kWarpsJ);  // of a thread
   const int tok = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -50,9 +50,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
     return;
   }
   const int g = h / p.R, hr = h - g * p.R;
-  const int2* meta = reinterpret_cast<const int2*>(p.ws + w.meta);
-  const float4* stats = reinterpret_cast<const float4*>(p.ws + w.stats);
-  const float4* part = reinterpret_cast<const float4*>(p.ws + w.rows);
+  const int2* meta = reinterpret_cast<const int2*>(p.ws + tiles.meta);
   const int64_t row = static_cast<int64_t>(tok) * p.Hq + h;
   // The row's sequence; with one token each it is the token's own number, so
   // its lengths are read along with the test of that.
@@ -73,6 +71,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   // place in their row tiles
   bool has_own, has_prefix = false;
   int ro, rp = 0;
+  const bool by8 = TR == 8 || (TR == 0 && static_cast<int64_t>(c1 - c0) * p.R <= kFewMost);
   {
     Seg own;
     own.own = 1;
@@ -82,9 +81,12 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
     own.len = len;
     const uint32_t x = static_cast<uint32_t>(tok - c0) * p.R + hr;
     int lo, hi;
-    tile_keys<TR>(p, own, x / TR, lo, hi);
+    if (by8)
+      tile_keys<8>(p, own, x / 8, lo, hi);
+    else
+      tile_keys<kRows>(p, own, x / kRows, lo, hi);
     has_own = hi > lo;
-    ro = x % TR;
+    ro = x % (by8 ? 8 : kRows);
   }
   if (p.P) {
     const int pfx = prefix_of(p, b);
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
       const int n = seg_len(p, false, pfx);
       has_prefix = prefix_klo(p, pfx, n) < n;
       const int tok0 = __ldg(p.cu_q + max(__ldg(p.cu_prefix + pfx), 0));
-      rp = (static_cast<uint32_t>(tok - tok0) * p.R + hr) % TR;
+      rp = (static_cast<uint32_t>(tok - tok0) * p.R + hr) % kRows;
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -103,6 +105,9 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
   if (!has_prefix) mp = make_int2(0, 0);
   if (!ok || (mo.y == 1 && mp.y == 0)) return;
   const int parts = mo.y + mp.y;
+  const FwdWs& w = TR == 0 && by8 ? few : tiles;
+  const float4* stats = reinterpret_cast<const float4*>(p.ws + w.stats);
+  const float4* part = reinterpret_cast<const float4*>(p.ws + w.rows);
   auto row_of = [&](int i) -> int64_t {
     if (i < mo.y)
       return mo.y > 1 ? cut_row(w, mo.x + i, i == 0, ro) : whole_row(w, p.total_q, p.Hq, true, tok, h);
@@ -172,6 +177,7 @@ __global__ void __launch_bounds__(kWarpsJ * 32)
 template <int HD>
 auto join_for(const CacheParams& p, int tile_rows) {
   if (tile_rows == 8) return p.dtype == 1 ? join_kernel<true, HD, 8> : join_kernel<false, HD, 8>;
+  if (tile_rows == 0) return p.dtype == 1 ? join_kernel<true, HD, 0> : join_kernel<false, HD, 0>;
   return p.dtype == 1 ? join_kernel<true, HD, kRows> : join_kernel<false, HD, kRows>;
 }
 
@@ -207,7 +213,7 @@ size_t fwd_workspace(int B, int P, int Hq, int Hkv, int d, int64_t total_q) {
 
 // A programmatic dependent of the tile kernel: its blocks are placed early and
 // wait for the results.
-cudaError_t launch_join(const CacheParams& p, const FwdWs& w, int tile_rows, cudaStream_t s) {
+cudaError_t launch_join(const CacheParams& p, const FwdWs& w, int tile_rows, cudaStream_t s, const FwdWs* few) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.total_q), (p.Hq + kHeadsJ - 1) / kHeadsJ);
   cfg.blockDim = dim3(kWarpsJ * 32);
@@ -220,7 +226,7 @@ cudaError_t launch_join(const CacheParams& p, const FwdWs& w, int tile_rows, cud
   auto k = p.d == 160   ? join_for<160>(p, tile_rows)
            : p.d == 128 ? join_for<128>(p, tile_rows)
                         : join_for<64>(p, tile_rows);
-  return cudaLaunchKernelEx(&cfg, k, p, w);
+  return cudaLaunchKernelEx(&cfg, k, p, w, few ? *few : w);
 }
 
 cudaError_t launch_fwd(const CacheParams& call, cudaStream_t s) {

@@ -262,7 +262,8 @@ extern "C" attn_status attn_varlen_cache8_append(
 }
 
 extern "C" size_t attn_varlen_cache8_fwd_workspace_size(int B, int P, int Hq, int Hkv, int head_dim, int64_t total_q) {
-  return attn_varlen_cache_fwd_workspace_size(B, P, Hq, Hkv, head_dim, total_q);
+  if (B < 0 || P < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || total_q < 0 || !dim_ok(head_dim)) return 0;
+  return fwd8_workspace(B, P, Hq, Hkv, head_dim, total_q);
 }
 
 extern "C" attn_status attn_varlen_cache8_fwd(
@@ -296,7 +297,7 @@ extern "C" attn_status attn_varlen_cache8_fwd(
   if (!out) return ATTN_ERR_INVALID;
   if (!strided_ok({{out, {out_ts, out_hs}}})) return ATTN_ERR_ALIGNMENT;
   if (!distinct(head_dim, {{total_q, out_ts}, {Hq, out_hs}})) return ATTN_ERR_INVALID;
-  if (!workspace_ok(workspace, workspace_bytes, fwd_workspace(B, P, Hq, Hkv, head_dim, total_q)))
+  if (!workspace_ok(workspace, workspace_bytes, fwd8_workspace(B, P, Hq, Hkv, head_dim, total_q)))
     return ATTN_ERR_WORKSPACE;
   p.out = out;
   p.out_ts = out_ts;

@@ -82,9 +82,14 @@ __device__ __forceinline__ void piece_done(PieceRing* r, uint32_t k_taken) {
   mbar_arrive(&r->empty[(k_taken - 1) & 3]);
 }
 
-// Joins the partial results behind the tile kernel (cache_fwd.cu).
-// (tile_rows: rows of its tiles, 128 or 8)
-cudaError_t launch_join(const CacheParams& p, const FwdWs& w, int tile_rows, cudaStream_t s);
+// Sequences with at most this many rows of a K/V head are the kernel for few rows' where
+// a call launches both (cache8_fwd.cu).
+constexpr int kFewMost = 16;
+
+// Joins the partial results behind the tile kernel (cache_fwd.cu).  tile_rows: rows of
+// its tiles, 128 or 8; 0: 8 for sequences with few rows, whose results lie at `few`, else
+// 128.
+cudaError_t launch_join(const CacheParams& p, const FwdWs& w, int tile_rows, cudaStream_t s, const FwdWs* few = nullptr);
 
 // One warp: this CTA's share as pieces, in the order of the segments.
 template <int TR = kRows>

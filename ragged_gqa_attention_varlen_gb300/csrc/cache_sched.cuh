@@ -113,6 +113,10 @@ template <int TR = kRows>
 __device__ __forceinline__ SegPlan seg_plan(const CacheParams& p, int s) {
   SegPlan g;
   g.s = seg_load(p, s);
+  if (p.most_rows) {
+    const int64_t rows = static_cast<int64_t>(g.s.ntok) * p.R;
+    if (rows < p.least_rows || rows > p.most_rows) g.s.ntok = 0;
+  }
   g.plen = g.s.own ? 0 : g.s.len;
   g.waits = !g.s.own;
   if (g.s.own && p.P) {
