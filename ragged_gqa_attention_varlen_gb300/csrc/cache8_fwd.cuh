@@ -884,9 +884,20 @@ __global__ void __launch_bounds__(kThreads8, 1)
             for (int i = 0; i < kCh; i += 2) {
               x[i] = ex2_approx(x[i]);
               x[i + 1] = ex2_approx(x[i + 1]);
-              pk[i >> 1] = Pack<false>::two(x[i], x[i + 1]);
               l2 = f2_add(l2, f2_make(x[i], x[i + 1]));
-              lr2 = f2_add(lr2, Pack<false>::unpack(pk[i >> 1]));
+              if constexpr (CAP) {
+                pk[i >> 1] = Pack<false>::two(x[i], x[i + 1]);
+                lr2 = f2_add(lr2, Pack<false>::unpack(pk[i >> 1]));
+              } else {
+                // Cut to fp16's 11 bits (those below 2^-14 are rounded once more, by 2^-25 at
+                // most): the sum that divides takes the bias out again.  Rounded and widened as
+                // above 413 us (192 rows a key) and 609 (a prompt), so 388 and 569; with a cap
+                // the same, drafts 228 and 230.
+                const float a = __int_as_float(__float_as_int(x[i]) & 0xffffe000);
+                const float b = __int_as_float(__float_as_int(x[i + 1]) & 0xffffe000);
+                pk[i >> 1] = Pack<false>::two(a, b);
+                lr2 = f2_add(lr2, f2_make(a, b));
+              }
             }
             const float rest = vref.of_p(vs[c0 >> 4]);
             if (rest < 1.f) {  // (a scale that is no power of two, or far below the others)
