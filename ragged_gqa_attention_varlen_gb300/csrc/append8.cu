@@ -12,7 +12,8 @@
 //         with top <= 448 now; 0 when all is 0
 //   q = rn(x / now), and held values become rn(q was / now).
 //
-// Rows are fp32 from the load to the one rounding.  A block of threads takes a run
+// Rows are fp32 from the load to the one rounding (values near a border of e4m3 in twice
+// the digits, below).  A block of threads takes a run
 // of tokens of one head of K or of V: the tokens that begin a block of slots (or a
 // sequence) own that block and bring in its other new tokens, so every block of
 // slots has one writer.  All its rows stay in registers between the maximum and
@@ -20,8 +21,8 @@
 //
 // Bound by a block's own latency: its rows, positions and held scales are three
 // dependent reads before the first product.  Measured: a token each of 64 sequences,
-// 8 heads of 128, normed and turned (bf16): 8.0 us; 9 prompts of up to 12000 tokens
-// (17 thousand in all), one head of 160: 15 us, 1.1 TB/s of its 16.5 MB.
+// 8 heads of 128, normed and turned (bf16): 8.6 us; 9 prompts of up to 12000 tokens
+// (17 thousand in all), one head of 160: 17.2 us, 1 TB/s of its 16.5 MB.
 #include <cuda_fp8.h>
 
 #include "../../include/attn_varlen.h"
@@ -48,16 +49,119 @@ __device__ __forceinline__ float pow2_scale(float top) {
   return __int_as_float(max(e, 1) << 23);
 }
 
-// turn_of (rotary.cuh) to fp32's accuracy: what is off here moves values across e4m3's
-// borders, where a whole step is the least that one can be wrong by.  The angle goes
-// to fp32 as its distance from the nearest quarter turn (off by 2^-27 of a half turn).
-__device__ __forceinline__ float2 exact_turn(int64_t pos, uint64_t per_pos) {
+// A value that lies within fp32's error of a border of e4m3 falls to one side or the
+// other by chance, a sixteenth apart: of the K rows of 17 thousand tokens, a few.  So
+// K rows are normed and turned in fp32 first, by at most kOffTurn or kOffNorm of their
+// size off, and the pairs with a value nearer than that to a border once more in twice
+// the digits (rows that turn through shared memory are not: they may be off by that).
+// Borders, e4m3's and those of its smallest numbers, are numbers of four bits after the
+// leading one, whatever the block's factor (a power of two): between two of them the
+// other bits count up.
+//
+// Two: two numbers that stand for their sum, |l| at most half a step of h.
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {  // |a| >= |b|
+  const float h = __fadd_rn(a, b);
+  return {h, __fsub_rn(b, __fsub_rn(h, a))};
+}
+__device__ __forceinline__ Two two_product(float a, float b) {
+  const float h = __fmul_rn(a, b);
+  return {h, __fmaf_rn(a, b, -h)};
+}
+// a c + b s.
+__device__ __forceinline__ Two two_dot(float a, Two c, float b, Two s) {
+  const Two p = two_product(a, c.h), q = two_product(b, s.h);
+  const float d = __fadd_rn(p.h, q.h), z = __fsub_rn(d, p.h);
+  const float off = __fadd_rn(__fsub_rn(p.h, __fsub_rn(d, z)), __fsub_rn(q.h, z));
+  return two_sum(d, off + (p.l + q.l) + fmaf(a, c.l, b * s.l));
+}
+// In fp32, with an odd last bit if it is not exact: a later rounding to fewer bits then
+// goes the way that the pair's own would.
+__device__ __forceinline__ float to_odd(Two x) {
+  const int b = __float_as_int(x.h);
+  return __int_as_float(x.l == 0.f || (b & 1) ? b : ((x.l > 0.f) == (x.h > 0.f) ? b + 1 : b - 1));
+}
+
+struct Turn {
+  Two c, s;
+};
+// (cos, sin) of `pos` times a turn fraction, off by less than 2^-27: the angle's distance
+// from the nearest quarter turn, at most pi / 4, into the Taylor series.
+__device__ __forceinline__ Turn turn_two(int64_t pos, uint64_t per_pos) {
+  const uint32_t u = static_cast<uint32_t>((static_cast<uint64_t>(pos) * per_pos + 0x80000000u) >> 32);
+  const uint32_t quarter = (u + 0x20000000u) >> 30;
+  const int32_t d = static_cast<int32_t>(u - (quarter << 30));
+  const float dh = static_cast<float>(d), dl = static_cast<float>(d - static_cast<int32_t>(dh));
+  constexpr double kTurn = 6.283185307179586477 / 4294967296.0;
+  constexpr float kHi = static_cast<float>(kTurn), kLo = static_cast<float>(kTurn - kHi);
+  Two t = two_product(dh, kHi);
+  t.l += fmaf(dh, kLo, dl * kHi);
+  const Two q = two_product(t.h, t.h);
+  float p = fmaf(q.h, 1.f / 362880, -1.f / 5040);
+  p = fmaf(q.h, fmaf(q.h, p, 1.f / 120), -1.f / 6);
+  Two sn = two_sum(t.h, t.h * q.h * p);
+  sn.l += fmaf(-0.5f * q.h, t.l, t.l);
+  float r = fmaf(q.h, -1.f / 3628800, 1.f / 40320);
+  r = fmaf(q.h, fmaf(q.h, r, -1.f / 720), 1.f / 24);
+  Two cn = two_sum(1.f, -0.5f * q.h);
+  cn.l += fmaf(q.h * q.h, r, -fmaf(t.h, t.l, 0.5f * q.l));
+  Turn x = quarter & 1 ? Turn{sn, cn} : Turn{cn, sn};
+  if ((quarter + 1) & 2) x.c = {-x.c.h, -x.c.l};
+  if (quarter & 2) x.s = {-x.s.h, -x.s.l};
+  return x;
+}
+__device__ __forceinline__ void turn_pair(const Turn& t, float& a, float& b) {
+  const float x = a;
+  a = to_odd(two_dot(x, t.c, -b, t.s));
+  b = to_odd(two_dot(b, t.c, x, t.s));
+}
+
+// turn_of (rotary.cuh) to fp32's accuracy.  The angle goes to fp32 as its distance from
+// the nearest quarter turn (off by 2^-27 of a half turn).
+__device__ __forceinline__ float2 turn_fp32(int64_t pos, uint64_t per_pos) {
   const uint32_t u = static_cast<uint32_t>((static_cast<uint64_t>(pos) * per_pos) >> 32);
   const uint32_t quarter = (u + 0x20000000u) >> 30;
   float sn, cn;
   sincospif(static_cast<float>(static_cast<int32_t>(u - (quarter << 30))) * 4.656612873077393e-10f, &sn, &cn);
   const float a = quarter & 1 ? sn : cn, b = quarter & 1 ? cn : sn;
   return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
+}
+
+// x w / the row's size.
+__device__ __forceinline__ float normed(float x, float w, float r0, float r1) {
+  const Two rw = two_product(r0, w), y = two_product(x, rw.h);
+  return to_odd(two_sum(y.h, fmaf(x, fmaf(r1, w, rw.l), y.l)));
+}
+
+// fp32's error of a turned pair, relative to the sum of its magnitudes, in 2^-24: sine and
+// cosine 1, the angle 0.6, the products and the sum 1/2 each; with a norm 2 for its factor
+// and products.
+constexpr float kOffTurn = 3.f / (1 << 24), kOffNorm = 6.f / (1 << 24);
+// Whether a value may lie on the other side of a border.
+__device__ __forceinline__ uint32_t near_border(float y, float off) {
+  return (__float_as_int(y + off) ^ __float_as_int(y - off)) & 0xfff80000u;
+}
+// Features fa and fb of a row once more.  A call, so that the rows keep their registers:
+// inlined, the kernel of prompts spilled (18.2 us; so 17.1, without any of this 15.1, all
+// pairs in twice the digits 19.8).
+template <bool BF16>
+__device__ __noinline__ float2 redo_pair(const uint16_t* row, int fa, int fb, int norm, const float* w, float r0, float r1, bool turned,
+                                         const int32_t* pos, uint64_t per_pos) {
+  float a = to_float<BF16>(row[fa]), b = to_float<BF16>(row[fb]);
+  if (norm) {
+    a = normed(a, w ? __ldg(w + fa) : 1.f, r0, r1);
+    b = normed(b, w ? __ldg(w + fb) : 1.f, r0, r1);
+  }
+  if (turned) turn_pair(turn_two(__ldg(pos), per_pos), a, b);
+  return make_float2(a, b);
+}
+// Turns pair e of a lane and notes it in `near` if a value is near a border.
+__device__ __forceinline__ void turn_checked(float& a, float& b, int e, float off, const float2& c, uint32_t& near) {
+  off *= fabsf(a) + fabsf(b);
+  turn2<true>(c, a, b);
+  if (near_border(a, off) | near_border(b, off)) near |= 1u << e;
 }
 
 __device__ __forceinline__ uint2 pack_e4m3(const float (&v)[8], float inv) {
@@ -86,7 +190,7 @@ struct Append8Smem {
 };
 
 template <bool BF16, int D, bool VEC, int NIT>
-__global__ void __launch_bounds__(kThreadsQ)
+__global__ void __launch_bounds__(kThreadsQ, NIT <= 2 ? 2 : 1)
     append8_kernel(const __grid_constant__ Append8Params p8, int ntok) {
   using S = RowShape<D>;
   __shared__ Append8Smem sm;
@@ -248,26 +352,66 @@ __global__ void __launch_bounds__(kThreadsQ)
 #pragma unroll
   for (int it = 0; it < NIT; ++it) {
     float(&x)[2][8] = v[it];
+    float r0 = 1.f, r1 = 0.f;  // 1 / the row's size, in two terms
+    uint32_t near = 0;         // pairs of this lane with a value near a border
+    const int n = min(max(pairs - 8 * j, 0), 8);  // its pairs that turn
     if (!is_v && p8.norm) {
-      float sq = 0.f;
+      float sq[4] = {};  // (four short sums: half the roundings of one)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sq = fmaf(x[0][e], x[0][e], fmaf(x[1][e], x[1][e], sq));
-      const float r = rsqrtf(row_sum<D>(sq) * (1.f / D) + p8.eps);
+      for (int e = 0; e < 8; ++e) sq[e & 3] = fmaf(x[0][e], x[0][e], fmaf(x[1][e], x[1][e], sq[e & 3]));
+      const float mean = row_sum<D>((sq[0] + sq[1]) + (sq[2] + sq[3])) / D + p8.eps;
+      r0 = rsqrtf(mean);
+      const Two m = two_product(mean, r0);  // a step of Newton's: r0 + r0 (1 - mean r0^2) / 2
+      r1 = 0.5f * r0 * (__fmaf_rn(-m.h, r0, 1.f) - m.l * r0);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[0][e] *= r * (p8.k_weight ? __ldg(p8.k_weight + u.a + e) : 1.f);
-        x[1][e] *= r * (p8.k_weight ? __ldg(p8.k_weight + u.b + e) : 1.f);
+        x[0][e] *= (r0 + r1) * (p8.k_weight ? __ldg(p8.k_weight + u.a + e) : 1.f);
+        x[1][e] *= (r0 + r1) * (p8.k_weight ? __ldg(p8.k_weight + u.b + e) : 1.f);
+      }
+      if (VEC && n < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // (of an interleaved lane the last four pairs alone may stay as they are)
+          const float a = p.r.interleaved ? x[e >> 2][2 * (e & 3)] : x[0][e], b = p.r.interleaved ? x[e >> 2][2 * (e & 3) + 1] : x[1][e];
+          if (e >= n && (near_border(a, fabsf(a) * kOffNorm) | near_border(b, fabsf(b) * kOffNorm))) near |= 1u << e;
+        }
       }
     }
     if (pairs) {
-      auto turn = [&](int i) { return exact_turn(__ldg(p.r.positions + sm.axis_row[i] + tok[it]), sm.per_pos[i]); };
-      if (VEC)
-        turn_item(x[0], x[1], j, pairs, p.r.interleaved, [&](int i, float2& a, float2& b) {
-          a = turn(i);
-          b = turn(i + 1);
-        });
-      else
+      auto turn = [&](int i) { return turn_fp32(__ldg(p.r.positions + sm.axis_row[i] + tok[it]), sm.per_pos[i]); };
+      if (VEC) {
+        const float off = p8.norm ? kOffNorm : kOffTurn;
+        if (!p.r.interleaved) {
+          if (n > 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) turn_checked(x[0][e], x[1][e], e, off, turn(8 * j + e), near);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (n > 4 * h) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) turn_checked(x[h][2 * e], x[h][2 * e + 1], 4 * h + e, off, turn(8 * j + 4 * h + e), near);
+            }
+        }
+      } else {
         turn_row(x, rowbuf[warp * (S::kRowsWarp + 1) + rg], j, pairs, p.r.interleaved, turn);
+      }
+    }
+    if (of[it] < 0) near = 0;
+    while (near) {  // (a pair in some ten thousand)
+      const int e = __ffs(near) - 1;
+      near &= near - 1;
+      const int fa = p.r.interleaved ? 16 * j + 2 * e : u.a + e, fb = p.r.interleaved ? fa + 1 : u.b + e;
+      const int i = 8 * j + e;
+      const float2 y = redo_pair<BF16>(src + tok[it] * src_ts, fa, fb, p8.norm, p8.k_weight, r0, r1, e < n,
+                                       e < n ? p.r.positions + sm.axis_row[i] + tok[it] : nullptr, sm.per_pos[i]);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {  // (features of this lane: units a and b)
+        const int f = (k & 8 ? u.b : u.a) + (k & 7);
+        if (f == fa) x[k >> 3][k & 7] = y.x;
+        if (f == fb) x[k >> 3][k & 7] = y.y;
+      }
     }
     float top = 0.f;
 #pragma unroll

@@ -220,3 +220,42 @@ def test_append_to_blocks_with_the_smallest_factors():
             assert torch.equal(got, ref8.e4m3(k[b, 0].cpu().double() / tiny[b])), b
             assert torch.equal(x[pages[b], :8].view(torch.uint8), old[pages[b], :8])
         assert float(x[pages[3], 8, 0, 5].float()) == 256.0
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("d,pairs,interleaved", [(160, 80, True), (160, 40, False), (128, 64, False), (64, 20, True)])
+def test_append_rounds_keys_as_64_bits_would(d, pairs, interleaved, norm):
+    """No K value falls to the other side of an e4m3 border, unless it lies there within what is left of
+    the arithmetic's error: sine and cosine are off by 2^-27; with a norm, the fp32 sum of squares by
+    20 additions' half steps (2^-25 each, half of it in the root) and the normed values by a step."""
+    T, dt = 40000, HF
+    pages = T // 64
+    k = normal(3, T, 1, d, dtype=dt, std=1.5)
+    pools = [torch.zeros(pages, 64, 1, d, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2)]
+    scales = [torch.zeros(pages, 4, 1, device="cuda") for _ in range(2)]
+    g = torch.Generator().manual_seed(2)
+    pos = torch.randint(0, 100000, (T,), generator=g, dtype=torch.int32).cuda()
+    inv = (10000.0 ** (-torch.arange(pairs, dtype=torch.float64) / pairs)).cuda()
+    w = (torch.rand(d, generator=g) + 0.5).cuda() if norm else None
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    C.attention_varlen_cache8_append(k, k, *pools, *scales, table, i32([0]), i32([0, T]), positions=pos, inv_freq=inv, interleaved=interleaved,
+                                     k_weight=w)
+    x = k[:, 0].double()
+    if norm:
+        x = x / (x.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w.double()
+    ang = pos.double()[:, None] * inv[None]
+    i = torch.arange(pairs, device="cuda")
+    ia, ib = (2 * i, 2 * i + 1) if interleaved else (i, i + pairs)
+    a, b = x[:, ia].clone(), x[:, ib].clone()
+    mag = x.abs()
+    x[:, ia], x[:, ib] = a * ang.cos() - b * ang.sin(), b * ang.cos() + a * ang.sin()
+    mag[:, ia] = mag[:, ib] = a.abs() + b.abs()
+    now = scales[0].view(T // 16, 1, 1).double()
+    assert torch.equal(now.flatten(), ref8.pow2_scale(x.view(T // 16, -1).abs().amax(1).cpu()).cuda())
+    x, mag, got = x.view(T // 16, 16, d) / now, mag.view(T // 16, 16, d) / now, pools[0].view(T // 16, 16, d).double()
+    off = mag * (2.0 ** -21 if norm else 2.0 ** -26)
+    wrong = (got != ref8.e4m3(x)) & (ref8.e4m3(x - off) == ref8.e4m3(x + off))
+    assert not wrong.any(), (int(wrong.sum()), wrong.numel())
+    # values lie anywhere between two borders, a step apart: the share of them that is within `off` of one
+    step = torch.exp2(torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -6))) - 3)
+    assert float((got != ref8.e4m3(x)).double().mean()) <= float((2 * off / step).mean())
