@@ -842,8 +842,9 @@ attn_status attn_varlen_cache8_fwd(
 
 /* Pages as wholes.  The calls below move what pages hold in any number of pools at
  * once -- K and V of every layer, scales too: all pools that one table's page
- * numbers index.  Strides and bytes are multiples of 4 (of 16, with 16-byte
- * aligned bases, they move fastest). */
+ * numbers index.  page_size is the slots of a page, also where no pool has that many
+ * rows.  Strides and bytes are multiples of 4 (of 16, with 16-byte aligned bases, they
+ * move fastest). */
 typedef struct {
   void *base;
   int64_t page_stride, row_stride, piece_stride; /* in BYTES */
@@ -865,7 +866,10 @@ typedef struct {
  * refs [num_pages] counts the table rows that hold a page, 0 means free; other
  * holders (prefix tables) count too and keep a page from being given away (a page
  * held by more rows than it counts is a count out of range).  Partly
- * filled pages have one holder (this call keeps it so).  New pages are the lowest
+ * filled pages have one holder (this call keeps it so).  Only what page numbers index
+ * moves: arrays with a row for each row of the table -- key_pos, scores -- stay as
+ * they are, and where they are in use the caller takes row parents[r] of them into row
+ * r (an index select into another array) in the same step.  New pages are the lowest
  * free ones, in the order of the rows, pages given back in this call among them.
  * Each output may be its input (in place; table_out with the same stride) or lies
  * apart from all inputs; entries of table_out from held_out[r] on are not written.

@@ -193,7 +193,8 @@ def attention_varlen_norm_rotary(q, k, q_weight=None, k_weight=None, positions=N
     ``[T, Hkv, d]`` (or None) -- x / sqrt(mean(x^2) + eps) times fp32 weights
     ``[d]`` (None: ones) -- and turn it by rotary positions in the same pass
     (``inv_freq`` None: no turn; otherwise as attention_varlen_rotary).  Returns
-    (q_out, k_out); ``q_out = q`` and ``k_out = k`` work in place."""
+    (q_out, k_out); ``q_out = q`` and ``k_out = k`` work in place.  With ``eps`` 0 a row
+    of zeros has no norm (NaN)."""
     return _run("norm", stream, q, (q, k, q_weight, k_weight, positions, inv_freq, pair_axis, interleaved, eps,
                                     q_out, k_out))
 
@@ -256,9 +257,15 @@ def attention_varlen_cache_fork(pools, table, lens, held, refs, parents, room=No
     ``parents[r] = r`` with some room reserves pages for an append, leaving a row
     out frees it.
 
+    What a table's rows hold beside the pages -- ``key_pos`` and ``scores`` -- does not
+    move: where they are in use, ``key_pos = key_pos[parents]`` (rows that go on) belongs
+    to the same step.  ``page_size`` is by default the largest number of rows in the
+    pools; with pools of scales alone it has to be given.
+
     Returns (table_out, lens_out, held_out, refs_out), by default in place.  Too few
-    pages or too narrow a table (DEV_NO_PAGES in ``status``), or anything out of
-    range (DEV_BAD_CACHE), and nothing is changed at all."""
+    pages or too narrow a table (DEV_NO_PAGES in ``status``), or anything out of range,
+    a page with more rows than it counts among it (DEV_BAD_CACHE), and nothing is
+    changed at all."""
     return _run("fork", stream, table, (pools, table, lens, held, refs, parents, room, table_out, lens_out, held_out,
                                         refs_out, page_size, workspace, status))
 

@@ -44,3 +44,27 @@ def test_fork_of_pages_that_others_hold_too():
     C.attention_varlen_cache_fork([pool], t, lens, held, refs, i32([-1, 1]), i32([0, 16]), status=st)
     torch.cuda.synchronize()
     assert int(st) == 0 and refs.tolist() == [2, 1, 0, 2, 0, 1] and t[1].tolist() == [5, 1] and held.tolist() == [0, 2]
+
+
+def test_beams_with_key_positions():
+    """Children of a row whose slots stand in another order read their parent's positions once the
+    caller has taken them along, as the documentation says."""
+    page, Hkv, d, Hq, N = 16, 1, 64, 4, 12
+    g = torch.Generator(device="cuda").manual_seed(5)
+    kc, vc = (torch.randn(N, page, Hkv, d, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    t, lens, held = i32([[3, 7, 0], [9, 0, 0], [4, 0, 0]]), i32([20, 5, 9]), i32([2, 1, 1])
+    refs = i32([0, 0, 0, 1, 1, 0, 0, 1, 0, 1, 0, 0])
+    key_pos = torch.stack([torch.randperm(48, device="cuda", generator=g) for _ in range(3)]).int()[:, None].contiguous()
+    q = torch.randn(3, Hq, d, device="cuda", generator=g).to(torch.bfloat16)
+    slopes = torch.full((3, Hq), 0.3, device="cuda")
+
+    def attend(positions):
+        return C.attention_varlen_cache_fwd(q[:1].expand(3, Hq, d).contiguous(), kc, vc, t, lens, i32([0, 1, 2, 3]), slopes, key_pos=positions,
+                                            q_pos=i32([30] * 3), window_left=25, window_right=0)[0]
+
+    want = attend(key_pos)[:1].clone()
+    parents = i32([0, 0, 0])
+    C.attention_varlen_cache_fork([kc, vc], t, lens, held, refs, parents)
+    got = attend(key_pos[parents.long()].contiguous())
+    assert all(torch.equal(got[r:r + 1], want) for r in range(3))
+    assert not torch.equal(attend(key_pos)[1:2], want)  # (left behind, they are the old row's)
