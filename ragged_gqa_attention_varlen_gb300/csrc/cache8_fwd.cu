@@ -50,14 +50,16 @@ bool encode_bytes(CUtensorMap* m, const CacheParams& p, const Pages& pg, int wid
 // Few rows a key: a sequence's tokens have at most kFewMost rows in a K/V head.  (The
 // kernel for few rows is right for any number; it takes 8 rows at a time and reads the
 // keys once for each 8.)  96 sequences over 425000 keys of 8 heads, d = 128, its time and
-// that of the tiles of 128 rows: 4 rows 166 and 371 us, 8 rows 173 and 372, 16 rows 323
-// and 373 (capped 333 and 419), 24 rows 471 and 373; 16 rows of one head of 160: 74 and
-// 74.  Prefixes bring the rows of many sequences together and stay with the tiles.
+// that of the tiles of 128 rows: 4 rows 167 and 409 us, 8 rows 175 and 409, 16 rows 328
+// and 411 (capped 355 and 440), 24 rows 482 and 411; 16 rows of one head of 160: 76 and
+// 78.  Prefixes bring the rows of many sequences together and stay with the tiles.
 //
 // What the host knows is the average.  Where it is above kFewMost, or with prefixes, the
 // tiles take all.  With one token a sequence (total_q = B) the kernel for few rows
-// takes all.  Otherwise both are launched and each takes its sequences by their own rows:
-// one prompt among single tokens would re-read its keys for every 8 of its rows.  255
+// takes all: idle tiles behind it would cost 96 single tokens 9 us of 156 (the same
+// number of tokens in a few of the sequences is right all the same, and slower).
+// Otherwise both are launched and each takes its sequences by their own rows: one
+// prompt among single tokens would re-read its keys for every 8 of its rows.  255
 // single tokens over 500 to 8000 keys and one prompt of 769, 32 heads over 8 of 128, both
 // kernels, the few-rows one alone, the tiles alone: a prompt behind nothing 442, 1053 and
 // 1188 us, behind 60000 keys 1804, 7270 and 2527; one sequence of 200 tokens over 16000

@@ -43,9 +43,10 @@
 // there, and 0 * NaN would reach O), 4-11 softmax as in cache_fwd.cuh.
 //
 // Measured with the join: 144 drafted tokens of 96 heads behind two prefixes of 12001
-// keys 214 us (575 TFLOP/s of the logits' and outputs' products), 64 single tokens of
-// 80 heads over 277000 keys in 16-row pages 58.5 us (1.5 TB/s), one token of 96 heads
-// over 700 keys 18.9 us.  A step takes about 4000 clk: 3600 of softmax (four passes of
+// keys 226 us (546 TFLOP/s of the logits' and outputs' products), 64 single tokens of
+// 80 heads over 277000 keys in 16-row pages 61 us (1.45 TB/s), one token of 96 heads
+// over 700 keys 19 us.  The second row sum is 11 and 2.5 us of the first two; without it
+// a step took about 4000 clk: 3600 of softmax (four passes of
 // 16 columns, two warps in each sub-partition, at half of the issue slots; the fetch
 // of instructions is the largest stall that is not a dependency), the rest the
 // hand-offs to the products (1300 clk of tensor work) and back.  Loading the next

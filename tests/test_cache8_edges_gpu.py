@@ -79,6 +79,29 @@ def test_rows_by_their_own_size(c, scales):
     assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
 
 
+@pytest.mark.parametrize("c", MIXED[:3])
+def test_both_kernels_captured_and_on_two_streams(c):
+    """Where both kernels work, the tiles start beside the other's last CTAs: the same bits captured,
+    replayed between other calls, and on two streams at once."""
+    kc, q, cu_q, opt, call = build(c, 16, seed=5)
+    want = attend(q, kc, cu_q, call)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pairs = [attend(q, kc, cu_q, call, stream=s) for _ in range(5) for s in (s1, s2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for r in pairs for x, y in zip(r, want))
+    out, lse, ws = torch.empty_like(q).contiguous(), torch.empty(q.shape[:2], device="cuda"), torch.empty(1 << 27, dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            attend(q, kc, cu_q, call, out=out, lse=lse, workspace=ws)
+    for _ in range(3):
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("odd", [False, True])
 @pytest.mark.parametrize("apart", [20, 30, 40])
 @pytest.mark.parametrize("Hq,cap", [(8, 0.0), (48, 0.0), (48, 3.0)])
